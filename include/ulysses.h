@@ -393,6 +393,166 @@ uly_status ulysses_loss_aggregate_noalloc(int32_t world, int64_t tokens, int32_t
                                           float *shard_sum, int64_t *shard_count, float *loss,
                                           void *stream);
 
+/*
+ * The token-wise operators around the attention layer.  Every rank runs them
+ * on its own tokens (the pages' layer is shard -> QKV projection -> attention
+ * -> output projection, "Paralelismul de Secvență Ulysses", section
+ * "Mecanismul de funcționare Ulysses"; a rank's norms, feed-forward products
+ * and loss need no exchange), so the seq layout [P][B][n/P][width] is taken as
+ * rows of tokens.
+ */
+
+/* Activation of ulysses_linear. */
+enum {
+  ULY_ACT_NONE = 0,    /* z                                                        */
+  ULY_ACT_GELU = 1,    /* tanh form: 0.5 z (1 + tanh(sqrt(2/pi)(z + 0.044715 z^3))) */
+  ULY_ACT_SILU = 2,    /* z / (1 + exp(-z))                                        */
+  ULY_ACT_SWIGLU = 3   /* silu(z_gate) z_up: w holds out_features gate rows, then
+                        * out_features up rows (bias and pre alike)                */
+};
+
+/* Bytes of device workspace ulysses_linear needs on the current device (0 for
+ * products with enough tiles to fill it: the workspace may then be NULL). */
+uly_status ulysses_linear_workspace_size(int64_t tokens, int32_t in_features, int32_t out_features,
+                                         int32_t activation, size_t *bytes);
+
+/*
+ * Matrix product with bias, activation and residual in its epilogue:
+ *   z(t) = x(t) w^T + bias,   y(t) = act(z(t)) + residual(t).
+ * bf16 in and out, fp32 accumulation; y is formed from the fp32 z and rounded
+ * once, and so is `pre`.
+ *   x:        DEVICE bf16 [tokens][in_features] (the seq layout's rows)
+ *   w:        DEVICE bf16 [nz][in_features], nz = out_features, or twice that
+ *             for ULY_ACT_SWIGLU
+ *   bias:     NULL or DEVICE bf16 [nz]
+ *   residual: NULL or DEVICE bf16 [tokens][out_features]; may be y itself
+ *   y:        DEVICE bf16 [tokens][out_features]
+ *   pre:      NULL or DEVICE bf16 [tokens][nz]: z, kept for the backward
+ * tokens >= 0 (0 does nothing); in_features and out_features multiples of 8
+ * (else ULY_ERR_ALIGN).  Few tokens are bound by w's bytes: the product is then
+ * cut along in_features over all SMs into fp32 partials (`workspace`), added in
+ * a fixed order.  Bitwise repeatable.  Outputs must not overlap anything else.
+ */
+uly_status ulysses_linear(int64_t tokens, int32_t in_features, int32_t out_features, int32_t activation,
+                          const void *x, const void *w, const void *bias, const void *residual, void *y, void *pre,
+                          void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bytes of device workspace ulysses_linear_bwd needs on the current device. */
+uly_status ulysses_linear_bwd_workspace_size(int64_t tokens, int32_t in_features, int32_t out_features,
+                                             int32_t activation, size_t *bytes);
+
+/*
+ * Backward of ulysses_linear (gradients of sum(y * dy); the residual's is dy):
+ *   dz = dy act'(z) (swiglu: by z_gate and z_up),  dx = dz w,
+ *   dw = sum over all tokens of dz^T x,  dbias = sum over all tokens of dz.
+ *   pre:   z as the forward kept it, bf16 [tokens][nz]; not read for ULY_ACT_NONE
+ *   dy:    DEVICE bf16 [tokens][out_features]
+ *   dx:    NULL or DEVICE bf16 [tokens][in_features]
+ *   dw:    NULL or DEVICE [nz][in_features] of dw_dtype (ULY_F32 or ULY_BF16)
+ *   dbias: NULL or DEVICE float [nz]
+ * dz is rounded to bf16 once, as the products' operand (dbias sums it before);
+ * fp32 accumulation; dx and a bf16 dw are rounded once.  tokens = 0 gives zero
+ * dw and dbias.  x is only read for dw, w only for dx.  Same rules as
+ * ulysses_linear; bitwise repeatable.
+ */
+uly_status ulysses_linear_bwd(int64_t tokens, int32_t in_features, int32_t out_features, int32_t activation,
+                              const void *x, const void *w, const void *pre, const void *dy, void *dx, void *dw,
+                              int32_t dw_dtype, float *dbias, void *workspace, size_t workspace_bytes, void *stream);
+
+/* What the gate of ulysses_residual_norm is broadcast along. */
+enum {
+  ULY_GATE_NONE = 0,
+  ULY_GATE_CHANNEL = 1,    /* [hidden]: one for all tokens                */
+  ULY_GATE_SEQUENCE = 2,   /* [B][hidden]: one for each sequence          */
+  ULY_GATE_TOKEN = 3       /* [P][B][n/P][hidden]: one for each token     */
+};
+
+/*
+ * Norms before and after a block, fused with the block's gate and the scale of
+ * the residual stream:
+ *   r = res_scale x + gate * N(h; w_post),   u = N(r; w_pre),
+ *   N(v; w)_j = w_j v_j / sqrt(mean_j v_j^2 + eps)   (w_post NULL: N(h) = h).
+ * x is the residual stream, h the block's output, r the new residual stream and
+ * u the next block's input; all in the seq layout [P][B][n/P][hidden] and of
+ * `dtype` (ULY_BF16 or ULY_F32), like gate, w_post and w_pre ([hidden]).
+ *   h NULL: r = res_scale x (the first block); needs no gate and no w_post
+ *   r NULL: not stored;   u NULL: not formed (w_pre is then not read)
+ * Sums in fp32; u is formed from the unrounded r; r and u are rounded once.
+ * Needs n % P == 0, hidden rows of a multiple of 16 bytes (else ULY_ERR_ALIGN)
+ * and at most 64 KB (else ULY_ERR_UNSUPPORTED), eps >= 0.  r may be x or h
+ * itself and u may be h itself; outputs otherwise overlap nothing.
+ */
+uly_status ulysses_residual_norm(int32_t batch, int32_t seq_len, int32_t world, int32_t hidden, int32_t dtype,
+                                 const void *x, const void *h, const void *gate, int32_t gate_mode,
+                                 const void *w_post, const void *w_pre, float res_scale, float eps, void *r, void *u,
+                                 void *stream);
+
+/* Bytes of device workspace ulysses_residual_norm_bwd needs on the current
+ * device: the column sums' partials. */
+uly_status ulysses_residual_norm_bwd_workspace_size(int32_t batch, int32_t seq_len, int32_t hidden, int32_t dtype,
+                                                    int32_t gate_mode, size_t *bytes);
+
+/*
+ * Backward of ulysses_residual_norm: the gradients of sum(r * dr) + sum(u * du).
+ *   r:  the forward's stored r (its root mean square is formed again from it)
+ *   dr: NULL (zero) or like r;  du: NULL (zero; r and w_pre are not read) or like u;
+ *       not both NULL
+ *   dx, dh: NULL or like x, h
+ *   dw_post, dw_pre: NULL or DEVICE float [hidden]
+ *   dgate: NULL or DEVICE float [hidden] (ULY_GATE_CHANNEL), float [B][hidden]
+ *          (ULY_GATE_SEQUENCE), or like the gate (ULY_GATE_TOKEN)
+ * h NULL as in the forward (no dh, dw_post, dgate).  Column sums in fp32, in a
+ * fixed order: bitwise repeatable.  Outputs overlap no input and no other
+ * output, but dx may be dr itself and dh may be du itself.
+ */
+uly_status ulysses_residual_norm_bwd(int32_t batch, int32_t seq_len, int32_t world, int32_t hidden, int32_t dtype,
+                                     const void *r, const void *h, const void *dr, const void *du, const void *gate,
+                                     int32_t gate_mode, const void *w_post, const void *w_pre, float res_scale,
+                                     float eps, void *dx, void *dh, float *dw_post, float *dw_pre, void *dgate,
+                                     void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bytes of device workspace ulysses_linear_loss needs. */
+uly_status ulysses_linear_loss_workspace_size(int32_t world, int64_t tokens, int32_t hidden, int32_t vocab,
+                                              size_t *bytes);
+
+/*
+ * ulysses_loss_aggregate straight from the hidden states: the logits are
+ * z = x w^T ("Integrarea cu Accelerate": every shard's loss is weighted by its
+ * valid-token count), formed tile by tile on the tensor cores and never stored.
+ *   x: DEVICE bf16 [P][tokens/P][hidden];  w: DEVICE bf16 [vocab][hidden]
+ * labels, ignore_index, shard_sum, shard_count, loss and errors as
+ * ulysses_loss_aggregate, on the unrounded fp32 logits.  hidden must be a
+ * multiple of 8 (else ULY_ERR_ALIGN); tokens and vocab are free.  Bitwise
+ * repeatable.
+ */
+uly_status ulysses_linear_loss(int32_t world, int64_t tokens, int32_t hidden, int32_t vocab, const void *x,
+                               const void *w, const int32_t *labels, int32_t ignore_index, float *shard_sum,
+                               int64_t *shard_count, float *loss, void *workspace, size_t workspace_bytes,
+                               void *stream);
+
+/* Bytes of device workspace ulysses_linear_loss_bwd needs on the current device. */
+uly_status ulysses_linear_loss_bwd_workspace_size(int32_t world, int64_t tokens, int32_t hidden, int32_t vocab,
+                                                  int32_t dw_dtype, int64_t piece_tokens, size_t *bytes);
+
+/*
+ * The loss and its gradients in one call:
+ *   dz(t)_v = (softmax(z(t))_v - [v == y_t]) / C   (counted tokens; else 0),
+ *   dx = dz w  (bf16, like x),   dw = sum over all tokens of dz^T x
+ *   ([vocab][hidden] of dw_dtype, ULY_F32 or ULY_BF16),
+ * with the global count C as the only denominator, as ulysses_loss_aggregate_bwd.
+ * The tokens are taken in pieces: a piece's exponentials are held in the
+ * workspace in bf16 (piece_tokens x vocab x 2 bytes), all tokens' never are.
+ * piece_tokens = 0: as many tokens as fit 4 GiB of them (at least 256).
+ * Several pieces sum dw in fp32 (for ULY_BF16 in vocab x hidden x 4 bytes of
+ * the workspace) and round it once.  Rows of ignored or invalid labels give
+ * zeros whatever x holds there.  With no counted token dx and dw are 0 and
+ * *loss is NaN.  Same rules as ulysses_linear_loss; bitwise repeatable.
+ */
+uly_status ulysses_linear_loss_bwd(int32_t world, int64_t tokens, int32_t hidden, int32_t vocab, const void *x,
+                                   const void *w, const int32_t *labels, int32_t ignore_index, void *dx, void *dw,
+                                   int32_t dw_dtype, int64_t piece_tokens, float *shard_sum, int64_t *shard_count,
+                                   float *loss, void *workspace, size_t workspace_bytes, void *stream);
+
 /* Device address of the current device's asynchronous error word (int32;
  * bit s set <=> status s was raised by a kernel since it was last cleared),
  * for callers that poll it themselves (e.g. with their own stream-ordered
@@ -414,7 +574,7 @@ uly_status ulysses_read_error_info(int32_t *info, int32_t n);
 /*
  * Failure detection (no counterpart on the pages: the tcgen05 kernels wait on
  * mbarriers, and every such wait is bounded).  Sets how many SM clock cycles a
- * pipeline wait of the attention and projection kernels launched from now on
+ * pipeline wait of the attention, projection and linear kernels launched from now on
  * may last before the kernel records ULY_ERR_TIMEOUT (and where, see
  * ulysses_read_error_info), drains its copies and MMAs, frees its tensor
  * memory and returns.  cycles = 0 restores the built-in limit (2e9 cycles,

@@ -1,0 +1,471 @@
+// Matrix products C[M][N] = A[M][K] B[N][K]^T on the 5th-generation tensor
+// cores with an epilogue of the caller's, for the token-wise operators (the
+// linear product and its gradients, the linear loss and its gradients).
+//
+// bf16 operands, fp32 accumulators.  A cluster of two CTAs on neighbouring SMs
+// computes one 256 x 256 tile (tcgen05 cta_group::2, M = 256): each CTA holds
+// 128 rows of A, 128 rows of B and the accumulator of its own 128 rows, so
+// every byte of B in shared memory feeds two tensor cores and a k-step of 64
+// costs each SM 32 KB of loads instead of the 48 KB of a 128 x 256 tile of its
+// own.  K runs in steps of 64 columns (one 128-byte swizzle span).  The kernel
+// is persistent: one cluster per SM pair walks the work units (a tile, or one
+// of `splits` parts of a tile's k-steps).
+//
+// Warps (384 threads): 0 TMA (both CTAs load their own halves, all completing
+// on the leader's barriers), 1 MMA issue (the leader CTA's), 2 tensor memory,
+// 4-11 epilogue: two warpgroups take the two 128-column halves of the CTA's
+// 128 rows, one row a thread, while the next tile fills the other accumulator.
+//
+// An operand is K-major (rows of K contiguous elements, 128-row boxes) or
+// MN-major (rows of M or N contiguous elements, 64 x 64 boxes).  Elements
+// past any edge are read as zeros and never stored, so M, N and K are free.
+//
+// Every wait is bounded (ULY_ERR_TIMEOUT); a launch that gives up lets its
+// copies land before it frees its tensor memory and returns.
+#pragma once
+
+#include <type_traits>
+
+#include "prof.cuh"
+#include "sm100.cuh"
+
+namespace uly {
+namespace gemm {
+
+using namespace sm100;
+
+constexpr int kTile = 256;       // rows and columns of a cluster's tile
+constexpr int kHalf = 128;       // rows of A and of B in one CTA
+constexpr int kBK = 64;
+constexpr int kStages = 6;
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 128 + 32 * kEpiWarps;
+constexpr uint32_t kOperandBytes = kHalf * kBK * 2;        // 16 KB
+constexpr uint32_t kStageBytes = 2 * kOperandBytes;        // one CTA's A and B of a k-step
+constexpr uint32_t kOffBar = kStages * kStageBytes;
+constexpr uint32_t kSmemBytes = kOffBar + 256 + 1024;      // barriers + alignment slack
+constexpr long long kLandCycles = 1 << 20;                 // after giving up: the copies in flight land (~0.5 ms)
+
+// The product and how it is cut into work.
+struct Shape {
+  int m_tiles, n_tiles, splits;
+  int k_steps;          // ceil(K / 64)
+  int group_m;          // tiles in flight form blocks of group_m rows of tiles (operands shared in L2)
+  int b_step, b_half;   // B row of tile nt, CTA r: nt * b_step + r * b_half
+  int *err;
+  long long wait_limit;
+};
+
+__device__ __forceinline__ uint32_t cluster_ctarank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+// The address of the same shared-memory location in the cluster's CTA `rank`.
+__device__ __forceinline__ uint32_t map_cta(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// Tile load into this CTA's shared memory, completing on a barrier of the
+// CTA pair's leader.
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap *map, uint32_t bar, int c0, int c1) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t dst_smem, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(ncols)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_relinquish_pair() {
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+// Arrive once on the barrier at `bar`'s offset in both CTAs when every MMA
+// this thread issued so far has completed.
+__device__ __forceinline__ void tc_commit_pair(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+      "h"((uint16_t)3)
+      : "memory");
+}
+__device__ __forceinline__ void mma_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                         uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(acc)
+      : "memory");
+}
+
+// Which tile and which part of its k-steps a work unit is.  The units of a
+// tile follow one another; tiles go down group_m rows before the next column.
+struct Unit {
+  int mt, nt, split, k0, k1;
+};
+__device__ __forceinline__ Unit unit_of(const Shape &s, int u) {
+  Unit r;
+  const int tile = u / s.splits;
+  r.split = u - tile * s.splits;
+  const int per = s.group_m * s.n_tiles, g = tile / per, in = tile - g * per;
+  const int first = g * s.group_m, rows = min(s.group_m, s.m_tiles - first);
+  r.nt = in / rows;
+  r.mt = first + in - r.nt * rows;
+  r.k0 = (int)((long long)s.k_steps * r.split / s.splits);
+  r.k1 = (int)((long long)s.k_steps * (r.split + 1) / s.splits);
+  return r;
+}
+
+// Epi::Params, and
+//   Epi::tile(params, unit, acc, row, half): one thread's 128 accumulators
+//   (tensor-memory columns [acc, acc + 128), waited for before it returns) of
+//   C row `row`, columns [128 half, +128) of tile column unit.nt.
+template <class Epi, bool A_MN, bool B_MN>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    gemm_pair_sm100_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                           const __grid_constant__ Shape sh, const __grid_constant__ typename Epi::Params ep) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sb = smem_u32(smem);
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + kOffBar);
+  enum { B_FULL = 0, B_EMPTY = kStages, B_ACCF = 2 * kStages, B_ACCE = B_ACCF + 2, B_N = B_ACCE + 2 };
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + kOffBar + 8 * B_N);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + kOffBar + 8 * B_N + 4);
+  auto bar = [&](int i) { return smem_u32(&bars[i]); };
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const int cluster = blockIdx.x >> 1, clusters = gridDim.x >> 1;
+  const int units = sh.m_tiles * sh.n_tiles * sh.splits;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < B_N; ++i) mbar_init(bar(i), i >= B_ACCE ? 2 * kEpiWarps : 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(&tmB);
+  }
+  if (warp == 2) {
+    tmem_alloc_pair(smem_u32(tmem_slot), 512);
+    tmem_relinquish_pair();
+    tc_fence_before();
+  }
+  __syncthreads();
+  cluster_sync();   // both CTAs' barriers exist before any arrival crosses over
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------------ TMA
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 1;   // the ring's slots start free
+      bool ok = true;
+      for (int u = cluster; ok && u < units; u += clusters) {
+        const Unit w = unit_of(sh, u);
+        const int a0 = w.mt * kTile + (int)rank * kHalf, b0 = w.nt * sh.b_step + (int)rank * sh.b_half;
+        for (int k = w.k0; k < w.k1; ++k) {
+          ok = mbar_wait(bar(B_EMPTY + stage), phase, abort_flag, sh.err, sh.wait_limit);
+          if (!ok) break;
+          const uint32_t sA = sb + stage * kStageBytes, sB = sA + kOperandBytes;
+          // the leader's barrier counts the bytes of both CTAs
+          const uint32_t full = map_cta(bar(B_FULL + stage), 0);
+          if (rank == 0) mbar_arrive_expect_tx(bar(B_FULL + stage), 2 * kStageBytes);
+          if (A_MN) {
+            tma_load_2d_pair(sA, &tmA, full, a0, k * kBK);
+            tma_load_2d_pair(sA + 8192, &tmA, full, a0 + 64, k * kBK);
+          } else {
+            tma_load_2d_pair(sA, &tmA, full, k * kBK, a0);
+          }
+          if (B_MN) {
+            tma_load_2d_pair(sB, &tmB, full, b0, k * kBK);
+            tma_load_2d_pair(sB + 8192, &tmB, full, b0 + 64, k * kBK);
+          } else {
+            tma_load_2d_pair(sB, &tmB, full, k * kBK, b0);
+          }
+          if (++stage == kStages) { stage = 0; phase ^= 1; }
+        }
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------------ MMA
+    if (lane == 0 && rank == 0) {
+      constexpr uint32_t idesc = idesc_bf16_f32(kTile, kTile, A_MN, B_MN);
+      // K-major: 16 K-elements are 32 bytes along a row; MN-major: 16 K-rows
+      // are 2048 bytes, the 64-element MN chunks 8 KB apart (LBO)
+      constexpr uint32_t astep = A_MN ? 2048 : 32, bstep = B_MN ? 2048 : 32;
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      int it = 0;
+      for (int u = cluster; ok && u < units; u += clusters, ++it) {
+        const Unit w = unit_of(sh, u);
+        const int buf = it & 1;
+        if (it >= 2) {
+          ok = mbar_wait(bar(B_ACCE + buf), (uint32_t)(((it >> 1) - 1) & 1), abort_flag, sh.err, sh.wait_limit);
+          if (!ok) break;
+          tc_fence_after();
+        }
+        const uint32_t acc = tmem + buf * kTile;
+        for (int k = w.k0; k < w.k1; ++k) {
+          const uint32_t sA = sb + stage * kStageBytes, sB = sA + kOperandBytes;
+          const uint64_t da = A_MN ? sdesc_sw128(sA, 8192, 1024) : sdesc_sw128(sA, 16, 1024);
+          const uint64_t db = B_MN ? sdesc_sw128(sB, 8192, 1024) : sdesc_sw128(sB, 16, 1024);
+          ok = mbar_wait(bar(B_FULL + stage), phase, abort_flag, sh.err, sh.wait_limit);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < kBK / 16; ++kk)
+            mma_pair(acc, sdesc_add(da, kk * astep), sdesc_add(db, kk * bstep), idesc,
+                     (k > w.k0 || kk > 0) ? 1u : 0u);
+          tc_commit_pair(bar(B_EMPTY + stage));
+          if (++stage == kStages) { stage = 0; phase ^= 1; }
+        }
+        if (!ok) break;
+        tc_commit_pair(bar(B_ACCF + buf));
+      }
+    }
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------- epilogue
+    const int quarter = warp & 3, half = (warp - 4) >> 2;
+    int it = 0;
+    for (int u = cluster; u < units; u += clusters, ++it) {
+      const int buf = it & 1;
+      if (!__all_sync(0xffffffffu, mbar_wait(bar(B_ACCF + buf), (uint32_t)((it >> 1) & 1), abort_flag, sh.err,
+                                             sh.wait_limit)))
+        break;
+      tc_fence_after();
+      const Unit w = unit_of(sh, u);
+      const uint32_t acc = tmem + ((uint32_t)(quarter * 32) << 16) + buf * kTile;
+      Epi::tile(ep, w, acc, w.mt * kTile + (int)rank * kHalf + quarter * 32 + lane, half);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) arrive_cluster(map_cta(bar(B_ACCE + buf), 0));
+    }
+  }
+
+  // Normal end: every copy was consumed by an MMA and every MMA was waited for
+  // by both CTAs' epilogues.  After giving up, copies and MMAs may still be in
+  // flight: give them time to finish before the pair parts.
+  tc_fence_before();
+  __syncthreads();
+  if (*abort_flag) {
+    const long long t0 = clock64();
+    while (clock64() - t0 < kLandCycles) __nanosleep(1000);
+  }
+  cluster_sync();
+  if (warp == 2) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+// ------------------------------------------------------------------- host
+
+// 2-D bf16 map of a [rows][inner] matrix with rows `stride` elements apart;
+// 64-column boxes of box_rows rows (128: a K-major operand, 64: an MN-major
+// one).  Elements past either edge read as zero.
+inline bool make_map(CUtensorMap *map, const void *base, long long inner, long long rows, long long stride,
+                     int box_rows) {
+  static std::atomic<void *> fn{nullptr};
+  void *p = fn.load(std::memory_order_acquire);
+  if (!p) {
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      return false;
+    fn.store(p, std::memory_order_release);
+  }
+  cuuint64_t dims[2] = {(cuuint64_t)inner, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)stride * 2};
+  cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
+  cuuint32_t es[2] = {1, 1};
+  return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p)(
+             map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Parts to cut each tile's k-steps into.  Work units on `clusters` SM pairs
+// take ceil(units / clusters) turns of ceil(k_steps / splits) k-steps (512
+// cycles of MMA each) plus an epilogue that overlaps the next unit; a cut
+// writes and reads fp32 partials (M x N of them for each part) and launches
+// one more kernel.  Few rows leave most of the machine idle without a cut; a
+// last turn that is almost empty costs a large product up to a turn.
+inline int choose_splits(long long M, long long N, long long m_tiles, long long n_tiles, long long k_steps, int sms) {
+  const double step_us = 512.0 / 1700.0, clusters = sms / 2;
+  int best = 1;
+  double best_t = 1e30;
+  for (int s = 1; s <= 32 && s * 2 <= (k_steps > 1 ? k_steps : 2); ++s) {
+    const double turns = (double)((m_tiles * n_tiles * s + (int)clusters - 1) / (int)clusters);
+    double t = turns * (double)((k_steps + s - 1) / s) * step_us + 2.0;
+    if (s > 1) t += 3.0 + (double)s * M * N * 8.0 / 5e6;
+    if (t < best_t * 0.97) { best_t = t; best = s; }
+  }
+  return best;
+}
+
+// Work units, raster and rest of a launch.  `n_tile` output columns of one
+// tile column: 256, or 128 where B holds two rows for each of them.
+inline Shape make_shape(long long M, long long N, long long K, int n_tile, int splits) {
+  Shape s = {};
+  s.m_tiles = (int)((M + kTile - 1) / kTile);
+  s.n_tiles = (int)((N + n_tile - 1) / n_tile);
+  s.splits = splits;
+  s.k_steps = (int)((K + kBK - 1) / kBK);
+  s.group_m = 8;
+  s.b_step = n_tile;
+  s.b_half = n_tile == kTile ? kHalf : (int)N;
+  s.err = error_word();
+  s.wait_limit = wait_limit_cycles();
+  return s;
+}
+
+template <class Epi, bool A_MN, bool B_MN>
+uly_status launch(const CUtensorMap &ta, const CUtensorMap &tb, const Shape &s, const typename Epi::Params &ep,
+                  cudaStream_t stream) {
+  static std::atomic<uint64_t> optin{0};
+  auto kernel = gemm_pair_sm100_kernel<Epi, A_MN, B_MN>;
+  if (!smem_optin(kernel, kSmemBytes, optin)) return ULY_ERR_CUDA;
+  const long long units = (long long)s.m_tiles * s.n_tiles * s.splits;
+  const int pairs = device_sm_count() / 2;
+  const int grid = 2 * (int)(units < pairs ? units : pairs);
+  kernel<<<grid, kThreads, kSmemBytes, stream>>>(ta, tb, s, ep);
+  note_launches(1);
+  return last_launch_status();
+}
+
+// ---------------------------------------------------- vectors of 8 columns
+__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&x)[8]) {
+  const uint4 u = __ldg(reinterpret_cast<const uint4 *>(p));
+  const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&u);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float2 f = __bfloat1622float2(h[e]);
+    x[2 * e] = f.x;
+    x[2 * e + 1] = f.y;
+  }
+}
+__device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&x)[8]) {
+  *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
+                                             pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+}
+__device__ __forceinline__ void load8(const float *p, float (&x)[8]) {
+  const float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 4);
+  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+}
+__device__ __forceinline__ void store8(float *p, const float (&x)[8]) {
+  reinterpret_cast<float4 *>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+  reinterpret_cast<float4 *>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+}
+
+// --------------------------------------------------------- plain epilogue
+// out = scale[row] * (A B^T) + add, in bf16 or fp32; N is a multiple of 8.
+// A row whose scale is 0 is stored as zeros whatever the product holds.
+struct PlainParams {
+  void *out;
+  const float *add;         // nullable fp32 [M][N] (may be `out` itself, fp32)
+  const float *row_scale;   // nullable [M]
+  float *part;              // splits > 1: fp32 [splits][M][N] instead of everything above
+  long long M;
+  int N, out_f32;
+};
+struct EpiPlain {
+  using Params = PlainParams;
+  static __device__ __forceinline__ void store(const Params &p, long long row, int col, float (&z)[8]) {
+    const long long at = row * p.N + col;
+    if (p.row_scale) {
+      const float f = __ldg(p.row_scale + row);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) z[e] = f == 0.f ? 0.f : z[e] * f;
+    }
+    if (p.add) {
+      float a[8];
+      load8(p.add + at, a);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) z[e] += a[e];
+    }
+    if (p.out_f32) store8(static_cast<float *>(p.out) + at, z);
+    else store8(static_cast<__nv_bfloat16 *>(p.out) + at, z);
+  }
+  static __device__ __forceinline__ void tile(const Params &p, const Unit &w, uint32_t acc, int row, int half) {
+#pragma unroll 1
+    for (int c = 0; c < kHalf; c += 32) {
+      uint32_t a[32];
+      tmem_ld32(acc + half * kHalf + c, a);
+      if (row < p.M) {
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const int col = w.nt * kTile + half * kHalf + c + 8 * g;
+          if (col < p.N) {
+            float z[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) z[e] = __uint_as_float(a[8 * g + e]);
+            if (p.part) store8(p.part + ((long long)w.split * p.M + row) * p.N + col, z);
+            else store(p, row, col, z);
+          }
+        }
+      }
+      __syncwarp();
+    }
+  }
+};
+
+// Sum of a cut product's partials, in the order of the parts, and its epilogue.
+static __global__ void __launch_bounds__(256) plain_join_kernel(const PlainParams p, int splits) {
+  const int vecs = p.N / 8;
+  const long long total = p.M * vecs;
+  for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < total;
+       i += (long long)gridDim.x * blockDim.x) {
+    const long long row = i / vecs;
+    const int col = (int)(i - row * vecs) * 8;
+    float z[8] = {};
+    for (int s = 0; s < splits; ++s) {
+      float v[8];
+      load8(p.part + ((long long)s * p.M + row) * p.N + col, v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) z[e] += v[e];
+    }
+    EpiPlain::store(p, row, col, z);
+  }
+}
+
+inline unsigned join_blocks(long long vecs) {
+  long long b = (vecs + 255) / 256;
+  const long long most = (long long)device_sm_count() * 8;
+  return (unsigned)(b < most ? (b < 1 ? 1 : b) : most);
+}
+
+inline size_t part_bytes(long long M, long long N, int splits) {
+  return splits > 1 ? (size_t)splits * M * N * sizeof(float) : 0;
+}
+
+// out[M][N] (+)= A B^T with a plain epilogue; `part` holds part_bytes().
+template <bool A_MN, bool B_MN>
+uly_status launch_plain(const CUtensorMap &ta, const CUtensorMap &tb, PlainParams p, long long K, int splits,
+                        float *part, int kernel_id, cudaStream_t stream) {
+  const long long k_steps = (K + kBK - 1) / kBK;
+  if (splits > k_steps) splits = (int)k_steps;   // a short last piece: no part without a k-step
+  p.part = splits > 1 ? part : nullptr;
+  prof::Scope scope(kernel_id, stream);
+  const uly_status st = launch<EpiPlain, A_MN, B_MN>(ta, tb, make_shape(p.M, p.N, K, kTile, splits), p, stream);
+  if (st != ULY_OK || splits == 1) return st;
+  plain_join_kernel<<<join_blocks(p.M * (p.N / 8)), 256, 0, stream>>>(p, splits);
+  note_launches(1);
+  return last_launch_status();
+}
+
+}  // namespace gemm
+}  // namespace uly

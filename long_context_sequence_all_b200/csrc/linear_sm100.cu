@@ -1,0 +1,346 @@
+// The linear product of a rank's tokens with its epilogue, and its gradients:
+//
+//   z = x W^T + bias        y = act(z) + residual
+//
+// act: identity, gelu (tanh form), silu, or swiglu, where W holds the gate's
+// rows and then the other factor's, y = silu(z_gate) z_up: a tile takes the
+// same 128 features of both, so the two halves of an accumulator row meet in
+// one thread.  y comes from the fp32 z; y and the optionally kept z are rounded
+// to bf16 once each.
+//
+// Backward: dz = dy act'(z) is formed once (bf16, the products' operand type;
+// the bias gradient takes it in fp32 before that rounding), then dx = dz W and
+// dW = dz^T x on the tensor cores, dW with both operands MN-major.
+//
+// Bound by the tensor cores from a few hundred tokens on, by W's bytes below.
+#include "gemm_sm100.cuh"
+#include "tokenwise.cuh"
+
+namespace uly {
+
+using namespace gemm;
+
+namespace {
+
+// 1 / (1 + e^-v): e^-v overflows to infinity for large negative v, and the
+// quotient is then 0.
+__device__ __forceinline__ float sigmoid_fast(float v) {
+  return __fdividef(1.f, 1.f + ex2_approx(v * -1.4426950408889634f));
+}
+
+// gelu, tanh form: 0.5 z (1 + tanh(t)) = z sigmoid(2t), t = sqrt(2/pi)(z + 0.044715 z^3).
+constexpr float kGelu2c = 1.5957691216057308f, kGelu3 = 0.044715f;
+
+template <int ACT>
+__device__ __forceinline__ float act_of(float z, float up) {
+  if (ACT == ULY_ACT_SILU) return z * sigmoid_fast(z);
+  if (ACT == ULY_ACT_SWIGLU) return z * sigmoid_fast(z) * up;
+  if (ACT == ULY_ACT_GELU) {
+    const float c = fminf(fmaxf(z, -20.f), 20.f);   // beyond, sigmoid(2t) is 0 or 1 and z^3 could overflow
+    return z * sigmoid_fast(kGelu2c * fmaf(kGelu3 * c * c, c, c));
+  }
+  return z;
+}
+
+// act'(z); swiglu: the derivatives by the gate (times up) and by up.
+template <int ACT>
+__device__ __forceinline__ float dact_of(float z) {
+  if (ACT == ULY_ACT_GELU) {
+    const float c = fminf(fmaxf(z, -20.f), 20.f);
+    const float s = sigmoid_fast(kGelu2c * fmaf(kGelu3 * c * c, c, c));
+    return fmaf(z * (s * (1.f - s)) * kGelu2c, fmaf(3.f * kGelu3 * c, c, 1.f), s);
+  }
+  const float s = sigmoid_fast(z);
+  return s * fmaf(z, 1.f - s, 1.f);
+}
+
+struct LinearParams {
+  const __nv_bfloat16 *bias, *residual;   // nullable
+  __nv_bfloat16 *y, *pre;                 // pre nullable: z [M][NZ]
+  float *part;                            // splits > 1: fp32 [splits][M][NZ] instead
+  long long M;
+  int N, NZ;                              // output features, rows of W
+};
+
+template <int ACT>
+struct EpiLinear {
+  using Params = LinearParams;
+  static constexpr bool kGated = ACT == ULY_ACT_SWIGLU;
+  static constexpr int kCols = kGated ? 64 : 128;   // output columns of one warpgroup
+
+  // eight outputs from their z (and the other factor's)
+  static __device__ __forceinline__ void store(const Params &p, long long row, int col, float (&z)[8], float (&up)[8]) {
+    if (p.bias) {
+      float b[8];
+      load8(p.bias + col, b);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) z[e] += b[e];
+      if (kGated) {
+        load8(p.bias + p.N + col, b);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) up[e] += b[e];
+      }
+    }
+    if (p.pre) {
+      store8(p.pre + row * p.NZ + col, z);
+      if (kGated) store8(p.pre + row * p.NZ + p.N + col, up);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) z[e] = act_of<ACT>(z[e], up[e]);
+    if (p.residual) {
+      float r[8];
+      load8(p.residual + row * p.N + col, r);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) z[e] += r[e];
+    }
+    store8(p.y + row * p.N + col, z);
+  }
+
+  static __device__ __forceinline__ void tile(const Params &p, const Unit &w, uint32_t acc, int row, int half) {
+#pragma unroll 1
+    for (int c = 0; c < kCols; c += 32) {
+      const int c0 = half * kCols + c;
+      uint32_t a[kGated ? 64 : 32];
+      if constexpr (kGated) tmem_ld32x2(acc + c0, acc + kHalf + c0, a);
+      else tmem_ld32(acc + c0, a);
+      if (row < p.M) {
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const int col = w.nt * 2 * kCols + c0 + 8 * g;
+          if (col < p.N) {
+            float z[8], up[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              z[e] = __uint_as_float(a[8 * g + e]);
+              up[e] = kGated ? __uint_as_float(a[(kGated ? 32 : 0) + 8 * g + e]) : 0.f;
+            }
+            if (p.part) {
+              float *o = p.part + ((long long)w.split * p.M + row) * p.NZ + col;
+              store8(o, z);
+              if (kGated) store8(o + p.N, up);
+            } else {
+              store(p, row, col, z, up);
+            }
+          }
+        }
+      }
+      __syncwarp();
+    }
+  }
+};
+
+template <int ACT>
+__global__ void __launch_bounds__(256) linear_join_kernel(const LinearParams p, int splits) {
+  const int vecs = p.N / 8;
+  const long long total = p.M * vecs;
+  for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < total;
+       i += (long long)gridDim.x * blockDim.x) {
+    const long long row = i / vecs;
+    const int col = (int)(i - row * vecs) * 8;
+    float z[8] = {}, up[8] = {};
+    for (int s = 0; s < splits; ++s) {
+      const float *o = p.part + ((long long)s * p.M + row) * p.NZ + col;
+      float v[8];
+      load8(o, v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) z[e] += v[e];
+      if (EpiLinear<ACT>::kGated) {
+        load8(o + p.N, v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) up[e] += v[e];
+      }
+    }
+    EpiLinear<ACT>::store(p, row, col, z, up);
+  }
+}
+
+template <int ACT>
+uly_status run_linear(const CUtensorMap &ta, const CUtensorMap &tb, LinearParams p, int K, int splits, float *part,
+                      cudaStream_t stream) {
+  p.part = splits > 1 ? part : nullptr;
+  prof::Scope scope(prof::K_LINEAR, stream);
+  const Shape s = make_shape(p.M, p.N, K, EpiLinear<ACT>::kCols * 2, splits);
+  const uly_status st = launch<EpiLinear<ACT>, false, false>(ta, tb, s, p, stream);
+  if (st != ULY_OK || splits == 1) return st;
+  linear_join_kernel<ACT><<<join_blocks(p.M * (p.N / 8)), 256, 0, stream>>>(p, splits);
+  note_launches(1);
+  return last_launch_status();
+}
+
+int gated(int act) { return act == ULY_ACT_SWIGLU ? 2 : 1; }
+
+int linear_splits(int64_t tokens, int32_t in, int32_t out, int32_t act) {
+  const int tile = kTile / gated(act);
+  return choose_splits(tokens, (long long)out * gated(act), (tokens + kTile - 1) / kTile, (out + tile - 1) / tile,
+                       (in + kBK - 1) / kBK, device_sm_count());
+}
+
+// ------------------------------------------------------------ dz and dbias
+// dz[t][c] for 8 columns a thread; rows of one CTA's strip summed per column
+// into a partial of the bias gradient (fp32, before dz is rounded).
+struct DzParams {
+  const __nv_bfloat16 *pre, *dy;   // pre null: act none, dz = dy (only the sums are formed)
+  __nv_bfloat16 *dz;
+  float *part;                     // [gridDim.y * 8][NZ]; null without a bias gradient
+  long long M;
+  int N, NZ, rows_per_cta;
+};
+
+template <int ACT>
+__global__ void __launch_bounds__(256) linear_dz_kernel(const DzParams p) {
+  constexpr bool kGated = ACT == ULY_ACT_SWIGLU;
+  const int strip = threadIdx.x >> 5, col = (blockIdx.x * 32 + (threadIdx.x & 31)) * 8;
+  if (col >= p.N) return;
+  float s0[8] = {}, s1[8] = {};
+  const long long r0 = (long long)blockIdx.y * p.rows_per_cta;
+  const long long r1 = r0 + p.rows_per_cta < p.M ? r0 + p.rows_per_cta : p.M;
+#pragma unroll 2
+  for (long long r = r0 + strip; r < r1; r += 8) {
+    float d[8], z[8];
+    load8(p.dy + r * p.N + col, d);
+    if (ACT == ULY_ACT_NONE) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s0[e] += d[e];
+      continue;
+    }
+    load8(p.pre + r * p.NZ + col, z);
+    if (kGated) {
+      float up[8], a[8], b[8];
+      load8(p.pre + r * p.NZ + p.N + col, up);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float s = sigmoid_fast(z[e]);
+        b[e] = d[e] * (z[e] * s);
+        a[e] = d[e] * up[e] * (s * fmaf(z[e], 1.f - s, 1.f));
+        s0[e] += a[e];
+        s1[e] += b[e];
+      }
+      store8(p.dz + r * p.NZ + col, a);
+      store8(p.dz + r * p.NZ + p.N + col, b);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        d[e] *= dact_of<ACT>(z[e]);
+        s0[e] += d[e];
+      }
+      store8(p.dz + r * p.NZ + col, d);
+    }
+  }
+  if (p.part) {
+    float *o = p.part + ((long long)blockIdx.y * 8 + strip) * p.NZ + col;
+    store8(o, s0);
+    if (kGated) store8(o + p.N, s1);
+  }
+}
+
+// CTAs along the tokens: about eight an SM in all, no shorter than 64 rows.
+int dz_row_ctas(int64_t tokens, int32_t out) {
+  const long long cols = (out / 8 + 31) / 32;
+  long long ctas = (long long)device_sm_count() * 8 / cols, most = (tokens + 63) / 64;
+  if (ctas > most) ctas = most;
+  return (int)(ctas < 1 ? 1 : ctas);
+}
+
+// Workspace of the backward: dz, the bias gradient's partials, a cut product's
+// partials (the two products run one after the other and share them).
+struct BwdPlan {
+  int nz, dx_splits, dw_splits, row_ctas;
+  size_t off_bias, off_part, bytes;
+};
+size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
+BwdPlan bwd_plan(int64_t tokens, int32_t in, int32_t out, int32_t act) {
+  BwdPlan q;
+  q.nz = out * gated(act);
+  const int sms = device_sm_count();
+  auto tiles = [](long long v) { return (v + kTile - 1) / kTile; };
+  q.dx_splits = choose_splits(tokens, in, tiles(tokens), tiles(in), (q.nz + kBK - 1) / kBK, sms);
+  q.dw_splits = choose_splits(q.nz, in, tiles(q.nz), tiles(in), (tokens + kBK - 1) / kBK, sms);
+  q.row_ctas = dz_row_ctas(tokens, out);
+  q.off_bias = act == ULY_ACT_NONE ? 0 : up256((size_t)tokens * q.nz * 2);
+  q.off_part = q.off_bias + up256((size_t)q.row_ctas * 8 * q.nz * sizeof(float));
+  const size_t a = part_bytes(tokens, in, q.dx_splits), b = part_bytes(q.nz, in, q.dw_splits);
+  q.bytes = q.off_part + up256(a > b ? a : b);
+  return q;
+}
+
+}  // namespace
+
+size_t linear_workspace_bytes(int64_t tokens, int32_t in, int32_t out, int32_t act) {
+  return part_bytes(tokens, (long long)out * gated(act), linear_splits(tokens, in, out, act));
+}
+
+uly_status linear_launch(int64_t tokens, int32_t in, int32_t out, int32_t act, const void *x, const void *w,
+                         const void *bias, const void *residual, void *y, void *pre, void *workspace,
+                         cudaStream_t stream) {
+  const int nz = out * gated(act);
+  CUtensorMap ta, tb;
+  if (!make_map(&ta, x, in, tokens, in, kHalf) || !make_map(&tb, w, in, nz, in, kHalf)) return ULY_ERR_CUDA;
+  LinearParams p = {};
+  p.bias = static_cast<const __nv_bfloat16 *>(bias);
+  p.residual = static_cast<const __nv_bfloat16 *>(residual);
+  p.y = static_cast<__nv_bfloat16 *>(y);
+  p.pre = static_cast<__nv_bfloat16 *>(pre);
+  p.M = tokens; p.N = out; p.NZ = nz;
+  const int splits = linear_splits(tokens, in, out, act);
+  float *part = static_cast<float *>(workspace);
+  switch (act) {
+    case ULY_ACT_GELU: return run_linear<ULY_ACT_GELU>(ta, tb, p, in, splits, part, stream);
+    case ULY_ACT_SILU: return run_linear<ULY_ACT_SILU>(ta, tb, p, in, splits, part, stream);
+    case ULY_ACT_SWIGLU: return run_linear<ULY_ACT_SWIGLU>(ta, tb, p, in, splits, part, stream);
+    default: return run_linear<ULY_ACT_NONE>(ta, tb, p, in, splits, part, stream);
+  }
+}
+
+size_t linear_bwd_workspace_bytes(int64_t tokens, int32_t in, int32_t out, int32_t act) {
+  return bwd_plan(tokens, in, out, act).bytes;
+}
+
+uly_status linear_bwd_launch(int64_t tokens, int32_t in, int32_t out, int32_t act, const void *x, const void *w,
+                             const void *pre, const void *dy, void *dx, void *dw, int32_t dw_dtype, float *dbias,
+                             void *workspace, cudaStream_t stream) {
+  const BwdPlan q = bwd_plan(tokens, in, out, act);
+  char *ws = static_cast<char *>(workspace);
+  float *bias_part = reinterpret_cast<float *>(ws + q.off_bias), *part = reinterpret_cast<float *>(ws + q.off_part);
+  const void *dz = act == ULY_ACT_NONE ? dy : workspace;
+  if (dbias || (act != ULY_ACT_NONE && (dx || dw))) {
+    DzParams p = {};
+    p.pre = static_cast<const __nv_bfloat16 *>(pre);
+    p.dy = static_cast<const __nv_bfloat16 *>(dy);
+    p.dz = static_cast<__nv_bfloat16 *>(workspace);
+    p.part = dbias ? bias_part : nullptr;
+    p.M = tokens; p.N = out; p.NZ = q.nz;
+    p.rows_per_cta = (int)((tokens + q.row_ctas - 1) / q.row_ctas);
+    const dim3 grid((out / 8 + 31) / 32, q.row_ctas);
+    prof::Scope scope(prof::K_LINEAR_DZ, stream);
+    switch (act) {
+      case ULY_ACT_GELU: linear_dz_kernel<ULY_ACT_GELU><<<grid, 256, 0, stream>>>(p); break;
+      case ULY_ACT_SILU: linear_dz_kernel<ULY_ACT_SILU><<<grid, 256, 0, stream>>>(p); break;
+      case ULY_ACT_SWIGLU: linear_dz_kernel<ULY_ACT_SWIGLU><<<grid, 256, 0, stream>>>(p); break;
+      default: linear_dz_kernel<ULY_ACT_NONE><<<grid, 256, 0, stream>>>(p);
+    }
+    note_launches(1);
+    scope.end();
+    if (last_launch_status() != ULY_OK) return ULY_ERR_CUDA;
+    if (dbias) {
+      const uly_status st = fold_columns_launch(bias_part, 1, (long long)q.row_ctas * 8, q.nz, dbias, stream);
+      if (st != ULY_OK) return st;
+    }
+  }
+  CUtensorMap ta, tb;
+  if (dx) {   // dx[tokens][in] = dz[tokens][nz] W[nz][in]
+    if (!make_map(&ta, dz, q.nz, tokens, q.nz, kHalf) || !make_map(&tb, w, in, q.nz, in, 64)) return ULY_ERR_CUDA;
+    PlainParams p = {};
+    p.out = dx; p.M = tokens; p.N = in;
+    const uly_status st = launch_plain<false, true>(ta, tb, p, q.nz, q.dx_splits, part, prof::K_LINEAR_DX, stream);
+    if (st != ULY_OK) return st;
+  }
+  if (dw) {   // dW[nz][in] = dz^T x
+    if (!make_map(&ta, dz, q.nz, tokens, q.nz, 64) || !make_map(&tb, x, in, tokens, in, 64)) return ULY_ERR_CUDA;
+    PlainParams p = {};
+    p.out = dw; p.out_f32 = dw_dtype == ULY_F32; p.M = q.nz; p.N = in;
+    return launch_plain<true, true>(ta, tb, p, tokens, q.dw_splits, part, prof::K_LINEAR_DW, stream);
+  }
+  return ULY_OK;
+}
+
+}  // namespace uly

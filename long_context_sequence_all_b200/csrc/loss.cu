@@ -25,6 +25,7 @@
 // stores: logits read once from HBM, dlogits written once.
 #include "common.cuh"
 #include "prof.cuh"
+#include "tokenwise.cuh"
 
 namespace uly {
 
@@ -409,6 +410,19 @@ uly_status loss_launch(int32_t P, int64_t tokens, int32_t vocab, int32_t dtype, 
   ce_finalize_kernel<<<1, 256, 0, stream>>>(psum, pcnt, P, nb, shard_sum, shard_count, loss);
   note_launches(2);
   return last_launch_status();
+}
+
+void loss_count_launch(const int32_t *labels, long long tokens, int vocab, int ignore_index, long long *count,
+                       cudaStream_t stream) {
+  ce_count_kernel<<<1, 1024, 0, stream>>>(labels, tokens, vocab, ignore_index, count);
+  note_launches(1);
+}
+
+void loss_finalize_launch(const double *psum, const long long *pcnt, int P, int nb, float *shard_sum,
+                          int64_t *shard_count, float *loss, cudaStream_t stream) {
+  prof::Scope scope(prof::K_LOSS_FINALIZE, stream);
+  ce_finalize_kernel<<<1, 256, 0, stream>>>(psum, pcnt, P, nb, shard_sum, shard_count, loss);
+  note_launches(1);
 }
 
 // Fused forward + backward.  `ws`: the forward's partials followed by one

@@ -44,7 +44,9 @@ const char *name(int k) {
       "kv_head_to_seq_sum", "shift_labels", "rope_table", "qkv_proj_sm100",
       "o_proj_sm100", "check_cu_seqlens", "attn_bwd_sm100", "attn_dq_convert",
       "seq_to_head_vec", "head_to_seq_vec", "qkv_dy", "qkv_proj_dx_sm100", "qkv_proj_dw_sm100",
-      "o_proj_do_sm100", "o_proj_dw_sm100"};
+      "o_proj_do_sm100", "o_proj_dw_sm100", "residual_norm", "residual_norm_bwd", "fold_columns",
+      "linear_sm100", "linear_dz", "linear_dx_sm100", "linear_dw_sm100", "linear_loss_sm100", "linear_loss_rows",
+      "linear_loss_dx_sm100", "linear_loss_dw_sm100"};
   return (k >= 0 && k < K_COUNT) ? names[k] : "unknown";
 }
 

@@ -40,6 +40,17 @@ enum Kernel {
   K_QKV_DW,
   K_O_PROJ_DO,
   K_O_PROJ_DWO,
+  K_RESIDUAL_NORM,
+  K_RESIDUAL_NORM_BWD,
+  K_FOLD_COLUMNS,
+  K_LINEAR,
+  K_LINEAR_DZ,
+  K_LINEAR_DX,
+  K_LINEAR_DW,
+  K_LINEAR_LOSS,
+  K_LINEAR_LOSS_ROWS,
+  K_LINEAR_LOSS_DX,
+  K_LINEAR_LOSS_DW,
   K_COUNT
 };
 

@@ -20,6 +20,8 @@ LIB_PATH = os.path.join(_HERE, "libulysses.so")
 
 ULY_F32, ULY_BF16 = 0, 1
 MASK_NONE, MASK_CAUSAL, MASK_DOC_CAUSAL = 0, 1, 2
+ACT_NONE, ACT_GELU, ACT_SILU, ACT_SWIGLU = 0, 1, 2, 3
+GATE_NONE, GATE_CHANNEL, GATE_SEQUENCE, GATE_TOKEN = 0, 1, 2, 3
 STATUS = {0: "ULY_OK", 1: "ULY_ERR_NULL", 2: "ULY_ERR_SHAPE", 3: "ULY_ERR_DTYPE",
           4: "ULY_ERR_ALIGN", 5: "ULY_ERR_ALIAS", 6: "ULY_ERR_UNSUPPORTED", 7: "ULY_ERR_CUDA",
           8: "ULY_ERR_LABEL", 9: "ULY_ERR_TIMEOUT", 10: "ULY_ERR_WORKSPACE"}
@@ -30,7 +32,11 @@ EXPORTS = ["ulysses_seq_to_head", "ulysses_head_to_seq", "ulysses_seq_to_head_ba
            "ulysses_qkv_proj_rope_bwd", "ulysses_o_proj_bwd", "ulysses_attn_fwd",
            "ulysses_attn_bwd_workspace_size", "ulysses_attn_bwd", "ulysses_loss_workspace_size",
            "ulysses_loss_aggregate", "ulysses_loss_aggregate_noalloc", "ulysses_loss_bwd_workspace_size",
-           "ulysses_loss_aggregate_bwd", "ulysses_read_error", "ulysses_read_error_info", "ulysses_error_word",
+           "ulysses_loss_aggregate_bwd", "ulysses_linear_workspace_size", "ulysses_linear",
+           "ulysses_linear_bwd_workspace_size", "ulysses_linear_bwd", "ulysses_residual_norm",
+           "ulysses_residual_norm_bwd_workspace_size", "ulysses_residual_norm_bwd",
+           "ulysses_linear_loss_workspace_size", "ulysses_linear_loss", "ulysses_linear_loss_bwd_workspace_size",
+           "ulysses_linear_loss_bwd", "ulysses_read_error", "ulysses_read_error_info", "ulysses_error_word",
            "ulysses_set_wait_limit", "ulysses_set_attn_block_order",
            "ulysses_status_string", "ulysses_profile_enable", "ulysses_profile_read",
            "ulysses_kernel_count", "ulysses_kernel_name",
@@ -104,6 +110,24 @@ def lib() -> ctypes.CDLL:
             L.ulysses_loss_aggregate_noalloc.restype = ctypes.c_int
             L.ulysses_loss_bwd_workspace_size.argtypes = [i32, i64, i32, ctypes.POINTER(sz)]
             L.ulysses_loss_aggregate_bwd.argtypes = [i32, i64, i32, i32, vp, vp, i32, vp, vp, vp, vp, vp, sz, vp]
+            f32, szp = ctypes.c_float, ctypes.POINTER(sz)
+            for name, args in (
+                    ("ulysses_linear_workspace_size", [i64, i32, i32, i32, szp]),
+                    ("ulysses_linear", [i64, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
+                    ("ulysses_linear_bwd_workspace_size", [i64, i32, i32, i32, szp]),
+                    ("ulysses_linear_bwd", [i64, i32, i32, i32, vp, vp, vp, vp, vp, vp, i32, vp, vp, sz, vp]),
+                    ("ulysses_residual_norm", [i32, i32, i32, i32, i32, vp, vp, vp, i32, vp, vp, f32, f32, vp, vp,
+                                               vp]),
+                    ("ulysses_residual_norm_bwd_workspace_size", [i32, i32, i32, i32, i32, szp]),
+                    ("ulysses_residual_norm_bwd", [i32, i32, i32, i32, i32, vp, vp, vp, vp, vp, i32, vp, vp, f32,
+                                                   f32, vp, vp, vp, vp, vp, vp, sz, vp]),
+                    ("ulysses_linear_loss_workspace_size", [i32, i64, i32, i32, szp]),
+                    ("ulysses_linear_loss", [i32, i64, i32, i32, vp, vp, vp, i32, vp, vp, vp, vp, sz, vp]),
+                    ("ulysses_linear_loss_bwd_workspace_size", [i32, i64, i32, i32, i32, i64, szp]),
+                    ("ulysses_linear_loss_bwd", [i32, i64, i32, i32, vp, vp, vp, i32, vp, vp, i32, i64, vp, vp, vp,
+                                                 vp, sz, vp])):
+                getattr(L, name).argtypes = args
+                getattr(L, name).restype = ctypes.c_int
             L.ulysses_read_error.argtypes = [ctypes.POINTER(i32)]
             L.ulysses_error_word.argtypes = [ctypes.POINTER(vp)]
             L.ulysses_error_word.restype = ctypes.c_int
@@ -493,6 +517,284 @@ def ulysses_loss_aggregate_noalloc(logits, labels, P, ignore_index=-100, shard_s
                                                 ignore_index, _p(shard_sum), _p(shard_count), _p(loss),
                                                 _stream(stream)), "ulysses_loss_aggregate_noalloc")
     return shard_sum, shard_count, loss
+
+
+# ------------------------------------------------------ token-wise operators
+
+def _want(where, t, shape, dtype, optional=False):
+    """Check one tensor of a call: dtype, shape, contiguous."""
+    if t is None:
+        if optional:
+            return
+        raise UlyssesError(1, f"{where}: missing tensor")
+    if t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
+        raise UlyssesError(3, f"{where}: dtype {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise UlyssesError(2, f"{where}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_contiguous():
+        raise UlyssesError(6, f"{where}: not contiguous (strides {tuple(t.stride())})")
+
+
+def _here(where, *tensors):
+    """Every tensor of a call is on the current CUDA device, where it launches."""
+    for t in tensors:
+        if t is not None and (not t.is_cuda or t.device.index != torch.cuda.current_device()):
+            raise UlyssesError(7, f"{where}: a tensor on {t.device}, not on the current CUDA device")
+
+
+def _alloc(shape, dtype, device, stream):
+    """An output or workspace whose memory belongs to the stream the call runs on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _size(fn, *args) -> int:
+    n = ctypes.c_size_t(0)
+    _check(getattr(lib(), fn)(*args, ctypes.byref(n)), fn)
+    return n.value
+
+
+def _workspace(where, ws, need, device, stream):
+    if ws is None:
+        return _alloc((max(need, 256),), torch.uint8, device, stream) if need else None
+    if ws.dtype != torch.uint8:
+        raise UlyssesError(3, f"{where}: workspace dtype {ws.dtype}")
+    _want(f"{where} workspace", ws, (ws.numel(),), torch.uint8)
+    return ws
+
+
+def _rows(x) -> int:
+    return x.numel() // x.shape[-1] if x.shape[-1] else 0
+
+
+def _features(where, x, w, activation):
+    if x.dim() < 1 or w.dim() != 2 or (activation == ACT_SWIGLU and w.shape[0] % 2):
+        raise UlyssesError(2, f"{where}: x {tuple(x.shape)}, w {tuple(w.shape)}")
+    return x.shape[-1], w.shape[0], w.shape[0] // 2 if activation == ACT_SWIGLU else w.shape[0]
+
+
+def ulysses_linear_workspace_size(tokens: int, in_features: int, out_features: int, activation=ACT_NONE) -> int:
+    return _size("ulysses_linear_workspace_size", tokens, in_features, out_features, activation)
+
+
+def ulysses_linear(x, w, bias=None, residual=None, activation=ACT_NONE, save_pre=False, y=None, pre=None,
+                   workspace=None, stream=None):
+    """y = act(x w^T + bias) + residual: x [..., K] bf16 (e.g. the seq layout), w
+    [N][K] (nn.Linear weight; ACT_SWIGLU: [2N][K], gate rows then up rows), bias
+    like w's rows, residual like y -> y [..., N]; with save_pre (or a given pre)
+    (y, pre), pre [..., rows of w] the product and bias before the activation."""
+    k, nz, n = _features("ulysses_linear", x, w, activation)
+    lead, bf = tuple(x.shape[:-1]), torch.bfloat16
+    _want("ulysses_linear x", x, (*lead, k), bf)
+    _want("ulysses_linear w", w, (nz, k), bf)
+    _want("ulysses_linear bias", bias, (nz,), bf, optional=True)
+    _want("ulysses_linear residual", residual, (*lead, n), bf, optional=True)
+    y = _alloc((*lead, n), bf, x.device, stream) if y is None else y
+    if save_pre and pre is None:
+        pre = _alloc((*lead, nz), bf, x.device, stream)
+    _want("ulysses_linear y", y, (*lead, n), bf)
+    _want("ulysses_linear pre", pre, (*lead, nz), bf, optional=True)
+    _here("ulysses_linear", x, w, bias, residual, y, pre, workspace)
+    tokens = _rows(x)
+    need = ulysses_linear_workspace_size(tokens, k, n, activation)
+    ws = _workspace("ulysses_linear", workspace, need, x.device, stream)
+    _check(lib().ulysses_linear(tokens, k, n, activation, _p(x), _p(w), _p(bias), _p(residual), _p(y), _p(pre),
+                                _p(ws), 0 if ws is None else ws.numel(), _stream(stream)), "ulysses_linear")
+    return y if pre is None else (y, pre)
+
+
+def ulysses_linear_bwd_workspace_size(tokens: int, in_features: int, out_features: int, activation=ACT_NONE) -> int:
+    return _size("ulysses_linear_bwd_workspace_size", tokens, in_features, out_features, activation)
+
+
+def ulysses_linear_bwd(x, w, dy, pre=None, activation=ACT_NONE, bias_grad=False, grad_dtype=torch.float32, dx=None,
+                       dw=None, dbias=None, workspace=None, stream=None):
+    """Backward of ulysses_linear: dy [..., N] and the forward's pre (not for
+    ACT_NONE) -> (dx like x, dw like w in grad_dtype (float32 or bfloat16), dbias
+    float32 [rows of w], or None without bias_grad).  The residual's gradient is dy."""
+    k, nz, n = _features("ulysses_linear_bwd", x, w, activation)
+    lead, bf = tuple(x.shape[:-1]), torch.bfloat16
+    _want("ulysses_linear_bwd x", x, (*lead, k), bf)
+    _want("ulysses_linear_bwd w", w, (nz, k), bf)
+    _want("ulysses_linear_bwd dy", dy, (*lead, n), bf)
+    if activation == ACT_NONE:
+        pre = None
+    else:
+        _want("ulysses_linear_bwd pre", pre, (*lead, nz), bf)
+    dx = _alloc(x.shape, bf, x.device, stream) if dx is None else dx
+    dw = _alloc(w.shape, grad_dtype, x.device, stream) if dw is None else dw
+    if bias_grad and dbias is None:
+        dbias = _alloc((nz,), torch.float32, x.device, stream)
+    _want("ulysses_linear_bwd dx", dx, x.shape, bf)
+    _want("ulysses_linear_bwd dw", dw, w.shape, (torch.float32, bf))
+    _want("ulysses_linear_bwd dbias", dbias, (nz,), torch.float32, optional=True)
+    _here("ulysses_linear_bwd", x, w, dy, pre, dx, dw, dbias, workspace)
+    tokens = _rows(x)
+    need = ulysses_linear_bwd_workspace_size(tokens, k, n, activation)
+    ws = _workspace("ulysses_linear_bwd", workspace, need, x.device, stream)
+    _check(lib().ulysses_linear_bwd(tokens, k, n, activation, _p(x), _p(w), _p(pre), _p(dy), _p(dx), _p(dw),
+                                    _dtype_code(dw), _p(dbias), _p(ws), 0 if ws is None else ws.numel(),
+                                    _stream(stream)), "ulysses_linear_bwd")
+    return dx, dw, dbias
+
+
+def _gate_shape(mode, shape):
+    return {GATE_CHANNEL: (shape[3],), GATE_SEQUENCE: (shape[1], shape[3]), GATE_TOKEN: tuple(shape)}.get(mode)
+
+
+def _want_norm(where, shape, dtype, w_pre, w_post, gate, gate_mode):
+    if len(shape) != 4:
+        raise UlyssesError(2, f"{where}: shape {tuple(shape)}, expected [P][B][n/P][hidden]")
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise UlyssesError(3, f"{where}: dtype {dtype}")
+    _want(f"{where} w_pre", w_pre, (shape[3],), dtype, optional=True)
+    _want(f"{where} w_post", w_post, (shape[3],), dtype, optional=True)
+    if gate_mode == GATE_NONE:
+        if gate is not None:
+            raise UlyssesError(2, f"{where}: a gate with GATE_NONE")
+    elif gate_mode in (GATE_CHANNEL, GATE_SEQUENCE, GATE_TOKEN):
+        _want(f"{where} gate", gate, _gate_shape(gate_mode, shape), dtype)
+    else:
+        raise UlyssesError(6, f"{where}: gate mode {gate_mode}")
+
+
+def ulysses_residual_norm(x, h=None, w_pre=None, w_post=None, gate=None, gate_mode=GATE_NONE, res_scale=1.0,
+                          eps=1e-6, r=None, u=None, stream=None):
+    """r = res_scale x + gate * N(h; w_post), u = N(r; w_pre) with N the root mean
+    square norm: x, h seq layout [P][B][n/P][hidden] (bf16 or float32), weights
+    [hidden], gate as its mode says -> (r, u).  Without w_pre u is None; without
+    h (the first block) r is None unless a tensor for it is given."""
+    where = "ulysses_residual_norm"
+    _want_norm(where, x.shape, x.dtype, w_pre, w_post, gate, gate_mode)
+    _want(f"{where} x", x, x.shape, x.dtype)
+    _want(f"{where} h", h, x.shape, x.dtype, optional=True)
+    if r is None and (h is not None or w_pre is None):
+        r = _alloc(x.shape, x.dtype, x.device, stream)
+    if u is None and w_pre is not None:
+        u = _alloc(x.shape, x.dtype, x.device, stream)
+    _want(f"{where} r", r, x.shape, x.dtype, optional=True)
+    _want(f"{where} u", u, x.shape, x.dtype, optional=True)
+    _here(where, x, h, w_pre, w_post, gate, r, u)
+    P, B, s, d = x.shape
+    _check(lib().ulysses_residual_norm(B, P * s, P, d, _dtype_code(x), _p(x), _p(h), _p(gate), gate_mode, _p(w_post),
+                                       _p(w_pre), float(res_scale), float(eps), _p(r), _p(u), _stream(stream)), where)
+    return r, u
+
+
+def ulysses_residual_norm_bwd_workspace_size(B: int, n: int, hidden: int, dtype=torch.bfloat16,
+                                             gate_mode=GATE_NONE) -> int:
+    return _size("ulysses_residual_norm_bwd_workspace_size", B, n, hidden,
+                 ULY_BF16 if dtype == torch.bfloat16 else ULY_F32, gate_mode)
+
+
+def ulysses_residual_norm_bwd(r, h=None, dr=None, du=None, w_pre=None, w_post=None, gate=None, gate_mode=GATE_NONE,
+                              res_scale=1.0, eps=1e-6, dx=None, dh=None, dw_pre=None, dw_post=None, dgate=None,
+                              workspace=None, stream=None):
+    """Backward of ulysses_residual_norm, from its stored r: the gradients of
+    sum(r * dr) + sum(u * du) -> (dx, dh, dw_pre, dw_post, dgate); dw_pre, dw_post
+    and a shared gate's gradient are float32, a token gate's is like the gate;
+    None for what the forward did not have."""
+    where = "ulysses_residual_norm_bwd"
+    _want_norm(where, r.shape, r.dtype, w_pre, w_post, gate, gate_mode)
+    for name, t in (("h", h), ("dr", dr), ("du", du)):
+        _want(f"{where} {name}", t, r.shape, r.dtype, optional=True)
+    _want(f"{where} r", r, r.shape, r.dtype)
+    P, B, s, d = r.shape
+    f32, dev = torch.float32, r.device
+    dx = _alloc(r.shape, r.dtype, dev, stream) if dx is None else dx
+    if dh is None and h is not None:
+        dh = _alloc(r.shape, r.dtype, dev, stream)
+    if dw_pre is None and du is not None:
+        dw_pre = _alloc((d,), f32, dev, stream)
+    if dw_post is None and w_post is not None:
+        dw_post = _alloc((d,), f32, dev, stream)
+    gdt = r.dtype if gate_mode == GATE_TOKEN else f32
+    if dgate is None and gate is not None:
+        dgate = _alloc(gate.shape, gdt, dev, stream)
+    _want(f"{where} dx", dx, r.shape, r.dtype)
+    _want(f"{where} dh", dh, r.shape, r.dtype, optional=True)
+    _want(f"{where} dw_pre", dw_pre, (d,), f32, optional=True)
+    _want(f"{where} dw_post", dw_post, (d,), f32, optional=True)
+    if dgate is not None:
+        _want(f"{where} dgate", dgate, _gate_shape(gate_mode, r.shape) or (0,), gdt)
+    _here(where, r, h, dr, du, w_pre, w_post, gate, dx, dh, dw_pre, dw_post, dgate, workspace)
+    need = ulysses_residual_norm_bwd_workspace_size(B, P * s, d, r.dtype, gate_mode)
+    ws = _workspace(where, workspace, need, dev, stream)
+    _check(lib().ulysses_residual_norm_bwd(B, P * s, P, d, _dtype_code(r), _p(r), _p(h), _p(dr), _p(du), _p(gate),
+                                           gate_mode, _p(w_post), _p(w_pre), float(res_scale), float(eps), _p(dx),
+                                           _p(dh), _p(dw_post), _p(dw_pre), _p(dgate), _p(ws), ws.numel(),
+                                           _stream(stream)), where)
+    return dx, dh, dw_pre, dw_post, dgate
+
+
+def _want_loss(where, x, w, labels):
+    if x.dim() != 2 or w.dim() != 2:
+        raise UlyssesError(2, f"{where}: x {tuple(x.shape)}, w {tuple(w.shape)}")
+    _want(f"{where} x", x, x.shape, torch.bfloat16)
+    _want(f"{where} w", w, (w.shape[0], x.shape[1]), torch.bfloat16)
+    _want(f"{where} labels", labels.reshape(-1) if labels.is_contiguous() else labels, (x.shape[0],), torch.int32)
+
+
+def _loss_outputs(where, P, dev, shard_sum, shard_count, loss, stream):
+    shard_sum = _alloc((P,), torch.float32, dev, stream) if shard_sum is None else shard_sum
+    shard_count = _alloc((P,), torch.int64, dev, stream) if shard_count is None else shard_count
+    loss = _alloc((1,), torch.float32, dev, stream) if loss is None else loss
+    _want(f"{where} shard_sum", shard_sum, (P,), torch.float32)
+    _want(f"{where} shard_count", shard_count, (P,), torch.int64)
+    _want(f"{where} loss", loss, (1,), torch.float32)
+    return shard_sum, shard_count, loss
+
+
+def ulysses_linear_loss_workspace_size(P: int, tokens: int, hidden: int, vocab: int) -> int:
+    return _size("ulysses_linear_loss_workspace_size", P, tokens, hidden, vocab)
+
+
+def ulysses_linear_loss(x, w, labels, P, ignore_index=-100, shard_sum=None, shard_count=None, loss=None,
+                        workspace=None, stream=None):
+    """ulysses_loss_aggregate without the logits: x [T][hidden] bf16 (shard r = rows
+    [r*T/P, (r+1)*T/P)), w [V][hidden] bf16, labels int32 [T] (or the seq layout)
+    -> (shard_sum, shard_count, loss) of the logits x w^T."""
+    where = "ulysses_linear_loss"
+    _want_loss(where, x, w, labels)
+    (T, d), V = x.shape, w.shape[0]
+    shard_sum, shard_count, loss = _loss_outputs(where, P, x.device, shard_sum, shard_count, loss, stream)
+    _here(where, x, w, labels, shard_sum, shard_count, loss, workspace)
+    need = ulysses_linear_loss_workspace_size(P, T, d, V)
+    ws = _workspace(where, workspace, need, x.device, stream)
+    _check(lib().ulysses_linear_loss(P, T, d, V, _p(x), _p(w), _p(labels), ignore_index, _p(shard_sum),
+                                     _p(shard_count), _p(loss), _p(ws), ws.numel(), _stream(stream)), where)
+    return shard_sum, shard_count, loss
+
+
+def ulysses_linear_loss_bwd_workspace_size(P: int, tokens: int, hidden: int, vocab: int, grad_dtype=torch.float32,
+                                           piece_tokens: int = 0) -> int:
+    return _size("ulysses_linear_loss_bwd_workspace_size", P, tokens, hidden, vocab,
+                 ULY_BF16 if grad_dtype == torch.bfloat16 else ULY_F32, piece_tokens)
+
+
+def ulysses_linear_loss_bwd(x, w, labels, P, ignore_index=-100, grad_dtype=torch.float32, piece_tokens=0, dx=None,
+                            dw=None, shard_sum=None, shard_count=None, loss=None, workspace=None, stream=None):
+    """The loss of ulysses_linear_loss and its gradients: returns (shard_sum,
+    shard_count, loss, dx bf16 like x, dw like w in grad_dtype (float32 or
+    bfloat16)).  piece_tokens: tokens whose exponentials the workspace holds at
+    a time (0: as many as fit 4 GiB)."""
+    where = "ulysses_linear_loss_bwd"
+    _want_loss(where, x, w, labels)
+    (T, d), V = x.shape, w.shape[0]
+    dx = _alloc(x.shape, x.dtype, x.device, stream) if dx is None else dx
+    dw = _alloc(w.shape, grad_dtype, x.device, stream) if dw is None else dw
+    _want(f"{where} dx", dx, x.shape, torch.bfloat16)
+    _want(f"{where} dw", dw, w.shape, (torch.float32, torch.bfloat16))
+    shard_sum, shard_count, loss = _loss_outputs(where, P, x.device, shard_sum, shard_count, loss, stream)
+    _here(where, x, w, labels, dx, dw, shard_sum, shard_count, loss, workspace)
+    need = ulysses_linear_loss_bwd_workspace_size(P, T, d, V, dw.dtype, piece_tokens)
+    ws = _workspace(where, workspace, need, x.device, stream)
+    _check(lib().ulysses_linear_loss_bwd(P, T, d, V, _p(x), _p(w), _p(labels), ignore_index, _p(dx), _p(dw),
+                                         _dtype_code(dw), piece_tokens, _p(shard_sum), _p(shard_count), _p(loss),
+                                         _p(ws), ws.numel(), _stream(stream)), where)
+    return shard_sum, shard_count, loss, dx, dw
 
 
 # -------------------------------------------------------------------- misc

@@ -244,3 +244,138 @@ def test_attn_block_order_setter_validates(L):
             assert L.ulysses_set_attn_block_order(bad) == 2
     finally:
         L.ulysses_set_attn_block_order(0)
+
+
+def _no_launch(L, fn, want, *args):
+    """A refused call: its status, and no kernel launched."""
+    before = L.ulysses_launch_count()
+    got = fn(*args)
+    assert got == want, (got, want)
+    assert L.ulysses_launch_count() == before
+
+
+def test_linear_validation(L):
+    vp = ctypes.c_void_p
+    x, w, b, r, y, pre, ws = (vp(1 << (30 + i)) for i in range(7))
+    n = ctypes.c_size_t(0)
+    f, size = L.ulysses_linear, L.ulysses_linear_workspace_size
+    args = lambda **k: [k.get("T", 1000), k.get("K", 512), k.get("N", 256), k.get("act", 0), k.get("x", x),
+                        k.get("w", w), k.get("b", b), k.get("r", r), k.get("y", y), k.get("pre", pre),
+                        k.get("ws", ws), k.get("wsb", 1 << 30), None]
+    for want, kw in ((2, dict(T=-1)), (2, dict(K=0)), (4, dict(K=510)), (4, dict(N=252)), (6, dict(act=4)),
+                     (6, dict(act=-1)), (1, dict(x=None)), (1, dict(w=None)), (1, dict(y=None)),
+                     (4, dict(x=vp((1 << 30) + 8))), (4, dict(b=vp((1 << 32) + 2))), (5, dict(y=x)), (5, dict(y=w)),
+                     (5, dict(y=vp((1 << 33) + 512))),          # partly the residual
+                     (5, dict(pre=y)), (5, dict(pre=r)), (5, dict(pre=b)), (2, dict(T=1 << 40)),
+                     (2, dict(T=(1 << 31) - 8192, N=1 << 20))):
+        _no_launch(L, f, want, *args(**kw))
+    assert f(*args(T=0, x=None, y=None)) == 0                   # no tokens: nothing to do
+    assert size(1, 2560, 1024, 0, ctypes.byref(n)) == 0 and n.value > 0     # cut along K
+    _no_launch(L, f, 10, *args(T=1, K=2560, N=1024, ws=None))
+    _no_launch(L, f, 10, *args(T=1, K=2560, N=1024, wsb=n.value - 1))
+    _no_launch(L, f, 5, *args(T=1, K=2560, N=1024, ws=x))
+    assert size(1, 2560, 1024, 0, None) == 1 and size(1, 2561, 1024, 0, ctypes.byref(n)) == 4
+    g = L.ulysses_linear_bwd
+    dy, dx, dw, db = r, y, pre, vp(1 << 40)
+    bargs = lambda **k: [k.get("T", 1000), 512, 256, k.get("act", 2), k.get("x", x), k.get("w", w), k.get("pre", b),
+                         k.get("dy", dy), k.get("dx", dx), k.get("dw", dw), k.get("dt", 0), k.get("db", db),
+                         k.get("ws", ws), k.get("wsb", 1 << 30), None]
+    for want, kw in ((1, dict(dx=None, dw=None, db=None)), (3, dict(dt=2)), (1, dict(dy=None)), (1, dict(x=None)),
+                     (1, dict(w=None)), (1, dict(pre=None)), (10, dict(ws=None)), (10, dict(wsb=64)),
+                     (4, dict(dw=vp((1 << 35) + 4))), (5, dict(dx=x)), (5, dict(dx=dy)), (5, dict(dw=b)),
+                     (5, dict(db=dw)), (5, dict(ws=dx))):
+        _no_launch(L, g, want, *bargs(**kw))
+
+
+def test_residual_norm_validation(L):
+    vp = ctypes.c_void_p
+    x, h, gt, wp, wq, r, u, ws = (vp(1 << (30 + i)) for i in range(8))
+    nan, inf = float("nan"), float("inf")
+    f = L.ulysses_residual_norm
+    args = lambda **k: [k.get("B", 2), k.get("n", 512), k.get("P", 4), k.get("D", 256), k.get("dt", 1),
+                        k.get("x", x), k.get("h", h), k.get("g", gt), k.get("mode", 1), k.get("wp", wp),
+                        k.get("wq", wq), k.get("a", 1.0), k.get("eps", 1e-6), k.get("r", r), k.get("u", u), None]
+    for want, kw in ((2, dict(B=0)), (2, dict(n=510)), (2, dict(P=0)), (2, dict(D=0)), (3, dict(dt=5)),
+                     (4, dict(D=260)), (4, dict(D=258, dt=0)), (6, dict(D=32776)), (6, dict(D=16388, dt=0)),
+                     (6, dict(mode=4)), (2, dict(eps=-1e-6)), (2, dict(eps=nan)), (2, dict(eps=inf)),
+                     (2, dict(a=nan)), (1, dict(x=None)), (1, dict(r=None, u=None)), (1, dict(wq=None)),
+                     (1, dict(g=None)), (1, dict(h=None)), (1, dict(h=None, mode=0)),
+                     (4, dict(x=vp((1 << 30) + 4))), (5, dict(u=x)), (5, dict(r=gt)), (5, dict(u=r)),
+                     (5, dict(r=vp((1 << 30) + 512)))):
+        _no_launch(L, f, want, *args(**kw))
+    g = L.ulysses_residual_norm_bwd
+    n = ctypes.c_size_t(0)
+    assert L.ulysses_residual_norm_bwd_workspace_size(2, 512, 256, 1, 1, ctypes.byref(n)) == 0 and n.value > 0
+    dr, du, dx, dh, dwp, dwq, dg = (vp(1 << (38 + i)) for i in range(7))
+    bargs = lambda **k: [2, 512, 4, 256, 1, k.get("r", r), k.get("h", h), k.get("dr", dr), k.get("du", du),
+                         k.get("g", gt), k.get("mode", 1), k.get("wp", wp), k.get("wq", wq), 1.0, 1e-6,
+                         k.get("dx", dx), k.get("dh", dh), k.get("dwp", dwp), k.get("dwq", dwq), k.get("dg", dg),
+                         k.get("ws", ws), k.get("wsb", n.value), None]
+    for want, kw in ((1, dict(dr=None, du=None)), (1, dict(r=None)), (1, dict(wq=None)), (1, dict(h=None)),
+                     (1, dict(wp=None)), (1, dict(du=None)), (1, dict(mode=0)), (10, dict(ws=None)),
+                     (10, dict(wsb=n.value - 1)), (5, dict(dx=du)), (5, dict(dh=dr)), (5, dict(dx=h)),
+                     (5, dict(dwp=dwq)), (5, dict(dg=ws)),
+                     (1, dict(dx=None, dh=None, dwp=None, dwq=None, dg=None))):
+        _no_launch(L, g, want, *bargs(**kw))
+
+
+def test_linear_loss_validation(L):
+    vp = ctypes.c_void_p
+    x, w, y, S, C, loss, ws, dx, dw = (vp(1 << (30 + i)) for i in range(9))
+    n = ctypes.c_size_t(0)
+    size = L.ulysses_linear_loss_workspace_size
+    assert size(4, 1024, 256, 1001, ctypes.byref(n)) == 0 and n.value > 0
+    f = L.ulysses_linear_loss
+    args = lambda **k: [k.get("P", 4), k.get("T", 1024), k.get("D", 256), k.get("V", 1001), k.get("x", x),
+                        k.get("w", w), k.get("y", y), -100, k.get("S", S), k.get("C", C), k.get("loss", loss),
+                        k.get("ws", ws), k.get("wsb", 1 << 30), None]
+    for want, kw in ((2, dict(P=0)), (2, dict(T=1023)), (2, dict(T=-4)), (2, dict(V=0)), (4, dict(D=252)),
+                     (1, dict(x=None)), (1, dict(w=None)), (1, dict(y=None)), (1, dict(S=None)), (10, dict(ws=None)),
+                     (10, dict(wsb=n.value - 1)), (4, dict(w=vp((1 << 31) + 2))), (5, dict(S=x)), (5, dict(ws=w)),
+                     (5, dict(loss=S)), (2, dict(T=1 << 34))):
+        _no_launch(L, f, want, *args(**kw))
+    bsize = L.ulysses_linear_loss_bwd_workspace_size
+    sizes = {}
+    for piece in (0, 256, 1024, 5000):
+        assert bsize(4, 1024, 256, 1001, 1, piece, ctypes.byref(n)) == 0
+        sizes[piece] = n.value
+    assert sizes[0] == sizes[1024] == sizes[5000] and sizes[256] < sizes[0] + 1001 * 256 * 4
+    assert bsize(4, 1024, 256, 1001, 2, 0, ctypes.byref(n)) == 3
+    assert bsize(4, 1024, 256, 1001, 1, -1, ctypes.byref(n)) == 2
+    g = L.ulysses_linear_loss_bwd
+    bargs = lambda **k: [4, 1024, 256, 1001, x, w, y, -100, k.get("dx", dx), k.get("dw", dw), k.get("dt", 1),
+                         k.get("piece", 0), S, C, loss, k.get("ws", ws), k.get("wsb", 1 << 30), None]
+    for want, kw in ((3, dict(dt=3)), (2, dict(piece=-1)), (1, dict(dx=None)), (1, dict(dw=None)),
+                     (10, dict(wsb=sizes[0] - 1)), (5, dict(dx=x)), (5, dict(dw=w)), (5, dict(dx=dw)),
+                     (4, dict(dx=vp((1 << 37) + 2)))):
+        _no_launch(L, g, want, *bargs(**kw))
+
+
+def test_tokenwise_binding_refuses_tensors_it_cannot_take(L):
+    """The binding checks type, shape, layout and device before the library is called."""
+    import torch
+    from long_context_sequence_all_b200 import ulysses as U
+    bf = torch.bfloat16
+    x, w = torch.zeros(4, 64, dtype=bf), torch.zeros(16, 64, dtype=bf)
+    y = torch.zeros(4, dtype=torch.int32)
+    q = torch.zeros(2, 1, 3, 64, dtype=bf)
+
+    def refused(status, fn, *a, **k):
+        with pytest.raises(U.UlyssesError) as e:
+            fn(*a, **k)
+        assert e.value.status == status, e.value
+
+    refused(3, U.ulysses_linear, x.float(), w)
+    refused(2, U.ulysses_linear, x, torch.zeros(16, 72, dtype=bf))
+    refused(2, U.ulysses_linear, x, w[:15], activation=U.ACT_SWIGLU)
+    refused(6, U.ulysses_linear, torch.zeros(64, 4, dtype=bf).t(), w)
+    refused(7, U.ulysses_linear, x, w)                                   # on the CPU
+    refused(3, U.ulysses_linear_bwd, x, w, torch.zeros(4, 16))
+    refused(2, U.ulysses_residual_norm, x)
+    refused(2, U.ulysses_residual_norm, q, q, gate=q)                    # a gate without a mode
+    refused(6, U.ulysses_residual_norm, q, q, gate=q, gate_mode=9)
+    refused(3, U.ulysses_residual_norm, q.half())
+    refused(7, U.ulysses_residual_norm, q, w_pre=None)
+    refused(3, U.ulysses_linear_loss, x.float(), w, y, 1)
+    refused(2, U.ulysses_linear_loss, q, w, y, 1)
+    refused(7, U.ulysses_linear_loss, x, w, y, 1)

@@ -1,0 +1,559 @@
+"""The token-wise operators (linear product with its epilogue, residual norm,
+linear loss; forward and backward) against plain implementations in 64 bits.
+
+Element-wise bounds, from the arithmetic of the GPU path:
+- a product of bf16 operands is exact, its fp32 accumulation errs by at most one
+  fp32 ulp an addition: K 2^-23 of the sum of |terms|;
+- a value stored in bf16 moves by half a step, 2^-8 |value|; an operand rounded
+  to bf16 before a product (dz; the loss's p and x') carries 2^-8 into it;
+- the activations' exponential and quotient are good to a few fp32 ulps: 2^-20
+  of a sigmoid, so an activation or its derivative errs by 2^-18 (2 + |z|);
+- a sum of D squares errs by D 2^-24, its inverse root by half of that.
+First-order terms only; the factor 1.05 covers products of two of them.
+"""
+import math
+
+import pytest
+import torch
+
+from helpers import LOSS_REL
+from long_context_sequence_all_b200 import ulysses as U
+
+pytestmark = pytest.mark.gpu
+
+U32 = 2.0 ** -23
+HALF = 2.0 ** -8
+MORE = 1.05
+ACTS = {"none": U.ACT_NONE, "gelu": U.ACT_GELU, "silu": U.ACT_SILU, "swiglu": U.ACT_SWIGLU}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    U.lib()
+    U.ulysses_read_error()
+
+
+def _gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def _rnd(g, *shape, scale=1.0, mean=0.0, dtype=torch.bfloat16):
+    return (torch.randn(*shape, generator=g, device="cuda") * scale + mean).to(dtype)
+
+
+def _within(got, ref, bound, what):
+    g = got.double()
+    assert torch.isfinite(g).all(), f"{what}: non-finite values"
+    worst = ((g - ref).abs() / bound.clamp_min(1e-30)).max().item() if g.numel() else 0.0
+    assert worst <= 1.0, f"{what}: worst err/bound {worst:.3f}"
+
+
+# ------------------------------------------------------------------- linear
+
+def _act64(z, act):
+    """(act(z), its derivatives by z, or by the gate's and the other factor's z)."""
+    if act == "none":
+        return z, torch.ones_like(z)
+    if act == "silu":
+        s = torch.sigmoid(z)
+        return z * s, s * (1 + z * (1 - s))
+    if act == "gelu":
+        c = math.sqrt(2 / math.pi)
+        t = torch.tanh(c * (z + 0.044715 * z ** 3))
+        return 0.5 * z * (1 + t), 0.5 * (1 + t) + 0.5 * z * (1 - t * t) * c * (1 + 3 * 0.044715 * z * z)
+    a, b = z.chunk(2, -1)
+    s = torch.sigmoid(a)
+    return a * s * b, torch.cat([b * s * (1 + a * (1 - s)), a * s], -1)
+
+
+LINEAR = [  # tokens, K, N, act, bias, residual
+    (1, 2560, 1024, "swiglu", False, False),     # one token: the product is cut along K
+    (1, 64, 8, "none", True, True),              # the smallest: a single k-step
+    (7, 72, 136, "gelu", True, False),           # a ragged k-step, a column tile and 8 columns
+    (130, 520, 264, "silu", False, True),        # two CTAs' rows, a ragged column tile
+    (257, 1032, 520, "swiglu", True, True),      # a second row tile of one row; the gate's last tile ends inside
+    (1000, 256, 2048, "gelu", True, True),
+    (4100, 640, 2560, "none", False, True),      # many tiles, each SM pair several
+]
+
+
+@pytest.mark.parametrize("T,K,N,act,bias,residual", LINEAR)
+def test_linear_forward(T, K, N, act, bias, residual):
+    g = _gen(T + K + N)
+    nz = 2 * N if act == "swiglu" else N
+    x, w = _rnd(g, T, K), _rnd(g, nz, K, scale=K ** -0.5)
+    b = _rnd(g, nz, scale=0.5) if bias else None
+    r = _rnd(g, T, N) if residual else None
+    y, pre = U.ulysses_linear(x, w, bias=b, residual=r, activation=ACTS[act], save_pre=True)
+    y2 = U.ulysses_linear(x, w, bias=b, residual=r, activation=ACTS[act])
+    assert torch.equal(y, y2)
+    xd, wd = x.double(), w.double()
+    z = xd @ wd.t() + (b.double() if bias else 0)
+    ez = (K + 2) * U32 * (xd.abs() @ wd.abs().t() + (b.double().abs() if bias else 0))
+    _within(pre, z, HALF * z.abs() + MORE * ez + 1e-30, "pre")
+    a, _ = _act64(z, act)
+    if act == "swiglu":
+        (zg, zu), (eg, eu) = z.chunk(2, -1), ez.chunk(2, -1)
+        ea = 1.1 * eg * zu.abs() + (zg * torch.sigmoid(zg)).abs() * eu + 2.0 ** -18 * (2 + zg.abs()) * zu.abs()
+    else:
+        ea = 1.13 * ez + (2.0 ** -18 * (2 + z.abs()) if act != "none" else 0)
+    ref = a + (r.double() if residual else 0)
+    _within(y, ref, HALF * ref.abs() + MORE * ea + U32 * (a.abs() + ref.abs()) + 1e-30, "y")
+    assert U.ulysses_read_error() == 0
+
+
+@pytest.mark.parametrize("T,K,N,act,bias,residual", LINEAR)
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_linear_backward(T, K, N, act, bias, residual, dtype):
+    g = _gen(2 * T + K + N)
+    nz = 2 * N if act == "swiglu" else N
+    x, w, dy = _rnd(g, T, K), _rnd(g, nz, K, scale=K ** -0.5), _rnd(g, T, N)
+    pre = _rnd(g, T, nz, scale=1.5) if act != "none" else None
+    dx, dw, db = U.ulysses_linear_bwd(x, w, dy, pre=pre, activation=ACTS[act], bias_grad=bias, grad_dtype=dtype)
+    again = U.ulysses_linear_bwd(x, w, dy, pre=pre, activation=ACTS[act], bias_grad=bias, grad_dtype=dtype)
+    assert torch.equal(dx, again[0]) and torch.equal(dw, again[1]) and dw.dtype == dtype
+    dyd, xd, wd = dy.double(), x.double(), w.double()
+    if act == "none":
+        dz, e32 = dyd, torch.zeros_like(dyd)
+        edz = e32
+    else:
+        z = pre.double()
+        _, d = _act64(z, act)
+        if act == "swiglu":
+            a, u = z.chunk(2, -1)
+            dz = torch.cat([dyd, dyd], -1) * d
+            f = 2.0 ** -18 * (2 + a.abs()) * dyd.abs()
+            e32 = torch.cat([f * u.abs(), f], -1)
+        else:
+            dz, e32 = dyd * d, 2.0 ** -18 * (2 + z.abs()) * dyd.abs()
+        edz = HALF * dz.abs() + e32
+    ref = dz @ wd
+    _within(dx, ref, HALF * ref.abs() + MORE * ((edz + nz * U32 * dz.abs()) @ wd.abs()) + 1e-30, "dx")
+    ref = dz.t() @ xd
+    bound = MORE * ((edz + T * U32 * dz.abs()).t() @ xd.abs()) + 1e-30
+    _within(dw, ref, bound + (HALF * ref.abs() if dtype == torch.bfloat16 else 0), "dw")
+    if bias:
+        assert torch.equal(db, again[2])
+        _within(db, dz.sum(0), MORE * (e32 + T * U32 * dz.abs()).sum(0) + 1e-30, "dbias")
+    assert U.ulysses_read_error() == 0
+
+
+def test_linear_gradient_against_differences():
+    """dx along a direction against the forward's own differences, in fp32 steps
+    wide enough for bf16 inputs: y is linear in x, so the difference is exact but
+    for the roundings of the two forwards (2^-8 |y| each)."""
+    g = _gen(5)
+    T, K, N = 64, 256, 128
+    x, w, dy, v = _rnd(g, T, K), _rnd(g, N, K, scale=K ** -0.5), _rnd(g, T, N), _rnd(g, T, K)
+    dx, _, _ = U.ulysses_linear_bwd(x, w, dy)
+    lo, hi = (x.float() - v.float()).bfloat16(), (x.float() + v.float()).bfloat16()
+    y0, y1 = U.ulysses_linear(lo, w).double(), U.ulysses_linear(hi, w).double()
+    want = ((y1 - y0) * dy.double()).sum()
+    have = (dx.double() * (hi.double() - lo.double())).sum()
+    slack = (HALF * (y0.abs() + y1.abs()) * dy.double().abs()).sum() + \
+        (HALF * dx.double().abs() * (hi.double() - lo.double()).abs()).sum()
+    assert abs(want - have) <= slack
+    # and of a sum over many entries the roundings largely cancel: their spread is sqrt(count) of one
+    assert abs(want - have) <= slack / math.sqrt(T) + 1.0
+
+
+def test_linear_activation_limits():
+    """Large, infinite and tiny products: the exponentials overflow to 0 or 1, never to NaN."""
+    w = torch.eye(8, device="cuda", dtype=torch.bfloat16)
+    v = torch.tensor([0.0, -0.0, 1e-30, -1e30, 1e30, -200.0, 200.0, 3e38], device="cuda").bfloat16()
+    x = torch.zeros(8, 8, device="cuda", dtype=torch.bfloat16)
+    x[range(8), range(8)] = v
+    for act in ("gelu", "silu"):
+        y = U.ulysses_linear(x, w, activation=ACTS[act])
+        want = torch.where(v > 0, v, torch.zeros_like(v))
+        want[2] = (v[2].float() * 0.5).bfloat16()
+        assert torch.equal(y.diagonal(), want), (act, y.diagonal())
+        dx, _, _ = U.ulysses_linear_bwd(x, w, torch.ones_like(x), pre=x.clone(), activation=ACTS[act])
+        slope = torch.tensor([0.5, 0.5, 0.5, 0, 1, 0, 1, 1], device="cuda").bfloat16()
+        assert torch.equal(dx.diagonal(), slope), (act, dx.diagonal())
+    assert U.ulysses_read_error() == 0
+
+
+def test_linear_in_place_leading_dims_and_guards():
+    """residual may be y; the seq layout's dims are kept; nothing behind the last row is written."""
+    g = _gen(9)
+    P, B, s, K, N = 2, 3, 37, 128, 264
+    x, w = _rnd(g, P, B, s, K), _rnd(g, N, K, scale=K ** -0.5)
+    buf = _rnd(g, P * B * s + 5, N)
+    before = buf.clone()
+    y = buf[:P * B * s].view(P, B, s, N)
+    want = U.ulysses_linear(x, w, residual=before[:P * B * s].view(P, B, s, N))
+    got = U.ulysses_linear(x, w, residual=y, y=y)
+    assert got.data_ptr() == buf.data_ptr() and torch.equal(got, want)
+    assert torch.equal(buf[P * B * s:], before[P * B * s:])
+    T = P * B * s
+    dxb = _rnd(g, T + 3, K)
+    keep = dxb.clone()
+    U.ulysses_linear_bwd(x.view(T, K), w, before[:T], dx=dxb[:T])
+    assert torch.equal(dxb[T:], keep[T:])
+
+
+def test_linear_no_tokens():
+    x, w = torch.empty(0, 64, device="cuda").bfloat16(), torch.ones(16, 64, device="cuda").bfloat16()
+    assert U.ulysses_linear(x, w).shape == (0, 16)
+    dx, dw, db = U.ulysses_linear_bwd(x, w, torch.empty(0, 16, device="cuda").bfloat16(), bias_grad=True)
+    assert dx.shape == (0, 64) and not dw.any() and not db.any()
+
+
+# ------------------------------------------------------------ residual norm
+
+def _rms64(v, w, eps):
+    i = 1 / torch.sqrt((v * v).mean(-1, keepdim=True) + eps)
+    return v * i * (1 if w is None else w), i
+
+
+def _norm_inputs(g, P, B, s, D, dtype, gate, post):
+    shape = (P, B, s, D)
+    mk = lambda *sh, **kw: _rnd(g, *sh, dtype=dtype, **kw)
+    gates = {"none": None, "channel": (D,), "sequence": (B, D), "token": shape}[gate]
+    return dict(x=mk(*shape), h=mk(*shape, scale=2.0), w_post=mk(D, scale=0.2, mean=1.0) if post else None,
+                w_pre=mk(D, scale=0.2, mean=1.0), gate=None if gates is None else mk(*gates, scale=0.7))
+
+
+def _gate64(gate, mode):
+    if gate is None:
+        return 1.0
+    return gate.double()[:, None, :] if mode == "sequence" else gate.double()
+
+
+MODES = {"none": U.GATE_NONE, "channel": U.GATE_CHANNEL, "sequence": U.GATE_SEQUENCE, "token": U.GATE_TOKEN}
+NORMS = [  # P, B, s, D, dtype, gate, post
+    (1, 1, 1, 2560, torch.bfloat16, "channel", True),
+    (1, 1, 1, 8, torch.bfloat16, "none", False),           # one vector
+    (2, 3, 5, 72, torch.bfloat16, "sequence", True),       # a few lanes of a warp, several rows a CTA
+    (3, 2, 7, 1028, torch.float32, "token", True),
+    (2, 2, 33, 520, torch.float32, "sequence", False),
+    (4, 1, 150, 2560, torch.bfloat16, "token", True),
+    (1, 2, 40, 4104, torch.bfloat16, "channel", True),     # two vectors a thread, the last ones absent
+    (1, 1, 9, 12288, torch.bfloat16, "sequence", True),    # more
+    (1, 2, 3, 16384, torch.float32, "channel", True),      # the widest row
+    (1, 1, 3, 32768, torch.bfloat16, "none", True),
+    (1, 700, 2, 64, torch.bfloat16, "sequence", True),     # more sequences than CTAs in flight
+]
+
+
+@pytest.mark.parametrize("P,B,s,D,dtype,gate,post", NORMS)
+def test_residual_norm_forward(P, B, s, D, dtype, gate, post):
+    a, eps = 0.75, 1e-6
+    t = _norm_inputs(_gen(B * s + D), P, B, s, D, dtype, gate, post)
+    r, u = U.ulysses_residual_norm(t["x"], t["h"], w_pre=t["w_pre"], w_post=t["w_post"], gate=t["gate"],
+                                   gate_mode=MODES[gate], res_scale=a, eps=eps)
+    half = HALF if dtype == torch.bfloat16 else 2.0 ** -24
+    esum = (D / 2 + 8) * 2.0 ** -24
+    branch = t["h"].double() if not post else _rms64(t["h"].double(), t["w_post"].double(), eps)[0]
+    branch = branch * _gate64(t["gate"], gate)
+    ref = a * t["x"].double() + branch
+    er = (esum if post else 0) * branch.abs() + 4 * U32 * (branch.abs() + (a * t["x"].double()).abs())
+    _within(r, ref, half * ref.abs() + MORE * er + 1e-30, "r")
+    wp = t["w_pre"].double()
+    un, i = _rms64(ref, wp, eps)
+    # the mean square moves with r: by 2 sum |r| er / D, relative to itself
+    em = (ref.abs() * er).mean(-1, keepdim=True) * i * i
+    eu = er * i * wp.abs() + (esum + em + 4 * U32) * un.abs()
+    _within(u, un, half * un.abs() + MORE * eu + 1e-30, "u")
+
+
+@pytest.mark.parametrize("P,B,s,D,dtype,gate,post", NORMS)
+def test_residual_norm_backward(P, B, s, D, dtype, gate, post):
+    a, eps = 0.75, 1e-6
+    g = _gen(3 * B * s + D)
+    t = _norm_inputs(g, P, B, s, D, dtype, gate, post)
+    r, dr, du = (_rnd(g, P, B, s, D, dtype=dtype) for _ in range(3))
+    kw = dict(dr=dr, du=du, w_pre=t["w_pre"], w_post=t["w_post"], gate=t["gate"], gate_mode=MODES[gate], res_scale=a,
+              eps=eps)
+    got = U.ulysses_residual_norm_bwd(r, t["h"], **kw)
+    again = U.ulysses_residual_norm_bwd(r, t["h"], **kw)
+    assert all((p is None) == (q is None) and (p is None or torch.equal(p, q)) for p, q in zip(got, again))
+    dx, dh, dw_pre, dw_post, dgate = got
+    # the formula's gradient, by differentiating the definition in 64 bits
+    leaf = {k: v.double().requires_grad_() for k, v in t.items() if v is not None and k != "x"}
+    rr = r.double().requires_grad_()
+    u, i = _rms64(rr, leaf["w_pre"], eps)
+    gr, gw = torch.autograd.grad((u * du.double()).sum() + (rr * dr.double()).sum(), [rr, leaf["w_pre"]])
+    n, ih = (leaf["h"], torch.ones(1, device="cuda").double()) if not post else _rms64(leaf["h"], leaf["w_post"], eps)
+    gate64 = _gate64(leaf.get("gate"), gate)
+    names = [k for k in ("h", "w_post", "gate") if k in leaf]
+    grads = dict(zip(names, torch.autograd.grad((n * gate64 * gr).sum(), [leaf[k] for k in names])))
+    half = HALF if dtype == torch.bfloat16 else 2.0 ** -24
+    e = (2 * D + 32) * 2.0 ** -24          # a row's two sums and the few products behind them
+    with torch.no_grad():
+        aw = (du.double() * t["w_pre"].double()).abs()
+        rn = (rr * i).abs()
+        m1 = dr.double().abs() + i * (aw + rn * (aw * rn).mean(-1, keepdim=True))      # sum of |terms| of dR
+        _within(dx, a * gr, half * (a * gr).abs() + e * a * m1 + 1e-30, "dx")
+        T = P * B * s
+        es = e + (T + 8) * 2.0 ** -24
+        _within(dw_pre, gw, es * (du.double().abs() * rn).sum((0, 1, 2)) + 1e-30, "dw_pre")
+        g64 = gate64.abs() if gate != "none" else 1.0
+        if post:
+            wp, hn = t["w_post"].double().abs(), (leaf["h"] * ih).abs()
+            b = m1 * g64 * wp
+            mh = ih * (b + hn * (b * hn).mean(-1, keepdim=True))
+            _within(dw_post, grads["w_post"], 2 * es * (m1 * g64 * hn).sum((0, 1, 2)) + 1e-30, "dw_post")
+        else:
+            mh = m1 * g64
+            assert dw_post is None
+        _within(dh, grads["h"], half * grads["h"].abs() + 2 * e * mh + 1e-30, "dh")
+        if gate == "none":
+            assert dgate is None
+        else:
+            mg = m1 * n.abs()
+            if gate == "token":
+                _within(dgate, grads["gate"], half * grads["gate"].abs() + 2 * e * mg + 1e-30, "dgate")
+            else:
+                mg = mg.sum((0, 2)) if gate == "sequence" else mg.sum((0, 1, 2))
+                _within(dgate, grads["gate"], 2 * es * mg + 1e-30, "dgate")
+
+
+def test_residual_norm_partial_calls():
+    """The first block (no branch), a branch without a following norm, and gradients of one side only."""
+    g = _gen(77)
+    P, B, s, D = 2, 1, 19, 256
+    x, h, w = _rnd(g, P, B, s, D), _rnd(g, P, B, s, D), _rnd(g, D, mean=1.0, scale=0.1)
+    r, u = U.ulysses_residual_norm(x, w_pre=w)
+    assert r is None
+    want, _ = _rms64(x.double(), w.double(), 1e-6)
+    _within(u, want, (HALF + 1e-4) * want.abs() + 1e-30, "first norm")
+    r2, u2 = U.ulysses_residual_norm(x, w_pre=w, r=torch.empty_like(x))
+    assert torch.equal(r2, x) and torch.equal(u2, u)
+    r3, none = U.ulysses_residual_norm(x, h)
+    assert none is None and torch.equal(r3, (x.float() + h.float()).bfloat16())
+    dr = _rnd(g, P, B, s, D)
+    dx, dh, dw_pre, dw_post, dgate = U.ulysses_residual_norm_bwd(x, h, dr=dr)
+    assert torch.equal(dx, dr) and torch.equal(dh, dr) and dw_pre is None and dw_post is None and dgate is None
+    both = U.ulysses_residual_norm_bwd(x, du=dr, w_pre=w)
+    zero = U.ulysses_residual_norm_bwd(x, du=dr, dr=torch.zeros_like(dr), w_pre=w)
+    assert torch.equal(both[0], zero[0]) and torch.equal(both[2], zero[2]) and both[1] is None
+    # in place: r over x or h, u over h
+    want_r, want_u = U.ulysses_residual_norm(x, h, w_pre=w)
+    for target in ("x", "h"):
+        xc, hc = x.clone(), h.clone()
+        rr, uu = U.ulysses_residual_norm(xc, hc, w_pre=w, r=xc if target == "x" else hc,
+                                         u=hc if target == "x" else None)
+        assert torch.equal(rr, want_r) and torch.equal(uu, want_u)
+    drc = dr.clone()
+    want_b = U.ulysses_residual_norm_bwd(x, h, dr=dr, du=h, w_pre=w)
+    got_b = U.ulysses_residual_norm_bwd(x, h, dr=drc, du=h, w_pre=w, dx=drc)
+    assert torch.equal(want_b[0], got_b[0]) and torch.equal(want_b[1], got_b[1])
+
+
+# -------------------------------------------------------------- linear loss
+
+def _loss64(x, w, y, P, ignore):
+    z = x.double() @ w.double().t()
+    keep = (y != ignore) & (y >= 0) & (y < w.shape[0])
+    at = torch.where(keep, y, torch.zeros_like(y)).long()[:, None]
+    lse = torch.logsumexp(z, 1)
+    per = torch.where(keep, lse - z.gather(1, at)[:, 0], torch.zeros_like(lse))
+    C = keep.sum()
+    dz = torch.exp(z - lse[:, None]).scatter_add(1, at, -torch.ones_like(lse)[:, None])
+    dz = torch.where(keep[:, None], dz / C, torch.zeros_like(dz))
+    return per.view(P, -1).sum(1), keep.view(P, -1).sum(1), per.sum() / C, dz
+
+
+LOSSES = [  # P, T, D, V, spread of the logits, ignored share, piece
+    (1, 1, 64, 100, 1.0, 0.0, 0),
+    (1, 3, 8, 1, 1.0, 0.0, 0),                 # a vocabulary of one: loss 0, gradient 0
+    (4, 256, 128, 8192, 1.0, 0.2, 0),
+    (3, 303, 136, 1003, 3.0, 0.5, 0),          # odd vocabulary, ragged rows
+    (2, 1100, 256, 513, 1.0, 0.1, 256),        # five pieces, the last one short
+    (2, 514, 64, 2049, 2.0, 0.0, 257),         # pieces that end inside a tile
+    (2, 1026, 72, 4099, 2.0, 0.3, 1024),       # a last piece of two rows
+    (1, 130, 64, 3000, 60.0, 0.0, 0),          # logits hundreds apart: rows change their reference
+]
+
+
+@pytest.mark.parametrize("P,T,D,V,spread,ignored,piece", LOSSES)
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_linear_loss(P, T, D, V, spread, ignored, piece, dtype):
+    g = _gen(T + V)
+    x, w = _rnd(g, T, D), _rnd(g, V, D, scale=spread * D ** -0.5)
+    y = torch.randint(0, V, (T,), generator=g, device="cuda", dtype=torch.int32)
+    y[torch.rand(T, generator=g, device="cuda") < ignored] = -100
+    y[0] = V - 1
+    S, C, L = U.ulysses_linear_loss(x, w, y, P)
+    S2, C2, L2, dx, dw = U.ulysses_linear_loss_bwd(x, w, y, P, grad_dtype=dtype, piece_tokens=piece)
+    again = U.ulysses_linear_loss_bwd(x, w, y, P, grad_dtype=dtype, piece_tokens=piece)
+    assert all(torch.equal(p, q) for p, q in zip((S2, C2, L2, dx, dw), again))
+    Sr, Cr, Lr, dz = _loss64(x, w, y, P, -100)
+    ez = D * U32 * (x.double().abs() @ w.double().abs().t()).amax(1, keepdim=True)   # one logit's error
+    es = 2 * ez.max() * Cr.max()
+    for a, b, c in ((S, C, L), (S2, C2, L2)):
+        assert torch.equal(b, Cr)
+        assert ((a.double() - Sr).abs() <= LOSS_REL * Sr.abs() + es + 1e-30).all()
+        assert abs(c.double() - Lr) <= LOSS_REL * Lr.abs() + 2 * ez.max() + 1e-30
+    xd, wd = x.double().abs(), w.double().abs()
+    soft = dz.abs()
+    ref = dz @ w.double()
+    _within(dx, ref, HALF * ref.abs() + MORE * (((HALF + 2 * ez + V * U32) * soft) @ wd) + 1e-12, "dx")
+    ref = dz.t() @ x.double()
+    bound = MORE * (((2 * HALF + 2 * ez + T * U32) * soft).t() @ xd) + 1e-12
+    _within(dw, ref, bound + (HALF * ref.abs() if dtype == torch.bfloat16 else 0), "dw")
+    assert U.ulysses_read_error() == 0
+
+
+def test_linear_loss_agrees_with_the_loss_from_logits():
+    """The same labels through ulysses_linear and ulysses_loss_aggregate: the
+    logits are rounded to bf16 there, 2^-8 of the largest at most."""
+    g = _gen(21)
+    P, T, D, V = 4, 512, 256, 4096
+    x, w = _rnd(g, T, D), _rnd(g, V, D, scale=D ** -0.5)
+    y = torch.randint(0, V, (T,), generator=g, device="cuda", dtype=torch.int32)
+    y[::9] = -100
+    logits = U.ulysses_linear(x, w)
+    S, C, L = U.ulysses_loss_aggregate(logits, y, P)
+    S2, C2, L2 = U.ulysses_linear_loss(x, w, y, P)
+    assert torch.equal(C, C2)
+    assert abs(L.item() - L2.item()) <= 2 * HALF * logits.abs().max().item()
+
+
+def test_linear_loss_ignored_rows_and_bad_labels():
+    """Rows that do not count may hold NaN and infinities; a label outside the
+    vocabulary is reported and not counted; no counted token: NaN and zeros."""
+    g = _gen(31)
+    P, T, D, V = 2, 300, 64, 700
+    x, w = _rnd(g, T, D), _rnd(g, V, D, scale=0.3)
+    y = torch.randint(0, V, (T,), generator=g, device="cuda", dtype=torch.int32)
+    clean = x.clone()
+    y[5:150:3] = -100
+    clean[5:150:3] = 0
+    x[5:150:6] = float("nan")
+    x[8:150:6] = float("inf")
+    want = U.ulysses_linear_loss_bwd(clean, w, y, P)
+    got = U.ulysses_linear_loss_bwd(x, w, y, P)
+    assert all(torch.equal(p, q) for p, q in zip(want, got))
+    assert not got[3][5:150:3].any()
+    assert U.ulysses_read_error() == 0
+    y[7], y[8] = V, -3
+    S, C, L, dx, dw = U.ulysses_linear_loss_bwd(x, w, y, P)
+    assert C.sum().item() == (((y >= 0) & (y < V)).sum()).item() and not dx[7:9].any()
+    assert U.ulysses_read_error() == 1 << 8
+    U.ulysses_linear_loss(x, w, y, P)
+    assert U.ulysses_read_error() == 1 << 8
+    y.fill_(-100)
+    S, C, L, dx, dw = U.ulysses_linear_loss_bwd(x, w, y, P)
+    assert torch.isnan(L).all() and not C.any() and not S.any() and not dx.any() and not dw.any()
+    e = U.ulysses_linear_loss_bwd(x[:0], w, y[:0], P)
+    assert torch.isnan(e[2]).all() and not e[1].any() and not e[4].any()
+
+
+def test_linear_loss_masked_vocabulary():
+    """Columns of the vocabulary at -inf or at the type's lowest value get no weight and no gradient."""
+    g = _gen(41)
+    T, D, V = 64, 64, 900
+    x = _rnd(g, T, D).abs() + 0.125          # positive, so that w's sign decides the logit's
+    w = _rnd(g, V, D, scale=0.2)
+    dead = torch.zeros(V, dtype=torch.bool, device="cuda")
+    dead[:300] = True                        # the whole of the first columns among them
+    dead[850:] = True
+    w[dead] = -1e30
+    y = torch.randint(300, 850, (T,), generator=g, device="cuda", dtype=torch.int32)
+    S, C, L, dx, dw = U.ulysses_linear_loss_bwd(x, w, y, 1)
+    Sr, Cr, Lr, dz = _loss64(x, w[300:850], y - 300, 1, -100)
+    assert abs(L.double() - Lr) <= 1e-4 * Lr
+    assert not dw[dead].any()
+    ref = dz @ w[300:850].double()
+    bound = HALF * ref.abs() + MORE * (((HALF + 2e-4 + V * U32) * dz.abs()) @ w[300:850].double().abs()) + 1e-12
+    _within(dx, ref, bound, "dx")
+
+
+# ------------------------------------------------------ streams, graphs, run
+
+def _block(x, p, P):
+    """A feed-forward block and the loss behind it, forward and backward."""
+    lead = x.shape[:-1]
+    _, u = U.ulysses_residual_norm(x, w_pre=p["n1"])
+    f, zf = U.ulysses_linear(u, p["w1"], activation=U.ACT_SWIGLU, save_pre=True)
+    h, _ = U.ulysses_linear(f, p["w2"], bias=p["b2"], save_pre=True)
+    r, v = U.ulysses_residual_norm(x, h, w_pre=p["n3"], w_post=p["n2"], gate=p["gate"], gate_mode=U.GATE_SEQUENCE,
+                                   res_scale=0.9)
+    flat = v.view(-1, v.shape[-1])
+    S, C, L, dv, dhead = U.ulysses_linear_loss_bwd(flat, p["head"], p["labels"], P)
+    dxr, dh, dn3, dn2, dgate = U.ulysses_residual_norm_bwd(r, h, du=dv.view(v.shape), w_pre=p["n3"], w_post=p["n2"],
+                                                           gate=p["gate"], gate_mode=U.GATE_SEQUENCE, res_scale=0.9)
+    df, dw2, db2 = U.ulysses_linear_bwd(f, p["w2"], dh, bias_grad=True)
+    du, dw1, _ = U.ulysses_linear_bwd(u, p["w1"], df, pre=zf, activation=U.ACT_SWIGLU)
+    dx, _, dn1, _, _ = U.ulysses_residual_norm_bwd(x, dr=dxr, du=du, w_pre=p["n1"])
+    assert dx.shape == (*lead, x.shape[-1])
+    return dict(L=L, x=dx, w1=dw1, w2=dw2, b2=db2, n1=dn1, n2=dn2, n3=dn3, gate=dgate, head=dhead)
+
+
+def _block_inputs(g, P, B, s, D, N, V):
+    p = dict(n1=_rnd(g, D, mean=1.0, scale=0.1), n2=_rnd(g, D, mean=1.0, scale=0.1),
+             n3=_rnd(g, D, mean=1.0, scale=0.1), gate=_rnd(g, B, D), w1=_rnd(g, 2 * N, D, scale=D ** -0.5),
+             w2=_rnd(g, D, N, scale=N ** -0.5), b2=_rnd(g, D, scale=0.1), head=_rnd(g, V, D, scale=D ** -0.5))
+    p["labels"] = torch.randint(0, V, (P * B * s,), generator=g, device="cuda", dtype=torch.int32)
+    p["labels"][::7] = -100
+    return _rnd(g, P, B, s, D), p
+
+
+def test_a_block_and_its_loss_together():
+    """The operators as a training step runs them, against 64-bit automatic
+    differentiation of the whole chain.  Each gradient passes at most eight
+    bf16 roundings (activations and gradients between the operators, operands
+    inside them); one is uniform within half a step, 2^-8 / sqrt(3) relative L2;
+    eight of them, even all in line, stay below 2e-2."""
+    P, B, s, D, N, V = 2, 2, 75, 256, 320, 1000
+    x, p = _block_inputs(_gen(51), P, B, s, D, N, V)
+    got = _block(x, p, P)
+    q = {k: v.double().requires_grad_() for k, v in p.items() if k != "labels"}
+    xd = x.double().requires_grad_()
+    u, _ = _rms64(xd, q["n1"], 1e-6)
+    a, b = (u @ q["w1"].t()).chunk(2, -1)
+    h = (a * torch.sigmoid(a) * b) @ q["w2"].t() + q["b2"]
+    r = 0.9 * xd + q["gate"][:, None, :] * _rms64(h, q["n2"], 1e-6)[0]
+    v, _ = _rms64(r, q["n3"], 1e-6)
+    L = torch.nn.functional.cross_entropy((v @ q["head"].t()).view(-1, V), p["labels"].long(), ignore_index=-100)
+    names = [k for k in got if k not in ("L", "x")]
+    grads = torch.autograd.grad(L, [xd] + [q[k] for k in names])
+    assert abs(got["L"].item() - L.item()) <= 2e-2 * L.item()
+    for k, ref in zip(["x"] + names, grads):
+        rel = ((got[k].double() - ref).norm() / ref.norm()).item()
+        assert rel <= 2e-2, f"{k}: relative L2 {rel:.3e}"
+    assert U.ulysses_read_error() == 0
+
+
+def test_block_on_another_stream_and_in_a_graph():
+    """The same bits on a side stream, in a captured graph replayed on new
+    inputs, and in two graphs replayed in turn."""
+    P, B, s, D, N, V = 2, 1, 60, 128, 136, 600
+    xa, p = _block_inputs(_gen(61), P, B, s, D, N, V)
+    xb = _rnd(_gen(62), P, B, s, D)
+    want = [_block(v, p, P) for v in (xa, xb)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = _block(xa, p, P)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    assert all(torch.equal(want[0][k], got[k]) for k in got)
+    x = xa.clone()
+    graphs = []
+    for _ in range(2):
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            graphs.append((gr, _block(x, p, P)))
+    for src, ref in ((xb, want[1]), (xa, want[0])):
+        x.copy_(src)
+        for gr, out in graphs:
+            gr.replay()
+        torch.cuda.synchronize()
+        for _, out in graphs:
+            assert all(torch.equal(ref[k], out[k]) for k in ref)
+    # an explicit stream argument, two calls at once on two streams with workspaces of their own
+    w = p["head"]
+    flat = xa.view(-1, D)
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    a = U.ulysses_linear_loss_bwd(flat, w, p["labels"], P, stream=s1)
+    b = U.ulysses_linear_loss_bwd(flat, w, p["labels"], P, stream=s2)
+    torch.cuda.synchronize()
+    assert all(torch.equal(i, j) for i, j in zip(a, b))
+    assert U.ulysses_read_error() == 0
