@@ -20,6 +20,11 @@
 // MN-major (rows of M or N contiguous elements, 64 x 64 boxes).  Elements
 // past any edge are read as zeros and never stored, so M, N and K are free.
 //
+// A thread holds one row of C, so its own 16-byte stores would fill half a
+// 32-byte sector each, 32 rows apart.  Two-byte outputs go through shared
+// memory instead, 32 x 32 values of a warp at a time, and leave by TMA (8192
+// x 2560 -> 2 x 10240 gated with z kept: 711 -> 675 us).
+//
 // Every wait is bounded (ULY_ERR_TIMEOUT); a launch that gives up lets its
 // copies land before it frees its tensor memory and returns.
 #pragma once
@@ -42,7 +47,9 @@ constexpr int kEpiWarps = 8;
 constexpr int kThreads = 128 + 32 * kEpiWarps;
 constexpr uint32_t kOperandBytes = kHalf * kBK * 2;        // 16 KB
 constexpr uint32_t kStageBytes = 2 * kOperandBytes;        // one CTA's A and B of a k-step
-constexpr uint32_t kOffBar = kStages * kStageBytes;
+constexpr uint32_t kOffOut = kStages * kStageBytes;       // output staging, two 2 KB slots for each epilogue warp
+constexpr uint32_t kOutSlot = 32 * 64;                    // 32 rows of 32 two-byte columns
+constexpr uint32_t kOffBar = kOffOut + kEpiWarps * 2 * kOutSlot;
 constexpr uint32_t kSmemBytes = kOffBar + 256 + 1024;      // barriers + alignment slack
 constexpr long long kLandCycles = 1 << 20;                 // after giving up: the copies in flight land (~0.5 ms)
 
@@ -109,6 +116,36 @@ __device__ __forceinline__ void mma_pair(uint32_t d_tmem, uint64_t a_desc, uint6
       : "memory");
 }
 
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, uint32_t src, int c0, int c1) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(src), "r"(c0), "r"(c1)
+               : "memory");
+}
+
+// One epilogue warp's way out: 32 rows (one a lane) x 32 two-byte columns
+// staged with the 64-byte swizzle of make_out_map(), two slots taken in turn.
+struct OutRing {
+  uint32_t base, slot;
+  int lane;
+  // v: this lane's 32 columns, packed; all lanes of the warp together
+  __device__ __forceinline__ void put(const CUtensorMap *map, int col, int row0, const uint32_t (&v)[16]) {
+    if (lane == 0) bulk_wait_group_read<1>();
+    __syncwarp();
+    const uint32_t at = base + slot * kOutSlot;
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      st_shared_v4(at + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4), v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      tma_store_2d(map, at, col, row0);
+      bulk_commit_group();
+    }
+    slot ^= 1;
+  }
+};
+
 // Which tile and which part of its k-steps a work unit is.  The units of a
 // tile follow one another; tiles go down group_m rows before the next column.
 struct Unit {
@@ -128,9 +165,9 @@ __device__ __forceinline__ Unit unit_of(const Shape &s, int u) {
 }
 
 // Epi::Params, and
-//   Epi::tile(params, unit, acc, row, half): one thread's 128 accumulators
-//   (tensor-memory columns [acc, acc + 128), waited for before it returns) of
-//   C row `row`, columns [128 half, +128) of tile column unit.nt.
+//   Epi::tile(params, unit, acc, row, half, out): one thread's 128 accumulators
+//   (read from tensor memory, columns [128 half, +128) from acc, before it
+//   returns) of C row `row`, in tile column unit.nt.
 template <class Epi, bool A_MN, bool B_MN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     gemm_pair_sm100_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
@@ -239,6 +276,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   } else if (warp >= 4) {
     // ------------------------------------------------------------- epilogue
     const int quarter = warp & 3, half = (warp - 4) >> 2;
+    OutRing out{sb + kOffOut + (uint32_t)(warp - 4) * 2 * kOutSlot, 0, lane};
     int it = 0;
     for (int u = cluster; u < units; u += clusters, ++it) {
       const int buf = it & 1;
@@ -248,11 +286,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       tc_fence_after();
       const Unit w = unit_of(sh, u);
       const uint32_t acc = tmem + ((uint32_t)(quarter * 32) << 16) + buf * kTile;
-      Epi::tile(ep, w, acc, w.mt * kTile + (int)rank * kHalf + quarter * 32 + lane, half);
+      Epi::tile(ep, w, acc, w.mt * kTile + (int)rank * kHalf + quarter * 32 + lane, half, out);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) arrive_cluster(map_cta(bar(B_ACCE + buf), 0));
     }
+    if (lane == 0) bulk_wait_all();
   }
 
   // Normal end: every copy was consumed by an MMA and every MMA was waited for
@@ -273,11 +312,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
 // ------------------------------------------------------------------- host
 
-// 2-D bf16 map of a [rows][inner] matrix with rows `stride` elements apart;
-// 64-column boxes of box_rows rows (128: a K-major operand, 64: an MN-major
-// one).  Elements past either edge read as zero.
-inline bool make_map(CUtensorMap *map, const void *base, long long inner, long long rows, long long stride,
-                     int box_rows) {
+// 2-D map of a [rows][inner] matrix of two-byte elements with rows `stride`
+// elements apart.  Elements past either edge read as zero and are not written.
+inline bool make_map_of(CUtensorMap *map, const void *base, long long inner, long long rows, long long stride,
+                        int box_cols, int box_rows, CUtensorMapSwizzle swizzle) {
   static std::atomic<void *> fn{nullptr};
   void *p = fn.load(std::memory_order_acquire);
   if (!p) {
@@ -289,12 +327,21 @@ inline bool make_map(CUtensorMap *map, const void *base, long long inner, long l
   }
   cuuint64_t dims[2] = {(cuuint64_t)inner, (cuuint64_t)rows};
   cuuint64_t strides[1] = {(cuuint64_t)stride * 2};
-  cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
+  cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
   cuuint32_t es[2] = {1, 1};
   return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p)(
              map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box, es,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// An operand: boxes of 64 columns and box_rows rows (128: K-major, 64: MN-major).
+inline bool make_map(CUtensorMap *map, const void *base, long long inner, long long rows, long long stride,
+                     int box_rows) {
+  return make_map_of(map, base, inner, rows, stride, kBK, box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+// An output leaving through an OutRing.
+inline bool make_out_map(CUtensorMap *map, const void *base, long long inner, long long rows, long long stride) {
+  return make_map_of(map, base, inner, rows, stride, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
 // Parts to cut each tile's k-steps into.  Work units on `clusters` SM pairs
@@ -372,59 +419,59 @@ __device__ __forceinline__ void store8(float *p, const float (&x)[8]) {
 }
 
 // --------------------------------------------------------- plain epilogue
-// out = scale[row] * (A B^T) + add, in bf16 or fp32; N is a multiple of 8.
-// A row whose scale is 0 is stored as zeros whatever the product holds.
+// out = A B^T + add, in bf16 or fp32; N is a multiple of 8.
 struct PlainParams {
+  CUtensorMap out_map;      // bf16 out (launch_plain fills it in)
   void *out;
   const float *add;         // nullable fp32 [M][N] (may be `out` itself, fp32)
-  const float *row_scale;   // nullable [M]
   float *part;              // splits > 1: fp32 [splits][M][N] instead of everything above
   long long M;
   int N, out_f32;
 };
 struct EpiPlain {
   using Params = PlainParams;
-  static __device__ __forceinline__ void store(const Params &p, long long row, int col, float (&z)[8]) {
-    const long long at = row * p.N + col;
-    if (p.row_scale) {
-      const float f = __ldg(p.row_scale + row);
+  static __device__ __forceinline__ void add8(const Params &p, long long row, int col, float (&z)[8]) {
+    if (!p.add) return;
+    float a[8];
+    load8(p.add + row * p.N + col, a);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) z[e] = f == 0.f ? 0.f : z[e] * f;
-    }
-    if (p.add) {
-      float a[8];
-      load8(p.add + at, a);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) z[e] += a[e];
-    }
-    if (p.out_f32) store8(static_cast<float *>(p.out) + at, z);
-    else store8(static_cast<__nv_bfloat16 *>(p.out) + at, z);
+    for (int e = 0; e < 8; ++e) z[e] += a[e];
   }
-  static __device__ __forceinline__ void tile(const Params &p, const Unit &w, uint32_t acc, int row, int half) {
+  static __device__ __forceinline__ void tile(const Params &p, const Unit &w, uint32_t acc, int row, int half,
+                                              OutRing &out) {
+    const bool ok = row < p.M, staged = !p.part && !p.out_f32;
+    const int row0 = row - out.lane;
 #pragma unroll 1
     for (int c = 0; c < kHalf; c += 32) {
-      uint32_t a[32];
+      const int col0 = w.nt * kTile + half * kHalf + c;
+      uint32_t a[32], v[16];
       tmem_ld32(acc + half * kHalf + c, a);
-      if (row < p.M) {
+      if (col0 >= p.N || row0 >= p.M) continue;   // the whole warp
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const int col = w.nt * kTile + half * kHalf + c + 8 * g;
-          if (col < p.N) {
-            float z[8];
+      for (int g = 0; g < 4; ++g) {
+        const int col = col0 + 8 * g;
+        float z[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) z[e] = __uint_as_float(a[8 * g + e]);
-            if (p.part) store8(p.part + ((long long)w.split * p.M + row) * p.N + col, z);
-            else store(p, row, col, z);
+        for (int e = 0; e < 8; ++e) z[e] = __uint_as_float(a[8 * g + e]);
+        if (ok && col < p.N) {
+          if (p.part) {
+            store8(p.part + ((long long)w.split * p.M + row) * p.N + col, z);
+          } else {
+            add8(p, row, col, z);
+            if (p.out_f32) store8(static_cast<float *>(p.out) + (long long)row * p.N + col, z);
           }
         }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[4 * g + e] = pack_bf16x2(z[2 * e], z[2 * e + 1]);
       }
       __syncwarp();
+      if (staged) out.put(&p.out_map, col0, row0, v);
     }
   }
 };
 
 // Sum of a cut product's partials, in the order of the parts, and its epilogue.
-static __global__ void __launch_bounds__(256) plain_join_kernel(const PlainParams p, int splits) {
+static __global__ void __launch_bounds__(256) plain_join_kernel(const __grid_constant__ PlainParams p, int splits) {
   const int vecs = p.N / 8;
   const long long total = p.M * vecs;
   for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < total;
@@ -438,7 +485,9 @@ static __global__ void __launch_bounds__(256) plain_join_kernel(const PlainParam
 #pragma unroll
       for (int e = 0; e < 8; ++e) z[e] += v[e];
     }
-    EpiPlain::store(p, row, col, z);
+    EpiPlain::add8(p, row, col, z);
+    if (p.out_f32) store8(static_cast<float *>(p.out) + row * p.N + col, z);
+    else store8(static_cast<__nv_bfloat16 *>(p.out) + row * p.N + col, z);
   }
 }
 
@@ -459,6 +508,7 @@ uly_status launch_plain(const CUtensorMap &ta, const CUtensorMap &tb, PlainParam
   const long long k_steps = (K + kBK - 1) / kBK;
   if (splits > k_steps) splits = (int)k_steps;   // a short last piece: no part without a k-step
   p.part = splits > 1 ? part : nullptr;
+  if (!p.part && !p.out_f32 && !make_out_map(&p.out_map, p.out, p.N, p.M, p.N)) return ULY_ERR_CUDA;
   prof::Scope scope(kernel_id, stream);
   const uly_status st = launch<EpiPlain, A_MN, B_MN>(ta, tb, make_shape(p.M, p.N, K, kTile, splits), p, stream);
   if (st != ULY_OK || splits == 1) return st;

@@ -9,23 +9,21 @@
 // row's pairs into its logsumexp.  No logit leaves the tensor memory.
 //
 // Gradient, in pieces of tokens: the logits are formed once.  The epilogue
-// stores p_tv = exp(z_tv - c_t) in bf16 against a reference c_t of the row (the
-// largest logit of the first 256 columns, a small product of its own).  bf16
-// has fp32's exponents, so p keeps its 8 significant bits wherever it lies
-// between e^-80 and e^40, and no second pass over it is needed: with
-// g_t = exp(c_t - lse_t) / C,
-//   dz_tv = g_t (p_tv - [v == y_t] exp(lse_t - c_t)),
-// the label's element of p is replaced once lse is known (as
-// exp(lse - c) expm1(z_y - lse), exact for confident tokens too), dx takes g_t
-// in its product's epilogue and dW takes it through x' = g_t x (bf16).  A row
-// with a logit more than 40 above c_t stores those 128 columns against their
-// own maximum instead and is brought to c_t = lse_t when its logsumexp is
-// known (a pass over that row alone).
-// Roundings to bf16: p, x', dx, (dW); each at most half a step, 2^-8 relative.
+// stores p = 2^15 exp(z - maximum) in fp16, the maximum that of the row's 128
+// columns, so every value is at most 2^15 and keeps 11 significant bits down
+// to e^-20 of that maximum (2^-40 of it absolute below).  When the row's pairs
+// have given its logsumexp, one pass brings p to
+//   dz_tv = (softmax_tv - [v == y_t]) / C   in bf16, in place
+// (the label's element as expm1(z_y - lse) / C, exact for confident tokens
+// too), and dx = dz W and dW = dz^T x are plain products.  So dz is rounded to
+// bf16 once, 2^-8 relative at most, after 2^-11 of the stored exponential.
 //
 // Three products of 2 T D V operations, the fewest that do not keep the
-// logits of all tokens in a wider type; bound by the tensor cores, with few
-// tokens by W's bytes.
+// logits in a wider type; bound by the tensor cores, with few tokens by W's
+// bytes.  The pass over p moves 4 bytes a logit: about a twentieth of the time
+// at D = 2560.  Forming the logits a second time instead would cost a third.
+#include <cuda_fp16.h>
+
 #include "gemm_sm100.cuh"
 #include "tokenwise.cuh"
 
@@ -36,29 +34,30 @@ using namespace gemm;
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kMaxAbove = 40.f;   // p up to e^40; sums over any vocabulary stay far inside fp32
-constexpr int kSlot = kHalf;        // columns behind one (reference, sum) pair
-constexpr int kProbe = kTile;       // columns the row references are taken from
+constexpr int kSlot = kHalf;        // columns behind one (maximum, sum) pair
+constexpr float kScale = 32768.f;   // of a stored exponential
 constexpr long long kPieceBytes = 4ll << 30;    // p of one piece of tokens
 constexpr long long kPairBytes = 128ll << 20;   // pairs of one forward piece
 
 struct LossParams {
+  CUtensorMap p_map;       // STORE_P: fp16 [rows][ldp]
   const int32_t *labels;   // of the piece's rows
-  float2 *pairs;           // [slots][rows_pad]: (reference, sum of exp(z - reference))
+  float2 *pairs;           // [slots][rows_pad]: (maximum, sum of exp(z - maximum))
   float *target;           // [rows]: z[label]
-  const float *ref;        // STORE_P: [rows] row references
-  __nv_bfloat16 *p;        // STORE_P: [rows][ldp]
-  long long ldp, rows_pad;
+  long long rows_pad;
   int rows, vocab, ignore_index;
 };
 
 template <bool STORE_P>
 struct EpiLoss {
   using Params = LossParams;
-  static __device__ __forceinline__ void tile(const Params &p, const Unit &w, uint32_t acc, int row, int half) {
+  static __device__ __forceinline__ void tile(const Params &p, const Unit &w, uint32_t acc, int row, int half,
+                                              OutRing &out) {
     const int col0 = w.nt * kTile + half * kSlot;
     const int ncol = min(kSlot, p.vocab - col0);   // columns of the vocabulary here; may be <= 0
     const bool ok = row < p.rows;
+    const int row0 = row - out.lane;
+    if (ncol <= 0 || row0 >= p.rows) return;       // the whole warp
     const int y = ok ? __ldg(p.labels + row) : p.ignore_index;
     const bool counted = y != p.ignore_index && y >= 0 && y < p.vocab;
     float m = -INFINITY;
@@ -75,11 +74,7 @@ struct EpiLoss {
           if (c + e < ncol) m = fmaxf(m, __uint_as_float(a[e]));
       }
     }
-    float ref = m == -INFINITY ? 0.f : m;   // every logit -inf: each term is 0
-    if (STORE_P && ok) {
-      const float r = __ldg(p.ref + row);
-      if (m - r <= kMaxAbove) ref = r;
-    }
+    const float ref = m == -INFINITY ? 0.f : m;   // every logit -inf: each term is 0
     float s[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
     for (int c = 0; c < kSlot; c += 32) {
@@ -91,144 +86,137 @@ struct EpiLoss {
         for (int e = 0; e < 32; ++e) t = y == col0 + c + e ? __uint_as_float(a[e]) : t;
         p.target[row] = t;
       }
-      if (c < ncol) {
-        float q[32];
+      __syncwarp();
+      if (c >= ncol) continue;
+      uint32_t v[16];
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          q[e] = ex2_approx((__uint_as_float(a[e]) - ref) * kLog2e);   // the difference first: exact at any size
-          if (c + 32 > ncol && c + e >= ncol) q[e] = 0.f;
-          s[e & 3] += q[e];
-        }
-        if (STORE_P && ok) {
-          __nv_bfloat16 *o = p.p + row * p.ldp + col0 + c;
-#pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            if (c + 8 * g < ncol) {
-              float v[8];
-#pragma unroll
-              for (int e = 0; e < 8; ++e) v[e] = counted ? q[8 * g + e] : 0.f;
-              store8(o + 8 * g, v);
-            }
-          }
+      for (int e = 0; e < 32; e += 2) {
+        // the difference first: exact at any size of the logits
+        float q0 = ex2_approx((__uint_as_float(a[e]) - ref) * kLog2e);
+        float q1 = ex2_approx((__uint_as_float(a[e + 1]) - ref) * kLog2e);
+        if (c + e >= ncol) q0 = 0.f;
+        if (c + e + 1 >= ncol) q1 = 0.f;
+        s[e & 2] += q0;
+        s[(e & 2) + 1] += q1;
+        if (STORE_P) {
+          const __half2 h = __floats2half2_rn(q0 * kScale, q1 * kScale);
+          v[e / 2] = *reinterpret_cast<const uint32_t *>(&h);
         }
       }
-      __syncwarp();
+      if (STORE_P) out.put(&p.p_map, col0 + c, row0, v);
     }
-    if (ok && ncol > 0)
-      p.pairs[(long long)(w.nt * 2 + half) * p.rows_pad + row] = make_float2(ref, (s[0] + s[1]) + (s[2] + s[3]));
+    if (ok) p.pairs[(long long)(w.nt * 2 + half) * p.rows_pad + row] = make_float2(ref, (s[0] + s[1]) + (s[2] + s[3]));
   }
 };
 
-// Row references from the probe's pairs: the larger of its (at most two) maxima.
-__global__ void __launch_bounds__(256) row_ref_kernel(const float2 *__restrict__ pairs, long long rows_pad, int slots,
-                                                      int rows, float *__restrict__ ref) {
-  const int r = blockIdx.x * blockDim.x + threadIdx.x;
-  if (r >= rows) return;
-  float m = pairs[r].x;
-  if (slots > 1) m = fmaxf(m, pairs[rows_pad + r].x);
-  ref[r] = m;
+__device__ __forceinline__ void merge(float &m, float &s, float m2, float s2) {
+  // (m, s) stands for s exp(m); an empty pair (s = 0) changes nothing
+  if (s2 == 0.f) return;
+  if (s == 0.f) { m = m2; s = s2; return; }
+  const float mm = fmaxf(m, m2);
+  s = s * exp2f((m - mm) * kLog2e) + s2 * exp2f((m2 - mm) * kLog2e);
+  m = mm;
 }
 
-// 32 rows a CTA, lane = row: the warps fold strips of a row's pairs, joined in
-// a fixed order, into lse and the row's loss.  GRAD: also the row's factor
-// g = exp(ref - lse) / C, the label's element of p, x' = g x, and rows with a
-// slot kept against its own maximum brought to the one reference lse.
+// Four rows a CTA: their pairs (one 32-byte sector for a slot of all four) are
+// folded in a fixed order into lse and the rows' losses.  GRAD: then p becomes
+// dz, and x is copied with zeros in the rows that do not count (a row of a
+// padded batch may hold anything, and 0 times NaN is not 0).
 struct RowsParams {
   const float2 *pairs;
-  const float *target, *ref;
+  const float *target;
   const int32_t *labels;
   float *row_loss;            // of the piece's rows
   const long long *count;
-  float *g;
-  __nv_bfloat16 *p, *xg;
-  const __nv_bfloat16 *x;
+  uint4 *p;                   // [rows][ldp / 8]: fp16 in, bf16 out
+  const uint4 *x;
+  uint4 *xk;                  // [rows][hidden / 8]
   long long ldp, rows_pad;
   int rows, slots, vocab, ignore_index, hidden;
   int *err;
 };
-constexpr int kRowWarps = 16;
+constexpr int kRowsCta = 4, kRowThreads = 512;
 
 template <bool GRAD>
-__global__ void __launch_bounds__(32 * kRowWarps) loss_rows_kernel(const RowsParams p) {
-  __shared__ float sh_m[kRowWarps][32], sh_s[kRowWarps][32];
-  __shared__ float sh_g[32], sh_lse[32];
-  __shared__ int sh_odd[32];
+__global__ void __launch_bounds__(kRowThreads) loss_rows_kernel(const RowsParams p) {
+  constexpr int kWarps = kRowThreads / 32;
+  __shared__ float sh_m[kWarps][kRowsCta], sh_s[kWarps][kRowsCta];
+  __shared__ float sh_lse[kRowsCta];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int row0 = blockIdx.x * 32, row = row0 + lane;
-  const bool ok = row < p.rows;
-  const float ref = GRAD && ok ? p.ref[row] : 0.f;
-  const int y = ok ? __ldg(p.labels + row) : p.ignore_index;
-  const bool counted = y != p.ignore_index && y >= 0 && y < p.vocab;
-  float m = -INFINITY, s = 0.f;
-  bool odd = false;
-  if (threadIdx.x < 32) sh_odd[threadIdx.x] = 0;
-  if (ok) {
-    for (int k = warp; k < p.slots; k += kRowWarps) {
-      const float2 v = __ldg(p.pairs + (long long)k * p.rows_pad + row);
-      if (GRAD && counted && v.x != ref) odd = true;
-      if (v.y == 0.f) continue;
-      const float mm = fmaxf(m, v.x);
-      s = s * exp2f((m - mm) * kLog2e) + v.y * exp2f((v.x - mm) * kLog2e);
-      m = mm;
-    }
+  const int row0 = blockIdx.x * kRowsCta, nrows = min(kRowsCta, p.rows - row0);
+  float m[kRowsCta], s[kRowsCta];
+#pragma unroll
+  for (int r = 0; r < kRowsCta; ++r) { m[r] = 0.f; s[r] = 0.f; }
+  for (int k = threadIdx.x; k < p.slots; k += kRowThreads) {
+    // rows past the last one are in the padding of the array: read, not used
+    const float4 *v = reinterpret_cast<const float4 *>(p.pairs + (long long)k * p.rows_pad + row0);
+    const float4 a = __ldg(v), b = __ldg(v + 1);
+    merge(m[0], s[0], a.x, a.y);
+    merge(m[1], s[1], a.z, a.w);
+    merge(m[2], s[2], b.x, b.y);
+    merge(m[3], s[3], b.z, b.w);
   }
-  sh_m[warp][lane] = m;
-  sh_s[warp][lane] = s;
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1)
+#pragma unroll
+    for (int r = 0; r < kRowsCta; ++r) {
+      const float m2 = __shfl_down_sync(0xffffffffu, m[r], off), s2 = __shfl_down_sync(0xffffffffu, s[r], off);
+      merge(m[r], s[r], m2, s2);
+    }
+  if (lane == 0)
+#pragma unroll
+    for (int r = 0; r < kRowsCta; ++r) { sh_m[warp][r] = m[r]; sh_s[warp][r] = s[r]; }
   __syncthreads();
-  if (odd) sh_odd[lane] = 1;
-  if (warp == 0) {
-    for (int k = 1; k < kRowWarps; ++k) {
-      const float m2 = sh_m[k][lane], s2 = sh_s[k][lane];
-      if (s2 == 0.f) continue;
-      const float mm = fmaxf(m, m2);
-      s = s * exp2f((m - mm) * kLog2e) + s2 * exp2f((m2 - mm) * kLog2e);
-      m = mm;
-    }
-    const float lse = m + logf(s);
-    if (ok) {
-      if (y != p.ignore_index && !counted) raise_error(p.err, ULY_ERR_LABEL);
-      p.row_loss[row] = counted ? lse - p.target[row] : 0.f;
-    }
-    sh_lse[lane] = counted ? lse : 0.f;
-    sh_g[lane] = 0.f;
+  if (threadIdx.x < nrows) {
+    const int r = threadIdx.x;
+    float mm = sh_m[0][r], ss = sh_s[0][r];
+    for (int k = 1; k < kWarps; ++k) merge(mm, ss, sh_m[k][r], sh_s[k][r]);
+    const float lse = mm + logf(ss);
+    const int y = __ldg(p.labels + row0 + r);
+    const bool counted = y != p.ignore_index && y >= 0 && y < p.vocab;
+    if (y != p.ignore_index && !counted) raise_error(p.err, ULY_ERR_LABEL);
+    p.row_loss[row0 + r] = counted ? lse - p.target[row0 + r] : 0.f;
+    sh_lse[r] = lse;
   }
   if (!GRAD) return;
   __syncthreads();
-  // a row that has columns against another reference: all of them against lse
-  for (int r = 0; r < 32; ++r) {
-    if (!sh_odd[r] || row0 + r >= p.rows) continue;
-    const float to = sh_lse[r];
-    __nv_bfloat16 *pr = p.p + (long long)(row0 + r) * p.ldp;
-    for (int v = threadIdx.x; v < p.vocab; v += blockDim.x) {
-      const float from = __ldg(p.pairs + (long long)(v / kSlot) * p.rows_pad + row0 + r).x;
-      pr[v] = __float2bfloat16_rn(__bfloat162float(pr[v]) * exp2f((from - to) * kLog2e));
-    }
-  }
-  __syncthreads();
-  if (warp == 0 && ok) {
-    float g = 0.f;
-    if (counted) {
-      const float lse = sh_lse[lane], base = sh_odd[lane] ? lse : ref;
-      const double inv = 1.0 / (double)*p.count;
-      g = (float)inv * expf(base - lse);
-      // z_y <= lse but for rounding: the label's softmax is at most 1
-      p.p[(long long)row * p.ldp + y] =
-          __float2bfloat16_rn(expf(lse - base) * expm1f(fminf(p.target[row] - lse, 0.f)));
-    }
-    p.g[row] = g;
-    sh_g[lane] = g;
-  }
-  __syncthreads();
-  const int vecs = p.hidden / 8, nrows = min(32, p.rows - row0);
-  for (int i = threadIdx.x; i < nrows * vecs; i += blockDim.x) {
-    const int r = i / vecs;
-    const long long at = (long long)(row0 + r) * p.hidden + (i - r * vecs) * 8;
-    const float g = sh_g[r];
-    float v[8];
-    load8(p.x + at, v);
+  const float inv = (float)(1.0 / (double)max(*p.count, 1ll));   // no counted token: every row is zeros
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  for (int r = 0; r < nrows; ++r) {
+    const int row = row0 + r, y = __ldg(p.labels + row);
+    const bool counted = y != p.ignore_index && y >= 0 && y < p.vocab;
+    const float lse = sh_lse[r];
+    uint4 *o = p.p + (long long)row * (p.ldp / 8);
+    const int vecs = (int)(p.ldp / 8);
+    // z_y <= lse but for rounding: the label's softmax is at most 1
+    const float dy = counted ? inv * expm1f(fminf(p.target[row] - lse, 0.f)) : 0.f;
+#pragma unroll 4
+    for (int i = threadIdx.x; i < vecs; i += kRowThreads) {
+      uint4 q = zero;
+      if (counted) {
+        const uint4 h = o[i];
+        const float f = exp2f((p.pairs[(long long)(i / (kSlot / 8)) * p.rows_pad + row].x - lse) * kLog2e) * (inv / kScale);
+        const __half2 *hp = reinterpret_cast<const __half2 *>(&h);
+        float v[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = g == 0.f ? 0.f : v[e] * g;   // an ignored row may hold anything
-    store8(p.xg + at, v);
+        for (int e = 0; e < 4; ++e) {
+          const float2 t = __half22float2(hp[e]);
+          v[2 * e] = t.x * f;
+          v[2 * e + 1] = t.y * f;
+        }
+        if (i == y / 8) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (e == y % 8) v[e] = dy;
+        }
+        q = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                       pack_bf16x2(v[6], v[7]));
+      }
+      o[i] = q;
+    }
+    const int xv = p.hidden / 8;
+    for (int i = threadIdx.x; i < xv; i += kRowThreads)
+      p.xk[(long long)row * xv + i] = counted ? __ldg(p.x + (long long)row * xv + i) : zero;
   }
 }
 
@@ -279,7 +267,7 @@ struct Plan {
   long long piece, rows_pad, ldp;
   int slots, dx_splits, dw_splits;
   bool dw_acc;   // dW of several pieces is summed in an fp32 array of the workspace
-  size_t psum, pcnt, count, row_loss, target, pairs, ref, g, p, xg, part, acc, bytes;   // offsets, total
+  size_t psum, pcnt, count, row_loss, target, pairs, p, xk, part, acc, bytes;   // offsets, total
 };
 
 Plan make_plan(int P, long long T, int D, int V, bool grad, int dw_dtype, long long piece_tokens) {
@@ -304,10 +292,8 @@ Plan make_plan(int P, long long T, int D, int V, bool grad, int dw_dtype, long l
     q.dx_splits = choose_splits(q.piece, D, tiles(q.piece), tiles(D), (V + kBK - 1) / kBK, sms);
     q.dw_splits = choose_splits(V, D, tiles(V), tiles(D), (q.piece + kBK - 1) / kBK, sms);
     q.dw_acc = q.piece < T && dw_dtype == ULY_BF16;
-    q.ref = take((size_t)q.piece * sizeof(float));
-    q.g = take((size_t)q.piece * sizeof(float));
     q.p = take((size_t)q.piece * q.ldp * 2);
-    q.xg = take((size_t)q.piece * D * 2);
+    q.xk = take((size_t)q.piece * D * 2);
     const size_t a = part_bytes(q.piece, D, q.dx_splits), b = part_bytes(V, D, q.dw_splits);
     q.part = take(a > b ? a : b);
     q.acc = take(q.dw_acc ? (size_t)V * D * sizeof(float) : 0);
@@ -318,6 +304,16 @@ Plan make_plan(int P, long long T, int D, int V, bool grad, int dw_dtype, long l
 
 template <typename T>
 T *at(void *ws, size_t off) { return reinterpret_cast<T *>(static_cast<char *>(ws) + off); }
+
+RowsParams rows_of(const Plan &q, const LossParams &p, void *ws, long long t0) {
+  RowsParams r = {};
+  r.pairs = p.pairs; r.target = p.target; r.labels = p.labels;
+  r.row_loss = at<float>(ws, q.row_loss) + t0;
+  r.ldp = q.ldp; r.rows_pad = q.rows_pad;
+  r.rows = p.rows; r.slots = (p.vocab + kSlot - 1) / kSlot; r.vocab = p.vocab; r.ignore_index = p.ignore_index;
+  r.err = error_word();
+  return r;
+}
 
 uly_status finish(const Plan &q, int P, long long T, int V, const int32_t *labels, int ignore_index, float *shard_sum,
                   int64_t *shard_count, float *loss, void *ws, cudaStream_t stream) {
@@ -355,13 +351,9 @@ uly_status linear_loss_launch(int32_t P, int64_t tokens, int32_t D, int32_t V, c
       const uly_status st = launch<EpiLoss<false>, false, false>(ta, tb, make_shape(rows, V, D, kTile, 1), p, stream);
       if (st != ULY_OK) return st;
     }
-    RowsParams r = {};
-    r.pairs = p.pairs; r.target = p.target; r.labels = p.labels;
-    r.row_loss = at<float>(ws, q.row_loss) + t0;
-    r.rows_pad = q.rows_pad; r.rows = rows; r.slots = (V + kSlot - 1) / kSlot; r.vocab = V; r.ignore_index = ignore_index;
-    r.err = error_word();
+    RowsParams r = rows_of(q, p, ws, t0);
     prof::Scope scope(prof::K_LINEAR_LOSS_ROWS, stream);
-    loss_rows_kernel<false><<<(rows + 31) / 32, 32 * kRowWarps, 0, stream>>>(r);
+    loss_rows_kernel<false><<<(rows + kRowsCta - 1) / kRowsCta, kRowThreads, 0, stream>>>(r);
     note_launches(1);
     if (last_launch_status() != ULY_OK) return ULY_ERR_CUDA;
   }
@@ -385,60 +377,46 @@ uly_status linear_loss_bwd_launch(int32_t P, int64_t tokens, int32_t D, int32_t 
     if (cudaMemsetAsync(dw, 0, (size_t)V * D * (dw_dtype == ULY_F32 ? 4 : 2), stream) != cudaSuccess)
       return ULY_ERR_CUDA;
   loss_count_launch(labels, tokens, V, ignore_index, count, stream);
-  CUtensorMap tw, tw_mn, tx, tp, tp_mn, tg_mn;
+  CUtensorMap tw, tw_mn, tx, tz, tz_mn, tk_mn;
   if (!make_map(&tw, w, D, V, D, kHalf) || !make_map(&tw_mn, w, D, V, D, 64)) return ULY_ERR_CUDA;
   for (long long t0 = 0; t0 < tokens; t0 += q.piece) {
     const int rows = (int)(tokens - t0 < q.piece ? tokens - t0 : q.piece);
-    __nv_bfloat16 *pp = at<__nv_bfloat16>(ws, q.p), *xg = at<__nv_bfloat16>(ws, q.xg);
-    if (!make_map(&tx, xb + t0 * D, D, rows, D, kHalf) || !make_map(&tp, pp, V, rows, q.ldp, kHalf) ||
-        !make_map(&tp_mn, pp, V, rows, q.ldp, 64) || !make_map(&tg_mn, xg, D, rows, D, 64))
-      return ULY_ERR_CUDA;
+    void *pp = at<char>(ws, q.p), *xk = at<char>(ws, q.xk);
     LossParams p = {};
+    if (!make_map(&tx, xb + t0 * D, D, rows, D, kHalf) || !make_map(&tz, pp, V, rows, q.ldp, kHalf) ||
+        !make_map(&tz_mn, pp, V, rows, q.ldp, 64) || !make_map(&tk_mn, xk, D, rows, D, 64) ||
+        !make_out_map(&p.p_map, pp, V, rows, q.ldp))
+      return ULY_ERR_CUDA;
     p.labels = labels + t0;
     p.pairs = at<float2>(ws, q.pairs);
     p.target = at<float>(ws, q.target);
     p.rows_pad = q.rows_pad;
-    p.rows = rows; p.ignore_index = ignore_index;
-    float *ref = at<float>(ws, q.ref);
+    p.rows = rows; p.vocab = V; p.ignore_index = ignore_index;
     {
       prof::Scope scope(prof::K_LINEAR_LOSS, stream);
-      // the row references: the same product over the first columns of the vocabulary
-      p.vocab = V < kProbe ? V : kProbe;
-      uly_status st = launch<EpiLoss<false>, false, false>(tx, tw, make_shape(rows, p.vocab, D, kTile, 1), p, stream);
-      if (st != ULY_OK) return st;
-      row_ref_kernel<<<(rows + 255) / 256, 256, 0, stream>>>(p.pairs, q.rows_pad, p.vocab > kSlot ? 2 : 1, rows, ref);
-      note_launches(1);
-      p.vocab = V;
-      p.ref = ref;
-      p.p = pp;
-      p.ldp = q.ldp;
-      st = launch<EpiLoss<true>, false, false>(tx, tw, make_shape(rows, V, D, kTile, 1), p, stream);
+      const uly_status st = launch<EpiLoss<true>, false, false>(tx, tw, make_shape(rows, V, D, kTile, 1), p, stream);
       if (st != ULY_OK) return st;
     }
-    RowsParams r = {};
-    r.pairs = p.pairs; r.target = p.target; r.ref = ref; r.labels = p.labels;
-    r.row_loss = at<float>(ws, q.row_loss) + t0;
+    RowsParams r = rows_of(q, p, ws, t0);
     r.count = count;
-    r.g = at<float>(ws, q.g);
-    r.p = pp; r.xg = xg; r.x = xb + t0 * D;
-    r.ldp = q.ldp; r.rows_pad = q.rows_pad;
-    r.rows = rows; r.slots = (V + kSlot - 1) / kSlot; r.vocab = V; r.ignore_index = ignore_index; r.hidden = D;
-    r.err = error_word();
+    r.p = static_cast<uint4 *>(pp);
+    r.x = reinterpret_cast<const uint4 *>(xb + t0 * D);
+    r.xk = static_cast<uint4 *>(xk);
+    r.hidden = D;
     {
       prof::Scope scope(prof::K_LINEAR_LOSS_ROWS, stream);
-      loss_rows_kernel<true><<<(rows + 31) / 32, 32 * kRowWarps, 0, stream>>>(r);
+      loss_rows_kernel<true><<<(rows + kRowsCta - 1) / kRowsCta, kRowThreads, 0, stream>>>(r);
       note_launches(1);
       if (last_launch_status() != ULY_OK) return ULY_ERR_CUDA;
     }
-    // dx = g (p W)
+    // dx = dz W
     PlainParams o = {};
     o.out = dxb + t0 * D;
-    o.row_scale = r.g;
     o.M = rows; o.N = D;
     float *part = at<float>(ws, q.part);
-    uly_status st = launch_plain<false, true>(tp, tw_mn, o, V, q.dx_splits, part, prof::K_LINEAR_LOSS_DX, stream);
+    uly_status st = launch_plain<false, true>(tz, tw_mn, o, V, q.dx_splits, part, prof::K_LINEAR_LOSS_DX, stream);
     if (st != ULY_OK) return st;
-    // dW (+)= p^T x'; the last piece writes the caller's type
+    // dW (+)= dz^T x; the last piece writes the caller's type
     const bool last = t0 + rows >= tokens;
     o = PlainParams{};
     o.M = V; o.N = D;
@@ -446,7 +424,7 @@ uly_status linear_loss_bwd_launch(int32_t P, int64_t tokens, int32_t D, int32_t 
     o.add = t0 > 0 ? acc : nullptr;
     o.out = last ? dw : acc;
     o.out_f32 = !last || dw_dtype == ULY_F32;
-    st = launch_plain<true, true>(tp_mn, tg_mn, o, rows, q.dw_splits, part, prof::K_LINEAR_LOSS_DW, stream);
+    st = launch_plain<true, true>(tz_mn, tk_mn, o, rows, q.dw_splits, part, prof::K_LINEAR_LOSS_DW, stream);
     if (st != ULY_OK) return st;
   }
   return finish(q, P, tokens, V, labels, ignore_index, shard_sum, shard_count, loss, ws, stream);

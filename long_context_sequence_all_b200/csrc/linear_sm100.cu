@@ -55,6 +55,7 @@ __device__ __forceinline__ float dact_of(float z) {
 }
 
 struct LinearParams {
+  CUtensorMap y_map, pre_map, up_map;     // y, and the parts of pre (up: swiglu)
   const __nv_bfloat16 *bias, *residual;   // nullable
   __nv_bfloat16 *y, *pre;                 // pre nullable: z [M][NZ]
   float *part;                            // splits > 1: fp32 [splits][M][NZ] instead
@@ -68,69 +69,83 @@ struct EpiLinear {
   static constexpr bool kGated = ACT == ULY_ACT_SWIGLU;
   static constexpr int kCols = kGated ? 64 : 128;   // output columns of one warpgroup
 
-  // eight outputs from their z (and the other factor's)
-  static __device__ __forceinline__ void store(const Params &p, long long row, int col, float (&z)[8], float (&up)[8]) {
-    if (p.bias) {
-      float b[8];
-      load8(p.bias + col, b);
+  static __device__ __forceinline__ void add_bias(const Params &p, int col, float (&z)[8], float (&up)[8]) {
+    if (!p.bias) return;
+    float b[8];
+    load8(p.bias + col, b);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) z[e] += b[e];
-      if (kGated) {
-        load8(p.bias + p.N + col, b);
+    for (int e = 0; e < 8; ++e) z[e] += b[e];
+    if (kGated) {
+      load8(p.bias + p.N + col, b);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) up[e] += b[e];
-      }
+      for (int e = 0; e < 8; ++e) up[e] += b[e];
     }
-    if (p.pre) {
-      store8(p.pre + row * p.NZ + col, z);
-      if (kGated) store8(p.pre + row * p.NZ + p.N + col, up);
-    }
+  }
+  // eight outputs from their z (and the other factor's), in z
+  static __device__ __forceinline__ void finish(const Params &p, long long row, int col, float (&z)[8],
+                                                const float (&up)[8], bool read_residual) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) z[e] = act_of<ACT>(z[e], up[e]);
-    if (p.residual) {
+    if (p.residual && read_residual) {
       float r[8];
       load8(p.residual + row * p.N + col, r);
 #pragma unroll
       for (int e = 0; e < 8; ++e) z[e] += r[e];
     }
-    store8(p.y + row * p.N + col, z);
   }
 
-  static __device__ __forceinline__ void tile(const Params &p, const Unit &w, uint32_t acc, int row, int half) {
+  static __device__ __forceinline__ void tile(const Params &p, const Unit &w, uint32_t acc, int row, int half,
+                                              OutRing &out) {
+    const bool ok = row < p.M;
+    const int row0 = row - out.lane;
 #pragma unroll 1
     for (int c = 0; c < kCols; c += 32) {
-      const int c0 = half * kCols + c;
+      const int c0 = half * kCols + c, col0 = w.nt * 2 * kCols + c0;
       uint32_t a[kGated ? 64 : 32];
       if constexpr (kGated) tmem_ld32x2(acc + c0, acc + kHalf + c0, a);
       else tmem_ld32(acc + c0, a);
-      if (row < p.M) {
+      if (col0 >= p.N || row0 >= p.M) continue;   // the whole warp
+      uint32_t vy[16], vz[16], vu[kGated ? 16 : 1];
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const int col = w.nt * 2 * kCols + c0 + 8 * g;
-          if (col < p.N) {
-            float z[8], up[8];
+      for (int g = 0; g < 4; ++g) {
+        const int col = col0 + 8 * g;
+        float z[8], up[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              z[e] = __uint_as_float(a[8 * g + e]);
-              up[e] = kGated ? __uint_as_float(a[(kGated ? 32 : 0) + 8 * g + e]) : 0.f;
-            }
-            if (p.part) {
-              float *o = p.part + ((long long)w.split * p.M + row) * p.NZ + col;
-              store8(o, z);
-              if (kGated) store8(o + p.N, up);
-            } else {
-              store(p, row, col, z, up);
-            }
-          }
+        for (int e = 0; e < 8; ++e) {
+          z[e] = __uint_as_float(a[8 * g + e]);
+          up[e] = kGated ? __uint_as_float(a[(kGated ? 32 : 0) + 8 * g + e]) : 0.f;
         }
+        if (p.part) {
+          if (ok && col < p.N) {
+            float *o = p.part + ((long long)w.split * p.M + row) * p.NZ + col;
+            store8(o, z);
+            if (kGated) store8(o + p.N, up);
+          }
+          continue;
+        }
+        if (col < p.N) add_bias(p, col, z, up);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          vz[4 * g + e] = pack_bf16x2(z[2 * e], z[2 * e + 1]);
+          if constexpr (kGated) vu[4 * g + e] = pack_bf16x2(up[2 * e], up[2 * e + 1]);
+        }
+        finish(p, row, col, z, up, ok && col < p.N);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) vy[4 * g + e] = pack_bf16x2(z[2 * e], z[2 * e + 1]);
       }
       __syncwarp();
+      if (p.part) continue;
+      out.put(&p.y_map, col0, row0, vy);
+      if (p.pre) {
+        out.put(&p.pre_map, col0, row0, vz);
+        if constexpr (kGated) out.put(&p.up_map, col0, row0, vu);
+      }
     }
   }
 };
 
 template <int ACT>
-__global__ void __launch_bounds__(256) linear_join_kernel(const LinearParams p, int splits) {
+__global__ void __launch_bounds__(256) linear_join_kernel(const __grid_constant__ LinearParams p, int splits) {
   const int vecs = p.N / 8;
   const long long total = p.M * vecs;
   for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < total;
@@ -150,7 +165,13 @@ __global__ void __launch_bounds__(256) linear_join_kernel(const LinearParams p, 
         for (int e = 0; e < 8; ++e) up[e] += v[e];
       }
     }
-    EpiLinear<ACT>::store(p, row, col, z, up);
+    EpiLinear<ACT>::add_bias(p, col, z, up);
+    if (p.pre) {
+      store8(p.pre + row * p.NZ + col, z);
+      if (EpiLinear<ACT>::kGated) store8(p.pre + row * p.NZ + p.N + col, up);
+    }
+    EpiLinear<ACT>::finish(p, row, col, z, up, true);
+    store8(p.y + row * p.N + col, z);
   }
 }
 
@@ -158,6 +179,10 @@ template <int ACT>
 uly_status run_linear(const CUtensorMap &ta, const CUtensorMap &tb, LinearParams p, int K, int splits, float *part,
                       cudaStream_t stream) {
   p.part = splits > 1 ? part : nullptr;
+  if (!p.part && (!make_out_map(&p.y_map, p.y, p.N, p.M, p.N) ||
+                  (p.pre && !make_out_map(&p.pre_map, p.pre, p.N, p.M, p.NZ)) ||
+                  (p.pre && p.NZ > p.N && !make_out_map(&p.up_map, p.pre + p.N, p.N, p.M, p.NZ))))
+    return ULY_ERR_CUDA;
   prof::Scope scope(prof::K_LINEAR, stream);
   const Shape s = make_shape(p.M, p.N, K, EpiLinear<ACT>::kCols * 2, splits);
   const uly_status st = launch<EpiLinear<ACT>, false, false>(ta, tb, s, p, stream);
