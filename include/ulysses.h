@@ -479,7 +479,7 @@ enum {
  *   r NULL: not stored;   u NULL: not formed (w_pre is then not read)
  * Sums in fp32; u is formed from the unrounded r; r and u are rounded once.
  * Needs n % P == 0, hidden rows of a multiple of 16 bytes (else ULY_ERR_ALIGN)
- * and at most 64 KB (else ULY_ERR_UNSUPPORTED), eps >= 0.  r may be x or h
+ * and at most 32 KB (else ULY_ERR_UNSUPPORTED), eps >= 0.  r may be x or h
  * itself and u may be h itself; outputs otherwise overlap nothing.
  */
 uly_status ulysses_residual_norm(int32_t batch, int32_t seq_len, int32_t world, int32_t hidden, int32_t dtype,

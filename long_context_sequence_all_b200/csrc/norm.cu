@@ -5,10 +5,8 @@
 //   N(v; w)_j = w_j v_j / sqrt(mean_j v_j^2 + eps)
 //   r = res_scale x + gate * N(h; w_post)        u = N(r; w_pre)
 //
-// One row per group of threads, one 16-byte vector of it per thread (rows over
-// 512 vectors: several), so every tensor is read once and written once: bound
-// by memory traffic.  Sums are fp32; u is taken from the fp32 r, and r and u
-// are rounded once.
+// Every tensor is read once and written once; bound by memory traffic.  Sums
+// are fp32; u is taken from the fp32 r, and r and u are rounded once.
 //
 // Backward, from the stored r (its own sum of squares is formed again beside
 // the other row sum, so no statistics are kept between the passes).  With
@@ -17,66 +15,115 @@
 //   dw_pre = sum_t du rn                         dN = gate dR
 //   dgate = sum dR N(h)   (over what the gate is broadcast along)
 //   b = dN * w_post, dh = (b - hn mean(b hn)) / rms(h),  dw_post = sum_t dN hn
-// The column sums stay in fp32 registers over all rows of a CTA; each CTA
+// The column sums stay in fp32 registers over all rows of a group; each group
 // writes one partial per column and a second kernel folds the partials in a
 // fixed order, so every output is bitwise repeatable.
+//
+// How: persistent groups of threads, one row at a time.  A group's rows arrive
+// by bulk copies in a ring of shared-memory stages, so the loads run ahead of
+// the two row sums (each a barrier of the group).  A thread takes up to five
+// 16-byte vectors of a row (backward: two, its column sums take the registers),
+// so few warps share a row: at 2560 bf16 columns two warps (backward: five)
+// instead of ten, which had left both directions waiting for barriers and
+// shuffles at 3.2 and 2.6 TB/s.  Arithmetic runs on pairs of fp32 values.
+#include <atomic>
+
 #include "common.cuh"
 #include "prof.cuh"
+#include "sm100.cuh"
 #include "tokenwise.cuh"
 
 namespace uly {
 
 namespace {
 
+// Two fp32 values in one 64-bit register pair.
+struct F2 {
+  unsigned long long v;
+};
+__device__ __forceinline__ F2 f2(float lo, float hi) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ F2 f2(float x) { return f2(x, x); }
+__device__ __forceinline__ void split(F2 a, float &lo, float &hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(a.v));
+}
+__device__ __forceinline__ float sum2(F2 a) {
+  float lo, hi;
+  split(a, lo, hi);
+  return lo + hi;
+}
+__device__ __forceinline__ F2 mul(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 add(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+
 template <typename T>
-struct Vec;   // one 16-byte vector
+struct Vec;   // one 16-byte vector as N pairs
 template <>
 struct Vec<__nv_bfloat16> {
-  static constexpr int N = 8;
-  static __device__ __forceinline__ void unpack(const uint4 &u, float (&x)[8]) {
-    const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&u);
+  static constexpr int N = 4;
+  static __device__ __forceinline__ void unpack(const uint4 &u, F2 (&x)[4]) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = f2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xffff0000u));
+  }
+  static __device__ __forceinline__ uint4 pack(const F2 (&x)[4]) {
+    uint32_t w[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const float2 f = __bfloat1622float2(h[e]);
-      x[2 * e] = f.x;
-      x[2 * e + 1] = f.y;
+      float lo, hi;
+      split(x[e], lo, hi);
+      w[e] = sm100::pack_bf16x2(lo, hi);
     }
-  }
-  static __device__ __forceinline__ uint4 pack(const float (&x)[8]) {
-    uint4 u;
-    __nv_bfloat162 *h = reinterpret_cast<__nv_bfloat162 *>(&u);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) h[e] = __floats2bfloat162_rn(x[2 * e], x[2 * e + 1]);
-    return u;
+    return make_uint4(w[0], w[1], w[2], w[3]);
   }
 };
 template <>
 struct Vec<float> {
-  static constexpr int N = 4;
-  static __device__ __forceinline__ void unpack(const uint4 &u, float (&x)[4]) {
-    x[0] = __uint_as_float(u.x); x[1] = __uint_as_float(u.y);
-    x[2] = __uint_as_float(u.z); x[3] = __uint_as_float(u.w);
+  static constexpr int N = 2;
+  static __device__ __forceinline__ void unpack(const uint4 &u, F2 (&x)[2]) {
+    x[0] = f2(__uint_as_float(u.x), __uint_as_float(u.y));
+    x[1] = f2(__uint_as_float(u.z), __uint_as_float(u.w));
   }
-  static __device__ __forceinline__ uint4 pack(const float (&x)[4]) {
-    return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+  static __device__ __forceinline__ uint4 pack(const F2 (&x)[2]) {
+    float a, b, c, d;
+    split(x[0], a, b);
+    split(x[1], c, d);
+    return make_uint4(__float_as_uint(a), __float_as_uint(b), __float_as_uint(c), __float_as_uint(d));
   }
 };
 
-constexpr int kMaxGroup = 512;   // threads of one row
-constexpr int kMaxVecs = 8;      // vectors of one thread
+constexpr int kMaxGroup = 512;                 // threads of one row
+constexpr int kMaxVecs = 2048;                 // vectors of one row (32 KB)
+constexpr int kWarpRows = 4;                   // groups of a CTA where a group is one warp
+constexpr int kMaxStages = 4;
+constexpr uint32_t kRingBytes = 200 * 1024;    // shared memory the stages of an SM's CTAs may take
 
-// Sums of K values over the threads of each group (group g = threads
-// [g*tpr, (g+1)*tpr), tpr a multiple of 32); every thread gets its group's.
-// Two buffers taken in turn, so one barrier a call is enough.
-template <int K>
-__device__ __forceinline__ void group_sum(float (&v)[K], int tpr, float (*sh)[K], int &turn) {
+// Sums of K values over a group: a warp, or the whole CTA (then also a barrier
+// of it; two buffers taken in turn, so one barrier a call is enough).
+template <int K, bool WARP>
+__device__ __forceinline__ void group_sum(float (&v)[K], float (*sh)[K], int &turn) {
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1)
 #pragma unroll
     for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], off);
-  if (tpr == 32) return;
-  const int warp = threadIdx.x >> 5, wpg = tpr >> 5, first = warp / wpg * wpg;
-  float (*buf)[K] = sh + 32 * turn;
+  if (WARP) return;
+  const int warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  float (*buf)[K] = sh + (kMaxGroup / 32) * turn;
   turn ^= 1;
   if ((threadIdx.x & 31) == 0)
 #pragma unroll
@@ -84,405 +131,579 @@ __device__ __forceinline__ void group_sum(float (&v)[K], int tpr, float (*sh)[K]
   __syncthreads();
 #pragma unroll
   for (int k = 0; k < K; ++k) v[k] = 0.f;
-  for (int w = 0; w < wpg; ++w)   // fixed order, the same in every thread
+  for (int w = 0; w < warps; ++w)   // fixed order, the same in every thread
 #pragma unroll
-    for (int k = 0; k < K; ++k) v[k] += buf[first + w][k];
+    for (int k = 0; k < K; ++k) v[k] += buf[w][k];
+}
+
+template <bool WARP>
+__device__ __forceinline__ void group_barrier() {
+  if (WARP) __syncwarp();
+  else __syncthreads();
+}
+
+// Tensors whose rows a stage holds, one after the other.
+struct RingSrc {
+  const void *p[5];
+  int n;
+  void add(const void *q, int &slot) {
+    slot = q ? n : -1;
+    if (q) p[n++] = q;
+  }
+};
+
+// A group's ring of stages.
+struct Ring {
+  uint8_t *base;
+  uint64_t *bars;
+  uint32_t row_bytes, stage_bytes;
+  int stages, at;        // at: the stage the next row is taken from
+  uint32_t phase;
+  // One thread: row `t` of every tensor into stage `st`.
+  __device__ __forceinline__ void issue(const RingSrc &src, long long t, int st) const {
+    const uint32_t bar = sm100::smem_u32(&bars[st]);
+    sm100::mbar_arrive_expect_tx(bar, src.n * row_bytes);
+    for (int k = 0; k < src.n; ++k)
+      sm100::bulk_load(sm100::smem_u32(base + st * stage_bytes + k * row_bytes),
+                       static_cast<const uint8_t *>(src.p[k]) + t * row_bytes, row_bytes, bar);
+  }
+  __device__ __forceinline__ void wait(volatile int *abort, int *err) const {
+    // giving up raises the error; the row is then computed from what is there
+    sm100::mbar_wait(sm100::smem_u32(&bars[at]), phase, abort, err);
+  }
+  __device__ __forceinline__ const uint4 *row(int slot) const {
+    return reinterpret_cast<const uint4 *>(base + at * stage_bytes + slot * row_bytes);
+  }
+  __device__ __forceinline__ void next() {
+    if (++at == stages) { at = 0; phase ^= 1; }
+  }
+};
+
+struct RingShape {
+  int slots, stages;   // tensors of a stage, stages of a group
+  int *err;
+};
+
+template <bool WARP>
+__device__ __forceinline__ Ring ring_setup(uint8_t *base, uint64_t *bars, volatile int *abort, int vecs,
+                                           const RingShape &s) {
+  const int grp = WARP ? threadIdx.x >> 5 : 0;
+  const uint32_t rb = (uint32_t)vecs * 16;
+  Ring r{base + (size_t)grp * s.stages * s.slots * rb, bars + grp * kMaxStages, rb, rb * s.slots, s.stages, 0, 0};
+  if ((WARP ? threadIdx.x & 31 : threadIdx.x) == 0)
+    for (int i = 0; i < s.stages; ++i) sm100::mbar_init(sm100::smem_u32(&r.bars[i]), 1);
+  if (threadIdx.x == 0) *abort = 0;
+  sm100::fence_mbar_init();
+  __syncthreads();
+  return r;
+}
+
+// After a wait that gave up the copies may still be in flight: let them land
+// before the CTA's shared memory is given away.
+__device__ __forceinline__ void ring_end(volatile int *abort) {
+  __syncthreads();
+  if (!*abort) return;
+  const long long t0 = clock64();
+  while (clock64() - t0 < (1 << 20)) __nanosleep(1000);
 }
 
 struct NormParams {
-  const void *x, *h, *gate, *w_post, *w_pre;
-  void *r, *u;
+  RingSrc src;
+  RingShape ring;
+  int sx, sh, sg;   // stage slots of x, h and a token's gate (-1: none)
+  const uint4 *gate, *w_post, *w_pre;
+  uint4 *r, *u;
   long long rows;
-  int vecs, tpr, gate_mode, B, s;
+  int vecs, gate_mode, B, s;
   float res_scale, eps, inv_d;
 };
 
-// Row of the gate that token `t` of the seq layout uses.
-__device__ __forceinline__ long long gate_row(int mode, long long t, int B, int s) {
-  return mode == ULY_GATE_TOKEN ? t : mode == ULY_GATE_SEQUENCE ? (t / s) % B : 0;
-}
-
-template <typename T, int NV>
-__global__ void __launch_bounds__(kMaxGroup) residual_norm_kernel(const NormParams p) {
+// One row a group; thread `l` of its `tpr` takes vectors l, l + tpr, ...
+template <typename T, int NV, bool WARP>
+__global__ void __launch_bounds__(kMaxGroup) residual_norm_kernel(const __grid_constant__ NormParams p) {
   constexpr int E = Vec<T>::N;
-  __shared__ float sh[64][1];
+  extern __shared__ __align__(128) uint8_t stage_mem[];
+  __shared__ uint64_t bars[kWarpRows * kMaxStages];
+  __shared__ int abort_flag;
+  __shared__ float sh[2 * (kMaxGroup / 32)][1];
   int turn = 0;
-  const int grp = threadIdx.x / p.tpr, l = threadIdx.x - grp * p.tpr, rpb = blockDim.x / p.tpr;
-  for (long long t0 = (long long)blockIdx.x * rpb; t0 < p.rows; t0 += (long long)gridDim.x * rpb) {
-    const long long t = t0 + grp;
-    const bool row_ok = t < p.rows;
-    const long long base = t * p.vecs;
-    const long long gbase = row_ok ? gate_row(p.gate_mode, t, p.B, p.s) * p.vecs : 0;
-    uint4 xv[NV], hv[NV], gv[NV];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int v = l + i * p.tpr;
-      const bool ok = row_ok && v < p.vecs;
-      xv[i] = ok ? __ldcs(static_cast<const uint4 *>(p.x) + base + v) : make_uint4(0, 0, 0, 0);
-      hv[i] = ok && p.h ? __ldcs(static_cast<const uint4 *>(p.h) + base + v) : make_uint4(0, 0, 0, 0);
-      if (p.gate_mode != ULY_GATE_NONE)
-        gv[i] = ok ? __ldg(static_cast<const uint4 *>(p.gate) + gbase + v) : make_uint4(0, 0, 0, 0);
+  Ring ring = ring_setup<WARP>(stage_mem, bars, &abort_flag, p.vecs, p.ring);
+  const int l = WARP ? threadIdx.x & 31 : threadIdx.x, tpr = WARP ? 32 : blockDim.x;
+  const long long first = WARP ? (long long)blockIdx.x * kWarpRows + (threadIdx.x >> 5) : blockIdx.x;
+  const long long step = WARP ? (long long)gridDim.x * kWarpRows : gridDim.x;
+  if (l == 0)
+    for (int k = 0; k < ring.stages; ++k)
+      if (first + k * step < p.rows) ring.issue(p.src, first + k * step, k);
+  int done = -1;   // stage whose row every thread has finished with, after the group's next barrier
+  for (long long t = first; t < p.rows; t += step, ring.next()) {
+    if (ring.stages == 1 && done >= 0) {   // no stage to run ahead into
+      group_barrier<WARP>();
+      if (l == 0) ring.issue(p.src, t, 0);
     }
-    float hscale = 1.f;
-    if (p.w_post) {
-      float ss[1] = {0.f};
+    ring.wait(&abort_flag, p.ring.err);
+    const uint4 *gv = nullptr;
+    if (p.gate_mode == ULY_GATE_TOKEN) gv = ring.row(p.sg);
+    else if (p.gate_mode == ULY_GATE_SEQUENCE) gv = p.gate + (t / p.s) % p.B * p.vecs;
+    else if (p.gate_mode == ULY_GATE_CHANNEL) gv = p.gate;
+    F2 r[NV][E], q = f2(0.f);
+    if (p.sh >= 0) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        float h[E];
-        Vec<T>::unpack(hv[i], h);
+        const int v = l + i * tpr;
+        if (v < p.vecs) {
+          Vec<T>::unpack(ring.row(p.sh)[v], r[i]);
+        } else {
 #pragma unroll
-        for (int e = 0; e < E; ++e) ss[0] = fmaf(h[e], h[e], ss[0]);
+          for (int e = 0; e < E; ++e) r[i][e] = f2(0.f);
+        }
+#pragma unroll
+        for (int e = 0; e < E; ++e) q = fma(r[i][e], r[i][e], q);
       }
-      group_sum<1>(ss, p.tpr, sh, turn);
-      hscale = rsqrtf(ss[0] * p.inv_d + p.eps);
     }
-    float r[NV][E];
-    float ss[1] = {0.f};
+    float ss[1] = {sum2(q)};
+    if (p.w_post || !WARP) group_sum<1, WARP>(ss, sh, turn);   // the barrier also frees the previous row's stage
+    if (WARP) __syncwarp();
+    if (l == 0 && done >= 0 && ring.stages > 1 && t + (ring.stages - 1) * step < p.rows)
+      ring.issue(p.src, t + (ring.stages - 1) * step, done);
+    const F2 hs = f2(p.w_post ? rsqrtf(ss[0] * p.inv_d + p.eps) : 1.f), a = f2(p.res_scale);
+    q = f2(0.f);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int v = l + i * p.tpr;
-      float h[E], x[E];
-      Vec<T>::unpack(hv[i], h);
-      Vec<T>::unpack(xv[i], x);
-      if (p.w_post && v < p.vecs) {
-        float w[E];
-        Vec<T>::unpack(__ldg(static_cast<const uint4 *>(p.w_post) + v), w);
+      const int v = l + i * tpr;
+      if (v < p.vecs) {
+        F2 x[E];
+        Vec<T>::unpack(ring.row(p.sx)[v], x);
+        if (p.w_post) {
+          F2 w[E];
+          Vec<T>::unpack(__ldg(p.w_post + v), w);
 #pragma unroll
-        for (int e = 0; e < E; ++e) h[e] *= hscale * w[e];
-      }
-      if (p.gate_mode != ULY_GATE_NONE) {
-        float g[E];
-        Vec<T>::unpack(gv[i], g);
+          for (int e = 0; e < E; ++e) r[i][e] = mul(r[i][e], mul(hs, w[e]));
+        }
+        if (gv) {
+          F2 g[E];
+          Vec<T>::unpack(gv[v], g);
 #pragma unroll
-        for (int e = 0; e < E; ++e) h[e] *= g[e];
+          for (int e = 0; e < E; ++e) r[i][e] = mul(r[i][e], g[e]);
+        }
+#pragma unroll
+        for (int e = 0; e < E; ++e) r[i][e] = p.sh >= 0 ? fma(a, x[e], r[i][e]) : mul(a, x[e]);
+        if (p.r) p.r[t * p.vecs + v] = Vec<T>::pack(r[i]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e) r[i][e] = f2(0.f);
       }
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        r[i][e] = p.h ? fmaf(p.res_scale, x[e], h[e]) : p.res_scale * x[e];
-        ss[0] = fmaf(r[i][e], r[i][e], ss[0]);
-      }
-      if (p.r && row_ok && v < p.vecs) static_cast<uint4 *>(p.r)[base + v] = Vec<T>::pack(r[i]);
+      for (int e = 0; e < E; ++e) q = fma(r[i][e], r[i][e], q);
     }
+    done = ring.at;
     if (!p.u) continue;
-    group_sum<1>(ss, p.tpr, sh, turn);
-    const float rscale = rsqrtf(ss[0] * p.inv_d + p.eps);
+    ss[0] = sum2(q);
+    group_sum<1, WARP>(ss, sh, turn);
+    const F2 rs = f2(rsqrtf(ss[0] * p.inv_d + p.eps));
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int v = l + i * p.tpr;
-      if (!row_ok || v >= p.vecs) continue;
-      float w[E], u[E];
-      Vec<T>::unpack(__ldg(static_cast<const uint4 *>(p.w_pre) + v), w);
+      const int v = l + i * tpr;
+      if (v >= p.vecs) continue;
+      F2 w[E];
+      Vec<T>::unpack(__ldg(p.w_pre + v), w);
 #pragma unroll
-      for (int e = 0; e < E; ++e) u[e] = r[i][e] * rscale * w[e];
-      static_cast<uint4 *>(p.u)[base + v] = Vec<T>::pack(u);
+      for (int e = 0; e < E; ++e) w[e] = mul(r[i][e], mul(rs, w[e]));
+      p.u[t * p.vecs + v] = Vec<T>::pack(w);
     }
   }
+  ring_end(&abort_flag);
 }
 
 struct NormBwdParams {
-  const void *r, *h, *dr, *du, *gate, *w_post, *w_pre;
-  void *dx, *dh, *dgate_tok;
-  float *part_pre, *part_post;   // [groups of all CTAs][vecs * E]; null where not asked for
-  float *part_gate;              // [units][groups of a CTA][vecs * E]
+  RingSrc src;
+  RingShape ring;
+  int sr, su, sh, sd, sg;        // stage slots of r, du, h, dr and a token's gate
+  const uint4 *gate, *w_post, *w_pre;
+  uint4 *dx, *dh, *dgate_tok;
+  float *part_pre, *part_post;   // [groups][vecs * 2 E]; null where not asked for
+  float *part_gate;              // [units][groups of a CTA][vecs * 2 E]
   long long rows_per_b;          // tokens of one gate row (P * s, or all of them)
-  int vecs, tpr, gate_mode, B, s, bs;   // bs = gate rows that units walk (B for sequence gates, else 1)
-  int upb;                       // units (runs of tokens) per gate row
+  int vecs, gate_mode, B, s;
+  int bs, upb;                   // gate rows that units walk (B for sequence gates, else 1); units (runs of tokens) each
   float res_scale, eps, inv_d;
 };
 
-template <typename T, int NV>
-__global__ void __launch_bounds__(kMaxGroup) residual_norm_bwd_kernel(const NormBwdParams p) {
-  constexpr int E = Vec<T>::N;
-  __shared__ float sh3[64][3], sh1[64][1];
+template <typename T, int NV, bool WARP>
+__global__ void __launch_bounds__(kMaxGroup, 1) residual_norm_bwd_kernel(const __grid_constant__ NormBwdParams p) {
+  constexpr int E = Vec<T>::N, G = WARP ? kWarpRows : 1;
+  extern __shared__ __align__(128) uint8_t stage_mem[];
+  __shared__ uint64_t bars[kWarpRows * kMaxStages];
+  __shared__ int abort_flag;
+  __shared__ float sh3[2 * (kMaxGroup / 32)][3], sh1[2 * (kMaxGroup / 32)][1];
   int turn3 = 0, turn1 = 0;
-  const int grp = threadIdx.x / p.tpr, l = threadIdx.x - grp * p.tpr, rpb = blockDim.x / p.tpr;
-  const uint4 zero = make_uint4(0, 0, 0, 0);
-  float a_pre[NV][E] = {}, a_post[NV][E] = {}, a_gate[NV][E] = {};
+  Ring ring = ring_setup<WARP>(stage_mem, bars, &abort_flag, p.vecs, p.ring);
+  const int l = WARP ? threadIdx.x & 31 : threadIdx.x, tpr = WARP ? 32 : blockDim.x;
+  const int grp = WARP ? threadIdx.x >> 5 : 0;
+  F2 a_pre[NV][E], a_post[NV][E], a_gate[NV][E];
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int e = 0; e < E; ++e) a_pre[i][e] = a_post[i][e] = a_gate[i][e] = f2(0.f);
   const int units = p.bs * p.upb;
   for (int unit = blockIdx.x; unit < units; unit += gridDim.x) {
     const int b = unit / p.upb, part = unit - b * p.upb;
-    const long long q0 = p.rows_per_b * part / p.upb, q1 = p.rows_per_b * (part + 1) / p.upb;
-    for (long long q = q0; q < q1; q += rpb) {
-      const bool row_ok = q + grp < q1;
-      long long t = row_ok ? q + grp : q;
-      if (p.bs > 1) {   // token q of sequence b: rank q / s, position q % s
-        const long long rk = t / p.s;
-        t = (rk * p.B + b) * p.s + (t - rk * p.s);
+    const long long q0 = p.rows_per_b * part / p.upb + grp, q1 = p.rows_per_b * (part + 1) / p.upb;
+    auto token = [&](long long k) {   // token k of gate row b: rank k / s, position k % s
+      if (p.bs == 1) return k;
+      const long long rk = k / p.s;
+      return (rk * p.B + b) * p.s + (k - rk * p.s);
+    };
+    if (WARP) __syncwarp();
+    else if (unit != blockIdx.x) __syncthreads();   // every thread is done with the last unit's stages
+    if (l == 0) {
+      int st = ring.at;
+      for (int k = 0; k < ring.stages && q0 + k * G < q1; ++k) {
+        ring.issue(p.src, token(q0 + k * G), st);
+        if (++st == ring.stages) st = 0;
       }
-      const long long base = t * p.vecs;
-      const long long gbase = gate_row(p.gate_mode, t, p.B, p.s) * p.vecs;
-      uint4 rv[NV], hv[NV], dv[NV], uv[NV], gv[NV];
+    }
+    int done = -1;
+    for (long long k = q0; k < q1; k += G, ring.next()) {
+      const long long base = token(k) * p.vecs;
+      if (ring.stages == 1 && done >= 0) {   // no stage to run ahead into
+        group_barrier<WARP>();
+        if (l == 0) ring.issue(p.src, token(k), 0);
+      }
+      ring.wait(&abort_flag, p.ring.err);
+      F2 rr = f2(0.f), ar = f2(0.f), hh = f2(0.f);   // sums of r^2, du w_pre r and h^2, taken together
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int v = l + i * p.tpr;
-        const bool ok = row_ok && v < p.vecs;
-        rv[i] = ok && p.r ? __ldcs(static_cast<const uint4 *>(p.r) + base + v) : zero;
-        uv[i] = ok && p.du ? __ldcs(static_cast<const uint4 *>(p.du) + base + v) : zero;
-        hv[i] = ok && p.h ? __ldcs(static_cast<const uint4 *>(p.h) + base + v) : zero;
-        dv[i] = ok && p.dr ? __ldcs(static_cast<const uint4 *>(p.dr) + base + v) : zero;
-        if (p.gate_mode != ULY_GATE_NONE) gv[i] = ok ? __ldg(static_cast<const uint4 *>(p.gate) + gbase + v) : zero;
+        const int v = l + i * tpr;
+        if (v < p.vecs) {
+          if (p.w_post) {
+            F2 h[E];
+            Vec<T>::unpack(ring.row(p.sh)[v], h);
+#pragma unroll
+            for (int e = 0; e < E; ++e) hh = fma(h[e], h[e], hh);
+          }
+          if (p.su >= 0) {
+            F2 r[E], u[E], w[E];
+            Vec<T>::unpack(ring.row(p.sr)[v], r);
+            Vec<T>::unpack(ring.row(p.su)[v], u);
+            Vec<T>::unpack(__ldg(p.w_pre + v), w);
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+              rr = fma(r[e], r[e], rr);
+              ar = fma(mul(u[e], w[e]), r[e], ar);
+            }
+          }
+        }
       }
-      // sums of r^2, du w_pre r and h^2 together
-      float s3[3] = {0.f, 0.f, 0.f};
+      float s3[3] = {sum2(rr), sum2(ar), sum2(hh)};
+      group_sum<3, WARP>(s3, sh3, turn3);   // the barrier also frees the previous row's stage
+      if (WARP) __syncwarp();
+      if (l == 0 && done >= 0 && ring.stages > 1 && k + (ring.stages - 1) * G < q1)
+        ring.issue(p.src, token(k + (ring.stages - 1) * G), done);
+      const float irs = rsqrtf(s3[0] * p.inv_d + p.eps);
+      const F2 ir = f2(irs), nc1 = f2(-s3[1] * irs * irs * p.inv_d);   // -mean(a rn) / rms(r)
+      const float ihs = p.w_post ? rsqrtf(s3[2] * p.inv_d + p.eps) : 1.f;
+      const F2 ih = f2(ihs), a = f2(p.res_scale);
+      F2 s1p = f2(0.f), dn[NV][E];
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int v = l + i * p.tpr;
-        float r[E], h[E];
-        Vec<T>::unpack(rv[i], r);
-        Vec<T>::unpack(hv[i], h);
+        const int v = l + i * tpr;
+        if (v < p.vecs) {
+          F2 (&d)[E] = dn[i];
 #pragma unroll
-        for (int e = 0; e < E; ++e) s3[2] = fmaf(h[e], h[e], s3[2]);
-        if (p.du && v < p.vecs) {
-          float u[E], w[E];
-          Vec<T>::unpack(uv[i], u);
-          Vec<T>::unpack(__ldg(static_cast<const uint4 *>(p.w_pre) + v), w);
+          for (int e = 0; e < E; ++e) d[e] = f2(0.f);
+          if (p.sd >= 0) Vec<T>::unpack(ring.row(p.sd)[v], d);
+          if (p.su >= 0) {
+            F2 r[E], u[E], w[E];
+            Vec<T>::unpack(ring.row(p.sr)[v], r);
+            Vec<T>::unpack(ring.row(p.su)[v], u);
+            Vec<T>::unpack(__ldg(p.w_pre + v), w);
 #pragma unroll
-          for (int e = 0; e < E; ++e) {
-            s3[0] = fmaf(r[e], r[e], s3[0]);
-            s3[1] = fmaf(u[e] * w[e], r[e], s3[1]);
+            for (int e = 0; e < E; ++e) {
+              d[e] = fma(ir, fma(nc1, r[e], mul(u[e], w[e])), d[e]);
+              a_pre[i][e] = fma(mul(u[e], ir), r[e], a_pre[i][e]);
+            }
+          }
+          if (p.dx) {
+            F2 o[E];
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[e] = mul(a, d[e]);
+            p.dx[base + v] = Vec<T>::pack(o);
+          }
+          if (p.sh >= 0) {
+            F2 h[E], w[E];
+            Vec<T>::unpack(ring.row(p.sh)[v], h);
+            if (p.w_post) {
+              Vec<T>::unpack(__ldg(p.w_post + v), w);
+#pragma unroll
+              for (int e = 0; e < E; ++e) h[e] = mul(h[e], ih);   // hn
+            } else {
+#pragma unroll
+              for (int e = 0; e < E; ++e) w[e] = f2(1.f);
+            }
+            if (p.gate_mode != ULY_GATE_NONE) {
+              F2 g[E], o[E];
+              Vec<T>::unpack(p.sg >= 0 ? ring.row(p.sg)[v] : __ldg(p.gate + (long long)b * p.vecs + v), g);
+#pragma unroll
+              for (int e = 0; e < E; ++e) {
+                o[e] = mul(d[e], mul(h[e], w[e]));   // dR N(h)
+                d[e] = mul(d[e], g[e]);
+              }
+              if (p.sg >= 0) {
+                if (p.dgate_tok) p.dgate_tok[base + v] = Vec<T>::pack(o);
+              } else {
+#pragma unroll
+                for (int e = 0; e < E; ++e) a_gate[i][e] = add(a_gate[i][e], o[e]);
+              }
+            }
+            if (p.w_post) {
+#pragma unroll
+              for (int e = 0; e < E; ++e) {
+                a_post[i][e] = fma(d[e], h[e], a_post[i][e]);
+                d[e] = mul(d[e], w[e]);
+                s1p = fma(d[e], h[e], s1p);
+              }
+            }
           }
         }
       }
-      group_sum<3>(s3, p.tpr, sh3, turn3);
-      const float ir = rsqrtf(s3[0] * p.inv_d + p.eps);
-      const float c1 = s3[1] * ir * ir * p.inv_d;      // mean(a rn) / rms(r), so that a rn-term is c1 * r
-      const float ih = p.w_post ? rsqrtf(s3[2] * p.inv_d + p.eps) : 1.f;
-      float s1[1] = {0.f};
-      float dn[NV][E];
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int v = l + i * p.tpr;
-        const bool ok = row_ok && v < p.vecs;
-        float r[E], d[E], h[E], w[E];
-        Vec<T>::unpack(dv[i], d);
-        if (p.du && v < p.vecs) {
-          float u[E];
-          Vec<T>::unpack(rv[i], r);
-          Vec<T>::unpack(uv[i], u);
-          Vec<T>::unpack(__ldg(static_cast<const uint4 *>(p.w_pre) + v), w);
-#pragma unroll
-          for (int e = 0; e < E; ++e) {
-            d[e] += ir * (u[e] * w[e] - c1 * r[e]);
-            if (ok) a_pre[i][e] = fmaf(u[e] * ir, r[e], a_pre[i][e]);
-          }
-        }
-        if (p.dx && ok) {
-          float o[E];
-#pragma unroll
-          for (int e = 0; e < E; ++e) o[e] = p.res_scale * d[e];
-          static_cast<uint4 *>(p.dx)[base + v] = Vec<T>::pack(o);
-        }
-        Vec<T>::unpack(hv[i], h);
-        if (p.w_post && v < p.vecs) {
-          Vec<T>::unpack(__ldg(static_cast<const uint4 *>(p.w_post) + v), w);
-        } else {
-#pragma unroll
-          for (int e = 0; e < E; ++e) w[e] = 1.f;
-        }
-#pragma unroll
-        for (int e = 0; e < E; ++e) dn[i][e] = d[e];
-        if (p.gate_mode != ULY_GATE_NONE) {
-          float g[E], o[E];
-          Vec<T>::unpack(gv[i], g);
-#pragma unroll
-          for (int e = 0; e < E; ++e) {
-            o[e] = d[e] * (h[e] * ih * w[e]);   // dR N(h)
-            dn[i][e] = d[e] * g[e];
-          }
-          if (p.gate_mode == ULY_GATE_TOKEN) {
-            if (p.dgate_tok && ok) static_cast<uint4 *>(p.dgate_tok)[base + v] = Vec<T>::pack(o);
-          } else if (ok) {
-#pragma unroll
-            for (int e = 0; e < E; ++e) a_gate[i][e] += o[e];
-          }
-        }
-        if (p.w_post && ok) {
-#pragma unroll
-          for (int e = 0; e < E; ++e) {
-            const float hn = h[e] * ih;
-            a_post[i][e] = fmaf(dn[i][e], hn, a_post[i][e]);
-            dn[i][e] *= w[e];
-            s1[0] = fmaf(dn[i][e], hn, s1[0]);
-          }
-        }
-      }
+      done = ring.at;
       if (!p.dh) continue;
-      float c2 = 0.f;
+      F2 nc2 = f2(0.f);
       if (p.w_post) {
-        group_sum<1>(s1, p.tpr, sh1, turn1);
-        c2 = s1[0] * p.inv_d;
+        float s1[1] = {sum2(s1p)};
+        group_sum<1, WARP>(s1, sh1, turn1);
+        nc2 = f2(-s1[0] * p.inv_d * ihs);
       }
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int v = l + i * p.tpr;
-        if (!row_ok || v >= p.vecs) continue;
-        float h[E], o[E];
-        Vec<T>::unpack(hv[i], h);
+        const int v = l + i * tpr;
+        if (v < p.vecs) {
+          if (p.w_post) {
+            F2 h[E];
+            Vec<T>::unpack(ring.row(p.sh)[v], h);
 #pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = p.w_post ? ih * (dn[i][e] - c2 * (h[e] * ih)) : dn[i][e];
-        static_cast<uint4 *>(p.dh)[base + v] = Vec<T>::pack(o);
+            for (int e = 0; e < E; ++e) dn[i][e] = mul(ih, fma(nc2, h[e], dn[i][e]));
+          }
+          p.dh[base + v] = Vec<T>::pack(dn[i]);
+        }
       }
     }
     if (p.part_gate) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int v = l + i * p.tpr;
+        const int v = l + i * tpr;
         if (v < p.vecs) {
-          float *o = p.part_gate + (((long long)unit * rpb + grp) * p.vecs + v) * E;
+          F2 *o = reinterpret_cast<F2 *>(p.part_gate) + (((long long)unit * G + grp) * p.vecs + v) * E;
 #pragma unroll
-          for (int e = 0; e < E; ++e) { o[e] = a_gate[i][e]; a_gate[i][e] = 0.f; }
+          for (int e = 0; e < E; ++e) {
+            o[e] = a_gate[i][e];
+            a_gate[i][e] = f2(0.f);
+          }
         }
       }
     }
   }
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int v = l + i * p.tpr;
-    if (v >= p.vecs) continue;
-    const long long at = (((long long)blockIdx.x * rpb + grp) * p.vecs + v) * E;
+    const int v = l + i * tpr;
+    if (v < p.vecs) {
+      const long long at = (((long long)blockIdx.x * G + grp) * p.vecs + v) * E;
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      if (p.part_pre) p.part_pre[at + e] = a_pre[i][e];
-      if (p.part_post) p.part_post[at + e] = a_post[i][e];
+      for (int e = 0; e < E; ++e) {
+        if (p.part_pre) reinterpret_cast<F2 *>(p.part_pre)[at + e] = a_pre[i][e];
+        if (p.part_post) reinterpret_cast<F2 *>(p.part_post)[at + e] = a_post[i][e];
+      }
     }
   }
+  ring_end(&abort_flag);
 }
 
-// Threads of a row, vectors of a thread and rows of a CTA for rows of `vecs`
-// vectors: one vector a thread up to 512 (2560 bf16: 320 threads), CTAs of
-// about 256 threads or one row.
+// ------------------------------------------------------------------- host
+
+// Groups and stages for rows of `vecs` vectors: a warp a row while `nv` vectors
+// a thread cover it, else the fewest warps that do; CTAs an SM by the registers
+// (`threads` of them an SM) and by two stages each at least (one only where a
+// single CTA's do not fit).
 struct RowShape {
-  int tpr, nv, rpb;
+  int tpr, nv, rpb, per_sm, stages;
+  uint32_t smem;
 };
-RowShape row_shape(int vecs) {
+RowShape row_shape(int vecs, int slots, int nv, int threads) {
   RowShape r;
-  r.nv = (vecs + kMaxGroup - 1) / kMaxGroup;
-  const int per = (vecs + r.nv - 1) / r.nv;
-  r.tpr = (per + 31) / 32 * 32;
-  r.rpb = r.tpr >= 256 ? 1 : 256 / r.tpr;
+  auto up32 = [](int v) { return (v + 31) / 32 * 32; };
+  r.tpr = up32((vecs + nv - 1) / nv);
+  if (r.tpr > kMaxGroup) r.tpr = kMaxGroup;
+  r.nv = (vecs + r.tpr - 1) / r.tpr;
+  r.rpb = r.tpr == 32 ? kWarpRows : 1;
+  const uint32_t stage = (uint32_t)vecs * 16 * slots * r.rpb;
+  r.per_sm = threads / (r.tpr * r.rpb);
+  if (r.per_sm < 1) r.per_sm = 1;
+  while (r.per_sm > 1 && kRingBytes / (stage * r.per_sm) < 2) --r.per_sm;
+  r.stages = (int)(kRingBytes / (stage * r.per_sm));
+  if (r.stages > kMaxStages) r.stages = kMaxStages;
+  r.smem = stage * r.stages;
   return r;
 }
+constexpr int kFwdVecs = 5, kFwdThreads = 576;   // up to 112 registers a thread
+constexpr int kBwdVecs = 2, kBwdThreads = 512;   // up to 128
 
-template <typename T>
-using FwdKernel = void (*)(NormParams);
-template <typename T>
-FwdKernel<T> fwd_kernel(int nv) {
-  switch (nv) {
-    case 1: return residual_norm_kernel<T, 1>;
-    case 2: return residual_norm_kernel<T, 2>;
-    case 3: case 4: return residual_norm_kernel<T, 4>;
-    default: return residual_norm_kernel<T, 8>;
-  }
+template <typename Params>
+struct Entry {
+  void (*kernel)(Params);
+  std::atomic<uint64_t> optin{0};
+};
+// The kernel for `nv` vectors a thread, opted into its shared memory.
+template <typename Params>
+uly_status run(Entry<Params> &e, int grid, int threads, uint32_t smem, const Params &p, cudaStream_t stream) {
+  if (!smem_optin(e.kernel, (int)kRingBytes, e.optin)) return ULY_ERR_CUDA;
+  e.kernel<<<grid, threads, smem, stream>>>(p);
+  note_launches(1);
+  return last_launch_status();
 }
-using BwdKernel = void (*)(NormBwdParams);
 template <typename T>
-BwdKernel bwd_kernel(int nv) {
-  switch (nv) {
-    case 1: return residual_norm_bwd_kernel<T, 1>;
-    case 2: return residual_norm_bwd_kernel<T, 2>;
-    case 3: case 4: return residual_norm_bwd_kernel<T, 4>;
-    default: return residual_norm_bwd_kernel<T, 8>;
-  }
+Entry<NormParams> &fwd_entry(const RowShape &r) {
+  static Entry<NormParams> warp[5] = {{residual_norm_kernel<T, 1, true>}, {residual_norm_kernel<T, 2, true>},
+                                      {residual_norm_kernel<T, 3, true>}, {residual_norm_kernel<T, 4, true>},
+                                      {residual_norm_kernel<T, 5, true>}};
+  static Entry<NormParams> cta[3] = {{residual_norm_kernel<T, 3, false>}, {residual_norm_kernel<T, 4, false>},
+                                     {residual_norm_kernel<T, 5, false>}};
+  return r.tpr == 32 ? warp[r.nv - 1] : cta[r.nv < 3 ? 0 : r.nv - 3];
+}
+template <typename T>
+Entry<NormBwdParams> &bwd_entry(const RowShape &r) {
+  static Entry<NormBwdParams> warp[2] = {{residual_norm_bwd_kernel<T, 1, true>}, {residual_norm_bwd_kernel<T, 2, true>}};
+  static Entry<NormBwdParams> cta[3] = {{residual_norm_bwd_kernel<T, 2, false>}, {residual_norm_bwd_kernel<T, 3, false>},
+                                        {residual_norm_bwd_kernel<T, 4, false>}};
+  return r.tpr == 32 ? warp[r.nv - 1] : cta[r.nv < 2 ? 0 : r.nv - 2];
 }
 
 // How the backward walks the tokens: `bs` gate rows, each cut into `upb` runs
-// of tokens, on `grid` CTAs.  About four CTAs an SM keep enough loads in
-// flight; the runs are no shorter than a CTA's rows.
+// of tokens, on `grid` CTAs.  The same whichever tensors a call has.
 struct BwdPlan {
   RowShape rs;
-  int bs, upb, grid;
+  int slots, bs, upb, grid;
   size_t off_pre, off_post, off_gate, bytes;
 };
-BwdPlan bwd_plan(int B, long long n, int vecs, int E, int gate_mode, bool pre, bool post, bool gate) {
+BwdPlan bwd_plan(int B, long long n, int hidden, int e, int gate_mode) {
   BwdPlan q;
-  q.rs = row_shape(vecs);
+  q.slots = gate_mode == ULY_GATE_TOKEN ? 5 : 4;
+  q.rs = row_shape(hidden / e, q.slots, kBwdVecs, kBwdThreads);
   q.bs = gate_mode == ULY_GATE_SEQUENCE ? B : 1;
   const long long rows = gate_mode == ULY_GATE_SEQUENCE ? n : (long long)B * n;
-  const int per_sm = q.rs.tpr * q.rs.rpb <= 320 ? 4 : 2;
-  const long long want = (long long)device_sm_count() * per_sm;
+  const long long want = (long long)device_sm_count() * q.rs.per_sm;
   long long upb = want / q.bs, most = (rows + q.rs.rpb - 1) / q.rs.rpb;
   if (upb < 1) upb = 1;
   if (upb > most) upb = most;
   q.upb = (int)upb;
   const long long units = (long long)q.bs * q.upb;
   q.grid = (int)(units < want ? units : want);
-  const size_t col = (size_t)vecs * E * sizeof(float) * q.rs.rpb;
+  const size_t col = (size_t)hidden * sizeof(float) * q.rs.rpb;
   q.off_pre = 0;
-  q.off_post = q.off_pre + (pre ? col * q.grid : 0);
-  q.off_gate = q.off_post + (post ? col * q.grid : 0);
-  q.bytes = q.off_gate + (gate && (gate_mode == ULY_GATE_CHANNEL || gate_mode == ULY_GATE_SEQUENCE) ? col * units : 0);
+  q.off_post = q.off_pre + col * q.grid;
+  q.off_gate = q.off_post + col * q.grid;
+  q.bytes = q.off_gate + (gate_mode == ULY_GATE_CHANNEL || gate_mode == ULY_GATE_SEQUENCE ? col * units : 0);
   return q;
+}
+
+// Column sums to fold: dst[k][c] = sum over i < parts of src[k][i][c], k < rows.
+struct FoldJob {
+  const float *src;
+  float *dst;
+  long long parts;
+  int rows;
+};
+struct FoldJobs {
+  FoldJob job[3];
+  int n, cols;
+};
+
+// Rows of all jobs along grid.y, 32 columns a CTA; 8 strips of partials are
+// added in a fixed order and joined through shared memory.
+__global__ void __launch_bounds__(256) fold_columns_kernel(const __grid_constant__ FoldJobs jobs) {
+  __shared__ float sh[8][33];
+  const int lane = threadIdx.x & 31, strip = threadIdx.x >> 5, cols = jobs.cols;
+  int total = 0;
+  for (int j = 0; j < jobs.n; ++j) total += jobs.job[j].rows;
+  for (int row = blockIdx.y; row < total; row += gridDim.y) {
+    int k = row, j = 0;
+    while (k >= jobs.job[j].rows) k -= jobs.job[j++].rows;
+    const long long parts = jobs.job[j].parts;
+    const int c = blockIdx.x * 32 + lane;
+    const float *s = jobs.job[j].src + (long long)k * parts * cols;
+    float a[8] = {};
+    if (c < cols) {
+      long long i = strip;
+      for (; i + 56 < parts; i += 64) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) a[e] += __ldcs(s + (i + 8 * e) * cols + c);
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e, i += 8)
+        if (i < parts) a[e] += __ldcs(s + i * cols + c);
+    }
+    sh[strip][lane] = ((a[0] + a[1]) + (a[2] + a[3])) + ((a[4] + a[5]) + (a[6] + a[7]));
+    __syncthreads();
+    if (strip == 0 && c < cols) {
+      float v = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v += sh[e][lane];
+      jobs.job[j].dst[(long long)k * cols + c] = v;
+    }
+    __syncthreads();
+  }
+}
+
+uly_status fold_launch(const FoldJobs &jobs, cudaStream_t stream) {
+  long long rows = 0;
+  for (int j = 0; j < jobs.n; ++j) rows += jobs.job[j].rows;
+  if (rows == 0) return ULY_OK;
+  prof::Scope scope(prof::K_FOLD_COLUMNS, stream);
+  fold_columns_kernel<<<dim3((jobs.cols + 31) / 32, (unsigned)(rows < 65535 ? rows : 65535)), 256, 0, stream>>>(jobs);
+  note_launches(1);
+  return last_launch_status();
 }
 
 }  // namespace
 
-// dst[k][c] = sum over i < parts of src[k][i][c], in a fixed order: 32 columns
-// a CTA, 8 strips of partials folded through shared memory.
-__global__ void __launch_bounds__(256) fold_columns_kernel(const float *__restrict__ src, long long parts, int cols,
-                                                           float *__restrict__ dst) {
-  __shared__ float sh[8][33];
-  const int lane = threadIdx.x & 31, strip = threadIdx.x >> 5;
-  const int c = blockIdx.x * 32 + lane;
-  const float *s = src + (long long)blockIdx.y * parts * cols;
-  float a[4] = {0.f, 0.f, 0.f, 0.f};
-  if (c < cols) {
-    long long i = strip;
-    for (; i + 24 < parts; i += 32) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) a[k] += __ldcs(s + (i + 8 * k) * cols + c);
-    }
-    for (int k = 0; i < parts; i += 8, ++k) a[k & 3] += __ldcs(s + i * cols + c);
-  }
-  sh[strip][lane] = (a[0] + a[1]) + (a[2] + a[3]);
-  __syncthreads();
-  if (strip == 0 && c < cols) {
-    float v = 0.f;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) v += sh[k][lane];
-    dst[(long long)blockIdx.y * cols + c] = v;
-  }
-}
-
 uly_status fold_columns_launch(const float *src, int rows, long long parts, int cols, float *dst,
                                cudaStream_t stream) {
-  prof::Scope scope(prof::K_FOLD_COLUMNS, stream);
-  for (int r0 = 0; r0 < rows; r0 += 65535) {
-    const int n = rows - r0 < 65535 ? rows - r0 : 65535;
-    fold_columns_kernel<<<dim3((cols + 31) / 32, n), 256, 0, stream>>>(src + (long long)r0 * parts * cols, parts,
-                                                                      cols, dst + (long long)r0 * cols);
-    note_launches(1);
-  }
-  return last_launch_status();
+  FoldJobs jobs = {};
+  jobs.job[0] = {src, dst, parts, rows};
+  jobs.n = 1;
+  jobs.cols = cols;
+  return fold_launch(jobs, stream);
 }
 
-bool residual_norm_supported(int vecs) { return vecs <= kMaxGroup * kMaxVecs; }
+bool residual_norm_supported(int vecs) { return vecs <= kMaxVecs; }
 
 uly_status residual_norm_launch(int32_t B, int32_t n, int32_t P, int32_t hidden, int32_t dtype, const void *x,
                                 const void *h, const void *gate, int32_t gate_mode, const void *w_post,
                                 const void *w_pre, float res_scale, float eps, void *r, void *u,
                                 cudaStream_t stream) {
+  const bool bf = dtype == ULY_BF16;
   NormParams p = {};
-  p.x = x; p.h = h; p.gate = gate; p.w_post = w_post; p.w_pre = w_pre; p.r = r; p.u = u;
+  p.src.add(x, p.sx);
+  p.src.add(h, p.sh);
+  p.src.add(gate_mode == ULY_GATE_TOKEN ? gate : nullptr, p.sg);
+  p.gate = static_cast<const uint4 *>(gate);
+  p.w_post = static_cast<const uint4 *>(w_post);
+  p.w_pre = static_cast<const uint4 *>(w_pre);
+  p.r = static_cast<uint4 *>(r);
+  p.u = static_cast<uint4 *>(u);
   p.rows = (long long)B * n;
-  p.vecs = hidden * (dtype == ULY_BF16 ? 2 : 4) / 16;
+  p.vecs = hidden / (bf ? 8 : 4);
   p.gate_mode = gate_mode; p.B = B; p.s = n / P;
   p.res_scale = res_scale; p.eps = eps; p.inv_d = 1.0f / hidden;
-  const RowShape rs = row_shape(p.vecs);
-  p.tpr = rs.tpr;
-  long long blocks = (p.rows + rs.rpb - 1) / rs.rpb;
-  if (blocks > (1LL << 30)) blocks = 1LL << 30;
+  const RowShape rs = row_shape(p.vecs, p.src.n, kFwdVecs, kFwdThreads);
+  p.ring = {p.src.n, rs.stages, error_word()};
+  const long long want = (long long)device_sm_count() * rs.per_sm, ctas = (p.rows + rs.rpb - 1) / rs.rpb;
+  const int grid = (int)(ctas < want ? ctas : want);
   prof::Scope scope(prof::K_RESIDUAL_NORM, stream);
-  if (dtype == ULY_BF16)
-    fwd_kernel<__nv_bfloat16>(rs.nv)<<<(unsigned)blocks, rs.tpr * rs.rpb, 0, stream>>>(p);
-  else
-    fwd_kernel<float>(rs.nv)<<<(unsigned)blocks, rs.tpr * rs.rpb, 0, stream>>>(p);
-  note_launches(1);
-  return last_launch_status();
+  return run(bf ? fwd_entry<__nv_bfloat16>(rs) : fwd_entry<float>(rs), grid, rs.tpr * rs.rpb, rs.smem, p, stream);
 }
 
 size_t residual_norm_bwd_workspace_bytes(int32_t B, int32_t n, int32_t hidden, int32_t dtype, int32_t gate_mode) {
-  const int e = dtype == ULY_BF16 ? 8 : 4;
-  return bwd_plan(B, n, hidden / e, e, gate_mode, true, true, true).bytes;
+  return bwd_plan(B, n, hidden, dtype == ULY_BF16 ? 8 : 4, gate_mode).bytes;
 }
 
 uly_status residual_norm_bwd_launch(int32_t B, int32_t n, int32_t P, int32_t hidden, int32_t dtype, const void *r,
@@ -490,37 +711,45 @@ uly_status residual_norm_bwd_launch(int32_t B, int32_t n, int32_t P, int32_t hid
                                     int32_t gate_mode, const void *w_post, const void *w_pre, float res_scale,
                                     float eps, void *dx, void *dh, float *dw_post, float *dw_pre, void *dgate,
                                     void *workspace, cudaStream_t stream) {
-  const int E = dtype == ULY_BF16 ? 8 : 4, vecs = hidden / E;
+  const bool bf = dtype == ULY_BF16;
   const bool shared_gate = gate_mode == ULY_GATE_CHANNEL || gate_mode == ULY_GATE_SEQUENCE;
-  const BwdPlan q = bwd_plan(B, n, vecs, E, gate_mode, dw_pre != nullptr, dw_post != nullptr, dgate != nullptr);
+  const BwdPlan q = bwd_plan(B, n, hidden, bf ? 8 : 4, gate_mode);
   char *ws = static_cast<char *>(workspace);
   NormBwdParams p = {};
-  p.r = r; p.h = h; p.dr = dr; p.du = du; p.gate = gate; p.w_post = w_post; p.w_pre = w_pre;
-  p.dx = dx; p.dh = dh;
-  p.dgate_tok = gate_mode == ULY_GATE_TOKEN ? dgate : nullptr;
+  p.src.add(r, p.sr);
+  p.src.add(du, p.su);
+  p.src.add(h, p.sh);
+  p.src.add(dr, p.sd);
+  p.src.add(gate_mode == ULY_GATE_TOKEN ? gate : nullptr, p.sg);
+  p.ring = {q.slots, q.rs.stages, error_word()};
+  p.gate = static_cast<const uint4 *>(gate);
+  p.w_post = static_cast<const uint4 *>(w_post);
+  p.w_pre = static_cast<const uint4 *>(w_pre);
+  p.dx = static_cast<uint4 *>(dx);
+  p.dh = static_cast<uint4 *>(dh);
+  p.dgate_tok = gate_mode == ULY_GATE_TOKEN ? static_cast<uint4 *>(dgate) : nullptr;
   p.part_pre = dw_pre ? reinterpret_cast<float *>(ws + q.off_pre) : nullptr;
   p.part_post = dw_post ? reinterpret_cast<float *>(ws + q.off_post) : nullptr;
   p.part_gate = shared_gate && dgate ? reinterpret_cast<float *>(ws + q.off_gate) : nullptr;
-  p.rows_per_b = q.bs > 1 ? n : (long long)B * n;
-  p.vecs = vecs; p.tpr = q.rs.tpr; p.gate_mode = gate_mode; p.B = B; p.s = n / P;
+  p.rows_per_b = gate_mode == ULY_GATE_SEQUENCE ? n : (long long)B * n;
+  p.vecs = hidden / (bf ? 8 : 4);
+  p.gate_mode = gate_mode; p.B = B; p.s = n / P;
   p.bs = q.bs; p.upb = q.upb;
   p.res_scale = res_scale; p.eps = eps; p.inv_d = 1.0f / hidden;
   {
     prof::Scope scope(prof::K_RESIDUAL_NORM_BWD, stream);
-    const int threads = q.rs.tpr * q.rs.rpb;
-    if (dtype == ULY_BF16) bwd_kernel<__nv_bfloat16>(q.rs.nv)<<<q.grid, threads, 0, stream>>>(p);
-    else bwd_kernel<float>(q.rs.nv)<<<q.grid, threads, 0, stream>>>(p);
-    note_launches(1);
-    if (last_launch_status() != ULY_OK) return ULY_ERR_CUDA;
+    const uly_status st = run(bf ? bwd_entry<__nv_bfloat16>(q.rs) : bwd_entry<float>(q.rs), q.grid,
+                              q.rs.tpr * q.rs.rpb, q.rs.smem, p, stream);
+    if (st != ULY_OK) return st;
   }
-  uly_status st = ULY_OK;
   const long long parts = (long long)q.grid * q.rs.rpb;
-  if (dw_pre) st = fold_columns_launch(p.part_pre, 1, parts, hidden, dw_pre, stream);
-  if (st == ULY_OK && dw_post) st = fold_columns_launch(p.part_post, 1, parts, hidden, dw_post, stream);
-  if (st == ULY_OK && p.part_gate)
-    st = fold_columns_launch(p.part_gate, q.bs, (long long)q.upb * q.rs.rpb, hidden, static_cast<float *>(dgate),
-                             stream);
-  return st;
+  FoldJobs jobs = {};
+  jobs.cols = hidden;
+  if (dw_pre) jobs.job[jobs.n++] = {p.part_pre, dw_pre, parts, 1};
+  if (dw_post) jobs.job[jobs.n++] = {p.part_post, dw_post, parts, 1};
+  if (p.part_gate)
+    jobs.job[jobs.n++] = {p.part_gate, static_cast<float *>(dgate), (long long)q.upb * q.rs.rpb, q.bs};
+  return fold_launch(jobs, stream);
 }
 
 }  // namespace uly

@@ -10,6 +10,7 @@ library is missing or cannot be loaded, every call fails loudly.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -69,6 +70,8 @@ _lock = threading.Lock()
 def lib() -> ctypes.CDLL:
     """Load the library (once).  Raises if it is missing: there is no fallback."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -521,33 +524,50 @@ def ulysses_loss_aggregate_noalloc(logits, labels, P, ignore_index=-100, shard_s
 
 # ------------------------------------------------------ token-wise operators
 
-def _want(where, t, shape, dtype, optional=False):
+# The smallest calls (one decoded token) take the GPU a few microseconds, so
+# these bindings keep their own work short: plain integers for pointers and
+# the stream, sizes of workspaces remembered per shape.
+
+_BF16, _F32 = torch.bfloat16, torch.float32
+
+
+def _want(where, name, t, shape, dtype):
     """Check one tensor of a call: dtype, shape, contiguous."""
     if t is None:
-        if optional:
-            return
-        raise UlyssesError(1, f"{where}: missing tensor")
-    if t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
-        raise UlyssesError(3, f"{where}: dtype {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
-        raise UlyssesError(2, f"{where}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+        raise UlyssesError(1, f"{where}: {name} is missing")
+    if t.dtype is not dtype:
+        raise UlyssesError(3, f"{where}: {name} has dtype {t.dtype}, expected {dtype}")
+    if t.shape != shape:
+        raise UlyssesError(2, f"{where}: {name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if not t.is_contiguous():
-        raise UlyssesError(6, f"{where}: not contiguous (strides {tuple(t.stride())})")
+        raise UlyssesError(6, f"{where}: {name} is not contiguous (strides {tuple(t.stride())})")
 
 
-def _here(where, *tensors):
-    """Every tensor of a call is on the current CUDA device, where it launches."""
+def _here(where, tensors):
+    """Every tensor of a call is on the current CUDA device, where it launches; its index."""
+    dev = tensors[0].get_device()
     for t in tensors:
-        if t is not None and (not t.is_cuda or t.device.index != torch.cuda.current_device()):
-            raise UlyssesError(7, f"{where}: a tensor on {t.device}, not on the current CUDA device")
+        if t is not None and (not t.is_cuda or t.get_device() != dev):
+            raise UlyssesError(7, f"{where}: tensors on {tensors[0].device} and {t.device}")
+    if dev != torch.cuda.current_device():
+        raise UlyssesError(7, f"{where}: tensors on cuda:{dev}, not on the current CUDA device")
+    return dev
 
 
-def _alloc(shape, dtype, device, stream):
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _raw_stream(stream, dev):
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _empty(shape, dtype, like, stream):
     """An output or workspace whose memory belongs to the stream the call runs on."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=dtype, device=like.device)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=dtype, device=like.device)
 
 
 def _size(fn, *args) -> int:
@@ -556,23 +576,25 @@ def _size(fn, *args) -> int:
     return n.value
 
 
-def _workspace(where, ws, need, device, stream):
+@functools.lru_cache(maxsize=4096)
+def _size_on(dev, fn, *args) -> int:
+    return _size(fn, *args)   # of the current device `dev`
+
+
+def _workspace(where, ws, need, like, stream):
+    """(tensor or None, its bytes) of a call that needs `need` bytes."""
     if ws is None:
-        return _alloc((max(need, 256),), torch.uint8, device, stream) if need else None
-    if ws.dtype != torch.uint8:
-        raise UlyssesError(3, f"{where}: workspace dtype {ws.dtype}")
-    _want(f"{where} workspace", ws, (ws.numel(),), torch.uint8)
-    return ws
-
-
-def _rows(x) -> int:
-    return x.numel() // x.shape[-1] if x.shape[-1] else 0
+        ws = _empty((need,), torch.uint8, like, stream) if need else None
+    elif ws.dtype is not torch.uint8 or not ws.is_contiguous():
+        raise UlyssesError(3, f"{where}: the workspace is not contiguous bytes")
+    return ws, 0 if ws is None else ws.numel()
 
 
 def _features(where, x, w, activation):
     if x.dim() < 1 or w.dim() != 2 or (activation == ACT_SWIGLU and w.shape[0] % 2):
         raise UlyssesError(2, f"{where}: x {tuple(x.shape)}, w {tuple(w.shape)}")
-    return x.shape[-1], w.shape[0], w.shape[0] // 2 if activation == ACT_SWIGLU else w.shape[0]
+    nz, k = w.shape
+    return x.shape[:-1], k, nz, nz // 2 if activation == ACT_SWIGLU else nz
 
 
 def ulysses_linear_workspace_size(tokens: int, in_features: int, out_features: int, activation=ACT_NONE) -> int:
@@ -585,23 +607,29 @@ def ulysses_linear(x, w, bias=None, residual=None, activation=ACT_NONE, save_pre
     [N][K] (nn.Linear weight; ACT_SWIGLU: [2N][K], gate rows then up rows), bias
     like w's rows, residual like y -> y [..., N]; with save_pre (or a given pre)
     (y, pre), pre [..., rows of w] the product and bias before the activation."""
-    k, nz, n = _features("ulysses_linear", x, w, activation)
-    lead, bf = tuple(x.shape[:-1]), torch.bfloat16
-    _want("ulysses_linear x", x, (*lead, k), bf)
-    _want("ulysses_linear w", w, (nz, k), bf)
-    _want("ulysses_linear bias", bias, (nz,), bf, optional=True)
-    _want("ulysses_linear residual", residual, (*lead, n), bf, optional=True)
-    y = _alloc((*lead, n), bf, x.device, stream) if y is None else y
-    if save_pre and pre is None:
-        pre = _alloc((*lead, nz), bf, x.device, stream)
-    _want("ulysses_linear y", y, (*lead, n), bf)
-    _want("ulysses_linear pre", pre, (*lead, nz), bf, optional=True)
-    _here("ulysses_linear", x, w, bias, residual, y, pre, workspace)
-    tokens = _rows(x)
-    need = ulysses_linear_workspace_size(tokens, k, n, activation)
-    ws = _workspace("ulysses_linear", workspace, need, x.device, stream)
-    _check(lib().ulysses_linear(tokens, k, n, activation, _p(x), _p(w), _p(bias), _p(residual), _p(y), _p(pre),
-                                _p(ws), 0 if ws is None else ws.numel(), _stream(stream)), "ulysses_linear")
+    where = "ulysses_linear"
+    lead, k, nz, n = _features(where, x, w, activation)
+    y_shape = (*lead, n)
+    _want(where, "x", x, (*lead, k), _BF16)
+    _want(where, "w", w, (nz, k), _BF16)
+    if bias is not None:
+        _want(where, "bias", bias, (nz,), _BF16)
+    if residual is not None:
+        _want(where, "residual", residual, y_shape, _BF16)
+    if y is None:
+        y = _empty(y_shape, _BF16, x, stream)
+    else:
+        _want(where, "y", y, y_shape, _BF16)
+    if pre is not None:
+        _want(where, "pre", pre, (*lead, nz), _BF16)
+    elif save_pre:
+        pre = _empty((*lead, nz), _BF16, x, stream)
+    dev = _here(where, (x, w, bias, residual, y, pre, workspace))
+    tokens = x.numel() // k if k else 0
+    need = _size_on(dev, "ulysses_linear_workspace_size", tokens, k, n, activation)
+    ws, ws_bytes = _workspace(where, workspace, need, x, stream)
+    _check(lib().ulysses_linear(tokens, k, n, activation, x.data_ptr(), w.data_ptr(), _ptr(bias), _ptr(residual),
+                                y.data_ptr(), _ptr(pre), _ptr(ws), ws_bytes, _raw_stream(stream, dev)), where)
     return y if pre is None else (y, pre)
 
 
@@ -614,48 +642,56 @@ def ulysses_linear_bwd(x, w, dy, pre=None, activation=ACT_NONE, bias_grad=False,
     """Backward of ulysses_linear: dy [..., N] and the forward's pre (not for
     ACT_NONE) -> (dx like x, dw like w in grad_dtype (float32 or bfloat16), dbias
     float32 [rows of w], or None without bias_grad).  The residual's gradient is dy."""
-    k, nz, n = _features("ulysses_linear_bwd", x, w, activation)
-    lead, bf = tuple(x.shape[:-1]), torch.bfloat16
-    _want("ulysses_linear_bwd x", x, (*lead, k), bf)
-    _want("ulysses_linear_bwd w", w, (nz, k), bf)
-    _want("ulysses_linear_bwd dy", dy, (*lead, n), bf)
+    where = "ulysses_linear_bwd"
+    lead, k, nz, n = _features(where, x, w, activation)
+    _want(where, "x", x, (*lead, k), _BF16)
+    _want(where, "w", w, (nz, k), _BF16)
+    _want(where, "dy", dy, (*lead, n), _BF16)
     if activation == ACT_NONE:
         pre = None
     else:
-        _want("ulysses_linear_bwd pre", pre, (*lead, nz), bf)
-    dx = _alloc(x.shape, bf, x.device, stream) if dx is None else dx
-    dw = _alloc(w.shape, grad_dtype, x.device, stream) if dw is None else dw
-    if bias_grad and dbias is None:
-        dbias = _alloc((nz,), torch.float32, x.device, stream)
-    _want("ulysses_linear_bwd dx", dx, x.shape, bf)
-    _want("ulysses_linear_bwd dw", dw, w.shape, (torch.float32, bf))
-    _want("ulysses_linear_bwd dbias", dbias, (nz,), torch.float32, optional=True)
-    _here("ulysses_linear_bwd", x, w, dy, pre, dx, dw, dbias, workspace)
-    tokens = _rows(x)
-    need = ulysses_linear_bwd_workspace_size(tokens, k, n, activation)
-    ws = _workspace("ulysses_linear_bwd", workspace, need, x.device, stream)
-    _check(lib().ulysses_linear_bwd(tokens, k, n, activation, _p(x), _p(w), _p(pre), _p(dy), _p(dx), _p(dw),
-                                    _dtype_code(dw), _p(dbias), _p(ws), 0 if ws is None else ws.numel(),
-                                    _stream(stream)), "ulysses_linear_bwd")
+        _want(where, "pre", pre, (*lead, nz), _BF16)
+    if dx is None:
+        dx = _empty(x.shape, _BF16, x, stream)
+    else:
+        _want(where, "dx", dx, x.shape, _BF16)
+    if dw is None:
+        dw = _empty(w.shape, grad_dtype, x, stream)
+    code = _dtype_code(dw)
+    _want(where, "dw", dw, w.shape, dw.dtype)
+    if dbias is not None:
+        _want(where, "dbias", dbias, (nz,), _F32)
+    elif bias_grad:
+        dbias = _empty((nz,), _F32, x, stream)
+    dev = _here(where, (x, w, dy, pre, dx, dw, dbias, workspace))
+    tokens = x.numel() // k if k else 0
+    need = _size_on(dev, "ulysses_linear_bwd_workspace_size", tokens, k, n, activation)
+    ws, ws_bytes = _workspace(where, workspace, need, x, stream)
+    _check(lib().ulysses_linear_bwd(tokens, k, n, activation, x.data_ptr(), w.data_ptr(), _ptr(pre), dy.data_ptr(),
+                                    dx.data_ptr(), dw.data_ptr(), code, _ptr(dbias), _ptr(ws), ws_bytes,
+                                    _raw_stream(stream, dev)), where)
     return dx, dw, dbias
-
-
-def _gate_shape(mode, shape):
-    return {GATE_CHANNEL: (shape[3],), GATE_SEQUENCE: (shape[1], shape[3]), GATE_TOKEN: tuple(shape)}.get(mode)
 
 
 def _want_norm(where, shape, dtype, w_pre, w_post, gate, gate_mode):
     if len(shape) != 4:
         raise UlyssesError(2, f"{where}: shape {tuple(shape)}, expected [P][B][n/P][hidden]")
-    if dtype not in (torch.bfloat16, torch.float32):
+    if dtype is not _BF16 and dtype is not _F32:
         raise UlyssesError(3, f"{where}: dtype {dtype}")
-    _want(f"{where} w_pre", w_pre, (shape[3],), dtype, optional=True)
-    _want(f"{where} w_post", w_post, (shape[3],), dtype, optional=True)
+    d = shape[3]
+    if w_pre is not None:
+        _want(where, "w_pre", w_pre, (d,), dtype)
+    if w_post is not None:
+        _want(where, "w_post", w_post, (d,), dtype)
     if gate_mode == GATE_NONE:
         if gate is not None:
             raise UlyssesError(2, f"{where}: a gate with GATE_NONE")
-    elif gate_mode in (GATE_CHANNEL, GATE_SEQUENCE, GATE_TOKEN):
-        _want(f"{where} gate", gate, _gate_shape(gate_mode, shape), dtype)
+    elif gate_mode == GATE_CHANNEL:
+        _want(where, "gate", gate, (d,), dtype)
+    elif gate_mode == GATE_SEQUENCE:
+        _want(where, "gate", gate, (shape[1], d), dtype)
+    elif gate_mode == GATE_TOKEN:
+        _want(where, "gate", gate, shape, dtype)
     else:
         raise UlyssesError(6, f"{where}: gate mode {gate_mode}")
 
@@ -667,19 +703,24 @@ def ulysses_residual_norm(x, h=None, w_pre=None, w_post=None, gate=None, gate_mo
     [hidden], gate as its mode says -> (r, u).  Without w_pre u is None; without
     h (the first block) r is None unless a tensor for it is given."""
     where = "ulysses_residual_norm"
-    _want_norm(where, x.shape, x.dtype, w_pre, w_post, gate, gate_mode)
-    _want(f"{where} x", x, x.shape, x.dtype)
-    _want(f"{where} h", h, x.shape, x.dtype, optional=True)
-    if r is None and (h is not None or w_pre is None):
-        r = _alloc(x.shape, x.dtype, x.device, stream)
-    if u is None and w_pre is not None:
-        u = _alloc(x.shape, x.dtype, x.device, stream)
-    _want(f"{where} r", r, x.shape, x.dtype, optional=True)
-    _want(f"{where} u", u, x.shape, x.dtype, optional=True)
-    _here(where, x, h, w_pre, w_post, gate, r, u)
-    P, B, s, d = x.shape
-    _check(lib().ulysses_residual_norm(B, P * s, P, d, _dtype_code(x), _p(x), _p(h), _p(gate), gate_mode, _p(w_post),
-                                       _p(w_pre), float(res_scale), float(eps), _p(r), _p(u), _stream(stream)), where)
+    shape, dtype = x.shape, x.dtype
+    _want_norm(where, shape, dtype, w_pre, w_post, gate, gate_mode)
+    _want(where, "x", x, shape, dtype)
+    if h is not None:
+        _want(where, "h", h, shape, dtype)
+    if r is not None:
+        _want(where, "r", r, shape, dtype)
+    elif h is not None or w_pre is None:
+        r = _empty(shape, dtype, x, stream)
+    if u is not None:
+        _want(where, "u", u, shape, dtype)
+    elif w_pre is not None:
+        u = _empty(shape, dtype, x, stream)
+    dev = _here(where, (x, h, w_pre, w_post, gate, r, u))
+    P, B, s, d = shape
+    _check(lib().ulysses_residual_norm(B, P * s, P, d, ULY_BF16 if dtype is _BF16 else ULY_F32, x.data_ptr(), _ptr(h),
+                                       _ptr(gate), gate_mode, _ptr(w_post), _ptr(w_pre), res_scale, eps, _ptr(r),
+                                       _ptr(u), _raw_stream(stream, dev)), where)
     return r, u
 
 
@@ -697,53 +738,59 @@ def ulysses_residual_norm_bwd(r, h=None, dr=None, du=None, w_pre=None, w_post=No
     and a shared gate's gradient are float32, a token gate's is like the gate;
     None for what the forward did not have."""
     where = "ulysses_residual_norm_bwd"
-    _want_norm(where, r.shape, r.dtype, w_pre, w_post, gate, gate_mode)
+    shape, dtype = r.shape, r.dtype
+    _want_norm(where, shape, dtype, w_pre, w_post, gate, gate_mode)
+    _want(where, "r", r, shape, dtype)
+    P, B, s, d = shape
     for name, t in (("h", h), ("dr", dr), ("du", du)):
-        _want(f"{where} {name}", t, r.shape, r.dtype, optional=True)
-    _want(f"{where} r", r, r.shape, r.dtype)
-    P, B, s, d = r.shape
-    f32, dev = torch.float32, r.device
-    dx = _alloc(r.shape, r.dtype, dev, stream) if dx is None else dx
-    if dh is None and h is not None:
-        dh = _alloc(r.shape, r.dtype, dev, stream)
-    if dw_pre is None and du is not None:
-        dw_pre = _alloc((d,), f32, dev, stream)
-    if dw_post is None and w_post is not None:
-        dw_post = _alloc((d,), f32, dev, stream)
-    gdt = r.dtype if gate_mode == GATE_TOKEN else f32
-    if dgate is None and gate is not None:
-        dgate = _alloc(gate.shape, gdt, dev, stream)
-    _want(f"{where} dx", dx, r.shape, r.dtype)
-    _want(f"{where} dh", dh, r.shape, r.dtype, optional=True)
-    _want(f"{where} dw_pre", dw_pre, (d,), f32, optional=True)
-    _want(f"{where} dw_post", dw_post, (d,), f32, optional=True)
-    if dgate is not None:
-        _want(f"{where} dgate", dgate, _gate_shape(gate_mode, r.shape) or (0,), gdt)
-    _here(where, r, h, dr, du, w_pre, w_post, gate, dx, dh, dw_pre, dw_post, dgate, workspace)
-    need = ulysses_residual_norm_bwd_workspace_size(B, P * s, d, r.dtype, gate_mode)
-    ws = _workspace(where, workspace, need, dev, stream)
-    _check(lib().ulysses_residual_norm_bwd(B, P * s, P, d, _dtype_code(r), _p(r), _p(h), _p(dr), _p(du), _p(gate),
-                                           gate_mode, _p(w_post), _p(w_pre), float(res_scale), float(eps), _p(dx),
-                                           _p(dh), _p(dw_post), _p(dw_pre), _p(dgate), _p(ws), ws.numel(),
-                                           _stream(stream)), where)
+        if t is not None:
+            _want(where, name, t, shape, dtype)
+
+    def out(name, t, wanted, like, dt):
+        if t is not None:
+            _want(where, name, t, like, dt)
+            return t
+        return _empty(like, dt, r, stream) if wanted else None
+
+    dx = out("dx", dx, True, shape, dtype)
+    dh = out("dh", dh, h is not None, shape, dtype)
+    dw_pre = out("dw_pre", dw_pre, du is not None, (d,), _F32)
+    dw_post = out("dw_post", dw_post, w_post is not None, (d,), _F32)
+    if gate is not None:
+        dgate = out("dgate", dgate, True, gate.shape, dtype if gate_mode == GATE_TOKEN else _F32)
+    elif dgate is not None:
+        raise UlyssesError(2, f"{where}: dgate without a gate")
+    dev = _here(where, (r, h, dr, du, w_pre, w_post, gate, dx, dh, dw_pre, dw_post, dgate, workspace))
+    code = ULY_BF16 if dtype is _BF16 else ULY_F32
+    need = _size_on(dev, "ulysses_residual_norm_bwd_workspace_size", B, P * s, d, code, gate_mode)
+    ws, ws_bytes = _workspace(where, workspace, need, r, stream)
+    _check(lib().ulysses_residual_norm_bwd(B, P * s, P, d, code, r.data_ptr(), _ptr(h), _ptr(dr), _ptr(du), _ptr(gate),
+                                           gate_mode, _ptr(w_post), _ptr(w_pre), res_scale, eps, _ptr(dx), _ptr(dh),
+                                           _ptr(dw_post), _ptr(dw_pre), _ptr(dgate), _ptr(ws), ws_bytes,
+                                           _raw_stream(stream, dev)), where)
     return dx, dh, dw_pre, dw_post, dgate
 
 
 def _want_loss(where, x, w, labels):
     if x.dim() != 2 or w.dim() != 2:
         raise UlyssesError(2, f"{where}: x {tuple(x.shape)}, w {tuple(w.shape)}")
-    _want(f"{where} x", x, x.shape, torch.bfloat16)
-    _want(f"{where} w", w, (w.shape[0], x.shape[1]), torch.bfloat16)
-    _want(f"{where} labels", labels.reshape(-1) if labels.is_contiguous() else labels, (x.shape[0],), torch.int32)
+    _want(where, "x", x, x.shape, _BF16)
+    _want(where, "w", w, (w.shape[0], x.shape[1]), _BF16)
+    if labels is not None and labels.dim() != 1 and labels.is_contiguous():
+        labels = labels.view(-1)
+    _want(where, "labels", labels, x.shape[:1], torch.int32)
 
 
-def _loss_outputs(where, P, dev, shard_sum, shard_count, loss, stream):
-    shard_sum = _alloc((P,), torch.float32, dev, stream) if shard_sum is None else shard_sum
-    shard_count = _alloc((P,), torch.int64, dev, stream) if shard_count is None else shard_count
-    loss = _alloc((1,), torch.float32, dev, stream) if loss is None else loss
-    _want(f"{where} shard_sum", shard_sum, (P,), torch.float32)
-    _want(f"{where} shard_count", shard_count, (P,), torch.int64)
-    _want(f"{where} loss", loss, (1,), torch.float32)
+def _loss_outputs(where, P, x, shard_sum, shard_count, loss, stream):
+    if shard_sum is None:
+        shard_sum = _empty((P,), _F32, x, stream)
+    if shard_count is None:
+        shard_count = _empty((P,), torch.int64, x, stream)
+    if loss is None:
+        loss = _empty((1,), _F32, x, stream)
+    _want(where, "shard_sum", shard_sum, (P,), _F32)
+    _want(where, "shard_count", shard_count, (P,), torch.int64)
+    _want(where, "loss", loss, (1,), _F32)
     return shard_sum, shard_count, loss
 
 
@@ -759,12 +806,13 @@ def ulysses_linear_loss(x, w, labels, P, ignore_index=-100, shard_sum=None, shar
     where = "ulysses_linear_loss"
     _want_loss(where, x, w, labels)
     (T, d), V = x.shape, w.shape[0]
-    shard_sum, shard_count, loss = _loss_outputs(where, P, x.device, shard_sum, shard_count, loss, stream)
-    _here(where, x, w, labels, shard_sum, shard_count, loss, workspace)
-    need = ulysses_linear_loss_workspace_size(P, T, d, V)
-    ws = _workspace(where, workspace, need, x.device, stream)
-    _check(lib().ulysses_linear_loss(P, T, d, V, _p(x), _p(w), _p(labels), ignore_index, _p(shard_sum),
-                                     _p(shard_count), _p(loss), _p(ws), ws.numel(), _stream(stream)), where)
+    shard_sum, shard_count, loss = _loss_outputs(where, P, x, shard_sum, shard_count, loss, stream)
+    dev = _here(where, (x, w, labels, shard_sum, shard_count, loss, workspace))
+    need = _size_on(dev, "ulysses_linear_loss_workspace_size", P, T, d, V)
+    ws, ws_bytes = _workspace(where, workspace, need, x, stream)
+    _check(lib().ulysses_linear_loss(P, T, d, V, x.data_ptr(), w.data_ptr(), labels.data_ptr(), ignore_index,
+                                     shard_sum.data_ptr(), shard_count.data_ptr(), loss.data_ptr(), _ptr(ws), ws_bytes,
+                                     _raw_stream(stream, dev)), where)
     return shard_sum, shard_count, loss
 
 
@@ -783,17 +831,22 @@ def ulysses_linear_loss_bwd(x, w, labels, P, ignore_index=-100, grad_dtype=torch
     where = "ulysses_linear_loss_bwd"
     _want_loss(where, x, w, labels)
     (T, d), V = x.shape, w.shape[0]
-    dx = _alloc(x.shape, x.dtype, x.device, stream) if dx is None else dx
-    dw = _alloc(w.shape, grad_dtype, x.device, stream) if dw is None else dw
-    _want(f"{where} dx", dx, x.shape, torch.bfloat16)
-    _want(f"{where} dw", dw, w.shape, (torch.float32, torch.bfloat16))
-    shard_sum, shard_count, loss = _loss_outputs(where, P, x.device, shard_sum, shard_count, loss, stream)
-    _here(where, x, w, labels, dx, dw, shard_sum, shard_count, loss, workspace)
-    need = ulysses_linear_loss_bwd_workspace_size(P, T, d, V, dw.dtype, piece_tokens)
-    ws = _workspace(where, workspace, need, x.device, stream)
-    _check(lib().ulysses_linear_loss_bwd(P, T, d, V, _p(x), _p(w), _p(labels), ignore_index, _p(dx), _p(dw),
-                                         _dtype_code(dw), piece_tokens, _p(shard_sum), _p(shard_count), _p(loss),
-                                         _p(ws), ws.numel(), _stream(stream)), where)
+    if dx is None:
+        dx = _empty(x.shape, _BF16, x, stream)
+    else:
+        _want(where, "dx", dx, x.shape, _BF16)
+    if dw is None:
+        dw = _empty(w.shape, grad_dtype, x, stream)
+    code = _dtype_code(dw)
+    _want(where, "dw", dw, w.shape, dw.dtype)
+    shard_sum, shard_count, loss = _loss_outputs(where, P, x, shard_sum, shard_count, loss, stream)
+    dev = _here(where, (x, w, labels, dx, dw, shard_sum, shard_count, loss, workspace))
+    need = _size_on(dev, "ulysses_linear_loss_bwd_workspace_size", P, T, d, V, code, piece_tokens)
+    ws, ws_bytes = _workspace(where, workspace, need, x, stream)
+    _check(lib().ulysses_linear_loss_bwd(P, T, d, V, x.data_ptr(), w.data_ptr(), labels.data_ptr(), ignore_index,
+                                         dx.data_ptr(), dw.data_ptr(), code, piece_tokens, shard_sum.data_ptr(),
+                                         shard_count.data_ptr(), loss.data_ptr(), _ptr(ws), ws_bytes,
+                                         _raw_stream(stream, dev)), where)
     return shard_sum, shard_count, loss, dx, dw
 
 

@@ -296,7 +296,7 @@ def test_residual_norm_validation(L):
                         k.get("x", x), k.get("h", h), k.get("g", gt), k.get("mode", 1), k.get("wp", wp),
                         k.get("wq", wq), k.get("a", 1.0), k.get("eps", 1e-6), k.get("r", r), k.get("u", u), None]
     for want, kw in ((2, dict(B=0)), (2, dict(n=510)), (2, dict(P=0)), (2, dict(D=0)), (3, dict(dt=5)),
-                     (4, dict(D=260)), (4, dict(D=258, dt=0)), (6, dict(D=32776)), (6, dict(D=16388, dt=0)),
+                     (4, dict(D=260)), (4, dict(D=258, dt=0)), (6, dict(D=16392)), (6, dict(D=8196, dt=0)),
                      (6, dict(mode=4)), (2, dict(eps=-1e-6)), (2, dict(eps=nan)), (2, dict(eps=inf)),
                      (2, dict(a=nan)), (1, dict(x=None)), (1, dict(r=None, u=None)), (1, dict(wq=None)),
                      (1, dict(g=None)), (1, dict(h=None)), (1, dict(h=None, mode=0)),

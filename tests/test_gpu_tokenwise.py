@@ -232,11 +232,17 @@ NORMS = [  # P, B, s, D, dtype, gate, post
     (3, 2, 7, 1028, torch.float32, "token", True),
     (2, 2, 33, 520, torch.float32, "sequence", False),
     (4, 1, 150, 2560, torch.bfloat16, "token", True),
-    (1, 2, 40, 4104, torch.bfloat16, "channel", True),     # two vectors a thread, the last ones absent
-    (1, 1, 9, 12288, torch.bfloat16, "sequence", True),    # more
-    (1, 2, 3, 16384, torch.float32, "channel", True),      # the widest row
-    (1, 1, 3, 32768, torch.bfloat16, "none", True),
+    (1, 2, 40, 4104, torch.bfloat16, "channel", True),     # the last threads' vectors absent
+    (1, 1, 9, 12288, torch.bfloat16, "sequence", True),
+    (1, 2, 3, 8192, torch.float32, "channel", True),       # the widest rows
+    (2, 1, 150, 16384, torch.bfloat16, "none", True),
+    (1, 1, 155, 16384, torch.bfloat16, "token", True),     # one stage only
     (1, 700, 2, 64, torch.bfloat16, "sequence", True),     # more sequences than CTAs in flight
+    (3, 2, 701, 256, torch.bfloat16, "channel", True),     # several rows a group, its ring refilled
+    (2, 3, 611, 2560, torch.bfloat16, "sequence", True),
+    (2, 2, 450, 1280, torch.bfloat16, "token", False),
+    (1, 1, 1801, 1028, torch.float32, "none", True),
+    (1, 2, 611, 640, torch.float32, "channel", True),
 ]
 
 
