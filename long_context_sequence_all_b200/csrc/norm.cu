@@ -15,9 +15,11 @@
 //   dw_pre = sum_t du rn                         dN = gate dR
 //   dgate = sum dR N(h)   (over what the gate is broadcast along)
 //   b = dN * w_post, dh = (b - hn mean(b hn)) / rms(h),  dw_post = sum_t dN hn
-// The column sums stay in fp32 registers over all rows of a group; each group
-// writes one partial per column and a second kernel folds the partials in a
-// fixed order, so every output is bitwise repeatable.
+// A gate shared by the tokens of a run is a factor of that run's sums, so with
+// A = sum_t dR hn over the run, dw_post = sum gate A and dgate = w_post A: two
+// column sums (A and dw_pre's) stay in fp32 registers over all rows of a group.
+// Each group writes one partial per column and run, and a second kernel folds
+// the partials in a fixed order, so every output is bitwise repeatable.
 //
 // How: persistent groups of threads, one row at a time.  A group's rows arrive
 // by bulk copies in a ring of shared-memory stages, so the loads run ahead of
@@ -26,6 +28,10 @@
 // so few warps share a row: at 2560 bf16 columns two warps (backward: five)
 // instead of ten, which had left both directions waiting for barriers and
 // shuffles at 3.2 and 2.6 TB/s.  Arithmetic runs on pairs of fp32 values.
+// 65536 x 2560 bf16 with a channel gate: forward 235 us (5.7 TB/s of its 1.34
+// GB), backward 402 us (5.0 TB/s of 2.01 GB) + 10.5 us of folding; the forward
+// is at the memory's rate but for the gaps between rows, the backward issues
+// about 3000 instructions a row and is bound by them as much.
 #include <atomic>
 
 #include "common.cuh"
@@ -213,12 +219,12 @@ struct NormParams {
   int sx, sh, sg;   // stage slots of x, h and a token's gate (-1: none)
   const uint4 *gate, *w_post, *w_pre;
   uint4 *r, *u;
-  long long rows;
-  int vecs, gate_mode, B, s;
+  int rows, vecs, gate_mode, B, s;
   float res_scale, eps, inv_d;
 };
 
-// One row a group; thread `l` of its `tpr` takes vectors l, l + tpr, ...
+// One row a group; thread `l` of its `tpr` takes vectors l, l + tpr, ...: NV of
+// them, of which only the last can lie behind the row's end.
 template <typename T, int NV, bool WARP>
 __global__ void __launch_bounds__(kMaxGroup) residual_norm_kernel(const __grid_constant__ NormParams p) {
   constexpr int E = Vec<T>::N;
@@ -229,69 +235,68 @@ __global__ void __launch_bounds__(kMaxGroup) residual_norm_kernel(const __grid_c
   int turn = 0;
   Ring ring = ring_setup<WARP>(stage_mem, bars, &abort_flag, p.vecs, p.ring);
   const int l = WARP ? threadIdx.x & 31 : threadIdx.x, tpr = WARP ? 32 : blockDim.x;
-  const long long first = WARP ? (long long)blockIdx.x * kWarpRows + (threadIdx.x >> 5) : blockIdx.x;
-  const long long step = WARP ? (long long)gridDim.x * kWarpRows : gridDim.x;
+  const int first = WARP ? blockIdx.x * kWarpRows + (threadIdx.x >> 5) : blockIdx.x;
+  const int step = WARP ? gridDim.x * kWarpRows : gridDim.x, rows = p.rows;
+  const bool tail = l + (NV - 1) * tpr < p.vecs;   // this thread's last vector exists
+  const bool branch = p.sh >= 0, post = p.w_post != nullptr, gated = p.gate_mode != ULY_GATE_NONE;
+  const uint4 zero = make_uint4(0, 0, 0, 0);
   if (l == 0)
     for (int k = 0; k < ring.stages; ++k)
-      if (first + k * step < p.rows) ring.issue(p.src, first + k * step, k);
+      if (first + (long long)k * step < rows) ring.issue(p.src, first + k * step, k);
   int done = -1;   // stage whose row every thread has finished with, after the group's next barrier
-  for (long long t = first; t < p.rows; t += step, ring.next()) {
+  for (long long t = first; t < rows; t += step, ring.next()) {
     if (ring.stages == 1 && done >= 0) {   // no stage to run ahead into
       group_barrier<WARP>();
       if (l == 0) ring.issue(p.src, t, 0);
     }
     ring.wait(&abort_flag, p.ring.err);
-    const uint4 *gv = nullptr;
+    const uint4 *gv = p.gate;
     if (p.gate_mode == ULY_GATE_TOKEN) gv = ring.row(p.sg);
-    else if (p.gate_mode == ULY_GATE_SEQUENCE) gv = p.gate + (t / p.s) % p.B * p.vecs;
-    else if (p.gate_mode == ULY_GATE_CHANNEL) gv = p.gate;
+    else if (p.gate_mode == ULY_GATE_SEQUENCE) gv += (long long)((int)t / p.s % p.B) * p.vecs;
     F2 r[NV][E], q = f2(0.f);
-    if (p.sh >= 0) {
+    if (branch) {
+      const uint4 *hv = ring.row(p.sh) + l;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int v = l + i * tpr;
-        if (v < p.vecs) {
-          Vec<T>::unpack(ring.row(p.sh)[v], r[i]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < E; ++e) r[i][e] = f2(0.f);
-        }
+        Vec<T>::unpack(i < NV - 1 || tail ? hv[i * tpr] : zero, r[i]);
 #pragma unroll
         for (int e = 0; e < E; ++e) q = fma(r[i][e], r[i][e], q);
       }
     }
     float ss[1] = {sum2(q)};
-    if (p.w_post || !WARP) group_sum<1, WARP>(ss, sh, turn);   // the barrier also frees the previous row's stage
+    if (post || !WARP) group_sum<1, WARP>(ss, sh, turn);   // the barrier also frees the previous row's stage
     if (WARP) __syncwarp();
-    if (l == 0 && done >= 0 && ring.stages > 1 && t + (ring.stages - 1) * step < p.rows)
-      ring.issue(p.src, t + (ring.stages - 1) * step, done);
-    const F2 hs = f2(p.w_post ? rsqrtf(ss[0] * p.inv_d + p.eps) : 1.f), a = f2(p.res_scale);
+    if (l == 0 && done >= 0 && ring.stages > 1 && t + (long long)(ring.stages - 1) * step < rows)
+      ring.issue(p.src, t + (long long)(ring.stages - 1) * step, done);
+    const F2 hs = f2(post ? rsqrtf(ss[0] * p.inv_d + p.eps) : 1.f), a = f2(p.res_scale);
+    const uint4 *xv = ring.row(p.sx) + l;
+    uint4 *rv = p.r + t * p.vecs + l;
     q = f2(0.f);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int v = l + i * tpr;
-      if (v < p.vecs) {
-        F2 x[E];
-        Vec<T>::unpack(ring.row(p.sx)[v], x);
-        if (p.w_post) {
+      const bool ok = i < NV - 1 || tail;
+      F2 x[E];
+      Vec<T>::unpack(ok ? xv[i * tpr] : zero, x);
+      if (branch) {
+        if (post) {
           F2 w[E];
-          Vec<T>::unpack(__ldg(p.w_post + v), w);
+          Vec<T>::unpack(ok ? __ldg(p.w_post + l + i * tpr) : zero, w);
 #pragma unroll
           for (int e = 0; e < E; ++e) r[i][e] = mul(r[i][e], mul(hs, w[e]));
         }
-        if (gv) {
+        if (gated) {
           F2 g[E];
-          Vec<T>::unpack(gv[v], g);
+          Vec<T>::unpack(ok ? gv[l + i * tpr] : zero, g);
 #pragma unroll
           for (int e = 0; e < E; ++e) r[i][e] = mul(r[i][e], g[e]);
         }
 #pragma unroll
-        for (int e = 0; e < E; ++e) r[i][e] = p.sh >= 0 ? fma(a, x[e], r[i][e]) : mul(a, x[e]);
-        if (p.r) p.r[t * p.vecs + v] = Vec<T>::pack(r[i]);
+        for (int e = 0; e < E; ++e) r[i][e] = fma(a, x[e], r[i][e]);
       } else {
 #pragma unroll
-        for (int e = 0; e < E; ++e) r[i][e] = f2(0.f);
+        for (int e = 0; e < E; ++e) r[i][e] = mul(a, x[e]);
       }
+      if (p.r && ok) rv[i * tpr] = Vec<T>::pack(r[i]);
 #pragma unroll
       for (int e = 0; e < E; ++e) q = fma(r[i][e], r[i][e], q);
     }
@@ -300,15 +305,16 @@ __global__ void __launch_bounds__(kMaxGroup) residual_norm_kernel(const __grid_c
     ss[0] = sum2(q);
     group_sum<1, WARP>(ss, sh, turn);
     const F2 rs = f2(rsqrtf(ss[0] * p.inv_d + p.eps));
+    uint4 *uv = p.u + t * p.vecs + l;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int v = l + i * tpr;
-      if (v >= p.vecs) continue;
-      F2 w[E];
-      Vec<T>::unpack(__ldg(p.w_pre + v), w);
+      if (i < NV - 1 || tail) {
+        F2 w[E];
+        Vec<T>::unpack(__ldg(p.w_pre + l + i * tpr), w);
 #pragma unroll
-      for (int e = 0; e < E; ++e) w[e] = mul(r[i][e], mul(rs, w[e]));
-      p.u[t * p.vecs + v] = Vec<T>::pack(w);
+        for (int e = 0; e < E; ++e) w[e] = mul(r[i][e], mul(rs, w[e]));
+        uv[i * tpr] = Vec<T>::pack(w);
+      }
     }
   }
   ring_end(&abort_flag);
@@ -320,9 +326,9 @@ struct NormBwdParams {
   int sr, su, sh, sd, sg;        // stage slots of r, du, h, dr and a token's gate
   const uint4 *gate, *w_post, *w_pre;
   uint4 *dx, *dh, *dgate_tok;
-  float *part_pre, *part_post;   // [groups][vecs * 2 E]; null where not asked for
-  float *part_gate;              // [units][groups of a CTA][vecs * 2 E]
-  long long rows_per_b;          // tokens of one gate row (P * s, or all of them)
+  float *part_pre;               // [groups][vecs * 2 E]: sums of du rn; null where not asked for
+  float *part_a;                 // [units][groups of a CTA][vecs * 2 E]: sums of dR hn (token gates: of dN hn)
+  int rows_per_b;                // tokens of one gate row (P * s, or all of them)
   int vecs, gate_mode, B, s;
   int bs, upb;                   // gate rows that units walk (B for sequence gates, else 1); units (runs of tokens) each
   float res_scale, eps, inv_d;
@@ -339,20 +345,20 @@ __global__ void __launch_bounds__(kMaxGroup, 1) residual_norm_bwd_kernel(const _
   Ring ring = ring_setup<WARP>(stage_mem, bars, &abort_flag, p.vecs, p.ring);
   const int l = WARP ? threadIdx.x & 31 : threadIdx.x, tpr = WARP ? 32 : blockDim.x;
   const int grp = WARP ? threadIdx.x >> 5 : 0;
-  F2 a_pre[NV][E], a_post[NV][E], a_gate[NV][E];
+  const bool tail = l + (NV - 1) * tpr < p.vecs;   // this thread's last vector exists
+  const bool post = p.w_post != nullptr, gated = p.gate_mode != ULY_GATE_NONE;
+  F2 a_pre[NV][E], a_a[NV][E];
 #pragma unroll
   for (int i = 0; i < NV; ++i)
 #pragma unroll
-    for (int e = 0; e < E; ++e) a_pre[i][e] = a_post[i][e] = a_gate[i][e] = f2(0.f);
+    for (int e = 0; e < E; ++e) a_pre[i][e] = a_a[i][e] = f2(0.f);
   const int units = p.bs * p.upb;
   for (int unit = blockIdx.x; unit < units; unit += gridDim.x) {
     const int b = unit / p.upb, part = unit - b * p.upb;
-    const long long q0 = p.rows_per_b * part / p.upb + grp, q1 = p.rows_per_b * (part + 1) / p.upb;
-    auto token = [&](long long k) {   // token k of gate row b: rank k / s, position k % s
-      if (p.bs == 1) return k;
-      const long long rk = k / p.s;
-      return (rk * p.B + b) * p.s + (k - rk * p.s);
-    };
+    const int q0 = (int)((long long)p.rows_per_b * part / p.upb) + grp;
+    const int q1 = (int)((long long)p.rows_per_b * (part + 1) / p.upb);
+    // token k of gate row b: rank k / s, position k % s
+    auto token = [&](int k) { return p.bs == 1 ? k : k + (k / p.s * (p.B - 1) + b) * p.s; };
     if (WARP) __syncwarp();
     else if (unit != blockIdx.x) __syncthreads();   // every thread is done with the last unit's stages
     if (l == 0) {
@@ -363,29 +369,34 @@ __global__ void __launch_bounds__(kMaxGroup, 1) residual_norm_bwd_kernel(const _
       }
     }
     int done = -1;
-    for (long long k = q0; k < q1; k += G, ring.next()) {
-      const long long base = token(k) * p.vecs;
+    int pos = p.bs == 1 ? 0 : q0 % p.s, t = token(q0);
+    for (int k = q0; k < q1; k += G, ring.next()) {
+      const long long base = (long long)t * p.vecs + l;
       if (ring.stages == 1 && done >= 0) {   // no stage to run ahead into
         group_barrier<WARP>();
-        if (l == 0) ring.issue(p.src, token(k), 0);
+        if (l == 0) ring.issue(p.src, t, 0);
       }
       ring.wait(&abort_flag, p.ring.err);
       F2 rr = f2(0.f), ar = f2(0.f), hh = f2(0.f);   // sums of r^2, du w_pre r and h^2, taken together
+      const uint4 *rv = ring.row(p.sr) + l, *uv = ring.row(p.su) + l, *hv = ring.row(p.sh) + l, *dv = ring.row(p.sd) + l;
+      const uint4 *gv = p.sg >= 0 ? ring.row(p.sg) + l : p.gate + (long long)b * p.vecs + l;
+      F2 hn[NV][E];
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int v = l + i * tpr;
-        if (v < p.vecs) {
-          if (p.w_post) {
-            F2 h[E];
-            Vec<T>::unpack(ring.row(p.sh)[v], h);
+        const int v = i * tpr;
+        if (i < NV - 1 || tail) {
+          if (p.sh >= 0) {
+            Vec<T>::unpack(hv[v], hn[i]);
+            if (post) {
 #pragma unroll
-            for (int e = 0; e < E; ++e) hh = fma(h[e], h[e], hh);
+              for (int e = 0; e < E; ++e) hh = fma(hn[i][e], hn[i][e], hh);
+            }
           }
           if (p.su >= 0) {
             F2 r[E], u[E], w[E];
-            Vec<T>::unpack(ring.row(p.sr)[v], r);
-            Vec<T>::unpack(ring.row(p.su)[v], u);
-            Vec<T>::unpack(__ldg(p.w_pre + v), w);
+            Vec<T>::unpack(rv[v], r);
+            Vec<T>::unpack(uv[v], u);
+            Vec<T>::unpack(__ldg(p.w_pre + l + v), w);
 #pragma unroll
             for (int e = 0; e < E; ++e) {
               rr = fma(r[e], r[e], rr);
@@ -401,22 +412,25 @@ __global__ void __launch_bounds__(kMaxGroup, 1) residual_norm_bwd_kernel(const _
         ring.issue(p.src, token(k + (ring.stages - 1) * G), done);
       const float irs = rsqrtf(s3[0] * p.inv_d + p.eps);
       const F2 ir = f2(irs), nc1 = f2(-s3[1] * irs * irs * p.inv_d);   // -mean(a rn) / rms(r)
-      const float ihs = p.w_post ? rsqrtf(s3[2] * p.inv_d + p.eps) : 1.f;
+      const float ihs = post ? rsqrtf(s3[2] * p.inv_d + p.eps) : 1.f;
       const F2 ih = f2(ihs), a = f2(p.res_scale);
       F2 s1p = f2(0.f), dn[NV][E];
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int v = l + i * tpr;
-        if (v < p.vecs) {
+        const int v = i * tpr;
+        if (i < NV - 1 || tail) {
           F2 (&d)[E] = dn[i];
+          if (p.sd >= 0) {
+            Vec<T>::unpack(dv[v], d);
+          } else {
 #pragma unroll
-          for (int e = 0; e < E; ++e) d[e] = f2(0.f);
-          if (p.sd >= 0) Vec<T>::unpack(ring.row(p.sd)[v], d);
+            for (int e = 0; e < E; ++e) d[e] = f2(0.f);
+          }
           if (p.su >= 0) {
             F2 r[E], u[E], w[E];
-            Vec<T>::unpack(ring.row(p.sr)[v], r);
-            Vec<T>::unpack(ring.row(p.su)[v], u);
-            Vec<T>::unpack(__ldg(p.w_pre + v), w);
+            Vec<T>::unpack(rv[v], r);
+            Vec<T>::unpack(uv[v], u);
+            Vec<T>::unpack(__ldg(p.w_pre + l + v), w);
 #pragma unroll
             for (int e = 0; e < E; ++e) {
               d[e] = fma(ir, fma(nc1, r[e], mul(u[e], w[e])), d[e]);
@@ -430,90 +444,85 @@ __global__ void __launch_bounds__(kMaxGroup, 1) residual_norm_bwd_kernel(const _
             p.dx[base + v] = Vec<T>::pack(o);
           }
           if (p.sh >= 0) {
-            F2 h[E], w[E];
-            Vec<T>::unpack(ring.row(p.sh)[v], h);
-            if (p.w_post) {
-              Vec<T>::unpack(__ldg(p.w_post + v), w);
+            F2 w[E];
+            if (post) {
+              Vec<T>::unpack(__ldg(p.w_post + l + v), w);
 #pragma unroll
-              for (int e = 0; e < E; ++e) h[e] = mul(h[e], ih);   // hn
-            } else {
-#pragma unroll
-              for (int e = 0; e < E; ++e) w[e] = f2(1.f);
+              for (int e = 0; e < E; ++e) hn[i][e] = mul(hn[i][e], ih);
             }
-            if (p.gate_mode != ULY_GATE_NONE) {
-              F2 g[E], o[E];
-              Vec<T>::unpack(p.sg >= 0 ? ring.row(p.sg)[v] : __ldg(p.gate + (long long)b * p.vecs + v), g);
+            if (p.sg < 0) {
 #pragma unroll
-              for (int e = 0; e < E; ++e) {
-                o[e] = mul(d[e], mul(h[e], w[e]));   // dR N(h)
-                d[e] = mul(d[e], g[e]);
-              }
+              for (int e = 0; e < E; ++e) a_a[i][e] = fma(d[e], hn[i][e], a_a[i][e]);
+            }
+            if (gated) {
+              F2 g[E];
+              Vec<T>::unpack(gv[v], g);
               if (p.sg >= 0) {
-                if (p.dgate_tok) p.dgate_tok[base + v] = Vec<T>::pack(o);
-              } else {
+                if (p.dgate_tok) {
+                  F2 o[E];
 #pragma unroll
-                for (int e = 0; e < E; ++e) a_gate[i][e] = add(a_gate[i][e], o[e]);
+                  for (int e = 0; e < E; ++e) o[e] = mul(d[e], post ? mul(hn[i][e], w[e]) : hn[i][e]);   // dR N(h)
+                  p.dgate_tok[base + v] = Vec<T>::pack(o);
+                }
+#pragma unroll
+                for (int e = 0; e < E; ++e) a_a[i][e] = fma(mul(d[e], g[e]), hn[i][e], a_a[i][e]);
               }
+#pragma unroll
+              for (int e = 0; e < E; ++e) d[e] = mul(d[e], g[e]);
             }
-            if (p.w_post) {
+            if (post) {
 #pragma unroll
               for (int e = 0; e < E; ++e) {
-                a_post[i][e] = fma(d[e], h[e], a_post[i][e]);
                 d[e] = mul(d[e], w[e]);
-                s1p = fma(d[e], h[e], s1p);
+                s1p = fma(d[e], hn[i][e], s1p);
               }
             }
           }
         }
       }
       done = ring.at;
+      if (p.bs > 1) {   // the group's next token
+        for (pos += G, t += G; pos >= p.s; pos -= p.s) t += (p.B - 1) * p.s;
+      } else {
+        t += G;
+      }
       if (!p.dh) continue;
       F2 nc2 = f2(0.f);
-      if (p.w_post) {
+      if (post) {
         float s1[1] = {sum2(s1p)};
         group_sum<1, WARP>(s1, sh1, turn1);
-        nc2 = f2(-s1[0] * p.inv_d * ihs);
+        nc2 = f2(-s1[0] * p.inv_d);
       }
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int v = l + i * tpr;
-        if (v < p.vecs) {
-          if (p.w_post) {
-            F2 h[E];
-            Vec<T>::unpack(ring.row(p.sh)[v], h);
+        if (i < NV - 1 || tail) {
+          if (post) {
 #pragma unroll
-            for (int e = 0; e < E; ++e) dn[i][e] = mul(ih, fma(nc2, h[e], dn[i][e]));
+            for (int e = 0; e < E; ++e) dn[i][e] = mul(ih, fma(nc2, hn[i][e], dn[i][e]));
           }
-          p.dh[base + v] = Vec<T>::pack(dn[i]);
+          p.dh[base + i * tpr] = Vec<T>::pack(dn[i]);
         }
       }
     }
-    if (p.part_gate) {
+    if (p.part_a) {
+      F2 *o = reinterpret_cast<F2 *>(p.part_a) + (((long long)unit * G + grp) * p.vecs + l) * E;
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int v = l + i * tpr;
-        if (v < p.vecs) {
-          F2 *o = reinterpret_cast<F2 *>(p.part_gate) + (((long long)unit * G + grp) * p.vecs + v) * E;
+      for (int i = 0; i < NV; ++i)
+        if (i < NV - 1 || tail)
 #pragma unroll
           for (int e = 0; e < E; ++e) {
-            o[e] = a_gate[i][e];
-            a_gate[i][e] = f2(0.f);
+            o[(long long)i * tpr * E + e] = a_a[i][e];
+            a_a[i][e] = f2(0.f);
           }
-        }
-      }
     }
   }
+  if (p.part_pre) {
+    F2 *o = reinterpret_cast<F2 *>(p.part_pre) + (((long long)blockIdx.x * G + grp) * p.vecs + l) * E;
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int v = l + i * tpr;
-    if (v < p.vecs) {
-      const long long at = (((long long)blockIdx.x * G + grp) * p.vecs + v) * E;
+    for (int i = 0; i < NV; ++i)
+      if (i < NV - 1 || tail)
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        if (p.part_pre) reinterpret_cast<F2 *>(p.part_pre)[at + e] = a_pre[i][e];
-        if (p.part_post) reinterpret_cast<F2 *>(p.part_post)[at + e] = a_post[i][e];
-      }
-    }
+        for (int e = 0; e < E; ++e) o[(long long)i * tpr * E + e] = a_pre[i][e];
   }
   ring_end(&abort_flag);
 }
@@ -522,13 +531,12 @@ __global__ void __launch_bounds__(kMaxGroup, 1) residual_norm_bwd_kernel(const _
 
 // Groups and stages for rows of `vecs` vectors: a warp a row while `nv` vectors
 // a thread cover it, else the fewest warps that do; CTAs an SM by the registers
-// (`threads` of them an SM) and by two stages each at least (one only where a
-// single CTA's do not fit).
+// and by two stages each at least (one only where a single CTA's do not fit).
 struct RowShape {
   int tpr, nv, rpb, per_sm, stages;
   uint32_t smem;
 };
-RowShape row_shape(int vecs, int slots, int nv, int threads) {
+RowShape row_shape(int vecs, int slots, int nv, bool backward) {
   RowShape r;
   auto up32 = [](int v) { return (v + 31) / 32 * 32; };
   r.tpr = up32((vecs + nv - 1) / nv);
@@ -536,6 +544,9 @@ RowShape row_shape(int vecs, int slots, int nv, int threads) {
   r.nv = (vecs + r.tpr - 1) / r.tpr;
   r.rpb = r.tpr == 32 ? kWarpRows : 1;
   const uint32_t stage = (uint32_t)vecs * 16 * slots * r.rpb;
+  // threads an SM holds by the kernels' registers: forward up to 64, beyond two
+  // vectors a thread up to 112; backward up to 104, then 128
+  const int threads = backward ? (r.nv == 1 ? 608 : 512) : (r.nv <= 2 ? 1024 : 576);
   r.per_sm = threads / (r.tpr * r.rpb);
   if (r.per_sm < 1) r.per_sm = 1;
   while (r.per_sm > 1 && kRingBytes / (stage * r.per_sm) < 2) --r.per_sm;
@@ -544,8 +555,7 @@ RowShape row_shape(int vecs, int slots, int nv, int threads) {
   r.smem = stage * r.stages;
   return r;
 }
-constexpr int kFwdVecs = 5, kFwdThreads = 576;   // up to 112 registers a thread
-constexpr int kBwdVecs = 2, kBwdThreads = 512;   // up to 128
+constexpr int kFwdVecs = 5, kBwdVecs = 2;
 
 template <typename Params>
 struct Entry {
@@ -582,12 +592,12 @@ Entry<NormBwdParams> &bwd_entry(const RowShape &r) {
 struct BwdPlan {
   RowShape rs;
   int slots, bs, upb, grid;
-  size_t off_pre, off_post, off_gate, bytes;
+  size_t off_pre, off_a, bytes;
 };
 BwdPlan bwd_plan(int B, long long n, int hidden, int e, int gate_mode) {
   BwdPlan q;
   q.slots = gate_mode == ULY_GATE_TOKEN ? 5 : 4;
-  q.rs = row_shape(hidden / e, q.slots, kBwdVecs, kBwdThreads);
+  q.rs = row_shape(hidden / e, q.slots, kBwdVecs, true);
   q.bs = gate_mode == ULY_GATE_SEQUENCE ? B : 1;
   const long long rows = gate_mode == ULY_GATE_SEQUENCE ? n : (long long)B * n;
   const long long want = (long long)device_sm_count() * q.rs.per_sm;
@@ -599,55 +609,70 @@ BwdPlan bwd_plan(int B, long long n, int hidden, int e, int gate_mode) {
   q.grid = (int)(units < want ? units : want);
   const size_t col = (size_t)hidden * sizeof(float) * q.rs.rpb;
   q.off_pre = 0;
-  q.off_post = q.off_pre + col * q.grid;
-  q.off_gate = q.off_post + col * q.grid;
-  q.bytes = q.off_gate + (gate_mode == ULY_GATE_CHANNEL || gate_mode == ULY_GATE_SEQUENCE ? col * units : 0);
+  q.off_a = q.off_pre + col * q.grid;
+  q.bytes = q.off_a + col * units;
   return q;
 }
 
-// Column sums to fold: dst[k][c] = sum over i < parts of src[k][i][c], k < rows.
+// Column sums to fold, k < rows:
+//   dst[k][c] = mul[c] sum over i < parts of weight[i / per_weight][c] src[k][i][c]
+// (mul, weight: nullable vectors of the operators' own type).
 struct FoldJob {
   const float *src;
   float *dst;
   long long parts;
   int rows;
+  const void *mul, *weight;
+  int per_weight;
 };
 struct FoldJobs {
   FoldJob job[3];
-  int n, cols;
+  int n, cols, bf16;
 };
+constexpr int kStrips = 16;
 
-// Rows of all jobs along grid.y, 32 columns a CTA; 8 strips of partials are
-// added in a fixed order and joined through shared memory.
-__global__ void __launch_bounds__(256) fold_columns_kernel(const __grid_constant__ FoldJobs jobs) {
-  __shared__ float sh[8][33];
+__device__ __forceinline__ float vector_at(const void *p, long long i, int bf16) {
+  return bf16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[i]) : static_cast<const float *>(p)[i];
+}
+
+// Rows of all jobs along grid.y, 32 columns a CTA; strips of partials are added
+// in a fixed order and joined through shared memory.
+__global__ void __launch_bounds__(32 * kStrips) fold_columns_kernel(const __grid_constant__ FoldJobs jobs) {
+  __shared__ float sh[kStrips][33];
   const int lane = threadIdx.x & 31, strip = threadIdx.x >> 5, cols = jobs.cols;
   int total = 0;
   for (int j = 0; j < jobs.n; ++j) total += jobs.job[j].rows;
   for (int row = blockIdx.y; row < total; row += gridDim.y) {
     int k = row, j = 0;
     while (k >= jobs.job[j].rows) k -= jobs.job[j++].rows;
-    const long long parts = jobs.job[j].parts;
+    const FoldJob &f = jobs.job[j];
+    const long long parts = f.parts;
     const int c = blockIdx.x * 32 + lane;
-    const float *s = jobs.job[j].src + (long long)k * parts * cols;
+    const float *s = f.src + (long long)k * parts * cols;
     float a[8] = {};
     if (c < cols) {
       long long i = strip;
-      for (; i + 56 < parts; i += 64) {
+      if (f.weight) {
+        for (int e = 0; i < parts; i += kStrips, e = (e + 1) & 7)
+          a[0] = fmaf(__ldcs(s + i * cols + c), vector_at(f.weight, i / f.per_weight * cols + c, jobs.bf16), a[0]);
+      } else {
+        for (; i + 7 * kStrips < parts; i += 8 * kStrips) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) a[e] += __ldcs(s + (i + 8 * e) * cols + c);
+          for (int e = 0; e < 8; ++e) a[e] += __ldcs(s + (i + kStrips * e) * cols + c);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e, i += kStrips)
+          if (i < parts) a[e] += __ldcs(s + i * cols + c);
       }
-#pragma unroll
-      for (int e = 0; e < 8; ++e, i += 8)
-        if (i < parts) a[e] += __ldcs(s + i * cols + c);
     }
     sh[strip][lane] = ((a[0] + a[1]) + (a[2] + a[3])) + ((a[4] + a[5]) + (a[6] + a[7]));
     __syncthreads();
     if (strip == 0 && c < cols) {
       float v = 0.f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v += sh[e][lane];
-      jobs.job[j].dst[(long long)k * cols + c] = v;
+      for (int e = 0; e < kStrips; ++e) v += sh[e][lane];
+      if (f.mul) v *= vector_at(f.mul, c, jobs.bf16);
+      f.dst[(long long)k * cols + c] = v;
     }
     __syncthreads();
   }
@@ -658,7 +683,8 @@ uly_status fold_launch(const FoldJobs &jobs, cudaStream_t stream) {
   for (int j = 0; j < jobs.n; ++j) rows += jobs.job[j].rows;
   if (rows == 0) return ULY_OK;
   prof::Scope scope(prof::K_FOLD_COLUMNS, stream);
-  fold_columns_kernel<<<dim3((jobs.cols + 31) / 32, (unsigned)(rows < 65535 ? rows : 65535)), 256, 0, stream>>>(jobs);
+  fold_columns_kernel<<<dim3((jobs.cols + 31) / 32, (unsigned)(rows < 65535 ? rows : 65535)), 32 * kStrips, 0, stream>>>(
+      jobs);
   note_launches(1);
   return last_launch_status();
 }
@@ -668,7 +694,7 @@ uly_status fold_launch(const FoldJobs &jobs, cudaStream_t stream) {
 uly_status fold_columns_launch(const float *src, int rows, long long parts, int cols, float *dst,
                                cudaStream_t stream) {
   FoldJobs jobs = {};
-  jobs.job[0] = {src, dst, parts, rows};
+  jobs.job[0] = {src, dst, parts, rows, nullptr, nullptr, 1};
   jobs.n = 1;
   jobs.cols = cols;
   return fold_launch(jobs, stream);
@@ -690,13 +716,13 @@ uly_status residual_norm_launch(int32_t B, int32_t n, int32_t P, int32_t hidden,
   p.w_pre = static_cast<const uint4 *>(w_pre);
   p.r = static_cast<uint4 *>(r);
   p.u = static_cast<uint4 *>(u);
-  p.rows = (long long)B * n;
+  p.rows = B * n;
   p.vecs = hidden / (bf ? 8 : 4);
   p.gate_mode = gate_mode; p.B = B; p.s = n / P;
   p.res_scale = res_scale; p.eps = eps; p.inv_d = 1.0f / hidden;
-  const RowShape rs = row_shape(p.vecs, p.src.n, kFwdVecs, kFwdThreads);
+  const RowShape rs = row_shape(p.vecs, p.src.n, kFwdVecs, false);
   p.ring = {p.src.n, rs.stages, error_word()};
-  const long long want = (long long)device_sm_count() * rs.per_sm, ctas = (p.rows + rs.rpb - 1) / rs.rpb;
+  const long long want = (long long)device_sm_count() * rs.per_sm, ctas = ((long long)p.rows + rs.rpb - 1) / rs.rpb;
   const int grid = (int)(ctas < want ? ctas : want);
   prof::Scope scope(prof::K_RESIDUAL_NORM, stream);
   return run(bf ? fwd_entry<__nv_bfloat16>(rs) : fwd_entry<float>(rs), grid, rs.tpr * rs.rpb, rs.smem, p, stream);
@@ -729,9 +755,8 @@ uly_status residual_norm_bwd_launch(int32_t B, int32_t n, int32_t P, int32_t hid
   p.dh = static_cast<uint4 *>(dh);
   p.dgate_tok = gate_mode == ULY_GATE_TOKEN ? static_cast<uint4 *>(dgate) : nullptr;
   p.part_pre = dw_pre ? reinterpret_cast<float *>(ws + q.off_pre) : nullptr;
-  p.part_post = dw_post ? reinterpret_cast<float *>(ws + q.off_post) : nullptr;
-  p.part_gate = shared_gate && dgate ? reinterpret_cast<float *>(ws + q.off_gate) : nullptr;
-  p.rows_per_b = gate_mode == ULY_GATE_SEQUENCE ? n : (long long)B * n;
+  p.part_a = dw_post || (shared_gate && dgate) ? reinterpret_cast<float *>(ws + q.off_a) : nullptr;
+  p.rows_per_b = gate_mode == ULY_GATE_SEQUENCE ? n : B * n;
   p.vecs = hidden / (bf ? 8 : 4);
   p.gate_mode = gate_mode; p.B = B; p.s = n / P;
   p.bs = q.bs; p.upb = q.upb;
@@ -742,13 +767,19 @@ uly_status residual_norm_bwd_launch(int32_t B, int32_t n, int32_t P, int32_t hid
                               q.rs.tpr * q.rs.rpb, q.rs.smem, p, stream);
     if (st != ULY_OK) return st;
   }
-  const long long parts = (long long)q.grid * q.rs.rpb;
+  const int run = q.upb * q.rs.rpb;   // partials of one gate row
   FoldJobs jobs = {};
   jobs.cols = hidden;
-  if (dw_pre) jobs.job[jobs.n++] = {p.part_pre, dw_pre, parts, 1};
-  if (dw_post) jobs.job[jobs.n++] = {p.part_post, dw_post, parts, 1};
-  if (p.part_gate)
-    jobs.job[jobs.n++] = {p.part_gate, static_cast<float *>(dgate), (long long)q.upb * q.rs.rpb, q.bs};
+  jobs.bf16 = bf;
+  if (dw_pre) jobs.job[jobs.n++] = {p.part_pre, dw_pre, (long long)q.grid * q.rs.rpb, 1, nullptr, nullptr, 1};
+  if (dw_post) {
+    FoldJob &f = jobs.job[jobs.n++];
+    f = {p.part_a, dw_post, (long long)q.bs * run, 1, nullptr, nullptr, run};
+    if (gate_mode == ULY_GATE_CHANNEL) f.mul = gate;
+    if (gate_mode == ULY_GATE_SEQUENCE) (q.bs > 1 ? f.weight : f.mul) = gate;
+  }
+  if (shared_gate && dgate)
+    jobs.job[jobs.n++] = {p.part_a, static_cast<float *>(dgate), run, q.bs, w_post, nullptr, 1};
   return fold_launch(jobs, stream);
 }
 

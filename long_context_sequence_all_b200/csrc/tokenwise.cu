@@ -59,6 +59,7 @@ uly_status norm_shape(int32_t batch, int32_t seq_len, int32_t world, int32_t hid
                       int32_t gate_mode) {
   if (dtype != ULY_BF16 && dtype != ULY_F32) return ULY_ERR_DTYPE;
   if (batch <= 0 || seq_len <= 0 || world <= 0 || hidden <= 0 || seq_len % world) return ULY_ERR_SHAPE;
+  if ((long long)batch * seq_len > kMaxRows) return ULY_ERR_SHAPE;
   if (gate_mode < ULY_GATE_NONE || gate_mode > ULY_GATE_TOKEN) return ULY_ERR_UNSUPPORTED;
   const int e = dtype == ULY_BF16 ? 8 : 4;
   if (hidden % e) return ULY_ERR_ALIGN;
