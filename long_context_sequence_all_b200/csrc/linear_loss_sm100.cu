@@ -24,7 +24,7 @@
 // at D = 2560.  Forming the logits a second time instead would cost a third.
 #include <cuda_fp16.h>
 
-#include "gemm_sm100.cuh"
+#include "skinny_sm100.cuh"
 #include "tokenwise.cuh"
 
 namespace uly {
@@ -117,6 +117,68 @@ __device__ __forceinline__ void merge(float &m, float &s, float m2, float s2) {
   s = s * exp2f((m - mm) * kLog2e) + s2 * exp2f((m2 - mm) * kLog2e);
   m = mm;
 }
+
+// Few tokens: the tile's 128 columns of the vocabulary are one slot; a warp a
+// token, four columns a lane.
+struct SkinnyLossParams {
+  LossParams l;
+  __half *p;        // null: no exponentials are kept
+  long long ldp;
+};
+struct SkinnyLoss {
+  using Params = SkinnyLossParams;
+  static __device__ __forceinline__ void finish(const Params &q, const skinny::Tile &tile, int index, int, int) {
+    const LossParams &p = q.l;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int col = index * kSlot + 4 * lane, ncol = p.vocab - index * kSlot;
+    // four tokens of a warp at a time: their shuffles overlap
+    for (int t0 = warp * 4; t0 < p.rows; t0 += skinny::kSkinnyThreads / 8) {
+      float z[4][4], m[4], s[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        tile.sum4(4 * lane, t0 + k, z[k]);   // padded tokens are in the tile
+        m[k] = -INFINITY;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (4 * lane + e < ncol) m[k] = fmaxf(m[k], z[k][e]);
+      }
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) m[k] = fmaxf(m[k], __shfl_xor_sync(0xffffffffu, m[k], off));
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int t = t0 + k;
+        const bool ok = t < p.rows;
+        const int y = ok ? __ldg(p.labels + t) : p.ignore_index;
+        const bool counted = y != p.ignore_index && y >= 0 && y < p.vocab;
+        if (m[k] == -INFINITY) m[k] = 0.f;   // every logit -inf: each term is 0
+        s[k] = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (counted && y == col + e) p.target[t] = z[k][e];
+          z[k][e] = 4 * lane + e < ncol ? ex2_approx((z[k][e] - m[k]) * kLog2e) : 0.f;
+          s[k] += z[k][e];
+        }
+        if (q.p && ok && 4 * lane < ncol) {
+          const __half2 a = __floats2half2_rn(z[k][0] * kScale, z[k][1] * kScale);
+          const __half2 b = __floats2half2_rn(z[k][2] * kScale, z[k][3] * kScale);
+          *reinterpret_cast<uint2 *>(q.p + t * q.ldp + col) =
+              make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+        }
+      }
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) s[k] += __shfl_xor_sync(0xffffffffu, s[k], off);
+      if (lane < 4 && t0 + lane < p.rows) {
+        const float mk = lane == 0 ? m[0] : lane == 1 ? m[1] : lane == 2 ? m[2] : m[3];
+        const float sk = lane == 0 ? s[0] : lane == 1 ? s[1] : lane == 2 ? s[2] : s[3];
+        p.pairs[(long long)index * p.rows_pad + t0 + lane] = make_float2(mk, sk);
+      }
+    }
+  }
+};
 
 // Four rows a CTA: their pairs (one 32-byte sector for a slot of all four) are
 // folded in a fixed order into lse and the rows' losses.  GRAD: then p becomes
@@ -305,6 +367,23 @@ Plan make_plan(int P, long long T, int D, int V, bool grad, int dw_dtype, long l
 template <typename T>
 T *at(void *ws, size_t off) { return reinterpret_cast<T *>(static_cast<char *>(ws) + off); }
 
+// The pairs, targets and (grad) exponentials of a piece's rows.
+template <bool GRAD>
+uly_status logits_pass(const __nv_bfloat16 *x, const void *w, int D, LossParams &p, void *pp, long long ldp,
+                       cudaStream_t stream) {
+  prof::Scope scope(prof::K_LINEAR_LOSS, stream);
+  const int rows = p.rows, V = p.vocab;
+  if (rows <= skinny::kMaxTokens) {   // bound by w's bytes
+    SkinnyLossParams s = {p, GRAD ? static_cast<__half *>(pp) : nullptr, ldp};
+    return skinny::launch<SkinnyLoss, false>(w, D, V, x, D, rows, D, (V + kSlot - 1) / kSlot, 1, kSlot, 64, s, stream);
+  }
+  CUtensorMap tx, tw;
+  if (!make_map(&tw, w, D, V, D, kHalf) || !make_map(&tx, x, D, rows, D, kHalf) ||
+      (GRAD && !make_out_map(&p.p_map, pp, V, rows, ldp)))
+    return ULY_ERR_CUDA;
+  return launch<EpiLoss<GRAD>, false, false>(tx, tw, make_shape(rows, V, D, kTile, 1), p, stream);
+}
+
 RowsParams rows_of(const Plan &q, const LossParams &p, void *ws, long long t0) {
   RowsParams r = {};
   r.pairs = p.pairs; r.target = p.target; r.labels = p.labels;
@@ -335,22 +414,16 @@ uly_status linear_loss_launch(int32_t P, int64_t tokens, int32_t D, int32_t V, c
                               float *loss, void *ws, cudaStream_t stream) {
   const Plan q = make_plan(P, tokens, D, V, false, ULY_F32, 0);
   const __nv_bfloat16 *xb = static_cast<const __nv_bfloat16 *>(x);
-  CUtensorMap ta, tb;
-  if (!make_map(&tb, w, D, V, D, kHalf)) return ULY_ERR_CUDA;
   for (long long t0 = 0; t0 < tokens; t0 += q.piece) {
     const int rows = (int)(tokens - t0 < q.piece ? tokens - t0 : q.piece);
-    if (!make_map(&ta, xb + t0 * D, D, rows, D, kHalf)) return ULY_ERR_CUDA;
     LossParams p = {};
     p.labels = labels + t0;
     p.pairs = at<float2>(ws, q.pairs);
     p.target = at<float>(ws, q.target);
     p.rows_pad = q.rows_pad;
     p.rows = rows; p.vocab = V; p.ignore_index = ignore_index;
-    {
-      prof::Scope scope(prof::K_LINEAR_LOSS, stream);
-      const uly_status st = launch<EpiLoss<false>, false, false>(ta, tb, make_shape(rows, V, D, kTile, 1), p, stream);
-      if (st != ULY_OK) return st;
-    }
+    const uly_status st = logits_pass<false>(xb + t0 * D, w, D, p, nullptr, 0, stream);
+    if (st != ULY_OK) return st;
     RowsParams r = rows_of(q, p, ws, t0);
     prof::Scope scope(prof::K_LINEAR_LOSS_ROWS, stream);
     loss_rows_kernel<false><<<(rows + kRowsCta - 1) / kRowsCta, kRowThreads, 0, stream>>>(r);
@@ -377,26 +450,22 @@ uly_status linear_loss_bwd_launch(int32_t P, int64_t tokens, int32_t D, int32_t 
     if (cudaMemsetAsync(dw, 0, (size_t)V * D * (dw_dtype == ULY_F32 ? 4 : 2), stream) != cudaSuccess)
       return ULY_ERR_CUDA;
   loss_count_launch(labels, tokens, V, ignore_index, count, stream);
-  CUtensorMap tw, tw_mn, tx, tz, tz_mn, tk_mn;
-  if (!make_map(&tw, w, D, V, D, kHalf) || !make_map(&tw_mn, w, D, V, D, 64)) return ULY_ERR_CUDA;
+  CUtensorMap tw_mn, tz, tz_mn, tk_mn;
+  if (!make_map(&tw_mn, w, D, V, D, 64)) return ULY_ERR_CUDA;
   for (long long t0 = 0; t0 < tokens; t0 += q.piece) {
     const int rows = (int)(tokens - t0 < q.piece ? tokens - t0 : q.piece);
     void *pp = at<char>(ws, q.p), *xk = at<char>(ws, q.xk);
     LossParams p = {};
-    if (!make_map(&tx, xb + t0 * D, D, rows, D, kHalf) || !make_map(&tz, pp, V, rows, q.ldp, kHalf) ||
-        !make_map(&tz_mn, pp, V, rows, q.ldp, 64) || !make_map(&tk_mn, xk, D, rows, D, 64) ||
-        !make_out_map(&p.p_map, pp, V, rows, q.ldp))
+    if (!make_map(&tz, pp, V, rows, q.ldp, kHalf) || !make_map(&tz_mn, pp, V, rows, q.ldp, 64) ||
+        !make_map(&tk_mn, xk, D, rows, D, 64))
       return ULY_ERR_CUDA;
     p.labels = labels + t0;
     p.pairs = at<float2>(ws, q.pairs);
     p.target = at<float>(ws, q.target);
     p.rows_pad = q.rows_pad;
     p.rows = rows; p.vocab = V; p.ignore_index = ignore_index;
-    {
-      prof::Scope scope(prof::K_LINEAR_LOSS, stream);
-      const uly_status st = launch<EpiLoss<true>, false, false>(tx, tw, make_shape(rows, V, D, kTile, 1), p, stream);
-      if (st != ULY_OK) return st;
-    }
+    uly_status st = logits_pass<true>(xb + t0 * D, w, D, p, pp, q.ldp, stream);
+    if (st != ULY_OK) return st;
     RowsParams r = rows_of(q, p, ws, t0);
     r.count = count;
     r.p = static_cast<uint4 *>(pp);
@@ -414,7 +483,9 @@ uly_status linear_loss_bwd_launch(int32_t P, int64_t tokens, int32_t D, int32_t 
     o.out = dxb + t0 * D;
     o.M = rows; o.N = D;
     float *part = at<float>(ws, q.part);
-    uly_status st = launch_plain<false, true>(tz, tw_mn, o, V, q.dx_splits, part, prof::K_LINEAR_LOSS_DX, stream);
+    st = rows <= skinny::kMaxTokens
+             ? skinny::launch_plain_mn(pp, q.ldp, w, o.out, rows, D, V, prof::K_LINEAR_LOSS_DX, stream)
+             : launch_plain<false, true>(tz, tw_mn, o, V, q.dx_splits, part, prof::K_LINEAR_LOSS_DX, stream);
     if (st != ULY_OK) return st;
     // dW (+)= dz^T x; the last piece writes the caller's type
     const bool last = t0 + rows >= tokens;

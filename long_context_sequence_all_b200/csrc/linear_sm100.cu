@@ -13,7 +13,7 @@
 // dW = dz^T x on the tensor cores, dW with both operands MN-major.
 //
 // Bound by the tensor cores from a few hundred tokens on, by W's bytes below.
-#include "gemm_sm100.cuh"
+#include "skinny_sm100.cuh"
 #include "tokenwise.cuh"
 
 namespace uly {
@@ -175,6 +175,56 @@ __global__ void __launch_bounds__(256) linear_join_kernel(const __grid_constant_
   }
 }
 
+// Few tokens: this CTA's slice of a tile's features, four of a token a thread.
+template <int ACT>
+struct SkinnyLinear {
+  using Params = LinearParams;
+  static constexpr bool kGated = ACT == ULY_ACT_SWIGLU;
+  static constexpr int kCols = kGated ? 64 : 128;
+  static __device__ __forceinline__ void finish(const Params &p, const skinny::Tile &tile, int index, int rank,
+                                                int ranks) {
+    skinny::for_slice(kCols, rank, ranks, (int)p.M, [&](int row, int t) {
+      const int col = index * kCols + row;   // N is a multiple of 8
+      if (col >= p.N) return;
+      float z[4], up[4] = {}, b[4];
+      tile.sum4(row, t, z);
+      if (kGated) tile.sum4(64 + row, t, up);
+      if (p.bias) {
+        skinny::load4(p.bias + col, b);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) z[e] += b[e];
+        if (kGated) {
+          skinny::load4(p.bias + p.N + col, b);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) up[e] += b[e];
+        }
+      }
+      if (p.pre) {
+        skinny::store4(p.pre + (long long)t * p.NZ + col, z);
+        if (kGated) skinny::store4(p.pre + (long long)t * p.NZ + p.N + col, up);
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) z[e] = act_of<ACT>(z[e], up[e]);
+      if (p.residual) {
+        skinny::load4(p.residual + (long long)t * p.N + col, b);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) z[e] += b[e];
+      }
+      skinny::store4(p.y + (long long)t * p.N + col, z);
+    });
+  }
+};
+
+template <int ACT>
+uly_status run_skinny(const void *x, const void *w, const LinearParams &p, int K, cudaStream_t stream) {
+  prof::Scope scope(prof::K_LINEAR, stream);
+  constexpr int cols = SkinnyLinear<ACT>::kCols;
+  const int tiles = (p.N + cols - 1) / cols;
+  return skinny::launch<SkinnyLinear<ACT>, false>(w, K, p.NZ, x, K, p.M, K, tiles,
+                                                  skinny::cluster_size(p.M, tiles, (K + kBK - 1) / kBK), cols,
+                                                  cols == 64 ? p.N : 64, p, stream);
+}
+
 template <int ACT>
 uly_status run_linear(const CUtensorMap &ta, const CUtensorMap &tb, LinearParams p, int K, int splits, float *part,
                       cudaStream_t stream) {
@@ -283,36 +333,46 @@ BwdPlan bwd_plan(int64_t tokens, int32_t in, int32_t out, int32_t act) {
   q.row_ctas = dz_row_ctas(tokens, out);
   q.off_bias = act == ULY_ACT_NONE ? 0 : up256((size_t)tokens * q.nz * 2);
   q.off_part = q.off_bias + up256((size_t)q.row_ctas * 8 * q.nz * sizeof(float));
+  if (tokens <= skinny::kMaxTokens) q.dx_splits = 1;
   const size_t a = part_bytes(tokens, in, q.dx_splits), b = part_bytes(q.nz, in, q.dw_splits);
   q.bytes = q.off_part + up256(a > b ? a : b);
   return q;
 }
 
+
+// Few tokens: the weights' bytes bound the product and the skinny kernel streams
+// them best.
+bool few_tokens(int64_t tokens) { return tokens <= skinny::kMaxTokens; }
+
+template <int ACT>
+uly_status linear_of(const void *x, const void *w, const LinearParams &p, int K, void *workspace, cudaStream_t stream) {
+  if (few_tokens(p.M)) return run_skinny<ACT>(x, w, p, K, stream);
+  CUtensorMap ta, tb;
+  if (!make_map(&ta, x, K, p.M, K, kHalf) || !make_map(&tb, w, K, p.NZ, K, kHalf)) return ULY_ERR_CUDA;
+  return run_linear<ACT>(ta, tb, p, K, linear_splits(p.M, K, p.N, ACT), static_cast<float *>(workspace), stream);
+}
+
 }  // namespace
 
 size_t linear_workspace_bytes(int64_t tokens, int32_t in, int32_t out, int32_t act) {
+  if (few_tokens(tokens)) return 0;
   return part_bytes(tokens, (long long)out * gated(act), linear_splits(tokens, in, out, act));
 }
 
 uly_status linear_launch(int64_t tokens, int32_t in, int32_t out, int32_t act, const void *x, const void *w,
                          const void *bias, const void *residual, void *y, void *pre, void *workspace,
                          cudaStream_t stream) {
-  const int nz = out * gated(act);
-  CUtensorMap ta, tb;
-  if (!make_map(&ta, x, in, tokens, in, kHalf) || !make_map(&tb, w, in, nz, in, kHalf)) return ULY_ERR_CUDA;
   LinearParams p = {};
   p.bias = static_cast<const __nv_bfloat16 *>(bias);
   p.residual = static_cast<const __nv_bfloat16 *>(residual);
   p.y = static_cast<__nv_bfloat16 *>(y);
   p.pre = static_cast<__nv_bfloat16 *>(pre);
-  p.M = tokens; p.N = out; p.NZ = nz;
-  const int splits = linear_splits(tokens, in, out, act);
-  float *part = static_cast<float *>(workspace);
+  p.M = tokens; p.N = out; p.NZ = out * gated(act);
   switch (act) {
-    case ULY_ACT_GELU: return run_linear<ULY_ACT_GELU>(ta, tb, p, in, splits, part, stream);
-    case ULY_ACT_SILU: return run_linear<ULY_ACT_SILU>(ta, tb, p, in, splits, part, stream);
-    case ULY_ACT_SWIGLU: return run_linear<ULY_ACT_SWIGLU>(ta, tb, p, in, splits, part, stream);
-    default: return run_linear<ULY_ACT_NONE>(ta, tb, p, in, splits, part, stream);
+    case ULY_ACT_GELU: return linear_of<ULY_ACT_GELU>(x, w, p, in, workspace, stream);
+    case ULY_ACT_SILU: return linear_of<ULY_ACT_SILU>(x, w, p, in, workspace, stream);
+    case ULY_ACT_SWIGLU: return linear_of<ULY_ACT_SWIGLU>(x, w, p, in, workspace, stream);
+    default: return linear_of<ULY_ACT_NONE>(x, w, p, in, workspace, stream);
   }
 }
 
@@ -352,7 +412,10 @@ uly_status linear_bwd_launch(int64_t tokens, int32_t in, int32_t out, int32_t ac
     }
   }
   CUtensorMap ta, tb;
-  if (dx) {   // dx[tokens][in] = dz[tokens][nz] W[nz][in]
+  if (dx && few_tokens(tokens)) {   // dx[tokens][in] = dz[tokens][nz] W[nz][in]
+    const uly_status st = skinny::launch_plain_mn(dz, q.nz, w, dx, tokens, in, q.nz, prof::K_LINEAR_DX, stream);
+    if (st != ULY_OK) return st;
+  } else if (dx) {
     if (!make_map(&ta, dz, q.nz, tokens, q.nz, kHalf) || !make_map(&tb, w, in, q.nz, in, 64)) return ULY_ERR_CUDA;
     PlainParams p = {};
     p.out = dx; p.M = tokens; p.N = in;
