@@ -21,8 +21,8 @@
 // past any edge are read as zeros and never stored, so M, N and K are free.
 //
 // A thread holds one row of C, so its own 16-byte stores would fill half a
-// 32-byte sector each, 32 rows apart.  Two-byte outputs go through shared
-// memory instead, 32 x 32 values of a warp at a time, and leave by TMA (8192
+// 32-byte sector each, 32 rows apart.  Outputs go through shared memory
+// instead, 64 bytes of a warp's 32 rows at a time, and leave by TMA (8192
 // x 2560 -> 2 x 10240 gated with z kept: 711 -> 675 us).
 //
 // Every wait is bounded (ULY_ERR_TIMEOUT); a launch that gives up lets its
@@ -42,14 +42,15 @@ using namespace sm100;
 constexpr int kTile = 256;       // rows and columns of a cluster's tile
 constexpr int kHalf = 128;       // rows of A and of B in one CTA
 constexpr int kBK = 64;
-constexpr int kStages = 6;
+constexpr int kStages = 5;
+constexpr int kOutSlots = 4;
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 128 + 32 * kEpiWarps;
 constexpr uint32_t kOperandBytes = kHalf * kBK * 2;        // 16 KB
 constexpr uint32_t kStageBytes = 2 * kOperandBytes;        // one CTA's A and B of a k-step
-constexpr uint32_t kOffOut = kStages * kStageBytes;       // output staging, two 2 KB slots for each epilogue warp
-constexpr uint32_t kOutSlot = 32 * 64;                    // 32 rows of 32 two-byte columns
-constexpr uint32_t kOffBar = kOffOut + kEpiWarps * 2 * kOutSlot;
+constexpr uint32_t kOffOut = kStages * kStageBytes;       // output staging, 2 KB slots for each epilogue warp
+constexpr uint32_t kOutSlot = 32 * 64;                    // 32 rows of 32 two-byte or 16 four-byte columns
+constexpr uint32_t kOffBar = kOffOut + kEpiWarps * kOutSlots * kOutSlot;
 constexpr uint32_t kSmemBytes = kOffBar + 256 + 1024;      // barriers + alignment slack
 constexpr long long kLandCycles = 1 << 20;                 // after giving up: the copies in flight land (~0.5 ms)
 
@@ -123,14 +124,14 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, uint32_t sr
                : "memory");
 }
 
-// One epilogue warp's way out: 32 rows (one a lane) x 32 two-byte columns
-// staged with the 64-byte swizzle of make_out_map(), two slots taken in turn.
+// One epilogue warp's way out: 32 rows (one a lane) x 64 bytes of columns
+// staged with the 64-byte swizzle of make_out_map(), the slots taken in turn.
 struct OutRing {
   uint32_t base, slot;
   int lane;
-  // v: this lane's 32 columns, packed; all lanes of the warp together
+  // v: this lane's columns (32 of two bytes, packed, or 16 of four); all lanes of the warp together
   __device__ __forceinline__ void put(const CUtensorMap *map, int col, int row0, const uint32_t (&v)[16]) {
-    if (lane == 0) bulk_wait_group_read<1>();
+    if (lane == 0) bulk_wait_group_read<kOutSlots - 1>();
     __syncwarp();
     const uint32_t at = base + slot * kOutSlot;
 #pragma unroll
@@ -142,7 +143,7 @@ struct OutRing {
       tma_store_2d(map, at, col, row0);
       bulk_commit_group();
     }
-    slot ^= 1;
+    slot = (slot + 1) % kOutSlots;
   }
 };
 
@@ -276,7 +277,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   } else if (warp >= 4) {
     // ------------------------------------------------------------- epilogue
     const int quarter = warp & 3, half = (warp - 4) >> 2;
-    OutRing out{sb + kOffOut + (uint32_t)(warp - 4) * 2 * kOutSlot, 0, lane};
+    OutRing out{sb + kOffOut + (uint32_t)(warp - 4) * kOutSlots * kOutSlot, 0, lane};
     int it = 0;
     for (int u = cluster; u < units; u += clusters, ++it) {
       const int buf = it & 1;
@@ -312,10 +313,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
 // ------------------------------------------------------------------- host
 
-// 2-D map of a [rows][inner] matrix of two-byte elements with rows `stride`
-// elements apart.  Elements past either edge read as zero and are not written.
+// 2-D map of a [rows][inner] matrix with rows `stride` elements apart.
+// Elements past either edge read as zero and are not written.
 inline bool make_map_of(CUtensorMap *map, const void *base, long long inner, long long rows, long long stride,
-                        int box_cols, int box_rows, CUtensorMapSwizzle swizzle) {
+                        int box_cols, int box_rows, CUtensorMapSwizzle swizzle, bool f32 = false) {
   static std::atomic<void *> fn{nullptr};
   void *p = fn.load(std::memory_order_acquire);
   if (!p) {
@@ -326,11 +327,11 @@ inline bool make_map_of(CUtensorMap *map, const void *base, long long inner, lon
     fn.store(p, std::memory_order_release);
   }
   cuuint64_t dims[2] = {(cuuint64_t)inner, (cuuint64_t)rows};
-  cuuint64_t strides[1] = {(cuuint64_t)stride * 2};
+  cuuint64_t strides[1] = {(cuuint64_t)stride * (f32 ? 4 : 2)};
   cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
   cuuint32_t es[2] = {1, 1};
   return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p)(
-             map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box, es,
+             map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box, es,
              CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -340,8 +341,9 @@ inline bool make_map(CUtensorMap *map, const void *base, long long inner, long l
   return make_map_of(map, base, inner, rows, stride, kBK, box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 // An output leaving through an OutRing.
-inline bool make_out_map(CUtensorMap *map, const void *base, long long inner, long long rows, long long stride) {
-  return make_map_of(map, base, inner, rows, stride, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+inline bool make_out_map(CUtensorMap *map, const void *base, long long inner, long long rows, long long stride,
+                         bool f32 = false) {
+  return make_map_of(map, base, inner, rows, stride, f32 ? 16 : 32, 32, CU_TENSOR_MAP_SWIZZLE_64B, f32);
 }
 
 // Parts to cut each tile's k-steps into.  Work units on `clusters` SM pairs
@@ -421,7 +423,7 @@ __device__ __forceinline__ void store8(float *p, const float (&x)[8]) {
 // --------------------------------------------------------- plain epilogue
 // out = A B^T + add, in bf16 or fp32; N is a multiple of 8.
 struct PlainParams {
-  CUtensorMap out_map;      // bf16 out (launch_plain fills it in)
+  CUtensorMap out_map;      // of out (launch_plain fills it in)
   void *out;
   const float *add;         // nullable fp32 [M][N] (may be `out` itself, fp32)
   float *part;              // splits > 1: fp32 [splits][M][N] instead of everything above
@@ -430,16 +432,9 @@ struct PlainParams {
 };
 struct EpiPlain {
   using Params = PlainParams;
-  static __device__ __forceinline__ void add8(const Params &p, long long row, int col, float (&z)[8]) {
-    if (!p.add) return;
-    float a[8];
-    load8(p.add + row * p.N + col, a);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) z[e] += a[e];
-  }
   static __device__ __forceinline__ void tile(const Params &p, const Unit &w, uint32_t acc, int row, int half,
                                               OutRing &out) {
-    const bool ok = row < p.M, staged = !p.part && !p.out_f32;
+    const bool ok = row < p.M;
     const int row0 = row - out.lane;
 #pragma unroll 1
     for (int c = 0; c < kHalf; c += 32) {
@@ -447,25 +442,43 @@ struct EpiPlain {
       uint32_t a[32], v[16];
       tmem_ld32(acc + half * kHalf + c, a);
       if (col0 >= p.N || row0 >= p.M) continue;   // the whole warp
+      if (p.part) {
+        if (ok) {
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const int col = col0 + 8 * g;
-        float z[8];
+          for (int g = 0; g < 4; ++g)
+            if (col0 + 8 * g < p.N) {
+              float z[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) z[e] = __uint_as_float(a[8 * g + e]);
-        if (ok && col < p.N) {
-          if (p.part) {
-            store8(p.part + ((long long)w.split * p.M + row) * p.N + col, z);
-          } else {
-            add8(p, row, col, z);
-            if (p.out_f32) store8(static_cast<float *>(p.out) + (long long)row * p.N + col, z);
-          }
+              for (int e = 0; e < 8; ++e) z[e] = __uint_as_float(a[8 * g + e]);
+              store8(p.part + ((long long)w.split * p.M + row) * p.N + col0 + 8 * g, z);
+            }
         }
+        __syncwarp();
+        continue;
+      }
+      if (p.add && ok) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[4 * g + e] = pack_bf16x2(z[2 * e], z[2 * e + 1]);
+        for (int g = 0; g < 4; ++g)
+          if (col0 + 8 * g < p.N) {
+            float z[8];
+            load8(p.add + (long long)row * p.N + col0 + 8 * g, z);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) a[8 * g + e] = __float_as_uint(__uint_as_float(a[8 * g + e]) + z[e]);
+          }
       }
       __syncwarp();
-      if (staged) out.put(&p.out_map, col0, row0, v);
+      if (p.out_f32) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) v[e] = a[16 * h + e];
+          if (col0 + 16 * h < p.N) out.put(&p.out_map, col0 + 16 * h, row0, v);
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) v[e] = pack_bf16x2(__uint_as_float(a[2 * e]), __uint_as_float(a[2 * e + 1]));
+        out.put(&p.out_map, col0, row0, v);
+      }
     }
   }
 };
@@ -485,7 +498,12 @@ static __global__ void __launch_bounds__(256) plain_join_kernel(const __grid_con
 #pragma unroll
       for (int e = 0; e < 8; ++e) z[e] += v[e];
     }
-    EpiPlain::add8(p, row, col, z);
+    if (p.add) {
+      float v[8];
+      load8(p.add + row * p.N + col, v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) z[e] += v[e];
+    }
     if (p.out_f32) store8(static_cast<float *>(p.out) + row * p.N + col, z);
     else store8(static_cast<__nv_bfloat16 *>(p.out) + row * p.N + col, z);
   }
@@ -508,7 +526,7 @@ uly_status launch_plain(const CUtensorMap &ta, const CUtensorMap &tb, PlainParam
   const long long k_steps = (K + kBK - 1) / kBK;
   if (splits > k_steps) splits = (int)k_steps;   // a short last piece: no part without a k-step
   p.part = splits > 1 ? part : nullptr;
-  if (!p.part && !p.out_f32 && !make_out_map(&p.out_map, p.out, p.N, p.M, p.N)) return ULY_ERR_CUDA;
+  if (!p.part && !make_out_map(&p.out_map, p.out, p.N, p.M, p.N, p.out_f32 != 0)) return ULY_ERR_CUDA;
   prof::Scope scope(kernel_id, stream);
   const uly_status st = launch<EpiPlain, A_MN, B_MN>(ta, tb, make_shape(p.M, p.N, K, kTile, splits), p, stream);
   if (st != ULY_OK || splits == 1) return st;

@@ -181,20 +181,17 @@ struct SkinnyLoss {
 };
 
 // Four rows a CTA: their pairs (one 32-byte sector for a slot of all four) are
-// folded in a fixed order into lse and the rows' losses.  GRAD: then p becomes
-// dz, and x is copied with zeros in the rows that do not count (a row of a
-// padded batch may hold anything, and 0 times NaN is not 0).
+// folded in a fixed order into lse and the rows' losses.  GRAD: and each slot's
+// factor exp(maximum - lse) / C of its stored exponentials, [row][slot].
 struct RowsParams {
   const float2 *pairs;
   const float *target;
   const int32_t *labels;
-  float *row_loss;            // of the piece's rows
+  float *row_loss, *row_lse;  // of the piece's rows
   const long long *count;
-  uint4 *p;                   // [rows][ldp / 8]: fp16 in, bf16 out
-  const uint4 *x;
-  uint4 *xk;                  // [rows][hidden / 8]
-  long long ldp, rows_pad;
-  int rows, slots, vocab, ignore_index, hidden;
+  float *factor;              // [rows][slots]
+  long long rows_pad;
+  int rows, slots, vocab, ignore_index;
   int *err;
 };
 constexpr int kRowsCta = 4, kRowThreads = 512;
@@ -238,46 +235,75 @@ __global__ void __launch_bounds__(kRowThreads) loss_rows_kernel(const RowsParams
     const bool counted = y != p.ignore_index && y >= 0 && y < p.vocab;
     if (y != p.ignore_index && !counted) raise_error(p.err, ULY_ERR_LABEL);
     p.row_loss[row0 + r] = counted ? lse - p.target[row0 + r] : 0.f;
-    sh_lse[r] = lse;
+    if (GRAD) p.row_lse[row0 + r] = sh_lse[r] = lse;
   }
   if (!GRAD) return;
   __syncthreads();
-  const float inv = (float)(1.0 / (double)max(*p.count, 1ll));   // no counted token: every row is zeros
+  const float f = (float)(1.0 / (double)max(*p.count, 1ll)) / kScale;   // no counted token: no row uses it
+  for (int k = threadIdx.x; k < p.slots; k += kRowThreads) {
+    const float2 *v = p.pairs + (long long)k * p.rows_pad + row0;
+    for (int r = 0; r < nrows; ++r)
+      p.factor[(long long)(row0 + r) * p.slots + k] = exp2f((v[r].x - sh_lse[r]) * kLog2e) * f;
+  }
+}
+
+// p becomes dz: kGradCols columns of one row a CTA.  The first CTA of a row also
+// copies x, with zeros in the rows that do not count (a row of a padded batch
+// may hold anything, and 0 times NaN is not 0).
+struct GradParams {
+  const float *factor, *row_lse, *target;
+  const int32_t *labels;
+  const long long *count;
+  uint4 *p;                   // [rows][ldp / 8]: fp16 in, bf16 out
+  const uint4 *x;
+  uint4 *xk;                  // [rows][hidden / 8]
+  long long ldp;
+  int slots, vocab, ignore_index, hidden;
+};
+constexpr int kGradThreads = 256, kGradVecs = 4, kGradCols = kGradThreads * kGradVecs * 8;
+
+__global__ void __launch_bounds__(kGradThreads) loss_grad_kernel(const GradParams p) {
+  const int row = blockIdx.x, y = __ldg(p.labels + row);
+  const bool counted = y != p.ignore_index && y >= 0 && y < p.vocab;
   const uint4 zero = make_uint4(0, 0, 0, 0);
-  for (int r = 0; r < nrows; ++r) {
-    const int row = row0 + r, y = __ldg(p.labels + row);
-    const bool counted = y != p.ignore_index && y >= 0 && y < p.vocab;
-    const float lse = sh_lse[r];
-    uint4 *o = p.p + (long long)row * (p.ldp / 8);
-    const int vecs = (int)(p.ldp / 8);
-    // z_y <= lse but for rounding: the label's softmax is at most 1
-    const float dy = counted ? inv * expm1f(fminf(p.target[row] - lse, 0.f)) : 0.f;
-#pragma unroll 4
-    for (int i = threadIdx.x; i < vecs; i += kRowThreads) {
-      uint4 q = zero;
-      if (counted) {
-        const uint4 h = o[i];
-        const float f = exp2f((p.pairs[(long long)(i / (kSlot / 8)) * p.rows_pad + row].x - lse) * kLog2e) * (inv / kScale);
-        const __half2 *hp = reinterpret_cast<const __half2 *>(&h);
-        float v[8];
+  const int vecs = (int)(p.ldp / 8), i0 = blockIdx.y * (kGradCols / 8) + threadIdx.x;
+  uint4 *o = p.p + (long long)row * vecs;
+  uint4 h[kGradVecs];
+  float f[kGradVecs];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 t = __half22float2(hp[e]);
-          v[2 * e] = t.x * f;
-          v[2 * e + 1] = t.y * f;
-        }
-        if (i == y / 8) {
+  for (int k = 0; k < kGradVecs; ++k) {
+    const int i = i0 + k * kGradThreads;
+    h[k] = counted && i < vecs ? __ldcs(o + i) : zero;
+    f[k] = counted && i < vecs ? __ldg(p.factor + (long long)row * p.slots + i / (kSlot / 8)) : 0.f;
+  }
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (e == y % 8) v[e] = dy;
-        }
-        q = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                       pack_bf16x2(v[6], v[7]));
+  for (int k = 0; k < kGradVecs; ++k) {
+    const int i = i0 + k * kGradThreads;
+    if (i >= vecs) break;
+    uint4 q = zero;
+    if (counted) {
+      const __half2 *hp = reinterpret_cast<const __half2 *>(&h[k]);
+      float v[8];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 t = __half22float2(hp[e]);
+        v[2 * e] = t.x * f[k];
+        v[2 * e + 1] = t.y * f[k];
       }
-      o[i] = q;
+      if (i == y / 8) {
+        // z_y <= lse but for rounding: the label's softmax is at most 1
+        const float dy = (float)(1.0 / (double)*p.count) * expm1f(fminf(p.target[row] - p.row_lse[row], 0.f));
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (e == y % 8) v[e] = dy;
+      }
+      q = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
     }
+    o[i] = q;
+  }
+  if (blockIdx.y == 0) {
     const int xv = p.hidden / 8;
-    for (int i = threadIdx.x; i < xv; i += kRowThreads)
+    for (int i = threadIdx.x; i < xv; i += kGradThreads)
       p.xk[(long long)row * xv + i] = counted ? __ldg(p.x + (long long)row * xv + i) : zero;
   }
 }
@@ -329,7 +355,7 @@ struct Plan {
   long long piece, rows_pad, ldp;
   int slots, dx_splits, dw_splits;
   bool dw_acc;   // dW of several pieces is summed in an fp32 array of the workspace
-  size_t psum, pcnt, count, row_loss, target, pairs, p, xk, part, acc, bytes;   // offsets, total
+  size_t psum, pcnt, count, row_loss, row_lse, target, pairs, factor, p, xk, part, acc, bytes;   // offsets, total
 };
 
 Plan make_plan(int P, long long T, int D, int V, bool grad, int dw_dtype, long long piece_tokens) {
@@ -354,6 +380,8 @@ Plan make_plan(int P, long long T, int D, int V, bool grad, int dw_dtype, long l
     q.dx_splits = choose_splits(q.piece, D, tiles(q.piece), tiles(D), (V + kBK - 1) / kBK, sms);
     q.dw_splits = choose_splits(V, D, tiles(V), tiles(D), (q.piece + kBK - 1) / kBK, sms);
     q.dw_acc = q.piece < T && dw_dtype == ULY_BF16;
+    q.row_lse = take((size_t)q.piece * sizeof(float));
+    q.factor = take((size_t)q.piece * q.slots * sizeof(float));
     q.p = take((size_t)q.piece * q.ldp * 2);
     q.xk = take((size_t)q.piece * D * 2);
     const size_t a = part_bytes(q.piece, D, q.dx_splits), b = part_bytes(V, D, q.dw_splits);
@@ -388,7 +416,7 @@ RowsParams rows_of(const Plan &q, const LossParams &p, void *ws, long long t0) {
   RowsParams r = {};
   r.pairs = p.pairs; r.target = p.target; r.labels = p.labels;
   r.row_loss = at<float>(ws, q.row_loss) + t0;
-  r.ldp = q.ldp; r.rows_pad = q.rows_pad;
+  r.rows_pad = q.rows_pad;
   r.rows = p.rows; r.slots = (p.vocab + kSlot - 1) / kSlot; r.vocab = p.vocab; r.ignore_index = p.ignore_index;
   r.err = error_word();
   return r;
@@ -467,15 +495,21 @@ uly_status linear_loss_bwd_launch(int32_t P, int64_t tokens, int32_t D, int32_t 
     uly_status st = logits_pass<true>(xb + t0 * D, w, D, p, pp, q.ldp, stream);
     if (st != ULY_OK) return st;
     RowsParams r = rows_of(q, p, ws, t0);
+    r.row_lse = at<float>(ws, q.row_lse);
+    r.factor = at<float>(ws, q.factor);
     r.count = count;
-    r.p = static_cast<uint4 *>(pp);
-    r.x = reinterpret_cast<const uint4 *>(xb + t0 * D);
-    r.xk = static_cast<uint4 *>(xk);
-    r.hidden = D;
+    GradParams g = {};
+    g.factor = r.factor; g.row_lse = r.row_lse; g.target = r.target; g.labels = r.labels; g.count = count;
+    g.p = static_cast<uint4 *>(pp);
+    g.x = reinterpret_cast<const uint4 *>(xb + t0 * D);
+    g.xk = static_cast<uint4 *>(xk);
+    g.ldp = q.ldp; g.slots = r.slots; g.vocab = V; g.ignore_index = ignore_index; g.hidden = D;
     {
       prof::Scope scope(prof::K_LINEAR_LOSS_ROWS, stream);
       loss_rows_kernel<true><<<(rows + kRowsCta - 1) / kRowsCta, kRowThreads, 0, stream>>>(r);
-      note_launches(1);
+      const long long cols = (q.ldp + kGradCols - 1) / kGradCols;
+      loss_grad_kernel<<<dim3(rows, (unsigned)cols), kGradThreads, 0, stream>>>(g);
+      note_launches(2);
       if (last_launch_status() != ULY_OK) return ULY_ERR_CUDA;
     }
     // dx = dz W
