@@ -56,7 +56,8 @@ constexpr long long kLandCycles = 1 << 20;                 // after giving up: t
 
 // The product and how it is cut into work.
 struct Shape {
-  int m_tiles, n_tiles, splits;
+  int m_tiles, n_tiles;
+  int full, splits;     // tiles taken whole, and the parts of each other one
   int k_steps;          // ceil(K / 64)
   int group_m;          // tiles in flight form blocks of group_m rows of tiles (operands shared in L2)
   int b_step, b_half;   // B row of tile nt, CTA r: nt * b_step + r * b_half
@@ -147,22 +148,54 @@ struct OutRing {
   }
 };
 
-// Which tile and which part of its k-steps a work unit is.  The units of a
-// tile follow one another; tiles go down group_m rows before the next column.
+// A tile's place; tiles go down group_m rows before the next column.
+__device__ __forceinline__ void place_of(const Shape &s, int tile, int &mt, int &nt) {
+  const int per = s.group_m * s.n_tiles, g = tile / per, in = tile - g * per;
+  const int first = g * s.group_m, rows = min(s.group_m, s.m_tiles - first);
+  nt = in / rows;
+  mt = first + in - nt * rows;
+}
+// Which tile and which of its k-steps a work unit is.  The parts of a cut tile
+// follow one another.
 struct Unit {
-  int mt, nt, split, k0, k1;
+  int mt, nt, part;   // part: index of its partial tile, -1 for a whole tile
+  int k0, k1;
 };
 __device__ __forceinline__ Unit unit_of(const Shape &s, int u) {
   Unit r;
-  const int tile = u / s.splits;
-  r.split = u - tile * s.splits;
-  const int per = s.group_m * s.n_tiles, g = tile / per, in = tile - g * per;
-  const int first = g * s.group_m, rows = min(s.group_m, s.m_tiles - first);
-  r.nt = in / rows;
-  r.mt = first + in - r.nt * rows;
-  r.k0 = (int)((long long)s.k_steps * r.split / s.splits);
-  r.k1 = (int)((long long)s.k_steps * (r.split + 1) / s.splits);
+  const int v = u - s.full;
+  if (v < 0) {
+    place_of(s, u, r.mt, r.nt);
+    r.part = -1;
+    r.k0 = 0;
+    r.k1 = s.k_steps;
+  } else {
+    const int t = v / s.splits, split = v - t * s.splits;
+    place_of(s, s.full + t, r.mt, r.nt);
+    r.part = s.splits > 1 ? v : -1;
+    r.k0 = (int)((long long)s.k_steps * split / s.splits);
+    r.k1 = (int)((long long)s.k_steps * (split + 1) / s.splits);
+  }
   return r;
+}
+__host__ __device__ __forceinline__ int units_of(const Shape &s) {
+  return s.full + (s.m_tiles * s.n_tiles - s.full) * s.splits;
+}
+
+// A partial tile: this warp's 32 rows of 128 accumulator columns, fp32.
+__device__ __forceinline__ void store_partial(const CUtensorMap *map, const Unit &w, uint32_t acc, int row_in_tile,
+                                              int half, OutRing &out) {
+#pragma unroll 1
+  for (int c = half * kHalf; c < (half + 1) * kHalf; c += 32) {
+    uint32_t a[32], v[16];
+    tmem_ld32(acc + c, a);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) v[e] = a[16 * h + e];
+      out.put(map, c + 16 * h, w.part * kTile + row_in_tile, v);
+    }
+  }
 }
 
 // Epi::Params, and
@@ -172,7 +205,7 @@ __device__ __forceinline__ Unit unit_of(const Shape &s, int u) {
 template <class Epi, bool A_MN, bool B_MN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     gemm_pair_sm100_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                           const __grid_constant__ Shape sh, const __grid_constant__ typename Epi::Params ep) {
+                           const __grid_constant__ CUtensorMap tmPart, const __grid_constant__ Shape sh, const __grid_constant__ typename Epi::Params ep) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sb = smem_u32(smem);
@@ -185,7 +218,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const int cluster = blockIdx.x >> 1, clusters = gridDim.x >> 1;
-  const int units = sh.m_tiles * sh.n_tiles * sh.splits;
+  const int units = units_of(sh);
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < B_N; ++i) mbar_init(bar(i), i >= B_ACCE ? 2 * kEpiWarps : 1);
@@ -287,7 +320,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       tc_fence_after();
       const Unit w = unit_of(sh, u);
       const uint32_t acc = tmem + ((uint32_t)(quarter * 32) << 16) + buf * kTile;
-      Epi::tile(ep, w, acc, w.mt * kTile + (int)rank * kHalf + quarter * 32 + lane, half, out);
+      const int row0 = (int)rank * kHalf + quarter * 32;
+      if (w.part >= 0) store_partial(&tmPart, w, acc, row0, half, out);
+      else Epi::tile(ep, w, acc, w.mt * kTile + row0 + lane, half, out);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) arrive_cluster(map_cta(bar(B_ACCE + buf), 0));
@@ -346,32 +381,49 @@ inline bool make_out_map(CUtensorMap *map, const void *base, long long inner, lo
   return make_map_of(map, base, inner, rows, stride, f32 ? 16 : 32, 32, CU_TENSOR_MAP_SWIZZLE_64B, f32);
 }
 
-// Parts to cut each tile's k-steps into.  Work units on `clusters` SM pairs
-// take ceil(units / clusters) turns of ceil(k_steps / splits) k-steps (512
-// cycles of MMA each) plus an epilogue that overlaps the next unit; a cut
-// writes and reads fp32 partials (M x N of them for each part) and launches
-// one more kernel.  Few rows leave most of the machine idle without a cut; a
-// last turn that is almost empty costs a large product up to a turn.
-inline int choose_splits(long long M, long long N, long long m_tiles, long long n_tiles, long long k_steps, int sms) {
-  const double step_us = 512.0 / 1700.0, clusters = sms / 2;
-  int best = 1;
-  double best_t = 1e30;
-  for (int s = 1; s <= 32 && s * 2 <= (k_steps > 1 ? k_steps : 2); ++s) {
-    const double turns = (double)((m_tiles * n_tiles * s + (int)clusters - 1) / (int)clusters);
-    double t = turns * (double)((k_steps + s - 1) / s) * step_us + 2.0;
-    if (s > 1) t += 3.0 + (double)s * M * N * 8.0 / 5e6;
-    if (t < best_t * 0.97) { best_t = t; best = s; }
+// How many tiles are taken whole and the parts of each of the others.  Whole
+// tiles in full turns of the SM pairs; a turn costs k_steps (512 cycles of MMA
+// each), the last one ceil(tiles left * splits / pairs) of k_steps / splits and,
+// if cut, a second kernel over fp32 partial tiles (written and read once) of at
+// most `budget` bytes.  320 tiles of 320 steps on 74 pairs: 4 turns and 24 tiles
+// cut in 3, 4.33 turns instead of 5.
+struct Cut {
+  int full = 0, splits = 1;
+  size_t bytes = 0;   // of the partial tiles
+};
+constexpr size_t kPartTile = (size_t)kTile * kTile * sizeof(float);
+inline Cut choose_cut(long long tiles, long long k_steps, size_t budget = SIZE_MAX) {
+  const double step_us = 512.0 / 1700.0;
+  const long long pairs = device_sm_count() / 2;
+  Cut best;
+  best.full = (int)tiles;
+  const long long full = tiles / pairs * pairs, left = tiles - full;
+  if (left == 0) return best;
+  double best_t = (double)k_steps * step_us;
+  for (int s = 2; s <= 32 && s * 2 <= k_steps; ++s) {
+    const size_t bytes = (size_t)left * s * kPartTile;
+    if (bytes > budget) break;
+    const double t = (double)((left * s + pairs - 1) / pairs) * (double)((k_steps + s - 1) / s) * step_us + 4.0 +
+                     (double)bytes * 2.0 / 5e6;
+    if (t < best_t * 0.98) {
+      best_t = t;
+      best.full = (int)full;
+      best.splits = s;
+      best.bytes = bytes;
+    }
   }
   return best;
 }
+inline long long tiles_of(long long n, int tile = kTile) { return (n + tile - 1) / tile; }
 
 // Work units, raster and rest of a launch.  `n_tile` output columns of one
 // tile column: 256, or 128 where B holds two rows for each of them.
-inline Shape make_shape(long long M, long long N, long long K, int n_tile, int splits) {
+inline Shape make_shape(long long M, long long N, long long K, int n_tile, const Cut &cut) {
   Shape s = {};
-  s.m_tiles = (int)((M + kTile - 1) / kTile);
-  s.n_tiles = (int)((N + n_tile - 1) / n_tile);
-  s.splits = splits;
+  s.m_tiles = (int)tiles_of(M);
+  s.n_tiles = (int)tiles_of(N, n_tile);
+  s.full = cut.full;
+  s.splits = cut.splits;
   s.k_steps = (int)((K + kBK - 1) / kBK);
   s.group_m = 8;
   s.b_step = n_tile;
@@ -381,16 +433,19 @@ inline Shape make_shape(long long M, long long N, long long K, int n_tile, int s
   return s;
 }
 
+// `part`: cut.bytes for the partial tiles of a shape that has any.
 template <class Epi, bool A_MN, bool B_MN>
 uly_status launch(const CUtensorMap &ta, const CUtensorMap &tb, const Shape &s, const typename Epi::Params &ep,
-                  cudaStream_t stream) {
+                  float *part, cudaStream_t stream) {
   static std::atomic<uint64_t> optin{0};
   auto kernel = gemm_pair_sm100_kernel<Epi, A_MN, B_MN>;
   if (!smem_optin(kernel, kSmemBytes, optin)) return ULY_ERR_CUDA;
-  const long long units = (long long)s.m_tiles * s.n_tiles * s.splits;
-  const int pairs = device_sm_count() / 2;
-  const int grid = 2 * (int)(units < pairs ? units : pairs);
-  kernel<<<grid, kThreads, kSmemBytes, stream>>>(ta, tb, s, ep);
+  const int units = units_of(s), pairs = device_sm_count() / 2;
+  const int grid = 2 * (units < pairs ? units : pairs);
+  CUtensorMap tp = ta;
+  if (s.splits > 1 && !make_out_map(&tp, part, kTile, (long long)(units - s.full) * kTile, kTile, true))
+    return ULY_ERR_CUDA;
+  kernel<<<grid, kThreads, kSmemBytes, stream>>>(ta, tb, tp, s, ep);
   note_launches(1);
   return last_launch_status();
 }
@@ -420,21 +475,76 @@ __device__ __forceinline__ void store8(float *p, const float (&x)[8]) {
   reinterpret_cast<float4 *>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
 }
 
+// Sum of the cut tiles' partials, in the order of the parts, and
+// Epi::join8(params, row, col, z, up) of eight columns (up: those 128 further on
+// in a tile whose B holds two rows for each column).
+template <class Epi>
+__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ typename Epi::Params p,
+                                                   const __grid_constant__ Shape s, const float *__restrict__ part,
+                                                   long long M, int N) {
+  constexpr int cols = Epi::kGated ? kHalf : kTile, vecs = cols / 8;
+  const int tiles = s.m_tiles * s.n_tiles - s.full;
+  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < (long long)tiles * kTile * vecs;
+       i += (long long)gridDim.x * 256) {
+    const int c = (int)(i % vecs) * 8, r = (int)(i / vecs % kTile), t = (int)(i / (vecs * kTile));
+    int mt, nt;
+    place_of(s, s.full + t, mt, nt);
+    const long long row = (long long)mt * kTile + r;
+    const int col = nt * cols + c;
+    if (row >= M || col >= N) continue;
+    float z[8] = {}, up[8] = {};
+    const float *src = part + ((long long)t * s.splits * kTile + r) * kTile + c;
+    for (int k = 0; k < s.splits; ++k, src += kTile * kTile) {
+      float v[8];
+      load8(src, v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) z[e] += v[e];
+      if (Epi::kGated) {
+        load8(src + kHalf, v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) up[e] += v[e];
+      }
+    }
+    Epi::join8(p, row, col, z, up);
+  }
+}
+template <class Epi>
+uly_status launch_join(const typename Epi::Params &p, const Shape &s, const float *part, long long M, int N,
+                       cudaStream_t stream) {
+  if (s.splits == 1) return ULY_OK;
+  const long long vecs = (long long)(s.m_tiles * s.n_tiles - s.full) * kTile * (Epi::kGated ? kHalf : kTile) / 8;
+  const long long want = (vecs + 255) / 256, most = (long long)device_sm_count() * 8;
+  join_kernel<Epi><<<(unsigned)(want < most ? want : most), 256, 0, stream>>>(p, s, part, M, N);
+  note_launches(1);
+  return last_launch_status();
+}
+
 // --------------------------------------------------------- plain epilogue
 // out = A B^T + add, in bf16 or fp32; N is a multiple of 8.
 struct PlainParams {
   CUtensorMap out_map;      // of out (launch_plain fills it in)
   void *out;
   const float *add;         // nullable fp32 [M][N] (may be `out` itself, fp32)
-  float *part;              // splits > 1: fp32 [splits][M][N] instead of everything above
   long long M;
   int N, out_f32;
 };
 struct EpiPlain {
   using Params = PlainParams;
+  static constexpr bool kGated = false;
+  static __device__ __forceinline__ void add8(const Params &p, long long row, int col, float (&z)[8]) {
+    float a[8];
+    load8(p.add + row * p.N + col, a);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) z[e] += a[e];
+  }
+  static __device__ __forceinline__ void join8(const Params &p, long long row, int col, float (&z)[8],
+                                               const float (&)[8]) {
+    if (p.add) add8(p, row, col, z);
+    if (p.out_f32) store8(static_cast<float *>(p.out) + row * p.N + col, z);
+    else store8(static_cast<__nv_bfloat16 *>(p.out) + row * p.N + col, z);
+  }
   static __device__ __forceinline__ void tile(const Params &p, const Unit &w, uint32_t acc, int row, int half,
                                               OutRing &out) {
-    const bool ok = row < p.M;
     const int row0 = row - out.lane;
 #pragma unroll 1
     for (int c = 0; c < kHalf; c += 32) {
@@ -442,28 +552,16 @@ struct EpiPlain {
       uint32_t a[32], v[16];
       tmem_ld32(acc + half * kHalf + c, a);
       if (col0 >= p.N || row0 >= p.M) continue;   // the whole warp
-      if (p.part) {
-        if (ok) {
-#pragma unroll
-          for (int g = 0; g < 4; ++g)
-            if (col0 + 8 * g < p.N) {
-              float z[8];
-#pragma unroll
-              for (int e = 0; e < 8; ++e) z[e] = __uint_as_float(a[8 * g + e]);
-              store8(p.part + ((long long)w.split * p.M + row) * p.N + col0 + 8 * g, z);
-            }
-        }
-        __syncwarp();
-        continue;
-      }
-      if (p.add && ok) {
+      if (p.add && row < p.M) {
 #pragma unroll
         for (int g = 0; g < 4; ++g)
           if (col0 + 8 * g < p.N) {
             float z[8];
-            load8(p.add + (long long)row * p.N + col0 + 8 * g, z);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) a[8 * g + e] = __float_as_uint(__uint_as_float(a[8 * g + e]) + z[e]);
+            for (int e = 0; e < 8; ++e) z[e] = __uint_as_float(a[8 * g + e]);
+            add8(p, row, col0 + 8 * g, z);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) a[8 * g + e] = __float_as_uint(z[e]);
           }
       }
       __syncwarp();
@@ -483,56 +581,20 @@ struct EpiPlain {
   }
 };
 
-// Sum of a cut product's partials, in the order of the parts, and its epilogue.
-static __global__ void __launch_bounds__(256) plain_join_kernel(const __grid_constant__ PlainParams p, int splits) {
-  const int vecs = p.N / 8;
-  const long long total = p.M * vecs;
-  for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < total;
-       i += (long long)gridDim.x * blockDim.x) {
-    const long long row = i / vecs;
-    const int col = (int)(i - row * vecs) * 8;
-    float z[8] = {};
-    for (int s = 0; s < splits; ++s) {
-      float v[8];
-      load8(p.part + ((long long)s * p.M + row) * p.N + col, v);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) z[e] += v[e];
-    }
-    if (p.add) {
-      float v[8];
-      load8(p.add + row * p.N + col, v);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) z[e] += v[e];
-    }
-    if (p.out_f32) store8(static_cast<float *>(p.out) + row * p.N + col, z);
-    else store8(static_cast<__nv_bfloat16 *>(p.out) + row * p.N + col, z);
-  }
-}
-
-inline unsigned join_blocks(long long vecs) {
-  long long b = (vecs + 255) / 256;
-  const long long most = (long long)device_sm_count() * 8;
-  return (unsigned)(b < most ? (b < 1 ? 1 : b) : most);
-}
-
-inline size_t part_bytes(long long M, long long N, int splits) {
-  return splits > 1 ? (size_t)splits * M * N * sizeof(float) : 0;
-}
-
-// out[M][N] (+)= A B^T with a plain epilogue; `part` holds part_bytes().
+// out[M][N] (+)= A B^T with a plain epilogue; `part` has room for part_bytes.
 template <bool A_MN, bool B_MN>
-uly_status launch_plain(const CUtensorMap &ta, const CUtensorMap &tb, PlainParams p, long long K, int splits,
-                        float *part, int kernel_id, cudaStream_t stream) {
-  const long long k_steps = (K + kBK - 1) / kBK;
-  if (splits > k_steps) splits = (int)k_steps;   // a short last piece: no part without a k-step
-  p.part = splits > 1 ? part : nullptr;
-  if (!p.part && !make_out_map(&p.out_map, p.out, p.N, p.M, p.N, p.out_f32 != 0)) return ULY_ERR_CUDA;
+uly_status launch_plain(const CUtensorMap &ta, const CUtensorMap &tb, PlainParams p, long long K, float *part,
+                        size_t part_bytes, int kernel_id, cudaStream_t stream) {
+  if (!make_out_map(&p.out_map, p.out, p.N, p.M, p.N, p.out_f32 != 0)) return ULY_ERR_CUDA;
+  const Cut cut = choose_cut(tiles_of(p.M) * tiles_of(p.N), (K + kBK - 1) / kBK, part_bytes);
+  const Shape s = make_shape(p.M, p.N, K, kTile, cut);
   prof::Scope scope(kernel_id, stream);
-  const uly_status st = launch<EpiPlain, A_MN, B_MN>(ta, tb, make_shape(p.M, p.N, K, kTile, splits), p, stream);
-  if (st != ULY_OK || splits == 1) return st;
-  plain_join_kernel<<<join_blocks(p.M * (p.N / 8)), 256, 0, stream>>>(p, splits);
-  note_launches(1);
-  return last_launch_status();
+  const uly_status st = launch<EpiPlain, A_MN, B_MN>(ta, tb, s, p, part, stream);
+  return st != ULY_OK ? st : launch_join<EpiPlain>(p, s, part, p.M, p.N, stream);
+}
+// Bytes of partial tiles for [M][N] of K.
+inline size_t plain_part_bytes(long long M, long long N, long long K) {
+  return choose_cut(tiles_of(M) * tiles_of(N), (K + kBK - 1) / kBK).bytes;
 }
 
 }  // namespace gemm

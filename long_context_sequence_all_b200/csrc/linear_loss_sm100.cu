@@ -353,9 +353,10 @@ long long piece_of(long long tokens, long long row_bytes, long long budget) {
 
 struct Plan {
   long long piece, rows_pad, ldp;
-  int slots, dx_splits, dw_splits;
+  int slots;
   bool dw_acc;   // dW of several pieces is summed in an fp32 array of the workspace
   size_t psum, pcnt, count, row_loss, row_lse, target, pairs, factor, p, xk, part, acc, bytes;   // offsets, total
+  size_t part_bytes;
 };
 
 Plan make_plan(int P, long long T, int D, int V, bool grad, int dw_dtype, long long piece_tokens) {
@@ -375,17 +376,14 @@ Plan make_plan(int P, long long T, int D, int V, bool grad, int dw_dtype, long l
   q.target = take((size_t)q.piece * sizeof(float));
   q.pairs = take((size_t)q.slots * q.rows_pad * sizeof(float2));
   if (grad) {
-    const int sms = device_sm_count();
-    auto tiles = [](long long v) { return (v + kTile - 1) / kTile; };
-    q.dx_splits = choose_splits(q.piece, D, tiles(q.piece), tiles(D), (V + kBK - 1) / kBK, sms);
-    q.dw_splits = choose_splits(V, D, tiles(V), tiles(D), (q.piece + kBK - 1) / kBK, sms);
     q.dw_acc = q.piece < T && dw_dtype == ULY_BF16;
     q.row_lse = take((size_t)q.piece * sizeof(float));
     q.factor = take((size_t)q.piece * q.slots * sizeof(float));
     q.p = take((size_t)q.piece * q.ldp * 2);
     q.xk = take((size_t)q.piece * D * 2);
-    const size_t a = part_bytes(q.piece, D, q.dx_splits), b = part_bytes(V, D, q.dw_splits);
-    q.part = take(a > b ? a : b);
+    const size_t a = plain_part_bytes(q.piece, D, V), b = plain_part_bytes(V, D, q.piece);
+    q.part_bytes = a > b ? a : b;
+    q.part = take(q.part_bytes);
     q.acc = take(q.dw_acc ? (size_t)V * D * sizeof(float) : 0);
   }
   q.bytes = at;
@@ -394,6 +392,13 @@ Plan make_plan(int P, long long T, int D, int V, bool grad, int dw_dtype, long l
 
 template <typename T>
 T *at(void *ws, size_t off) { return reinterpret_cast<T *>(static_cast<char *>(ws) + off); }
+
+// No tile of the logits is cut: its epilogue needs the whole sums.
+Cut whole(long long rows, long long V) {
+  Cut c;
+  c.full = (int)(tiles_of(rows) * tiles_of(V));
+  return c;
+}
 
 // The pairs, targets and (grad) exponentials of a piece's rows.
 template <bool GRAD>
@@ -409,7 +414,7 @@ uly_status logits_pass(const __nv_bfloat16 *x, const void *w, int D, LossParams 
   if (!make_map(&tw, w, D, V, D, kHalf) || !make_map(&tx, x, D, rows, D, kHalf) ||
       (GRAD && !make_out_map(&p.p_map, pp, V, rows, ldp)))
     return ULY_ERR_CUDA;
-  return launch<EpiLoss<GRAD>, false, false>(tx, tw, make_shape(rows, V, D, kTile, 1), p, stream);
+  return launch<EpiLoss<GRAD>, false, false>(tx, tw, make_shape(rows, V, D, kTile, whole(rows, V)), p, nullptr, stream);
 }
 
 RowsParams rows_of(const Plan &q, const LossParams &p, void *ws, long long t0) {
@@ -519,7 +524,7 @@ uly_status linear_loss_bwd_launch(int32_t P, int64_t tokens, int32_t D, int32_t 
     float *part = at<float>(ws, q.part);
     st = rows <= skinny::kMaxTokens
              ? skinny::launch_plain_mn(pp, q.ldp, w, o.out, rows, D, V, prof::K_LINEAR_LOSS_DX, stream)
-             : launch_plain<false, true>(tz, tw_mn, o, V, q.dx_splits, part, prof::K_LINEAR_LOSS_DX, stream);
+             : launch_plain<false, true>(tz, tw_mn, o, V, part, q.part_bytes, prof::K_LINEAR_LOSS_DX, stream);
     if (st != ULY_OK) return st;
     // dW (+)= dz^T x; the last piece writes the caller's type
     const bool last = t0 + rows >= tokens;
@@ -529,7 +534,7 @@ uly_status linear_loss_bwd_launch(int32_t P, int64_t tokens, int32_t D, int32_t 
     o.add = t0 > 0 ? acc : nullptr;
     o.out = last ? dw : acc;
     o.out_f32 = !last || dw_dtype == ULY_F32;
-    st = launch_plain<true, true>(tz_mn, tk_mn, o, rows, q.dw_splits, part, prof::K_LINEAR_LOSS_DW, stream);
+    st = launch_plain<true, true>(tz_mn, tk_mn, o, rows, part, q.part_bytes, prof::K_LINEAR_LOSS_DW, stream);
     if (st != ULY_OK) return st;
   }
   return finish(q, P, tokens, V, labels, ignore_index, shard_sum, shard_count, loss, ws, stream);

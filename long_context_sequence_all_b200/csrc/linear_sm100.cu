@@ -58,7 +58,6 @@ struct LinearParams {
   CUtensorMap y_map, pre_map, up_map;     // y, and the parts of pre (up: swiglu)
   const __nv_bfloat16 *bias, *residual;   // nullable
   __nv_bfloat16 *y, *pre;                 // pre nullable: z [M][NZ]
-  float *part;                            // splits > 1: fp32 [splits][M][NZ] instead
   long long M;
   int N, NZ;                              // output features, rows of W
 };
@@ -94,6 +93,17 @@ struct EpiLinear {
     }
   }
 
+  static __device__ __forceinline__ void join8(const Params &p, long long row, int col, float (&z)[8],
+                                               float (&up)[8]) {
+    add_bias(p, col, z, up);
+    if (p.pre) {
+      store8(p.pre + row * p.NZ + col, z);
+      if (kGated) store8(p.pre + row * p.NZ + p.N + col, up);
+    }
+    finish(p, row, col, z, up, true);
+    store8(p.y + row * p.N + col, z);
+  }
+
   static __device__ __forceinline__ void tile(const Params &p, const Unit &w, uint32_t acc, int row, int half,
                                               OutRing &out) {
     const bool ok = row < p.M;
@@ -115,14 +125,6 @@ struct EpiLinear {
           z[e] = __uint_as_float(a[8 * g + e]);
           up[e] = kGated ? __uint_as_float(a[(kGated ? 32 : 0) + 8 * g + e]) : 0.f;
         }
-        if (p.part) {
-          if (ok && col < p.N) {
-            float *o = p.part + ((long long)w.split * p.M + row) * p.NZ + col;
-            store8(o, z);
-            if (kGated) store8(o + p.N, up);
-          }
-          continue;
-        }
         if (col < p.N) add_bias(p, col, z, up);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -134,7 +136,6 @@ struct EpiLinear {
         for (int e = 0; e < 4; ++e) vy[4 * g + e] = pack_bf16x2(z[2 * e], z[2 * e + 1]);
       }
       __syncwarp();
-      if (p.part) continue;
       out.put(&p.y_map, col0, row0, vy);
       if (p.pre) {
         out.put(&p.pre_map, col0, row0, vz);
@@ -143,37 +144,6 @@ struct EpiLinear {
     }
   }
 };
-
-template <int ACT>
-__global__ void __launch_bounds__(256) linear_join_kernel(const __grid_constant__ LinearParams p, int splits) {
-  const int vecs = p.N / 8;
-  const long long total = p.M * vecs;
-  for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < total;
-       i += (long long)gridDim.x * blockDim.x) {
-    const long long row = i / vecs;
-    const int col = (int)(i - row * vecs) * 8;
-    float z[8] = {}, up[8] = {};
-    for (int s = 0; s < splits; ++s) {
-      const float *o = p.part + ((long long)s * p.M + row) * p.NZ + col;
-      float v[8];
-      load8(o, v);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) z[e] += v[e];
-      if (EpiLinear<ACT>::kGated) {
-        load8(o + p.N, v);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) up[e] += v[e];
-      }
-    }
-    EpiLinear<ACT>::add_bias(p, col, z, up);
-    if (p.pre) {
-      store8(p.pre + row * p.NZ + col, z);
-      if (EpiLinear<ACT>::kGated) store8(p.pre + row * p.NZ + p.N + col, up);
-    }
-    EpiLinear<ACT>::finish(p, row, col, z, up, true);
-    store8(p.y + row * p.N + col, z);
-  }
-}
 
 // Few tokens: this CTA's slice of a tile's features, four of a token a thread.
 template <int ACT>
@@ -225,29 +195,24 @@ uly_status run_skinny(const void *x, const void *w, const LinearParams &p, int K
                                                   cols == 64 ? p.N : 64, p, stream);
 }
 
-template <int ACT>
-uly_status run_linear(const CUtensorMap &ta, const CUtensorMap &tb, LinearParams p, int K, int splits, float *part,
-                      cudaStream_t stream) {
-  p.part = splits > 1 ? part : nullptr;
-  if (!p.part && (!make_out_map(&p.y_map, p.y, p.N, p.M, p.N) ||
-                  (p.pre && !make_out_map(&p.pre_map, p.pre, p.N, p.M, p.NZ)) ||
-                  (p.pre && p.NZ > p.N && !make_out_map(&p.up_map, p.pre + p.N, p.N, p.M, p.NZ))))
-    return ULY_ERR_CUDA;
-  prof::Scope scope(prof::K_LINEAR, stream);
-  const Shape s = make_shape(p.M, p.N, K, EpiLinear<ACT>::kCols * 2, splits);
-  const uly_status st = launch<EpiLinear<ACT>, false, false>(ta, tb, s, p, stream);
-  if (st != ULY_OK || splits == 1) return st;
-  linear_join_kernel<ACT><<<join_blocks(p.M * (p.N / 8)), 256, 0, stream>>>(p, splits);
-  note_launches(1);
-  return last_launch_status();
-}
-
 int gated(int act) { return act == ULY_ACT_SWIGLU ? 2 : 1; }
 
-int linear_splits(int64_t tokens, int32_t in, int32_t out, int32_t act) {
-  const int tile = kTile / gated(act);
-  return choose_splits(tokens, (long long)out * gated(act), (tokens + kTile - 1) / kTile, (out + tile - 1) / tile,
-                       (in + kBK - 1) / kBK, device_sm_count());
+Cut linear_cut(int64_t tokens, int32_t in, int32_t out, int32_t act) {
+  return choose_cut(tiles_of(tokens) * tiles_of(out, kTile / gated(act)), (in + kBK - 1) / kBK);
+}
+
+template <int ACT>
+uly_status run_linear(const void *x, const void *w, LinearParams p, int K, float *part, cudaStream_t stream) {
+  CUtensorMap ta, tb;
+  if (!make_map(&ta, x, K, p.M, K, kHalf) || !make_map(&tb, w, K, p.NZ, K, kHalf) ||
+      !make_out_map(&p.y_map, p.y, p.N, p.M, p.N) || (p.pre && !make_out_map(&p.pre_map, p.pre, p.N, p.M, p.NZ)) ||
+      (p.pre && p.NZ > p.N && !make_out_map(&p.up_map, p.pre + p.N, p.N, p.M, p.NZ)))
+    return ULY_ERR_CUDA;
+  using Epi = EpiLinear<ACT>;
+  const Shape s = make_shape(p.M, p.N, K, Epi::kCols * 2, linear_cut(p.M, K, p.N, ACT));
+  prof::Scope scope(prof::K_LINEAR, stream);
+  const uly_status st = launch<Epi, false, false>(ta, tb, s, p, part, stream);
+  return st != ULY_OK ? st : launch_join<Epi>(p, s, part, p.M, p.N, stream);
 }
 
 // ------------------------------------------------------------ dz and dbias
@@ -319,23 +284,19 @@ int dz_row_ctas(int64_t tokens, int32_t out) {
 // Workspace of the backward: dz, the bias gradient's partials, a cut product's
 // partials (the two products run one after the other and share them).
 struct BwdPlan {
-  int nz, dx_splits, dw_splits, row_ctas;
-  size_t off_bias, off_part, bytes;
+  int nz, row_ctas;
+  size_t off_bias, off_part, part, bytes;
 };
 size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
 BwdPlan bwd_plan(int64_t tokens, int32_t in, int32_t out, int32_t act) {
   BwdPlan q;
   q.nz = out * gated(act);
-  const int sms = device_sm_count();
-  auto tiles = [](long long v) { return (v + kTile - 1) / kTile; };
-  q.dx_splits = choose_splits(tokens, in, tiles(tokens), tiles(in), (q.nz + kBK - 1) / kBK, sms);
-  q.dw_splits = choose_splits(q.nz, in, tiles(q.nz), tiles(in), (tokens + kBK - 1) / kBK, sms);
   q.row_ctas = dz_row_ctas(tokens, out);
   q.off_bias = act == ULY_ACT_NONE ? 0 : up256((size_t)tokens * q.nz * 2);
   q.off_part = q.off_bias + up256((size_t)q.row_ctas * 8 * q.nz * sizeof(float));
-  if (tokens <= skinny::kMaxTokens) q.dx_splits = 1;
-  const size_t a = part_bytes(tokens, in, q.dx_splits), b = part_bytes(q.nz, in, q.dw_splits);
-  q.bytes = q.off_part + up256(a > b ? a : b);
+  const size_t a = plain_part_bytes(tokens, in, q.nz), b = plain_part_bytes(q.nz, in, tokens);
+  q.part = a > b ? a : b;
+  q.bytes = q.off_part + up256(q.part);
   return q;
 }
 
@@ -347,16 +308,14 @@ bool few_tokens(int64_t tokens) { return tokens <= skinny::kMaxTokens; }
 template <int ACT>
 uly_status linear_of(const void *x, const void *w, const LinearParams &p, int K, void *workspace, cudaStream_t stream) {
   if (few_tokens(p.M)) return run_skinny<ACT>(x, w, p, K, stream);
-  CUtensorMap ta, tb;
-  if (!make_map(&ta, x, K, p.M, K, kHalf) || !make_map(&tb, w, K, p.NZ, K, kHalf)) return ULY_ERR_CUDA;
-  return run_linear<ACT>(ta, tb, p, K, linear_splits(p.M, K, p.N, ACT), static_cast<float *>(workspace), stream);
+  return run_linear<ACT>(x, w, p, K, static_cast<float *>(workspace), stream);
 }
 
 }  // namespace
 
 size_t linear_workspace_bytes(int64_t tokens, int32_t in, int32_t out, int32_t act) {
   if (few_tokens(tokens)) return 0;
-  return part_bytes(tokens, (long long)out * gated(act), linear_splits(tokens, in, out, act));
+  return linear_cut(tokens, in, out, act).bytes;
 }
 
 uly_status linear_launch(int64_t tokens, int32_t in, int32_t out, int32_t act, const void *x, const void *w,
@@ -419,14 +378,14 @@ uly_status linear_bwd_launch(int64_t tokens, int32_t in, int32_t out, int32_t ac
     if (!make_map(&ta, dz, q.nz, tokens, q.nz, kHalf) || !make_map(&tb, w, in, q.nz, in, 64)) return ULY_ERR_CUDA;
     PlainParams p = {};
     p.out = dx; p.M = tokens; p.N = in;
-    const uly_status st = launch_plain<false, true>(ta, tb, p, q.nz, q.dx_splits, part, prof::K_LINEAR_DX, stream);
+    const uly_status st = launch_plain<false, true>(ta, tb, p, q.nz, part, q.part, prof::K_LINEAR_DX, stream);
     if (st != ULY_OK) return st;
   }
   if (dw) {   // dW[nz][in] = dz^T x
     if (!make_map(&ta, dz, q.nz, tokens, q.nz, 64) || !make_map(&tb, x, in, tokens, in, 64)) return ULY_ERR_CUDA;
     PlainParams p = {};
     p.out = dw; p.out_f32 = dw_dtype == ULY_F32; p.M = q.nz; p.N = in;
-    return launch_plain<true, true>(ta, tb, p, tokens, q.dw_splits, part, prof::K_LINEAR_DW, stream);
+    return launch_plain<true, true>(ta, tb, p, tokens, part, q.part, prof::K_LINEAR_DW, stream);
   }
   return ULY_OK;
 }

@@ -77,6 +77,11 @@ LINEAR = [  # tokens, K, N, act, bias, residual
     (257, 1032, 520, "swiglu", True, True),      # a second row tile of one row; the gate's last tile ends inside
     (1000, 256, 2048, "gelu", True, True),
     (4100, 640, 2560, "none", False, True),      # many tiles, each SM pair several
+    (2300, 8192, 2304, "silu", True, True),      # 81 tiles: a turn of 74 and the other 7 cut along K
+    (600, 4096, 3320, "swiglu", True, True),     # the same, gated, with a ragged tile among the cut ones
+    (128, 1032, 520, "gelu", True, True),        # the most tokens of the kernel for few, and one more
+    (129, 1032, 520, "gelu", True, True),
+    (33, 4096, 136, "swiglu", False, True),      # a tile's k-steps shared by a cluster
 ]
 
 
