@@ -270,10 +270,12 @@ def test_linear_validation(L):
                      (2, dict(T=(1 << 31) - 8192, N=1 << 20))):
         _no_launch(L, f, want, *args(**kw))
     assert f(*args(T=0, x=None, y=None)) == 0                   # no tokens: nothing to do
-    assert size(1, 2560, 1024, 0, ctypes.byref(n)) == 0 and n.value > 0     # cut along K
-    _no_launch(L, f, 10, *args(T=1, K=2560, N=1024, ws=None))
-    _no_launch(L, f, 10, *args(T=1, K=2560, N=1024, wsb=n.value - 1))
-    _no_launch(L, f, 5, *args(T=1, K=2560, N=1024, ws=x))
+    assert size(1, 2560, 1024, 0, ctypes.byref(n)) == 0 and n.value == 0    # few tokens need none
+    cut = dict(T=2300, K=8192, N=2304)                          # 81 tiles: 7 of them cut along K
+    assert size(2300, 8192, 2304, 0, ctypes.byref(n)) == 0 and n.value > 0
+    _no_launch(L, f, 10, *args(**cut, ws=None))
+    _no_launch(L, f, 10, *args(**cut, wsb=n.value - 1))
+    _no_launch(L, f, 5, *args(**cut, ws=x))
     assert size(1, 2560, 1024, 0, None) == 1 and size(1, 2561, 1024, 0, ctypes.byref(n)) == 4
     g = L.ulysses_linear_bwd
     dy, dx, dw, db = r, y, pre, vp(1 << 40)
