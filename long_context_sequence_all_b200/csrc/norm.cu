@@ -21,11 +21,13 @@
 // Each group writes one partial per column and run, and a second kernel folds
 // the partials in a fixed order, so every output is bitwise repeatable.
 //
-// How: persistent groups of threads, one row at a time.  A group's rows arrive
-// by bulk copies in a ring of shared-memory stages, so the loads run ahead of
-// the two row sums (each a barrier of the group).  A thread takes up to five
-// 16-byte vectors of a row (backward: two, its column sums take the registers),
-// so few warps share a row: at 2560 bf16 columns two warps (backward: five)
+// How: persistent teams, a warp or a CTA.  A team's rows arrive by bulk copies
+// in a ring of shared-memory stages, so the loads run ahead of the two row sums
+// (each a barrier of the team).  A thread takes up to five 16-byte vectors of a
+// row (backward: two, its column sums take the registers).  Short rows share a
+// warp, a power of two of lanes each, and arrive several at a time (253074 x 160
+// with one row a warp: 142 us, 71 us so); of long ones few warps share a
+// row: at 2560 bf16 columns two warps (backward: five)
 // instead of ten, which had left both directions waiting for barriers and
 // shuffles at 3.2 and 2.6 TB/s.  Arithmetic runs on pairs of fp32 values.
 // 65536 x 2560 bf16 with a channel gate: forward 235 us (5.7 TB/s of its 1.34
@@ -115,19 +117,25 @@ struct Vec<float> {
 
 constexpr int kMaxGroup = 512;                 // threads of one row
 constexpr int kMaxVecs = 2048;                 // vectors of one row (32 KB)
-constexpr int kWarpRows = 4;                   // groups of a CTA where a group is one warp
+constexpr int kWarpTeams = 4;                  // teams of a CTA where a team is one warp
 constexpr int kMaxStages = 4;
 constexpr uint32_t kRingBytes = 200 * 1024;    // shared memory the stages of an SM's CTAs may take
 
-// Sums of K values over a group: a warp, or the whole CTA (then also a barrier
-// of it; two buffers taken in turn, so one barrier a call is enough).
+// Sums of K values over a row's threads: `g` lanes of a warp (a power of two),
+// or the whole CTA (then also a barrier of it; two buffers taken in turn, so one
+// barrier a call is enough).
 template <int K, bool WARP>
-__device__ __forceinline__ void group_sum(float (&v)[K], float (*sh)[K], int &turn) {
+__device__ __forceinline__ void row_sum(float (&v)[K], int g, float (*sh)[K], int &turn) {
+  if (WARP) {
+    for (int off = g >> 1; off > 0; off >>= 1)
+#pragma unroll
+      for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], off);
+    return;
+  }
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1)
 #pragma unroll
     for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], off);
-  if (WARP) return;
   const int warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   float (*buf)[K] = sh + (kMaxGroup / 32) * turn;
   turn ^= 1;
@@ -143,7 +151,7 @@ __device__ __forceinline__ void group_sum(float (&v)[K], float (*sh)[K], int &tu
 }
 
 template <bool WARP>
-__device__ __forceinline__ void group_barrier() {
+__device__ __forceinline__ void team_barrier() {
   if (WARP) __syncwarp();
   else __syncthreads();
 }
@@ -158,60 +166,84 @@ struct RingSrc {
   }
 };
 
-// A group's ring of stages.
+struct RingShape {
+  int slots, stages;   // tensors of a stage, stages of a team
+  int lanes;           // of a row where a team is a warp
+  int *err;
+};
+
+// A team's ring of stages, each of `rows` rows of every tensor, and this
+// thread's place in it: thread `l` of `lanes` of row `sub` of a stage.
+template <bool WARP>
 struct Ring {
   uint8_t *base;
   uint64_t *bars;
-  uint32_t row_bytes, stage_bytes;
-  int stages, at;        // at: the stage the next row is taken from
+  uint32_t row_bytes, slot_bytes, stage_bytes;
+  int stages, at;        // at: the stage the next rows are taken from
   uint32_t phase;
-  // One thread: row `t` of every tensor into stage `st`.
-  __device__ __forceinline__ void issue(const RingSrc &src, long long t, int st) const {
+  int l, lanes, sub, rows;
+
+  __device__ __forceinline__ Ring(uint8_t *mem, uint64_t *barriers, volatile int *abort, int vecs, const RingShape &s) {
+    const int team = WARP ? threadIdx.x >> 5 : 0, lane = threadIdx.x & 31;
+    lanes = WARP ? s.lanes : blockDim.x;
+    rows = WARP ? 32 / s.lanes : 1;
+    l = WARP ? lane & (s.lanes - 1) : threadIdx.x;
+    sub = WARP ? lane / s.lanes : 0;
+    row_bytes = (uint32_t)vecs * 16;
+    slot_bytes = row_bytes * rows;
+    stage_bytes = slot_bytes * s.slots;
+    stages = s.stages;
+    base = mem + (size_t)team * stages * stage_bytes;
+    bars = barriers + team * kMaxStages;
+    at = 0;
+    phase = 0;
+    if (l == 0 && sub == 0)
+      for (int i = 0; i < stages; ++i) sm100::mbar_init(sm100::smem_u32(&bars[i]), 1);
+    if (threadIdx.x == 0) *abort = 0;
+    sm100::fence_mbar_init();
+    __syncthreads();
+  }
+  __device__ __forceinline__ uint32_t slot(int st, int k) const {
+    return sm100::smem_u32(base + st * stage_bytes + k * slot_bytes);
+  }
+  // The team: `n` rows of every tensor from token `t` on, into stage `st`.
+  __device__ __forceinline__ void issue(const RingSrc &src, long long t, int n, int st) const {
+    if (l != 0 || sub != 0) return;
     const uint32_t bar = sm100::smem_u32(&bars[st]);
-    sm100::mbar_arrive_expect_tx(bar, src.n * row_bytes);
+    sm100::mbar_arrive_expect_tx(bar, src.n * n * row_bytes);
     for (int k = 0; k < src.n; ++k)
-      sm100::bulk_load(sm100::smem_u32(base + st * stage_bytes + k * row_bytes),
-                       static_cast<const uint8_t *>(src.p[k]) + t * row_bytes, row_bytes, bar);
+      sm100::bulk_load(slot(st, k), static_cast<const uint8_t *>(src.p[k]) + t * row_bytes, n * row_bytes, bar);
+  }
+  // The same for rows that do not follow one another: `t` is this thread's row.
+  __device__ __forceinline__ void issue_each(const RingSrc &src, long long t, int n, int st) const {
+    const uint32_t bar = sm100::smem_u32(&bars[st]);
+    if (l == 0 && sub == 0) sm100::mbar_arrive_expect_tx(bar, src.n * n * row_bytes);
+    if (WARP) __syncwarp();
+    if (l == 0 && sub < n)
+      for (int k = 0; k < src.n; ++k)
+        sm100::bulk_load(slot(st, k) + sub * row_bytes, static_cast<const uint8_t *>(src.p[k]) + t * row_bytes, row_bytes,
+                         bar);
   }
   __device__ __forceinline__ void wait(volatile int *abort, int *err) const {
-    // giving up raises the error; the row is then computed from what is there
+    // giving up raises the error; the rows are then computed from what is there
     sm100::mbar_wait(sm100::smem_u32(&bars[at]), phase, abort, err);
   }
-  __device__ __forceinline__ const uint4 *row(int slot) const {
-    return reinterpret_cast<const uint4 *>(base + at * stage_bytes + slot * row_bytes);
+  // this thread's first vector of its row of tensor `k`
+  __device__ __forceinline__ const uint4 *row(int k) const {
+    return reinterpret_cast<const uint4 *>(base + at * stage_bytes + k * slot_bytes + sub * row_bytes) + l;
   }
   __device__ __forceinline__ void next() {
     if (++at == stages) { at = 0; phase ^= 1; }
   }
+  // After a wait that gave up the copies may still be in flight: let them land
+  // before the CTA's shared memory is given away.
+  __device__ __forceinline__ void end(volatile int *abort) const {
+    __syncthreads();
+    if (!*abort) return;
+    const long long t0 = clock64();
+    while (clock64() - t0 < (1 << 20)) __nanosleep(1000);
+  }
 };
-
-struct RingShape {
-  int slots, stages;   // tensors of a stage, stages of a group
-  int *err;
-};
-
-template <bool WARP>
-__device__ __forceinline__ Ring ring_setup(uint8_t *base, uint64_t *bars, volatile int *abort, int vecs,
-                                           const RingShape &s) {
-  const int grp = WARP ? threadIdx.x >> 5 : 0;
-  const uint32_t rb = (uint32_t)vecs * 16;
-  Ring r{base + (size_t)grp * s.stages * s.slots * rb, bars + grp * kMaxStages, rb, rb * s.slots, s.stages, 0, 0};
-  if ((WARP ? threadIdx.x & 31 : threadIdx.x) == 0)
-    for (int i = 0; i < s.stages; ++i) sm100::mbar_init(sm100::smem_u32(&r.bars[i]), 1);
-  if (threadIdx.x == 0) *abort = 0;
-  sm100::fence_mbar_init();
-  __syncthreads();
-  return r;
-}
-
-// After a wait that gave up the copies may still be in flight: let them land
-// before the CTA's shared memory is given away.
-__device__ __forceinline__ void ring_end(volatile int *abort) {
-  __syncthreads();
-  if (!*abort) return;
-  const long long t0 = clock64();
-  while (clock64() - t0 < (1 << 20)) __nanosleep(1000);
-}
 
 struct NormParams {
   RingSrc src;
@@ -223,39 +255,42 @@ struct NormParams {
   float res_scale, eps, inv_d;
 };
 
-// One row a group; thread `l` of its `tpr` takes vectors l, l + tpr, ...: NV of
-// them, of which only the last can lie behind the row's end.
+// Thread `l` of a row's `tpr` takes its vectors l, l + tpr, ...: NV of them, of
+// which only the last can lie behind the row's end.
 template <typename T, int NV, bool WARP>
 __global__ void __launch_bounds__(kMaxGroup) residual_norm_kernel(const __grid_constant__ NormParams p) {
   constexpr int E = Vec<T>::N;
   extern __shared__ __align__(128) uint8_t stage_mem[];
-  __shared__ uint64_t bars[kWarpRows * kMaxStages];
+  __shared__ uint64_t bars[kWarpTeams * kMaxStages];
   __shared__ int abort_flag;
   __shared__ float sh[2 * (kMaxGroup / 32)][1];
   int turn = 0;
-  Ring ring = ring_setup<WARP>(stage_mem, bars, &abort_flag, p.vecs, p.ring);
-  const int l = WARP ? threadIdx.x & 31 : threadIdx.x, tpr = WARP ? 32 : blockDim.x;
-  const int first = WARP ? blockIdx.x * kWarpRows + (threadIdx.x >> 5) : blockIdx.x;
-  const int step = WARP ? gridDim.x * kWarpRows : gridDim.x, rows = p.rows;
+  Ring<WARP> ring(stage_mem, bars, &abort_flag, p.vecs, p.ring);
+  const int l = ring.l, tpr = ring.lanes, rows = p.rows;
+  const long long first = (WARP ? (long long)blockIdx.x * kWarpTeams + (threadIdx.x >> 5) : blockIdx.x) * ring.rows;
+  const long long step = (WARP ? (long long)gridDim.x * kWarpTeams : gridDim.x) * ring.rows;
   const bool tail = l + (NV - 1) * tpr < p.vecs;   // this thread's last vector exists
   const bool branch = p.sh >= 0, post = p.w_post != nullptr, gated = p.gate_mode != ULY_GATE_NONE;
   const uint4 zero = make_uint4(0, 0, 0, 0);
-  if (l == 0)
-    for (int k = 0; k < ring.stages; ++k)
-      if (first + (long long)k * step < rows) ring.issue(p.src, first + k * step, k);
-  int done = -1;   // stage whose row every thread has finished with, after the group's next barrier
-  for (long long t = first; t < rows; t += step, ring.next()) {
+  auto issue = [&](long long t, int st) {
+    if (t < rows) ring.issue(p.src, t, (int)min((long long)ring.rows, rows - t), st);
+  };
+  for (int k = 0; k < ring.stages; ++k) issue(first + k * step, k);
+  int done = -1;   // stage whose rows every thread has finished with, after the team's next barrier
+  for (long long t0 = first; t0 < rows; t0 += step, ring.next()) {
     if (ring.stages == 1 && done >= 0) {   // no stage to run ahead into
-      group_barrier<WARP>();
-      if (l == 0) ring.issue(p.src, t, 0);
+      team_barrier<WARP>();
+      issue(t0, 0);
     }
     ring.wait(&abort_flag, p.ring.err);
-    const uint4 *gv = p.gate;
+    const long long t = t0 + ring.sub;
+    const bool row_ok = !WARP || t < rows;
+    const uint4 *gv = p.gate + l;
     if (p.gate_mode == ULY_GATE_TOKEN) gv = ring.row(p.sg);
     else if (p.gate_mode == ULY_GATE_SEQUENCE) gv += (long long)((int)t / p.s % p.B) * p.vecs;
     F2 r[NV][E], q = f2(0.f);
     if (branch) {
-      const uint4 *hv = ring.row(p.sh) + l;
+      const uint4 *hv = ring.row(p.sh);
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         Vec<T>::unpack(i < NV - 1 || tail ? hv[i * tpr] : zero, r[i]);
@@ -264,12 +299,11 @@ __global__ void __launch_bounds__(kMaxGroup) residual_norm_kernel(const __grid_c
       }
     }
     float ss[1] = {sum2(q)};
-    if (post || !WARP) group_sum<1, WARP>(ss, sh, turn);   // the barrier also frees the previous row's stage
+    if (post || !WARP) row_sum<1, WARP>(ss, tpr, sh, turn);   // a CTA's barrier also frees the previous stage
     if (WARP) __syncwarp();
-    if (l == 0 && done >= 0 && ring.stages > 1 && t + (long long)(ring.stages - 1) * step < rows)
-      ring.issue(p.src, t + (long long)(ring.stages - 1) * step, done);
+    if (done >= 0 && ring.stages > 1) issue(t0 + (ring.stages - 1) * step, done);
     const F2 hs = f2(post ? rsqrtf(ss[0] * p.inv_d + p.eps) : 1.f), a = f2(p.res_scale);
-    const uint4 *xv = ring.row(p.sx) + l;
+    const uint4 *xv = ring.row(p.sx);
     uint4 *rv = p.r + t * p.vecs + l;
     q = f2(0.f);
 #pragma unroll
@@ -286,7 +320,7 @@ __global__ void __launch_bounds__(kMaxGroup) residual_norm_kernel(const __grid_c
         }
         if (gated) {
           F2 g[E];
-          Vec<T>::unpack(ok ? gv[l + i * tpr] : zero, g);
+          Vec<T>::unpack(ok ? gv[i * tpr] : zero, g);
 #pragma unroll
           for (int e = 0; e < E; ++e) r[i][e] = mul(r[i][e], g[e]);
         }
@@ -296,19 +330,19 @@ __global__ void __launch_bounds__(kMaxGroup) residual_norm_kernel(const __grid_c
 #pragma unroll
         for (int e = 0; e < E; ++e) r[i][e] = mul(a, x[e]);
       }
-      if (p.r && ok) rv[i * tpr] = Vec<T>::pack(r[i]);
+      if (p.r && ok && row_ok) rv[i * tpr] = Vec<T>::pack(r[i]);
 #pragma unroll
       for (int e = 0; e < E; ++e) q = fma(r[i][e], r[i][e], q);
     }
     done = ring.at;
     if (!p.u) continue;
     ss[0] = sum2(q);
-    group_sum<1, WARP>(ss, sh, turn);
+    row_sum<1, WARP>(ss, tpr, sh, turn);
     const F2 rs = f2(rsqrtf(ss[0] * p.inv_d + p.eps));
     uint4 *uv = p.u + t * p.vecs + l;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      if (i < NV - 1 || tail) {
+      if ((i < NV - 1 || tail) && row_ok) {
         F2 w[E];
         Vec<T>::unpack(__ldg(p.w_pre + l + i * tpr), w);
 #pragma unroll
@@ -317,7 +351,7 @@ __global__ void __launch_bounds__(kMaxGroup) residual_norm_kernel(const __grid_c
       }
     }
   }
-  ring_end(&abort_flag);
+  ring.end(&abort_flag);
 }
 
 struct NormBwdParams {
@@ -326,8 +360,8 @@ struct NormBwdParams {
   int sr, su, sh, sd, sg;        // stage slots of r, du, h, dr and a token's gate
   const uint4 *gate, *w_post, *w_pre;
   uint4 *dx, *dh, *dgate_tok;
-  float *part_pre;               // [groups][vecs * 2 E]: sums of du rn; null where not asked for
-  float *part_a;                 // [units][groups of a CTA][vecs * 2 E]: sums of dR hn (token gates: of dN hn)
+  float *part_pre;               // [teams][vecs * 2 E]: sums of du rn; null where not asked for
+  float *part_a;                 // [units][teams of a CTA][vecs * 2 E]: sums of dR hn (token gates: of dN hn)
   int rows_per_b;                // tokens of one gate row (P * s, or all of them)
   int vecs, gate_mode, B, s;
   int bs, upb;                   // gate rows that units walk (B for sequence gates, else 1); units (runs of tokens) each
@@ -336,15 +370,15 @@ struct NormBwdParams {
 
 template <typename T, int NV, bool WARP>
 __global__ void __launch_bounds__(kMaxGroup, 1) residual_norm_bwd_kernel(const __grid_constant__ NormBwdParams p) {
-  constexpr int E = Vec<T>::N, G = WARP ? kWarpRows : 1;
+  constexpr int E = Vec<T>::N, kTeams = WARP ? kWarpTeams : 1;
   extern __shared__ __align__(128) uint8_t stage_mem[];
-  __shared__ uint64_t bars[kWarpRows * kMaxStages];
+  __shared__ uint64_t bars[kWarpTeams * kMaxStages];
   __shared__ int abort_flag;
   __shared__ float sh3[2 * (kMaxGroup / 32)][3], sh1[2 * (kMaxGroup / 32)][1];
   int turn3 = 0, turn1 = 0;
-  Ring ring = ring_setup<WARP>(stage_mem, bars, &abort_flag, p.vecs, p.ring);
-  const int l = WARP ? threadIdx.x & 31 : threadIdx.x, tpr = WARP ? 32 : blockDim.x;
-  const int grp = WARP ? threadIdx.x >> 5 : 0;
+  Ring<WARP> ring(stage_mem, bars, &abort_flag, p.vecs, p.ring);
+  const int l = ring.l, tpr = ring.lanes, team = WARP ? threadIdx.x >> 5 : 0;
+  const int G = kTeams * ring.rows;   // tokens of a turn of the CTA's teams
   const bool tail = l + (NV - 1) * tpr < p.vecs;   // this thread's last vector exists
   const bool post = p.w_post != nullptr, gated = p.gate_mode != ULY_GATE_NONE;
   F2 a_pre[NV][E], a_a[NV][E];
@@ -352,39 +386,64 @@ __global__ void __launch_bounds__(kMaxGroup, 1) residual_norm_bwd_kernel(const _
   for (int i = 0; i < NV; ++i)
 #pragma unroll
     for (int e = 0; e < E; ++e) a_pre[i][e] = a_a[i][e] = f2(0.f);
+  // Column sums of a warp's rows: lanes of the same columns, then the first row's lanes store.
+  auto store_sums = [&](F2 (&v)[NV][E], float *part, long long index) {
+    F2 *o = reinterpret_cast<F2 *>(part) + (index * p.vecs + l) * E;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        if (WARP)
+          for (int off = tpr; off < 32; off <<= 1) {
+            F2 w;
+            w.v = __shfl_xor_sync(0xffffffffu, v[i][e].v, off);
+            v[i][e] = add(v[i][e], w);
+          }
+        if ((i < NV - 1 || tail) && ring.sub == 0) o[(long long)i * tpr * E + e] = v[i][e];
+        v[i][e] = f2(0.f);
+      }
+  };
   const int units = p.bs * p.upb;
   for (int unit = blockIdx.x; unit < units; unit += gridDim.x) {
     const int b = unit / p.upb, part = unit - b * p.upb;
-    const int q0 = (int)((long long)p.rows_per_b * part / p.upb) + grp;
+    const int q0 = (int)((long long)p.rows_per_b * part / p.upb) + team * ring.rows;
     const int q1 = (int)((long long)p.rows_per_b * (part + 1) / p.upb);
     // token k of gate row b: rank k / s, position k % s
     auto token = [&](int k) { return p.bs == 1 ? k : k + (k / p.s * (p.B - 1) + b) * p.s; };
+    auto issue = [&](int k, int st) {
+      if (k >= q1) return;
+      const int n = min(ring.rows, q1 - k);
+      if (p.bs == 1 || !WARP) ring.issue(p.src, token(k), n, st);
+      else ring.issue_each(p.src, token(min(k + ring.sub, q1 - 1)), n, st);
+    };
     if (WARP) __syncwarp();
     else if (unit != blockIdx.x) __syncthreads();   // every thread is done with the last unit's stages
-    if (l == 0) {
+    {
       int st = ring.at;
-      for (int k = 0; k < ring.stages && q0 + k * G < q1; ++k) {
-        ring.issue(p.src, token(q0 + k * G), st);
+      for (int k = 0; k < ring.stages; ++k) {
+        issue(q0 + k * G, st);
         if (++st == ring.stages) st = 0;
       }
     }
     int done = -1;
-    int pos = p.bs == 1 ? 0 : q0 % p.s, t = token(q0);
+    int pos = p.bs == 1 ? 0 : (q0 + ring.sub) % p.s, t = token(q0 + ring.sub);
     for (int k = q0; k < q1; k += G, ring.next()) {
       const long long base = (long long)t * p.vecs + l;
+      const bool row_ok = !WARP || k + ring.sub < q1;
+      const bool ok_tail = tail && row_ok;
       if (ring.stages == 1 && done >= 0) {   // no stage to run ahead into
-        group_barrier<WARP>();
-        if (l == 0) ring.issue(p.src, t, 0);
+        team_barrier<WARP>();
+        issue(k, 0);
       }
       ring.wait(&abort_flag, p.ring.err);
       F2 rr = f2(0.f), ar = f2(0.f), hh = f2(0.f);   // sums of r^2, du w_pre r and h^2, taken together
-      const uint4 *rv = ring.row(p.sr) + l, *uv = ring.row(p.su) + l, *hv = ring.row(p.sh) + l, *dv = ring.row(p.sd) + l;
-      const uint4 *gv = p.sg >= 0 ? ring.row(p.sg) + l : p.gate + (long long)b * p.vecs + l;
+      const uint4 *rv = ring.row(p.sr), *uv = ring.row(p.su), *hv = ring.row(p.sh), *dv = ring.row(p.sd);
+      const uint4 *gv = p.sg >= 0 ? ring.row(p.sg) : p.gate + (long long)b * p.vecs + l;
       F2 hn[NV][E];
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int v = i * tpr;
-        if (i < NV - 1 || tail) {
+        if (i < NV - 1 ? row_ok : ok_tail) {
           if (p.sh >= 0) {
             Vec<T>::unpack(hv[v], hn[i]);
             if (post) {
@@ -406,10 +465,9 @@ __global__ void __launch_bounds__(kMaxGroup, 1) residual_norm_bwd_kernel(const _
         }
       }
       float s3[3] = {sum2(rr), sum2(ar), sum2(hh)};
-      group_sum<3, WARP>(s3, sh3, turn3);   // the barrier also frees the previous row's stage
+      row_sum<3, WARP>(s3, tpr, sh3, turn3);   // a CTA's barrier also frees the previous stage
       if (WARP) __syncwarp();
-      if (l == 0 && done >= 0 && ring.stages > 1 && k + (ring.stages - 1) * G < q1)
-        ring.issue(p.src, token(k + (ring.stages - 1) * G), done);
+      if (done >= 0 && ring.stages > 1) issue(k + (ring.stages - 1) * G, done);
       const float irs = rsqrtf(s3[0] * p.inv_d + p.eps);
       const F2 ir = f2(irs), nc1 = f2(-s3[1] * irs * irs * p.inv_d);   // -mean(a rn) / rms(r)
       const float ihs = post ? rsqrtf(s3[2] * p.inv_d + p.eps) : 1.f;
@@ -418,7 +476,7 @@ __global__ void __launch_bounds__(kMaxGroup, 1) residual_norm_bwd_kernel(const _
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int v = i * tpr;
-        if (i < NV - 1 || tail) {
+        if (i < NV - 1 ? row_ok : ok_tail) {
           F2 (&d)[E] = dn[i];
           if (p.sd >= 0) {
             Vec<T>::unpack(dv[v], d);
@@ -490,12 +548,12 @@ __global__ void __launch_bounds__(kMaxGroup, 1) residual_norm_bwd_kernel(const _
       F2 nc2 = f2(0.f);
       if (post) {
         float s1[1] = {sum2(s1p)};
-        group_sum<1, WARP>(s1, sh1, turn1);
+        row_sum<1, WARP>(s1, tpr, sh1, turn1);
         nc2 = f2(-s1[0] * p.inv_d);
       }
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        if (i < NV - 1 || tail) {
+        if (i < NV - 1 ? row_ok : ok_tail) {
           if (post) {
 #pragma unroll
             for (int e = 0; e < E; ++e) dn[i][e] = mul(ih, fma(nc2, hn[i][e], dn[i][e]));
@@ -504,50 +562,44 @@ __global__ void __launch_bounds__(kMaxGroup, 1) residual_norm_bwd_kernel(const _
         }
       }
     }
-    if (p.part_a) {
-      F2 *o = reinterpret_cast<F2 *>(p.part_a) + (((long long)unit * G + grp) * p.vecs + l) * E;
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-        if (i < NV - 1 || tail)
-#pragma unroll
-          for (int e = 0; e < E; ++e) {
-            o[(long long)i * tpr * E + e] = a_a[i][e];
-            a_a[i][e] = f2(0.f);
-          }
-    }
+    if (p.part_a) store_sums(a_a, p.part_a, (long long)unit * kTeams + team);
   }
-  if (p.part_pre) {
-    F2 *o = reinterpret_cast<F2 *>(p.part_pre) + (((long long)blockIdx.x * G + grp) * p.vecs + l) * E;
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if (i < NV - 1 || tail)
-#pragma unroll
-        for (int e = 0; e < E; ++e) o[(long long)i * tpr * E + e] = a_pre[i][e];
-  }
-  ring_end(&abort_flag);
+  if (p.part_pre) store_sums(a_pre, p.part_pre, (long long)blockIdx.x * kTeams + team);
+  ring.end(&abort_flag);
 }
 
 // ------------------------------------------------------------------- host
 
-// Groups and stages for rows of `vecs` vectors: a warp a row while `nv` vectors
-// a thread cover it, else the fewest warps that do; CTAs an SM by the registers
-// and by two stages each at least (one only where a single CTA's do not fit).
+// Teams and stages for rows of `vecs` vectors: lanes of a warp (a power of two)
+// while `nv` vectors a lane cover a row, else the fewest warps that do; CTAs an
+// SM by the registers and by two stages each at least (one only where a single
+// CTA's do not fit).
 struct RowShape {
-  int tpr, nv, rpb, per_sm, stages;
+  int lanes, nv, teams, rows;   // threads of a row, vectors of each; teams of a CTA, rows of a team
+  int threads, per_sm, stages;
   uint32_t smem;
 };
 RowShape row_shape(int vecs, int slots, int nv, bool backward) {
   RowShape r;
-  auto up32 = [](int v) { return (v + 31) / 32 * 32; };
-  r.tpr = up32((vecs + nv - 1) / nv);
-  if (r.tpr > kMaxGroup) r.tpr = kMaxGroup;
-  r.nv = (vecs + r.tpr - 1) / r.tpr;
-  r.rpb = r.tpr == 32 ? kWarpRows : 1;
-  const uint32_t stage = (uint32_t)vecs * 16 * slots * r.rpb;
-  // threads an SM holds by the kernels' registers: forward up to 64, beyond two
-  // vectors a thread up to 112; backward up to 104, then 128
-  const int threads = backward ? (r.nv == 1 ? 608 : 512) : (r.nv <= 2 ? 1024 : 576);
-  r.per_sm = threads / (r.tpr * r.rpb);
+  auto need = [&](int lanes) { return (vecs + lanes - 1) / lanes; };
+  if (vecs <= 32 * nv) {
+    r.lanes = 1;
+    while (need(r.lanes) > nv) r.lanes *= 2;
+    r.teams = kWarpTeams;
+    r.rows = 32 / r.lanes;
+    r.threads = 32 * kWarpTeams;
+  } else {
+    r.lanes = (need(nv) + 31) / 32 * 32;
+    if (r.lanes > kMaxGroup) r.lanes = kMaxGroup;
+    r.teams = r.rows = 1;
+    r.threads = r.lanes;
+  }
+  r.nv = need(r.lanes);
+  const uint32_t stage = (uint32_t)vecs * 16 * slots * r.teams * r.rows;
+  // threads an SM holds by the kernels' registers: up to 128, forward 112 where a
+  // team is a CTA and 64 up to two vectors a thread
+  const int room = backward ? 512 : r.nv <= 2 ? 1024 : r.teams > 1 ? 512 : 576;
+  r.per_sm = room / r.threads;
   if (r.per_sm < 1) r.per_sm = 1;
   while (r.per_sm > 1 && kRingBytes / (stage * r.per_sm) < 2) --r.per_sm;
   r.stages = (int)(kRingBytes / (stage * r.per_sm));
@@ -577,14 +629,14 @@ Entry<NormParams> &fwd_entry(const RowShape &r) {
                                       {residual_norm_kernel<T, 5, true>}};
   static Entry<NormParams> cta[3] = {{residual_norm_kernel<T, 3, false>}, {residual_norm_kernel<T, 4, false>},
                                      {residual_norm_kernel<T, 5, false>}};
-  return r.tpr == 32 ? warp[r.nv - 1] : cta[r.nv < 3 ? 0 : r.nv - 3];
+  return r.teams > 1 ? warp[r.nv - 1] : cta[r.nv < 3 ? 0 : r.nv - 3];
 }
 template <typename T>
 Entry<NormBwdParams> &bwd_entry(const RowShape &r) {
   static Entry<NormBwdParams> warp[2] = {{residual_norm_bwd_kernel<T, 1, true>}, {residual_norm_bwd_kernel<T, 2, true>}};
   static Entry<NormBwdParams> cta[3] = {{residual_norm_bwd_kernel<T, 2, false>}, {residual_norm_bwd_kernel<T, 3, false>},
                                         {residual_norm_bwd_kernel<T, 4, false>}};
-  return r.tpr == 32 ? warp[r.nv - 1] : cta[r.nv < 2 ? 0 : r.nv - 2];
+  return r.teams > 1 ? warp[r.nv - 1] : cta[r.nv < 2 ? 0 : r.nv - 2];
 }
 
 // How the backward walks the tokens: `bs` gate rows, each cut into `upb` runs
@@ -601,13 +653,13 @@ BwdPlan bwd_plan(int B, long long n, int hidden, int e, int gate_mode) {
   q.bs = gate_mode == ULY_GATE_SEQUENCE ? B : 1;
   const long long rows = gate_mode == ULY_GATE_SEQUENCE ? n : (long long)B * n;
   const long long want = (long long)device_sm_count() * q.rs.per_sm;
-  long long upb = want / q.bs, most = (rows + q.rs.rpb - 1) / q.rs.rpb;
+  long long upb = want / q.bs, turn = q.rs.teams * q.rs.rows, most = (rows + turn - 1) / turn;
   if (upb < 1) upb = 1;
   if (upb > most) upb = most;
   q.upb = (int)upb;
   const long long units = (long long)q.bs * q.upb;
   q.grid = (int)(units < want ? units : want);
-  const size_t col = (size_t)hidden * sizeof(float) * q.rs.rpb;
+  const size_t col = (size_t)hidden * sizeof(float) * q.rs.teams;
   q.off_pre = 0;
   q.off_a = q.off_pre + col * q.grid;
   q.bytes = q.off_a + col * units;
@@ -721,11 +773,11 @@ uly_status residual_norm_launch(int32_t B, int32_t n, int32_t P, int32_t hidden,
   p.gate_mode = gate_mode; p.B = B; p.s = n / P;
   p.res_scale = res_scale; p.eps = eps; p.inv_d = 1.0f / hidden;
   const RowShape rs = row_shape(p.vecs, p.src.n, kFwdVecs, false);
-  p.ring = {p.src.n, rs.stages, error_word()};
-  const long long want = (long long)device_sm_count() * rs.per_sm, ctas = ((long long)p.rows + rs.rpb - 1) / rs.rpb;
+  p.ring = {p.src.n, rs.stages, rs.lanes, error_word()};
+  const long long want = (long long)device_sm_count() * rs.per_sm, turn = rs.teams * rs.rows, ctas = (p.rows + turn - 1) / turn;
   const int grid = (int)(ctas < want ? ctas : want);
   prof::Scope scope(prof::K_RESIDUAL_NORM, stream);
-  return run(bf ? fwd_entry<__nv_bfloat16>(rs) : fwd_entry<float>(rs), grid, rs.tpr * rs.rpb, rs.smem, p, stream);
+  return run(bf ? fwd_entry<__nv_bfloat16>(rs) : fwd_entry<float>(rs), grid, rs.threads, rs.smem, p, stream);
 }
 
 size_t residual_norm_bwd_workspace_bytes(int32_t B, int32_t n, int32_t hidden, int32_t dtype, int32_t gate_mode) {
@@ -747,7 +799,7 @@ uly_status residual_norm_bwd_launch(int32_t B, int32_t n, int32_t P, int32_t hid
   p.src.add(h, p.sh);
   p.src.add(dr, p.sd);
   p.src.add(gate_mode == ULY_GATE_TOKEN ? gate : nullptr, p.sg);
-  p.ring = {q.slots, q.rs.stages, error_word()};
+  p.ring = {q.slots, q.rs.stages, q.rs.lanes, error_word()};
   p.gate = static_cast<const uint4 *>(gate);
   p.w_post = static_cast<const uint4 *>(w_post);
   p.w_pre = static_cast<const uint4 *>(w_pre);
@@ -764,14 +816,14 @@ uly_status residual_norm_bwd_launch(int32_t B, int32_t n, int32_t P, int32_t hid
   {
     prof::Scope scope(prof::K_RESIDUAL_NORM_BWD, stream);
     const uly_status st = run(bf ? bwd_entry<__nv_bfloat16>(q.rs) : bwd_entry<float>(q.rs), q.grid,
-                              q.rs.tpr * q.rs.rpb, q.rs.smem, p, stream);
+                              q.rs.threads, q.rs.smem, p, stream);
     if (st != ULY_OK) return st;
   }
-  const int run = q.upb * q.rs.rpb;   // partials of one gate row
+  const int run = q.upb * q.rs.teams;   // partials of one gate row
   FoldJobs jobs = {};
   jobs.cols = hidden;
   jobs.bf16 = bf;
-  if (dw_pre) jobs.job[jobs.n++] = {p.part_pre, dw_pre, (long long)q.grid * q.rs.rpb, 1, nullptr, nullptr, 1};
+  if (dw_pre) jobs.job[jobs.n++] = {p.part_pre, dw_pre, (long long)q.grid * q.rs.teams, 1, nullptr, nullptr, 1};
   if (dw_post) {
     FoldJob &f = jobs.job[jobs.n++];
     f = {p.part_a, dw_post, (long long)q.bs * run, 1, nullptr, nullptr, run};

@@ -245,6 +245,10 @@ NORMS = [  # P, B, s, D, dtype, gate, post
     (1, 700, 2, 64, torch.bfloat16, "sequence", True),     # more sequences than CTAs in flight
     (3, 2, 701, 256, torch.bfloat16, "channel", True),     # several rows a group, its ring refilled
     (2, 3, 611, 2560, torch.bfloat16, "sequence", True),
+    (2, 3, 500, 160, torch.bfloat16, "sequence", True),    # short rows, several a warp, runs that end inside one
+    (1, 1, 5000, 8, torch.bfloat16, "channel", True),
+    (2, 2, 777, 24, torch.float32, "token", True),
+    (1, 3, 1999, 204, torch.float32, "sequence", True),
     (2, 2, 450, 1280, torch.bfloat16, "token", False),
     (1, 1, 1801, 1028, torch.float32, "none", True),
     (1, 2, 611, 640, torch.float32, "channel", True),
