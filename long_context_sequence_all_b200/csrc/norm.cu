@@ -369,7 +369,7 @@ struct NormBwdParams {
 };
 
 template <typename T, int NV, bool WARP>
-__global__ void __launch_bounds__(kMaxGroup, 1) residual_norm_bwd_kernel(const __grid_constant__ NormBwdParams p) {
+__global__ void __maxnreg__(sizeof(T) == 4 && NV == 2 && !WARP ? 96 : 128) residual_norm_bwd_kernel(const __grid_constant__ NormBwdParams p) {
   constexpr int E = Vec<T>::N, kTeams = WARP ? kWarpTeams : 1;
   extern __shared__ __align__(128) uint8_t stage_mem[];
   __shared__ uint64_t bars[kWarpTeams * kMaxStages];
@@ -579,7 +579,7 @@ struct RowShape {
   int threads, per_sm, stages;
   uint32_t smem;
 };
-RowShape row_shape(int vecs, int slots, int nv, bool backward) {
+RowShape row_shape(int vecs, int slots, int nv, bool backward, bool f32) {
   RowShape r;
   auto need = [&](int lanes) { return (vecs + lanes - 1) / lanes; };
   if (vecs <= 32 * nv) {
@@ -596,9 +596,10 @@ RowShape row_shape(int vecs, int slots, int nv, bool backward) {
   }
   r.nv = need(r.lanes);
   const uint32_t stage = (uint32_t)vecs * 16 * slots * r.teams * r.rows;
-  // threads an SM holds by the kernels' registers: up to 128, forward 112 where a
-  // team is a CTA and 64 up to two vectors a thread
-  const int room = backward ? 512 : r.nv <= 2 ? 1024 : r.teams > 1 ? 512 : 576;
+  // threads an SM holds by the kernels' registers: up to 128; forward 112 where a
+  // team is a CTA and 64 up to two vectors a thread; backward 96 for two fp32
+  // vectors where a team is a CTA (50000 x 640: 155 -> 142 us by the fourth CTA)
+  const int room = backward ? (f32 && r.nv == 2 && r.teams == 1 ? 640 : 512) : r.nv <= 2 ? 1024 : r.teams > 1 ? 512 : 576;
   r.per_sm = room / r.threads;
   if (r.per_sm < 1) r.per_sm = 1;
   while (r.per_sm > 1 && kRingBytes / (stage * r.per_sm) < 2) --r.per_sm;
@@ -649,7 +650,7 @@ struct BwdPlan {
 BwdPlan bwd_plan(int B, long long n, int hidden, int e, int gate_mode) {
   BwdPlan q;
   q.slots = gate_mode == ULY_GATE_TOKEN ? 5 : 4;
-  q.rs = row_shape(hidden / e, q.slots, kBwdVecs, true);
+  q.rs = row_shape(hidden / e, q.slots, kBwdVecs, true, e == 4);
   q.bs = gate_mode == ULY_GATE_SEQUENCE ? B : 1;
   const long long rows = gate_mode == ULY_GATE_SEQUENCE ? n : (long long)B * n;
   const long long want = (long long)device_sm_count() * q.rs.per_sm;
@@ -772,7 +773,7 @@ uly_status residual_norm_launch(int32_t B, int32_t n, int32_t P, int32_t hidden,
   p.vecs = hidden / (bf ? 8 : 4);
   p.gate_mode = gate_mode; p.B = B; p.s = n / P;
   p.res_scale = res_scale; p.eps = eps; p.inv_d = 1.0f / hidden;
-  const RowShape rs = row_shape(p.vecs, p.src.n, kFwdVecs, false);
+  const RowShape rs = row_shape(p.vecs, p.src.n, kFwdVecs, false, !bf);
   p.ring = {p.src.n, rs.stages, rs.lanes, error_word()};
   const long long want = (long long)device_sm_count() * rs.per_sm, turn = rs.teams * rs.rows, ctas = (p.rows + turn - 1) / turn;
   const int grid = (int)(ctas < want ? ctas : want);
