@@ -3,8 +3,9 @@
 // linear product and its gradients, the linear loss and its gradients).
 //
 // bf16 operands, fp32 accumulators.  A cluster of two CTAs on neighbouring SMs
-// computes one 256 x 256 tile (tcgen05 cta_group::2, M = 256): each CTA holds
-// 128 rows of A, 128 rows of B and the accumulator of its own 128 rows, so
+// computes one 256 x 256 tile (tcgen05 cta_group::2, M = 256; 256 x 128 where
+// that puts more SMs to work on a small product): each CTA holds 128 rows of A,
+// half the rows of B and the accumulator of its own 128 rows, so
 // every byte of B in shared memory feeds two tensor cores and a k-step of 64
 // costs each SM 32 KB of loads instead of the 48 KB of a 128 x 256 tile of its
 // own.  K runs in steps of 64 columns (one 128-byte swizzle span).  The kernel
@@ -13,7 +14,7 @@
 //
 // Warps (384 threads): 0 TMA (both CTAs load their own halves, all completing
 // on the leader's barriers), 1 MMA issue (the leader CTA's), 2 tensor memory,
-// 4-11 epilogue: two warpgroups take the two 128-column halves of the CTA's
+// 4-11 epilogue: two warpgroups take the two halves of the columns of the CTA's
 // 128 rows, one row a thread, while the next tile fills the other accumulator.
 //
 // An operand is K-major (rows of K contiguous elements, 128-row boxes) or
@@ -39,19 +40,25 @@ namespace gemm {
 
 using namespace sm100;
 
-constexpr int kTile = 256;       // rows and columns of a cluster's tile
-constexpr int kHalf = 128;       // rows of A and of B in one CTA
+constexpr int kTile = 256;       // rows of a cluster's tile, and its columns unless it is a narrow one (128)
+constexpr int kNarrow = 128;
+constexpr int kHalf = 128;       // rows of A in one CTA
 constexpr int kBK = 64;
-constexpr int kStages = 5;
 constexpr int kOutSlots = 4;
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 128 + 32 * kEpiWarps;
-constexpr uint32_t kOperandBytes = kHalf * kBK * 2;        // 16 KB
-constexpr uint32_t kStageBytes = 2 * kOperandBytes;        // one CTA's A and B of a k-step
-constexpr uint32_t kOffOut = kStages * kStageBytes;       // output staging, 2 KB slots for each epilogue warp
+constexpr uint32_t kABytes = kHalf * kBK * 2;             // 16 KB
 constexpr uint32_t kOutSlot = 32 * 64;                    // 32 rows of 32 two-byte or 16 four-byte columns
-constexpr uint32_t kOffBar = kOffOut + kEpiWarps * kOutSlots * kOutSlot;
-constexpr uint32_t kSmemBytes = kOffBar + 256 + 1024;      // barriers + alignment slack
+// Shared memory of one CTA for tiles of TN columns: the ring of k-steps, the
+// epilogue warps' output slots, barriers.
+template <int TN>
+struct Layout {
+  static constexpr int kStages = TN == kTile ? 5 : 6;
+  static constexpr uint32_t kStage = kABytes + TN / 2 * kBK * 2;
+  static constexpr uint32_t kOffOut = kStages * kStage;
+  static constexpr uint32_t kOffBar = kOffOut + kEpiWarps * kOutSlots * kOutSlot;
+  static constexpr uint32_t kBytes = kOffBar + 256 + 1024;   // barriers + alignment slack
+};
 constexpr long long kLandCycles = 1 << 20;                 // after giving up: the copies in flight land (~0.5 ms)
 
 // The product and how it is cut into work.
@@ -182,11 +189,12 @@ __host__ __device__ __forceinline__ int units_of(const Shape &s) {
   return s.full + (s.m_tiles * s.n_tiles - s.full) * s.splits;
 }
 
-// A partial tile: this warp's 32 rows of 128 accumulator columns, fp32.
+// A partial tile [256][TN]: this warp's 32 rows of half the columns, fp32.
+template <int TN>
 __device__ __forceinline__ void store_partial(const CUtensorMap *map, const Unit &w, uint32_t acc, int row_in_tile,
                                               int half, OutRing &out) {
 #pragma unroll 1
-  for (int c = half * kHalf; c < (half + 1) * kHalf; c += 32) {
+  for (int c = half * TN / 2; c < (half + 1) * TN / 2; c += 32) {
     uint32_t a[32], v[16];
     tmem_ld32(acc + c, a);
 #pragma unroll
@@ -199,20 +207,23 @@ __device__ __forceinline__ void store_partial(const CUtensorMap *map, const Unit
 }
 
 // Epi::Params, and
-//   Epi::tile(params, unit, acc, row, half, out): one thread's 128 accumulators
-//   (read from tensor memory, columns [128 half, +128) from acc, before it
-//   returns) of C row `row`, in tile column unit.nt.
-template <class Epi, bool A_MN, bool B_MN>
+//   Epi::tile<TN>(params, unit, acc, row, half, out): one thread's TN / 2
+//   accumulators (read from tensor memory, that half of the columns from acc on,
+//   before it returns) of C row `row`, in tile column unit.nt.
+template <class Epi, int TN, bool A_MN, bool B_MN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     gemm_pair_sm100_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                           const __grid_constant__ CUtensorMap tmPart, const __grid_constant__ Shape sh, const __grid_constant__ typename Epi::Params ep) {
+                           const __grid_constant__ CUtensorMap tmPart, const __grid_constant__ Shape sh,
+                           const __grid_constant__ typename Epi::Params ep) {
+  using L = Layout<TN>;
+  constexpr int kStages = L::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sb = smem_u32(smem);
-  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + kOffBar);
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::kOffBar);
   enum { B_FULL = 0, B_EMPTY = kStages, B_ACCF = 2 * kStages, B_ACCE = B_ACCF + 2, B_N = B_ACCE + 2 };
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + kOffBar + 8 * B_N);
-  volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + kOffBar + 8 * B_N + 4);
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::kOffBar + 8 * B_N);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kOffBar + 8 * B_N + 4);
   auto bar = [&](int i) { return smem_u32(&bars[i]); };
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -249,10 +260,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int k = w.k0; k < w.k1; ++k) {
           ok = mbar_wait(bar(B_EMPTY + stage), phase, abort_flag, sh.err, sh.wait_limit);
           if (!ok) break;
-          const uint32_t sA = sb + stage * kStageBytes, sB = sA + kOperandBytes;
+          const uint32_t sA = sb + stage * L::kStage, sB = sA + kABytes;
           // the leader's barrier counts the bytes of both CTAs
           const uint32_t full = map_cta(bar(B_FULL + stage), 0);
-          if (rank == 0) mbar_arrive_expect_tx(bar(B_FULL + stage), 2 * kStageBytes);
+          if (rank == 0) mbar_arrive_expect_tx(bar(B_FULL + stage), 2 * L::kStage);
           if (A_MN) {
             tma_load_2d_pair(sA, &tmA, full, a0, k * kBK);
             tma_load_2d_pair(sA + 8192, &tmA, full, a0 + 64, k * kBK);
@@ -261,7 +272,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
           if (B_MN) {
             tma_load_2d_pair(sB, &tmB, full, b0, k * kBK);
-            tma_load_2d_pair(sB + 8192, &tmB, full, b0 + 64, k * kBK);
+            if (TN == kTile) tma_load_2d_pair(sB + 8192, &tmB, full, b0 + 64, k * kBK);
           } else {
             tma_load_2d_pair(sB, &tmB, full, k * kBK, b0);
           }
@@ -272,7 +283,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMA
     if (lane == 0 && rank == 0) {
-      constexpr uint32_t idesc = idesc_bf16_f32(kTile, kTile, A_MN, B_MN);
+      constexpr uint32_t idesc = idesc_bf16_f32(kTile, TN, A_MN, B_MN);
       // K-major: 16 K-elements are 32 bytes along a row; MN-major: 16 K-rows
       // are 2048 bytes, the 64-element MN chunks 8 KB apart (LBO)
       constexpr uint32_t astep = A_MN ? 2048 : 32, bstep = B_MN ? 2048 : 32;
@@ -288,9 +299,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (!ok) break;
           tc_fence_after();
         }
-        const uint32_t acc = tmem + buf * kTile;
+        const uint32_t acc = tmem + buf * TN;
         for (int k = w.k0; k < w.k1; ++k) {
-          const uint32_t sA = sb + stage * kStageBytes, sB = sA + kOperandBytes;
+          const uint32_t sA = sb + stage * L::kStage, sB = sA + kABytes;
           const uint64_t da = A_MN ? sdesc_sw128(sA, 8192, 1024) : sdesc_sw128(sA, 16, 1024);
           const uint64_t db = B_MN ? sdesc_sw128(sB, 8192, 1024) : sdesc_sw128(sB, 16, 1024);
           ok = mbar_wait(bar(B_FULL + stage), phase, abort_flag, sh.err, sh.wait_limit);
@@ -310,7 +321,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   } else if (warp >= 4) {
     // ------------------------------------------------------------- epilogue
     const int quarter = warp & 3, half = (warp - 4) >> 2;
-    OutRing out{sb + kOffOut + (uint32_t)(warp - 4) * kOutSlots * kOutSlot, 0, lane};
+    OutRing out{sb + L::kOffOut + (uint32_t)(warp - 4) * kOutSlots * kOutSlot, 0, lane};
     int it = 0;
     for (int u = cluster; u < units; u += clusters, ++it) {
       const int buf = it & 1;
@@ -319,15 +330,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         break;
       tc_fence_after();
       const Unit w = unit_of(sh, u);
-      const uint32_t acc = tmem + ((uint32_t)(quarter * 32) << 16) + buf * kTile;
+      const uint32_t acc = tmem + ((uint32_t)(quarter * 32) << 16) + buf * TN;
       const int row0 = (int)rank * kHalf + quarter * 32;
-      if (w.part >= 0) store_partial(&tmPart, w, acc, row0, half, out);
-      else Epi::tile(ep, w, acc, w.mt * kTile + row0 + lane, half, out);
+      if (w.part >= 0) store_partial<TN>(&tmPart, w, acc, row0, half, out);
+      else Epi::template tile<TN>(ep, w, acc, w.mt * kTile + row0 + lane, half, out);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) arrive_cluster(map_cta(bar(B_ACCE + buf), 0));
     }
-    if (lane == 0) bulk_wait_all();
+    if (lane == 0) bulk_wait_group_read<0>();   // the slots' memory outlives the copies out of it
   }
 
   // Normal end: every copy was consumed by an MMA and every MMA was waited for
@@ -381,45 +392,54 @@ inline bool make_out_map(CUtensorMap *map, const void *base, long long inner, lo
   return make_map_of(map, base, inner, rows, stride, f32 ? 16 : 32, 32, CU_TENSOR_MAP_SWIZZLE_64B, f32);
 }
 
-// How many tiles are taken whole and the parts of each of the others.  Whole
-// tiles in full turns of the SM pairs; a turn costs k_steps (512 cycles of MMA
-// each), the last one ceil(tiles left * splits / pairs) of k_steps / splits and,
-// if cut, a second kernel over fp32 partial tiles (written and read once) of at
-// most `budget` bytes.  320 tiles of 320 steps on 74 pairs: 4 turns and 24 tiles
-// cut in 3, 4.33 turns instead of 5.
+// The tiles' width, how many of them are taken whole and the parts of each of the
+// others: the least of a sum of microseconds.  Whole tiles in full turns of the SM
+// pairs; a turn costs k_steps (0.3, bound by the tensor cores; 0.25 for a narrow
+// tile, bound by its loads), the last one ceil(tiles left * splits / pairs) of
+// k_steps / splits and, if cut, a second kernel over fp32 partial tiles (written
+// and read once, mostly in L2) of at most `budget` bytes; the last tile's epilogue
+// is not hidden.
+// 320 tiles of 320 steps on 74 pairs: 4 turns and 24 tiles cut in 3, 4.33 turns
+// instead of 5.  1003 x 1032 -> 1544: 52 narrow tiles 11.9 us, 28 wide ones 13.8;
+// 256 x 10240 -> 2560: 10 wide tiles cut in 7 20.6 us, narrow ones 25.7.
 struct Cut {
+  int tn = kTile;     // columns of a tile
   int full = 0, splits = 1;
   size_t bytes = 0;   // of the partial tiles
 };
-constexpr size_t kPartTile = (size_t)kTile * kTile * sizeof(float);
-inline Cut choose_cut(long long tiles, long long k_steps, size_t budget = SIZE_MAX) {
-  const double step_us = 512.0 / 1700.0;
+inline Cut choose_cut(long long m_tiles, long long n_tiles, long long n_narrow, long long k_steps,
+                      size_t budget = SIZE_MAX) {
   const long long pairs = device_sm_count() / 2;
   Cut best;
-  best.full = (int)tiles;
-  const long long full = tiles / pairs * pairs, left = tiles - full;
-  if (left == 0) return best;
-  double best_t = (double)k_steps * step_us;
-  for (int s = 2; s <= 32 && s * 2 <= k_steps; ++s) {
-    const size_t bytes = (size_t)left * s * kPartTile;
-    if (bytes > budget) break;
-    const double t = (double)((left * s + pairs - 1) / pairs) * (double)((k_steps + s - 1) / s) * step_us + 4.0 +
-                     (double)bytes * 2.0 / 5e6;
-    if (t < best_t * 0.98) {
-      best_t = t;
-      best.full = (int)full;
-      best.splits = s;
-      best.bytes = bytes;
+  double best_us = 1e300;
+  for (int tn : {kTile, kNarrow}) {
+    const long long tiles = m_tiles * (tn == kTile ? n_tiles : n_narrow);
+    const long long full = tiles / pairs * pairs, left = tiles - full;
+    const double step = tn == kTile ? 0.3 : 0.25, end = tn == kTile ? 2.0 : 1.2;
+    for (int s = 1; s <= 32 && (s == 1 || (left > 0 && s * 2 <= k_steps)); ++s) {
+      const size_t bytes = s == 1 ? 0 : (size_t)left * s * kTile * tn * sizeof(float);
+      if (bytes > budget) break;
+      const double us = (double)(full / pairs * k_steps) * step + end +
+                        (double)((left * s + pairs - 1) / pairs) * (double)((k_steps + s - 1) / s) * step +
+                        (s == 1 ? 0.0 : 3.5 + (double)bytes * 2.0 / 1e7);
+      if (us < best_us * 0.98) {
+        best_us = us;
+        best.tn = tn;
+        best.full = (int)(s == 1 ? tiles : full);
+        best.splits = s;
+        best.bytes = bytes;
+      }
     }
   }
   return best;
 }
 inline long long tiles_of(long long n, int tile = kTile) { return (n + tile - 1) / tile; }
 
-// Work units, raster and rest of a launch.  `n_tile` output columns of one
-// tile column: 256, or 128 where B holds two rows for each of them.
-inline Shape make_shape(long long M, long long N, long long K, int n_tile, const Cut &cut) {
+// Work units, raster and rest of a launch.  `per_col` rows of B stand behind one
+// output column (1, or 2: N rows further on).
+inline Shape make_shape(long long M, long long N, long long K, int per_col, const Cut &cut) {
   Shape s = {};
+  const int n_tile = cut.tn / per_col;
   s.m_tiles = (int)tiles_of(M);
   s.n_tiles = (int)tiles_of(N, n_tile);
   s.full = cut.full;
@@ -427,27 +447,34 @@ inline Shape make_shape(long long M, long long N, long long K, int n_tile, const
   s.k_steps = (int)((K + kBK - 1) / kBK);
   s.group_m = 8;
   s.b_step = n_tile;
-  s.b_half = n_tile == kTile ? kHalf : (int)N;
+  s.b_half = per_col == 1 ? cut.tn / 2 : (int)N;
   s.err = error_word();
   s.wait_limit = wait_limit_cycles();
   return s;
 }
+// K-major rows of B in one box (one CTA's share of a tile).
+inline int b_box(const Cut &cut) { return cut.tn / 2; }
 
 // `part`: cut.bytes for the partial tiles of a shape that has any.
-template <class Epi, bool A_MN, bool B_MN>
-uly_status launch(const CUtensorMap &ta, const CUtensorMap &tb, const Shape &s, const typename Epi::Params &ep,
-                  float *part, cudaStream_t stream) {
+template <class Epi, int TN, bool A_MN, bool B_MN>
+uly_status launch_tn(const CUtensorMap &ta, const CUtensorMap &tb, const Shape &s, const typename Epi::Params &ep,
+                     float *part, cudaStream_t stream) {
   static std::atomic<uint64_t> optin{0};
-  auto kernel = gemm_pair_sm100_kernel<Epi, A_MN, B_MN>;
-  if (!smem_optin(kernel, kSmemBytes, optin)) return ULY_ERR_CUDA;
+  auto kernel = gemm_pair_sm100_kernel<Epi, TN, A_MN, B_MN>;
+  if (!smem_optin(kernel, Layout<TN>::kBytes, optin)) return ULY_ERR_CUDA;
   const int units = units_of(s), pairs = device_sm_count() / 2;
   const int grid = 2 * (units < pairs ? units : pairs);
   CUtensorMap tp = ta;
-  if (s.splits > 1 && !make_out_map(&tp, part, kTile, (long long)(units - s.full) * kTile, kTile, true))
-    return ULY_ERR_CUDA;
-  kernel<<<grid, kThreads, kSmemBytes, stream>>>(ta, tb, tp, s, ep);
+  if (s.splits > 1 && !make_out_map(&tp, part, TN, (long long)(units - s.full) * kTile, TN, true)) return ULY_ERR_CUDA;
+  kernel<<<grid, kThreads, Layout<TN>::kBytes, stream>>>(ta, tb, tp, s, ep);
   note_launches(1);
   return last_launch_status();
+}
+template <class Epi, bool A_MN, bool B_MN>
+uly_status launch(const CUtensorMap &ta, const CUtensorMap &tb, const Shape &s, const Cut &cut,
+                  const typename Epi::Params &ep, float *part, cudaStream_t stream) {
+  return cut.tn == kTile ? launch_tn<Epi, kTile, A_MN, B_MN>(ta, tb, s, ep, part, stream)
+                         : launch_tn<Epi, kNarrow, A_MN, B_MN>(ta, tb, s, ep, part, stream);
 }
 
 // ---------------------------------------------------- vectors of 8 columns
@@ -476,13 +503,13 @@ __device__ __forceinline__ void store8(float *p, const float (&x)[8]) {
 }
 
 // Sum of the cut tiles' partials, in the order of the parts, and
-// Epi::join8(params, row, col, z, up) of eight columns (up: those 128 further on
-// in a tile whose B holds two rows for each column).
-template <class Epi>
+// Epi::join8(params, row, col, z, up) of eight columns (up: those half a tile
+// further on, in a tile whose B holds two rows for each column).
+template <class Epi, int TN>
 __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ typename Epi::Params p,
                                                    const __grid_constant__ Shape s, const float *__restrict__ part,
                                                    long long M, int N) {
-  constexpr int cols = Epi::kGated ? kHalf : kTile, vecs = cols / 8;
+  constexpr int cols = Epi::kGated ? TN / 2 : TN, vecs = cols / 8;
   const int tiles = s.m_tiles * s.n_tiles - s.full;
   for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < (long long)tiles * kTile * vecs;
        i += (long long)gridDim.x * 256) {
@@ -493,14 +520,14 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ typen
     const int col = nt * cols + c;
     if (row >= M || col >= N) continue;
     float z[8] = {}, up[8] = {};
-    const float *src = part + ((long long)t * s.splits * kTile + r) * kTile + c;
-    for (int k = 0; k < s.splits; ++k, src += kTile * kTile) {
+    const float *src = part + ((long long)t * s.splits * kTile + r) * TN + c;
+    for (int k = 0; k < s.splits; ++k, src += kTile * TN) {
       float v[8];
       load8(src, v);
 #pragma unroll
       for (int e = 0; e < 8; ++e) z[e] += v[e];
       if (Epi::kGated) {
-        load8(src + kHalf, v);
+        load8(src + TN / 2, v);
 #pragma unroll
         for (int e = 0; e < 8; ++e) up[e] += v[e];
       }
@@ -509,12 +536,13 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ typen
   }
 }
 template <class Epi>
-uly_status launch_join(const typename Epi::Params &p, const Shape &s, const float *part, long long M, int N,
-                       cudaStream_t stream) {
+uly_status launch_join(const typename Epi::Params &p, const Shape &s, const Cut &cut, const float *part, long long M,
+                       int N, cudaStream_t stream) {
   if (s.splits == 1) return ULY_OK;
-  const long long vecs = (long long)(s.m_tiles * s.n_tiles - s.full) * kTile * (Epi::kGated ? kHalf : kTile) / 8;
+  const long long vecs = (long long)(s.m_tiles * s.n_tiles - s.full) * kTile * (cut.tn / (Epi::kGated ? 2 : 1)) / 8;
   const long long want = (vecs + 255) / 256, most = (long long)device_sm_count() * 8;
-  join_kernel<Epi><<<(unsigned)(want < most ? want : most), 256, 0, stream>>>(p, s, part, M, N);
+  auto kernel = cut.tn == kTile ? join_kernel<Epi, kTile> : join_kernel<Epi, kNarrow>;
+  kernel<<<(unsigned)(want < most ? want : most), 256, 0, stream>>>(p, s, part, M, N);
   note_launches(1);
   return last_launch_status();
 }
@@ -543,14 +571,15 @@ struct EpiPlain {
     if (p.out_f32) store8(static_cast<float *>(p.out) + row * p.N + col, z);
     else store8(static_cast<__nv_bfloat16 *>(p.out) + row * p.N + col, z);
   }
+  template <int TN>
   static __device__ __forceinline__ void tile(const Params &p, const Unit &w, uint32_t acc, int row, int half,
                                               OutRing &out) {
     const int row0 = row - out.lane;
 #pragma unroll 1
-    for (int c = 0; c < kHalf; c += 32) {
-      const int col0 = w.nt * kTile + half * kHalf + c;
+    for (int c = 0; c < TN / 2; c += 32) {
+      const int col0 = w.nt * TN + half * TN / 2 + c;
       uint32_t a[32], v[16];
-      tmem_ld32(acc + half * kHalf + c, a);
+      tmem_ld32(acc + half * TN / 2 + c, a);
       if (col0 >= p.N || row0 >= p.M) continue;   // the whole warp
       if (p.add && row < p.M) {
 #pragma unroll
@@ -581,20 +610,19 @@ struct EpiPlain {
   }
 };
 
-// out[M][N] (+)= A B^T with a plain epilogue; `part` has room for part_bytes.
-template <bool A_MN, bool B_MN>
+inline Cut plain_cut(long long M, long long N, long long K, size_t budget = SIZE_MAX) {
+  return choose_cut(tiles_of(M), tiles_of(N), tiles_of(N, kNarrow), (K + kBK - 1) / kBK, budget);
+}
+// out[M][N] (+)= A B^T with a plain epilogue, B MN-major; `part` has room for part_bytes.
+template <bool A_MN>
 uly_status launch_plain(const CUtensorMap &ta, const CUtensorMap &tb, PlainParams p, long long K, float *part,
                         size_t part_bytes, int kernel_id, cudaStream_t stream) {
   if (!make_out_map(&p.out_map, p.out, p.N, p.M, p.N, p.out_f32 != 0)) return ULY_ERR_CUDA;
-  const Cut cut = choose_cut(tiles_of(p.M) * tiles_of(p.N), (K + kBK - 1) / kBK, part_bytes);
-  const Shape s = make_shape(p.M, p.N, K, kTile, cut);
+  const Cut cut = plain_cut(p.M, p.N, K, part_bytes);
+  const Shape s = make_shape(p.M, p.N, K, 1, cut);
   prof::Scope scope(kernel_id, stream);
-  const uly_status st = launch<EpiPlain, A_MN, B_MN>(ta, tb, s, p, part, stream);
-  return st != ULY_OK ? st : launch_join<EpiPlain>(p, s, part, p.M, p.N, stream);
-}
-// Bytes of partial tiles for [M][N] of K.
-inline size_t plain_part_bytes(long long M, long long N, long long K) {
-  return choose_cut(tiles_of(M) * tiles_of(N), (K + kBK - 1) / kBK).bytes;
+  const uly_status st = launch<EpiPlain, A_MN, true>(ta, tb, s, cut, p, part, stream);
+  return st != ULY_OK ? st : launch_join<EpiPlain>(p, s, cut, part, p.M, p.N, stream);
 }
 
 }  // namespace gemm

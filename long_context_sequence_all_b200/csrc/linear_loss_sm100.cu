@@ -51,8 +51,10 @@ struct LossParams {
 template <bool STORE_P>
 struct EpiLoss {
   using Params = LossParams;
+  template <int TN>
   static __device__ __forceinline__ void tile(const Params &p, const Unit &w, uint32_t acc, int row, int half,
                                               OutRing &out) {
+    static_assert(TN / 2 == kSlot, "a warpgroup's columns are one slot");
     const int col0 = w.nt * kTile + half * kSlot;
     const int ncol = min(kSlot, p.vocab - col0);   // columns of the vocabulary here; may be <= 0
     const bool ok = row < p.rows;
@@ -381,7 +383,7 @@ Plan make_plan(int P, long long T, int D, int V, bool grad, int dw_dtype, long l
     q.factor = take((size_t)q.piece * q.slots * sizeof(float));
     q.p = take((size_t)q.piece * q.ldp * 2);
     q.xk = take((size_t)q.piece * D * 2);
-    const size_t a = plain_part_bytes(q.piece, D, V), b = plain_part_bytes(V, D, q.piece);
+    const size_t a = plain_cut(q.piece, D, V).bytes, b = plain_cut(V, D, q.piece).bytes;
     q.part_bytes = a > b ? a : b;
     q.part = take(q.part_bytes);
     q.acc = take(q.dw_acc ? (size_t)V * D * sizeof(float) : 0);
@@ -393,7 +395,7 @@ Plan make_plan(int P, long long T, int D, int V, bool grad, int dw_dtype, long l
 template <typename T>
 T *at(void *ws, size_t off) { return reinterpret_cast<T *>(static_cast<char *>(ws) + off); }
 
-// No tile of the logits is cut: its epilogue needs the whole sums.
+// Whole tiles of 256 columns: the epilogue needs the finished sums of its slots.
 Cut whole(long long rows, long long V) {
   Cut c;
   c.full = (int)(tiles_of(rows) * tiles_of(V));
@@ -416,7 +418,7 @@ uly_status logits_pass(const __nv_bfloat16 *x, const void *w, int D, LossParams 
   if (!make_map(&tw, w, D, V, D, kHalf) || !make_map(&tx, x, D, rows, D, kHalf) ||
       (GRAD && !make_out_map(&p.p_map, pp, V, rows, ldp)))
     return ULY_ERR_CUDA;
-  return launch<EpiLoss<GRAD>, false, false>(tx, tw, make_shape(rows, V, D, kTile, whole(rows, V)), p, nullptr, stream);
+  return launch_tn<EpiLoss<GRAD>, kTile, false, false>(tx, tw, make_shape(rows, V, D, 1, whole(rows, V)), p, nullptr, stream);
 }
 
 RowsParams rows_of(const Plan &q, const LossParams &p, void *ws, long long t0) {
@@ -526,7 +528,7 @@ uly_status linear_loss_bwd_launch(int32_t P, int64_t tokens, int32_t D, int32_t 
     float *part = at<float>(ws, q.part);
     st = rows <= skinny::kMaxTokens
              ? skinny::launch_plain_mn(pp, q.ldp, w, o.out, rows, D, V, prof::K_LINEAR_LOSS_DX, stream)
-             : launch_plain<false, true>(tz, tw_mn, o, V, part, q.part_bytes, prof::K_LINEAR_LOSS_DX, stream);
+             : launch_plain<false>(tz, tw_mn, o, V, part, q.part_bytes, prof::K_LINEAR_LOSS_DX, stream);
     if (st != ULY_OK) return st;
     // dW (+)= dz^T x; the last piece writes the caller's type
     const bool last = t0 + rows >= tokens;
@@ -536,7 +538,7 @@ uly_status linear_loss_bwd_launch(int32_t P, int64_t tokens, int32_t D, int32_t 
     o.add = t0 > 0 ? acc : nullptr;
     o.out = last ? dw : acc;
     o.out_f32 = !last || dw_dtype == ULY_F32;
-    st = launch_plain<true, true>(tz_mn, tk_mn, o, rows, part, q.part_bytes, prof::K_LINEAR_LOSS_DW, stream);
+    st = launch_plain<true>(tz_mn, tk_mn, o, rows, part, q.part_bytes, prof::K_LINEAR_LOSS_DW, stream);
     if (st != ULY_OK) return st;
   }
   return finish(q, P, tokens, V, labels, ignore_index, shard_sum, shard_count, loss, ws, stream);

@@ -66,7 +66,6 @@ template <int ACT>
 struct EpiLinear {
   using Params = LinearParams;
   static constexpr bool kGated = ACT == ULY_ACT_SWIGLU;
-  static constexpr int kCols = kGated ? 64 : 128;   // output columns of one warpgroup
 
   static __device__ __forceinline__ void add_bias(const Params &p, int col, float (&z)[8], float (&up)[8]) {
     if (!p.bias) return;
@@ -80,19 +79,6 @@ struct EpiLinear {
       for (int e = 0; e < 8; ++e) up[e] += b[e];
     }
   }
-  // eight outputs from their z (and the other factor's), in z
-  static __device__ __forceinline__ void finish(const Params &p, long long row, int col, float (&z)[8],
-                                                const float (&up)[8], bool read_residual) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) z[e] = act_of<ACT>(z[e], up[e]);
-    if (p.residual && read_residual) {
-      float r[8];
-      load8(p.residual + row * p.N + col, r);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) z[e] += r[e];
-    }
-  }
-
   static __device__ __forceinline__ void join8(const Params &p, long long row, int col, float (&z)[8],
                                                float (&up)[8]) {
     add_bias(p, col, z, up);
@@ -100,21 +86,54 @@ struct EpiLinear {
       store8(p.pre + row * p.NZ + col, z);
       if (kGated) store8(p.pre + row * p.NZ + p.N + col, up);
     }
-    finish(p, row, col, z, up, true);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) z[e] = act_of<ACT>(z[e], up[e]);
+    if (p.residual) {
+      float r[8];
+      load8(p.residual + row * p.N + col, r);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) z[e] += r[e];
+    }
     store8(p.y + row * p.N + col, z);
   }
 
+  // A row's next 32 columns of the residual: asked for a turn of the loop ahead.
+  struct Ahead {
+    uint4 v[4];
+    __device__ __forceinline__ void load(const Params &p, int row, int col, bool ok) {
+      if (p.residual && ok)
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+          if (col + 8 * g < p.N) v[g] = __ldg(reinterpret_cast<const uint4 *>(p.residual + (long long)row * p.N + col) + g);
+    }
+    __device__ __forceinline__ void add(const Params &p, int g, float (&z)[8]) const {
+      if (!p.residual) return;
+      const uint32_t w[4] = {v[g].x, v[g].y, v[g].z, v[g].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        z[2 * e] += __uint_as_float(w[e] << 16);
+        z[2 * e + 1] += __uint_as_float(w[e] & 0xffff0000u);
+      }
+    }
+  };
+
+  template <int TN>
   static __device__ __forceinline__ void tile(const Params &p, const Unit &w, uint32_t acc, int row, int half,
                                               OutRing &out) {
+    constexpr int cols = kGated ? TN / 4 : TN / 2;   // output columns of one warpgroup
     const bool ok = row < p.M;
-    const int row0 = row - out.lane;
+    const int row0 = row - out.lane, first = w.nt * 2 * cols + half * cols;
+    Ahead next = {};
+    next.load(p, row, first, ok);
 #pragma unroll 1
-    for (int c = 0; c < kCols; c += 32) {
-      const int c0 = half * kCols + c, col0 = w.nt * 2 * kCols + c0;
+    for (int c = 0; c < cols; c += 32) {
+      const int c0 = half * cols + c, col0 = first + c;
       uint32_t a[kGated ? 64 : 32];
-      if constexpr (kGated) tmem_ld32x2(acc + c0, acc + kHalf + c0, a);
+      if constexpr (kGated) tmem_ld32x2(acc + c0, acc + TN / 2 + c0, a);
       else tmem_ld32(acc + c0, a);
       if (col0 >= p.N || row0 >= p.M) continue;   // the whole warp
+      const Ahead res = next;
+      if (c + 32 < cols) next.load(p, row, col0 + 32, ok);
       uint32_t vy[16], vz[16], vu[kGated ? 16 : 1];
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
@@ -131,7 +150,9 @@ struct EpiLinear {
           vz[4 * g + e] = pack_bf16x2(z[2 * e], z[2 * e + 1]);
           if constexpr (kGated) vu[4 * g + e] = pack_bf16x2(up[2 * e], up[2 * e + 1]);
         }
-        finish(p, row, col, z, up, ok && col < p.N);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) z[e] = act_of<ACT>(z[e], up[e]);
+        res.add(p, g, z);
 #pragma unroll
         for (int e = 0; e < 4; ++e) vy[4 * g + e] = pack_bf16x2(z[2 * e], z[2 * e + 1]);
       }
@@ -198,21 +219,23 @@ uly_status run_skinny(const void *x, const void *w, const LinearParams &p, int K
 int gated(int act) { return act == ULY_ACT_SWIGLU ? 2 : 1; }
 
 Cut linear_cut(int64_t tokens, int32_t in, int32_t out, int32_t act) {
-  return choose_cut(tiles_of(tokens) * tiles_of(out, kTile / gated(act)), (in + kBK - 1) / kBK);
+  return choose_cut(tiles_of(tokens), tiles_of(out, kTile / gated(act)), tiles_of(out, kNarrow / gated(act)),
+                    (in + kBK - 1) / kBK);
 }
 
 template <int ACT>
 uly_status run_linear(const void *x, const void *w, LinearParams p, int K, float *part, cudaStream_t stream) {
+  const Cut cut = linear_cut(p.M, K, p.N, ACT);
   CUtensorMap ta, tb;
-  if (!make_map(&ta, x, K, p.M, K, kHalf) || !make_map(&tb, w, K, p.NZ, K, kHalf) ||
+  if (!make_map(&ta, x, K, p.M, K, kHalf) || !make_map(&tb, w, K, p.NZ, K, b_box(cut)) ||
       !make_out_map(&p.y_map, p.y, p.N, p.M, p.N) || (p.pre && !make_out_map(&p.pre_map, p.pre, p.N, p.M, p.NZ)) ||
       (p.pre && p.NZ > p.N && !make_out_map(&p.up_map, p.pre + p.N, p.N, p.M, p.NZ)))
     return ULY_ERR_CUDA;
   using Epi = EpiLinear<ACT>;
-  const Shape s = make_shape(p.M, p.N, K, Epi::kCols * 2, linear_cut(p.M, K, p.N, ACT));
+  const Shape s = make_shape(p.M, p.N, K, gated(ACT), cut);
   prof::Scope scope(prof::K_LINEAR, stream);
-  const uly_status st = launch<Epi, false, false>(ta, tb, s, p, part, stream);
-  return st != ULY_OK ? st : launch_join<Epi>(p, s, part, p.M, p.N, stream);
+  const uly_status st = launch<Epi, false, false>(ta, tb, s, cut, p, part, stream);
+  return st != ULY_OK ? st : launch_join<Epi>(p, s, cut, part, p.M, p.N, stream);
 }
 
 // ------------------------------------------------------------ dz and dbias
@@ -294,7 +317,7 @@ BwdPlan bwd_plan(int64_t tokens, int32_t in, int32_t out, int32_t act) {
   q.row_ctas = dz_row_ctas(tokens, out);
   q.off_bias = act == ULY_ACT_NONE ? 0 : up256((size_t)tokens * q.nz * 2);
   q.off_part = q.off_bias + up256((size_t)q.row_ctas * 8 * q.nz * sizeof(float));
-  const size_t a = plain_part_bytes(tokens, in, q.nz), b = plain_part_bytes(q.nz, in, tokens);
+  const size_t a = plain_cut(tokens, in, q.nz).bytes, b = plain_cut(q.nz, in, tokens).bytes;
   q.part = a > b ? a : b;
   q.bytes = q.off_part + up256(q.part);
   return q;
@@ -378,14 +401,14 @@ uly_status linear_bwd_launch(int64_t tokens, int32_t in, int32_t out, int32_t ac
     if (!make_map(&ta, dz, q.nz, tokens, q.nz, kHalf) || !make_map(&tb, w, in, q.nz, in, 64)) return ULY_ERR_CUDA;
     PlainParams p = {};
     p.out = dx; p.M = tokens; p.N = in;
-    const uly_status st = launch_plain<false, true>(ta, tb, p, q.nz, part, q.part, prof::K_LINEAR_DX, stream);
+    const uly_status st = launch_plain<false>(ta, tb, p, q.nz, part, q.part, prof::K_LINEAR_DX, stream);
     if (st != ULY_OK) return st;
   }
   if (dw) {   // dW[nz][in] = dz^T x
     if (!make_map(&ta, dz, q.nz, tokens, q.nz, 64) || !make_map(&tb, x, in, tokens, in, 64)) return ULY_ERR_CUDA;
     PlainParams p = {};
     p.out = dw; p.out_f32 = dw_dtype == ULY_F32; p.M = q.nz; p.N = in;
-    return launch_plain<true, true>(ta, tb, p, tokens, part, q.part, prof::K_LINEAR_DW, stream);
+    return launch_plain<true>(ta, tb, p, tokens, part, q.part, prof::K_LINEAR_DW, stream);
   }
   return ULY_OK;
 }
