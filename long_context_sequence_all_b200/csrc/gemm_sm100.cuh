@@ -132,26 +132,35 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, uint32_t sr
                : "memory");
 }
 
-// One epilogue warp's way out: 32 rows (one a lane) x 64 bytes of columns
-// staged with the 64-byte swizzle of make_out_map(), the slots taken in turn.
+// One epilogue warp's way out: 32 rows (one a lane) x 64 bytes of columns a slot,
+// staged with the 64-byte swizzle of make_out_map(); two slots are one turn (one
+// proxy fence, two stores), two turns are under way at a time.
 struct OutRing {
-  uint32_t base, slot;
+  uint32_t base, turn;   // turn: which two of the four slots
   int lane;
-  // v: this lane's columns (32 of two bytes, packed, or 16 of four); all lanes of the warp together
-  __device__ __forceinline__ void put(const CUtensorMap *map, int col, int row0, const uint32_t (&v)[16]) {
-    if (lane == 0) bulk_wait_group_read<kOutSlots - 1>();
+  // All lanes of the warp together: the turn's slots are free ...
+  __device__ __forceinline__ void begin() {
+    if (lane == 0) bulk_wait_group_read<1>();
     __syncwarp();
-    const uint32_t at = base + slot * kOutSlot;
+  }
+  // ... take this lane's columns (32 of two bytes, packed, or 16 of four) ...
+  __device__ __forceinline__ uint32_t slot(int i) const { return base + (2 * turn + i) * kOutSlot; }
+  __device__ __forceinline__ void write(int i, const uint32_t (&v)[16]) const {
+    const uint32_t at = slot(i) + lane * 64;
 #pragma unroll
     for (int c = 0; c < 4; ++c)
-      st_shared_v4(at + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4), v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+      st_shared_v4(at + ((c ^ ((lane >> 1) & 3)) << 4), v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+  }
+  // ... and leave: slot i for columns from col<i> of map<i> (a null map: nothing).
+  __device__ __forceinline__ void end(const CUtensorMap *map0, int col0, const CUtensorMap *map1, int col1, int row0) {
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) {
-      tma_store_2d(map, at, col, row0);
+      if (map0) tma_store_2d(map0, slot(0), col0, row0);
+      if (map1) tma_store_2d(map1, slot(1), col1, row0);
       bulk_commit_group();
     }
-    slot = (slot + 1) % kOutSlots;
+    turn ^= 1;
   }
 };
 
@@ -197,12 +206,14 @@ __device__ __forceinline__ void store_partial(const CUtensorMap *map, const Unit
   for (int c = half * TN / 2; c < (half + 1) * TN / 2; c += 32) {
     uint32_t a[32], v[16];
     tmem_ld32(acc + c, a);
+    out.begin();
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
 #pragma unroll
       for (int e = 0; e < 16; ++e) v[e] = a[16 * h + e];
-      out.put(map, c + 16 * h, w.part * kTile + row_in_tile, v);
+      out.write(h, v);
     }
+    out.end(map, c, map, c + 16, w.part * kTile + row_in_tile);
   }
 }
 
@@ -325,11 +336,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     int it = 0;
     for (int u = cluster; u < units; u += clusters, ++it) {
       const int buf = it & 1;
+      const Unit w = unit_of(sh, u);
       if (!__all_sync(0xffffffffu, mbar_wait(bar(B_ACCF + buf), (uint32_t)((it >> 1) & 1), abort_flag, sh.err,
                                              sh.wait_limit)))
         break;
       tc_fence_after();
-      const Unit w = unit_of(sh, u);
       const uint32_t acc = tmem + ((uint32_t)(quarter * 32) << 16) + buf * TN;
       const int row0 = (int)rank * kHalf + quarter * 32;
       if (w.part >= 0) store_partial<TN>(&tmPart, w, acc, row0, half, out);
@@ -576,14 +587,14 @@ struct EpiPlain {
                                               OutRing &out) {
     const int row0 = row - out.lane;
 #pragma unroll 1
-    for (int c = 0; c < TN / 2; c += 32) {
+    for (int c = 0; c < TN / 2; c += 64) {
       const int col0 = w.nt * TN + half * TN / 2 + c;
-      uint32_t a[32], v[16];
-      tmem_ld32(acc + half * TN / 2 + c, a);
+      uint32_t a[64], v[16];
+      tmem_ld64(acc + half * TN / 2 + c, a);
       if (col0 >= p.N || row0 >= p.M) continue;   // the whole warp
       if (p.add && row < p.M) {
 #pragma unroll
-        for (int g = 0; g < 4; ++g)
+        for (int g = 0; g < 8; ++g)
           if (col0 + 8 * g < p.N) {
             float z[8];
 #pragma unroll
@@ -594,17 +605,31 @@ struct EpiPlain {
           }
       }
       __syncwarp();
+      const CUtensorMap *map = &p.out_map;
       if (p.out_f32) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
+          const int c0 = col0 + 32 * h;
+          if (c0 >= p.N) break;
+          out.begin();
 #pragma unroll
-          for (int e = 0; e < 16; ++e) v[e] = a[16 * h + e];
-          if (col0 + 16 * h < p.N) out.put(&p.out_map, col0 + 16 * h, row0, v);
+          for (int i = 0; i < 2; ++i) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) v[e] = a[32 * h + 16 * i + e];
+            out.write(i, v);
+          }
+          out.end(map, c0, c0 + 16 < p.N ? map : nullptr, c0 + 16, row0);
         }
       } else {
+        out.begin();
 #pragma unroll
-        for (int e = 0; e < 16; ++e) v[e] = pack_bf16x2(__uint_as_float(a[2 * e]), __uint_as_float(a[2 * e + 1]));
-        out.put(&p.out_map, col0, row0, v);
+        for (int i = 0; i < 2; ++i) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            v[e] = pack_bf16x2(__uint_as_float(a[32 * i + 2 * e]), __uint_as_float(a[32 * i + 2 * e + 1]));
+          out.write(i, v);
+        }
+        out.end(map, col0, col0 + 32 < p.N ? map : nullptr, col0 + 32, row0);
       }
     }
   }

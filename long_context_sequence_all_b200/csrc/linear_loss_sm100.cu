@@ -62,50 +62,50 @@ struct EpiLoss {
     if (ncol <= 0 || row0 >= p.rows) return;       // the whole warp
     const int y = ok ? __ldg(p.labels + row) : p.ignore_index;
     const bool counted = y != p.ignore_index && y >= 0 && y < p.vocab;
-    float m = -INFINITY;
-#pragma unroll 1
-    for (int c = 0; c < kSlot; c += 32) {
-      uint32_t a[32];
-      tmem_ld32(acc + half * kSlot + c, a);
-      if (c + 32 <= ncol) {
+    // the row's 128 logits stay in registers from here on
+    uint32_t a[kSlot];
+    tmem_ld128(acc + half * kSlot, a);
+    if (ncol < kSlot) {
 #pragma unroll
-        for (int e = 0; e < 32; ++e) m = fmaxf(m, __uint_as_float(a[e]));
-      } else {
-#pragma unroll
-        for (int e = 0; e < 32; ++e)
-          if (c + e < ncol) m = fmaxf(m, __uint_as_float(a[e]));
-      }
+      for (int e = 0; e < kSlot; ++e)
+        if (e >= ncol) a[e] = __float_as_uint(-INFINITY);
     }
+    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+    for (int e = 0; e < kSlot; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(a[e]));
+    const float m = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
     const float ref = m == -INFINITY ? 0.f : m;   // every logit -inf: each term is 0
+    if (counted && y >= col0 && y < col0 + kSlot) {
+      float t = 0.f;
+#pragma unroll
+      for (int e = 0; e < kSlot; ++e) t = y == col0 + e ? __uint_as_float(a[e]) : t;
+      p.target[row] = t;
+    }
+    __syncwarp();
     float s[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 1
-    for (int c = 0; c < kSlot; c += 32) {
-      uint32_t a[32];
-      tmem_ld32(acc + half * kSlot + c, a);
-      if (counted && y >= col0 + c && y < col0 + c + 32) {
-        float t = 0.f;
 #pragma unroll
-        for (int e = 0; e < 32; ++e) t = y == col0 + c + e ? __uint_as_float(a[e]) : t;
-        p.target[row] = t;
-      }
-      __syncwarp();
-      if (c >= ncol) continue;
-      uint32_t v[16];
+    for (int c = 0; c < kSlot; c += 64) {
+      if (c >= ncol) break;
+      if (STORE_P) out.begin();
 #pragma unroll
-      for (int e = 0; e < 32; e += 2) {
-        // the difference first: exact at any size of the logits
-        float q0 = ex2_approx((__uint_as_float(a[e]) - ref) * kLog2e);
-        float q1 = ex2_approx((__uint_as_float(a[e + 1]) - ref) * kLog2e);
-        if (c + e >= ncol) q0 = 0.f;
-        if (c + e + 1 >= ncol) q1 = 0.f;
-        s[e & 2] += q0;
-        s[(e & 2) + 1] += q1;
-        if (STORE_P) {
-          const __half2 h = __floats2half2_rn(q0 * kScale, q1 * kScale);
-          v[e / 2] = *reinterpret_cast<const uint32_t *>(&h);
+      for (int h = 0; h < 2; ++h) {
+        uint32_t v[16];
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+          // the difference first: exact at any size of the logits
+          const float q0 = ex2_approx((__uint_as_float(a[c + 32 * h + e]) - ref) * kLog2e);
+          const float q1 = ex2_approx((__uint_as_float(a[c + 32 * h + e + 1]) - ref) * kLog2e);
+          s[e & 2] += q0;
+          s[(e & 2) + 1] += q1;
+          if (STORE_P) {
+            const __half2 x = __floats2half2_rn(q0 * kScale, q1 * kScale);
+            v[e / 2] = *reinterpret_cast<const uint32_t *>(&x);
+          }
         }
+        if (STORE_P) out.write(h, v);
       }
-      if (STORE_P) out.put(&p.p_map, col0 + c, row0, v);
+      if (STORE_P)
+        out.end(&p.p_map, col0 + c, c + 32 < ncol ? &p.p_map : nullptr, col0 + c + 32, row0);
     }
     if (ok) p.pairs[(long long)(w.nt * 2 + half) * p.rows_pad + row] = make_float2(ref, (s[0] + s[1]) + (s[2] + s[3]));
   }

@@ -157,10 +157,16 @@ struct EpiLinear {
         for (int e = 0; e < 4; ++e) vy[4 * g + e] = pack_bf16x2(z[2 * e], z[2 * e + 1]);
       }
       __syncwarp();
-      out.put(&p.y_map, col0, row0, vy);
-      if (p.pre) {
-        out.put(&p.pre_map, col0, row0, vz);
-        if constexpr (kGated) out.put(&p.up_map, col0, row0, vu);
+      out.begin();
+      out.write(0, vy);
+      if (p.pre) out.write(1, vz);
+      out.end(&p.y_map, col0, p.pre ? &p.pre_map : nullptr, col0, row0);
+      if constexpr (kGated) {
+        if (p.pre) {
+          out.begin();
+          out.write(0, vu);
+          out.end(&p.up_map, col0, nullptr, 0, row0);
+        }
       }
     }
   }
