@@ -343,6 +343,54 @@ __global__ void __launch_bounds__(256) shard_sum_kernel(const float *__restrict_
   }
 }
 
+// The same and the fold over the shards in one launch, for up to 8 shards of a
+// modest batch: 32 warps in equal parts to the shards, their sums joined in warp
+// order.
+constexpr int kCloseShards = 8;
+constexpr long long kCloseTokens = 16384;
+__global__ void __launch_bounds__(1024) loss_close_kernel(const float *__restrict__ row_loss,
+                                                          const int32_t *__restrict__ labels, long long per, int P,
+                                                          int vocab, int ignore_index, float *__restrict__ shard_sum,
+                                                          int64_t *__restrict__ shard_count, float *__restrict__ loss) {
+  __shared__ double sh_s[32];
+  __shared__ int sh_c[32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, each = 32 / P, r = warp / each;
+  double a = 0.0;
+  int c = 0;
+  if (r < P) {
+    const long long t0 = (long long)r * per;
+#pragma unroll 4
+    for (long long i = (warp - r * each) * 32 + lane; i < per; i += 32 * each) {
+      const int y = __ldg(labels + t0 + i);
+      if (y != ignore_index && y >= 0 && y < vocab) {
+        a += (double)row_loss[t0 + i];
+        ++c;
+      }
+    }
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) {
+    a += __shfl_down_sync(0xffffffffu, a, off);
+    c += __shfl_down_sync(0xffffffffu, c, off);
+  }
+  if (lane == 0) { sh_s[warp] = a; sh_c[warp] = c; }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    double all = 0.0;
+    long long n = 0;
+    for (int k = 0; k < P; ++k) {
+      double s = 0.0;
+      long long m = 0;
+      for (int w = 0; w < each; ++w) { s += sh_s[k * each + w]; m += sh_c[k * each + w]; }
+      shard_sum[k] = (float)s;
+      shard_count[k] = m;
+      all += s;
+      n += m;
+    }
+    *loss = (float)(all / (double)n);   // 0/0 -> NaN when no token is valid
+  }
+}
+
 size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
 long long round_up(long long v, long long m) { return (v + m - 1) / m * m; }
 
@@ -433,6 +481,13 @@ RowsParams rows_of(const Plan &q, const LossParams &p, void *ws, long long t0) {
 
 uly_status finish(const Plan &q, int P, long long T, int V, const int32_t *labels, int ignore_index, float *shard_sum,
                   int64_t *shard_count, float *loss, void *ws, cudaStream_t stream) {
+  if (P <= kCloseShards && T <= kCloseTokens) {
+    prof::Scope scope(prof::K_LOSS_FINALIZE, stream);
+    loss_close_kernel<<<1, 1024, 0, stream>>>(at<float>(ws, q.row_loss), labels, T / P, P, V, ignore_index, shard_sum,
+                                              shard_count, loss);
+    note_launches(1);
+    return last_launch_status();
+  }
   shard_sum_kernel<<<P, 256, 0, stream>>>(at<float>(ws, q.row_loss), labels, T / P, V, ignore_index,
                                           at<double>(ws, q.psum), at<long long>(ws, q.pcnt));
   note_launches(1);

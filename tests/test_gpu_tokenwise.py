@@ -382,6 +382,9 @@ LOSSES = [  # P, T, D, V, spread of the logits, ignored share, piece
     (2, 1100, 256, 513, 1.0, 0.1, 256),        # five pieces, the last one short
     (2, 514, 64, 2049, 2.0, 0.0, 257),         # pieces that end inside a tile
     (2, 1026, 72, 4099, 2.0, 0.3, 1024),       # a last piece of two rows
+    (11, 319, 64, 300, 1.0, 0.2, 0),           # more shards than are summed in one go
+    (5, 16395, 8, 40, 1.0, 0.2, 0),            # more tokens than are
+    (7, 63, 64, 300, 1.0, 0.2, 0),
     (1, 130, 64, 3000, 60.0, 0.0, 0),          # logits hundreds apart
 ]
 
