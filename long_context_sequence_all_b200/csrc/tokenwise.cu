@@ -82,7 +82,7 @@ uly_status loss_shape(int32_t world, int64_t tokens, int32_t hidden, int32_t voc
   if (hidden % 8) return ULY_ERR_ALIGN;
   auto tiles = [](long long v) { return (v + 255) / 256; };
   const long long most = 0x7fffffffLL / 32;
-  if (vocab > kMaxRows || hidden > kMaxRows || tiles(tokens) * tiles(vocab) > most ||
+  if (vocab > (1 << 28) || hidden > kMaxRows || tiles(tokens) * tiles(vocab) > most ||
       tiles(tokens) * tiles(hidden) > most || tiles(vocab) * tiles(hidden) > most)
     return ULY_ERR_SHAPE;
   return ULY_OK;

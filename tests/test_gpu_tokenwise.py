@@ -13,6 +13,9 @@ Element-wise bounds, from the arithmetic of the GPU path:
 First-order terms only; the factor 1.05 covers products of two of them.
 """
 import math
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -576,3 +579,59 @@ def test_block_on_another_stream_and_in_a_graph():
     torch.cuda.synchronize()
     assert all(torch.equal(i, j) for i, j in zip(a, b))
     assert U.ulysses_read_error() == 0
+
+
+def test_products_report_a_wait_that_ran_out():
+    """A pipeline wait cut short is reported in the error word, the launch ends
+    and frees its tensor memory: the next call is right again."""
+    g = _gen(71)
+    calls = []
+    for T, K, N in ((600, 512, 512), (9, 2048, 256)):        # a pair of CTAs a tile; the clusters for few tokens
+        x, w = _rnd(g, T, K), _rnd(g, N, K, scale=K ** -0.5)
+        calls.append((x, w, U.ulysses_linear(x, w)))
+    torch.cuda.synchronize()
+    for x, w, want in calls:
+        assert U.lib().ulysses_set_wait_limit(300) == 0
+        try:
+            U.ulysses_linear(x, w)
+            torch.cuda.synchronize()
+        finally:
+            U.lib().ulysses_set_wait_limit(0)
+        assert U.ulysses_read_error() & (1 << 9)
+        assert torch.equal(U.ulysses_linear(x, w), want)
+        assert U.ulysses_read_error() == 0
+
+
+@pytest.mark.parametrize("op", ["linear", "norm", "loss"])
+def test_first_call_of_a_process_may_be_captured(op):
+    """Nothing an operator sets up on its first call is forbidden in a capture."""
+    code = f"""
+import torch
+from long_context_sequence_all_b200 import ulysses as U
+torch.cuda.init()
+m = lambda *s: torch.ones(*s, device="cuda", dtype=torch.bfloat16)
+x, w, y = m(300, 64), m(512, 64), torch.zeros(300, device="cuda", dtype=torch.int32)
+q, v = m(1, 1, 300, 64), m(64)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    if "{op}" == "linear":
+        out = U.ulysses_linear(x, w)
+        back = U.ulysses_linear_bwd(x, w, out)
+    elif "{op}" == "norm":
+        out, _ = U.ulysses_residual_norm(q, q, w_pre=v)
+        back = U.ulysses_residual_norm_bwd(q, q, du=q, w_pre=v)
+    else:
+        out = U.ulysses_linear_loss(x, w, y, 2)[2]
+        back = U.ulysses_linear_loss_bwd(x, w, y, 2)
+g.replay()
+torch.cuda.synchronize()
+want = {{"linear": 64.0, "norm": 2.0}}.get("{op}")
+print(out.flatten()[0].item())
+assert want is None or out.flatten()[0].item() == want
+assert want is not None or abs(out.item() - 6.238325) < 1e-4      # log(512): all logits equal
+assert U.ulysses_read_error() == 0
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stdout + r.stderr
