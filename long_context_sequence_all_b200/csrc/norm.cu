@@ -21,19 +21,23 @@
 // Each group writes one partial per column and run, and a second kernel folds
 // the partials in a fixed order, so every output is bitwise repeatable.
 //
-// How: persistent teams, a warp or a CTA.  A team's rows arrive by bulk copies
-// in a ring of shared-memory stages, so the loads run ahead of the two row sums
-// (each a barrier of the team).  A thread takes up to five 16-byte vectors of a
+// How: persistent teams of a warp or of several.  A team's rows arrive by bulk
+// copies in a ring of shared-memory stages, so the loads run ahead of the two row
+// sums (each a barrier of the team).  The CTA's teams share the weights, and a
+// gate that all tokens share, in shared memory (where two stages fit beside them):
+// from L1, which the streams keep emptying, their latency was the forward's
+// largest stall.  A thread takes up to five 16-byte vectors of a
 // row (backward: two, its column sums take the registers).  Short rows share a
-// warp, a power of two of lanes each, and arrive several at a time (253074 x 160
-// with one row a warp: 142 us, 71 us so); of long ones few warps share a
-// row: at 2560 bf16 columns two warps (backward: five)
-// instead of ten, which had left both directions waiting for barriers and
-// shuffles at 3.2 and 2.6 TB/s.  Arithmetic runs on pairs of fp32 values.
-// 65536 x 2560 bf16 with a channel gate: forward 235 us (5.7 TB/s of its 1.34
-// GB), backward 402 us (5.0 TB/s of 2.01 GB) + 10.5 us of folding; the forward
-// is at the memory's rate but for the gaps between rows, the backward issues
-// about 3000 instructions a row and is bound by them as much.
+// warp, a power of two of lanes each, and arrive several at a time (253074 x 160:
+// 142 us with one row a warp, 65 us so); of long ones few warps share a row: at
+// 2560 bf16 columns two warps (backward: five) instead of ten, which had left both
+// directions waiting for barriers and shuffles at 3.2 and 2.6 TB/s.  Arithmetic
+// runs on pairs of fp32 values.
+// 65536 x 2560 bf16 with a channel gate: forward 249 us (5.4 TB/s of its 1.34
+// GB), backward 416 us (4.8 TB/s of 2.01 GB) + 10 us of folding.  The forward is
+// near the memory's rate (a copy: 6.5 TB/s); the backward issues about 3800
+// instructions a row and is bound by their latency (with a gate of every token it
+// moves a third more in 452 us).
 #include <atomic>
 
 #include "common.cuh"
@@ -115,19 +119,26 @@ struct Vec<float> {
   }
 };
 
-constexpr int kMaxGroup = 512;                 // threads of one row
+constexpr int kMaxLanes = 512;                 // threads of one row
 constexpr int kMaxVecs = 2048;                 // vectors of one row (32 KB)
-constexpr int kWarpTeams = 4;                  // teams of a CTA where a team is one warp
+constexpr int kMaxTeams = 10;                  // teams of a CTA
+constexpr int kWarpTeams = 4;                  // ... where a team is one warp
 constexpr int kMaxStages = 4;
-constexpr uint32_t kRingBytes = 200 * 1024;    // shared memory the stages of an SM's CTAs may take
+constexpr uint32_t kRingBytes = 200 * 1024;    // shared memory the stages (and weights) of an SM's CTAs may take
 
-// Sums of K values over a row's threads: `g` lanes of a warp (a power of two),
-// or the whole CTA (then also a barrier of it; two buffers taken in turn, so one
-// barrier a call is enough).
-template <int K, bool WARP>
-__device__ __forceinline__ void row_sum(float (&v)[K], int g, float (*sh)[K], int &turn) {
+// Sums of K values over a row's threads: `lanes` of a warp (a power of two), or a
+// team of several warps (then also a barrier of it: named barrier team + 1; two
+// buffers taken in turn, so one barrier a call is enough).
+template <bool WARP, bool STAGED>
+__device__ __forceinline__ void team_barrier(int team, int lanes) {
+  if (WARP) __syncwarp();
+  else if (!STAGED) __syncthreads();   // the CTA's only team
+  else sm100::named_bar_sync(team + 1, lanes);
+}
+template <int K, bool WARP, bool STAGED>
+__device__ __forceinline__ void row_sum(float (&v)[K], int lanes, int team, float (*sh)[K], int &turn) {
   if (WARP) {
-    for (int off = g >> 1; off > 0; off >>= 1)
+    for (int off = lanes >> 1; off > 0; off >>= 1)
 #pragma unroll
       for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], off);
     return;
@@ -136,24 +147,18 @@ __device__ __forceinline__ void row_sum(float (&v)[K], int g, float (*sh)[K], in
   for (int off = 16; off > 0; off >>= 1)
 #pragma unroll
     for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], off);
-  const int warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  float (*buf)[K] = sh + (kMaxGroup / 32) * turn;
+  const int warp = threadIdx.x >> 5, warps = STAGED ? lanes >> 5 : blockDim.x >> 5, first = STAGED ? team * warps : 0;
+  float (*buf)[K] = sh + 32 * turn;
   turn ^= 1;
   if ((threadIdx.x & 31) == 0)
 #pragma unroll
     for (int k = 0; k < K; ++k) buf[warp][k] = v[k];
-  __syncthreads();
+  team_barrier<WARP, STAGED>(team, lanes);
 #pragma unroll
   for (int k = 0; k < K; ++k) v[k] = 0.f;
   for (int w = 0; w < warps; ++w)   // fixed order, the same in every thread
 #pragma unroll
-    for (int k = 0; k < K; ++k) v[k] += buf[w][k];
-}
-
-template <bool WARP>
-__device__ __forceinline__ void team_barrier() {
-  if (WARP) __syncwarp();
-  else __syncthreads();
+    for (int k = 0; k < K; ++k) v[k] += buf[first + w][k];
 }
 
 // Tensors whose rows a stage holds, one after the other.
@@ -168,13 +173,19 @@ struct RingSrc {
 
 struct RingShape {
   int slots, stages;   // tensors of a stage, stages of a team
-  int lanes;           // of a row where a team is a warp
+  int lanes;           // threads of a row: of a warp, or a whole team of warps
   int *err;
+};
+
+// Vectors that all rows share.
+struct Shared3 {
+  const uint4 *p[3];   // nullable
 };
 
 // A team's ring of stages, each of `rows` rows of every tensor, and this
 // thread's place in it: thread `l` of `lanes` of row `sub` of a stage.
-template <bool WARP>
+// STAGED: the vectors all rows share are brought into shared memory first.
+template <bool WARP, bool STAGED>
 struct Ring {
   uint8_t *base;
   uint64_t *bars;
@@ -183,17 +194,28 @@ struct Ring {
   uint32_t phase;
   int l, lanes, sub, rows;
 
-  __device__ __forceinline__ Ring(uint8_t *mem, uint64_t *barriers, volatile int *abort, int vecs, const RingShape &s) {
-    const int team = WARP ? threadIdx.x >> 5 : 0, lane = threadIdx.x & 31;
-    lanes = WARP ? s.lanes : blockDim.x;
+  int team;
+  uint8_t *mem;
+
+  __device__ __forceinline__ Ring(uint8_t *smem, uint64_t *barriers, volatile int *abort, int vecs, const RingShape &s,
+                                  const Shared3 &all) {
+    const int lane = threadIdx.x & 31;
+    lanes = WARP || STAGED ? s.lanes : blockDim.x;
+    team = WARP ? threadIdx.x >> 5 : STAGED ? threadIdx.x / s.lanes : 0;
     rows = WARP ? 32 / s.lanes : 1;
-    l = WARP ? lane & (s.lanes - 1) : threadIdx.x;
+    l = WARP ? lane & (s.lanes - 1) : STAGED ? threadIdx.x - team * s.lanes : threadIdx.x;
     sub = WARP ? lane / s.lanes : 0;
     row_bytes = (uint32_t)vecs * 16;
     slot_bytes = row_bytes * rows;
     stage_bytes = slot_bytes * s.slots;
     stages = s.stages;
-    base = mem + (size_t)team * stages * stage_bytes;
+    mem = smem;
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
+      if (STAGED && all.p[k])
+        for (int i = threadIdx.x; i < vecs; i += blockDim.x)
+          reinterpret_cast<uint4 *>(mem + k * row_bytes)[i] = __ldg(all.p[k] + i);
+    base = mem + (STAGED ? 3 * row_bytes : 0) + (size_t)team * stages * stage_bytes;
     bars = barriers + team * kMaxStages;
     at = 0;
     phase = 0;
@@ -203,6 +225,11 @@ struct Ring {
     sm100::fence_mbar_init();
     __syncthreads();
   }
+  // vector i * lanes + l of those that all rows share
+  __device__ __forceinline__ uint4 common(const Shared3 &all, int k, int at) const {
+    return STAGED ? reinterpret_cast<const uint4 *>(mem + k * row_bytes)[l + at] : __ldg(all.p[k] + l + at);
+  }
+  __device__ __forceinline__ void barrier() const { team_barrier<WARP, STAGED>(team, lanes); }
   __device__ __forceinline__ uint32_t slot(int st, int k) const {
     return sm100::smem_u32(base + st * stage_bytes + k * slot_bytes);
   }
@@ -249,7 +276,8 @@ struct NormParams {
   RingSrc src;
   RingShape ring;
   int sx, sh, sg;   // stage slots of x, h and a token's gate (-1: none)
-  const uint4 *gate, *w_post, *w_pre;
+  Shared3 all;      // w_post, w_pre, a gate that all tokens share
+  const uint4 *gate;
   uint4 *r, *u;
   int rows, vecs, gate_mode, B, s;
   float res_scale, eps, inv_d;
@@ -257,20 +285,21 @@ struct NormParams {
 
 // Thread `l` of a row's `tpr` takes its vectors l, l + tpr, ...: NV of them, of
 // which only the last can lie behind the row's end.
-template <typename T, int NV, bool WARP>
-__global__ void __launch_bounds__(kMaxGroup) residual_norm_kernel(const __grid_constant__ NormParams p) {
+template <typename T, int NV, bool WARP, bool STAGED>
+__global__ void __launch_bounds__(!WARP ? 640 : NV <= 2 ? 1024 : 512) residual_norm_kernel(const __grid_constant__ NormParams p) {
   constexpr int E = Vec<T>::N;
   extern __shared__ __align__(128) uint8_t stage_mem[];
-  __shared__ uint64_t bars[kWarpTeams * kMaxStages];
+  __shared__ uint64_t bars[kMaxTeams * kMaxStages];
   __shared__ int abort_flag;
-  __shared__ float sh[2 * (kMaxGroup / 32)][1];
+  __shared__ float sh[2 * 32][1];
   int turn = 0;
-  Ring<WARP> ring(stage_mem, bars, &abort_flag, p.vecs, p.ring);
+  Ring<WARP, STAGED> ring(stage_mem, bars, &abort_flag, p.vecs, p.ring, p.all);
   const int l = ring.l, tpr = ring.lanes, rows = p.rows;
-  const long long first = (WARP ? (long long)blockIdx.x * kWarpTeams + (threadIdx.x >> 5) : blockIdx.x) * ring.rows;
-  const long long step = (WARP ? (long long)gridDim.x * kWarpTeams : gridDim.x) * ring.rows;
+  const int teams = WARP ? kWarpTeams : STAGED ? blockDim.x / tpr : 1;
+  const long long first = ((long long)blockIdx.x * teams + ring.team) * ring.rows;
+  const long long step = (long long)gridDim.x * teams * ring.rows;
   const bool tail = l + (NV - 1) * tpr < p.vecs;   // this thread's last vector exists
-  const bool branch = p.sh >= 0, post = p.w_post != nullptr, gated = p.gate_mode != ULY_GATE_NONE;
+  const bool branch = p.sh >= 0, post = p.all.p[0] != nullptr, gated = p.gate_mode != ULY_GATE_NONE;
   const uint4 zero = make_uint4(0, 0, 0, 0);
   auto issue = [&](long long t, int st) {
     if (t < rows) ring.issue(p.src, t, (int)min((long long)ring.rows, rows - t), st);
@@ -279,15 +308,15 @@ __global__ void __launch_bounds__(kMaxGroup) residual_norm_kernel(const __grid_c
   int done = -1;   // stage whose rows every thread has finished with, after the team's next barrier
   for (long long t0 = first; t0 < rows; t0 += step, ring.next()) {
     if (ring.stages == 1 && done >= 0) {   // no stage to run ahead into
-      team_barrier<WARP>();
+      ring.barrier();
       issue(t0, 0);
     }
     ring.wait(&abort_flag, p.ring.err);
     const long long t = t0 + ring.sub;
     const bool row_ok = !WARP || t < rows;
-    const uint4 *gv = p.gate + l;
-    if (p.gate_mode == ULY_GATE_TOKEN) gv = ring.row(p.sg);
-    else if (p.gate_mode == ULY_GATE_SEQUENCE) gv += (long long)((int)t / p.s % p.B) * p.vecs;
+    const bool own_gate = p.sg >= 0, all_gate = p.gate_mode == ULY_GATE_CHANNEL;
+    const uint4 *gv = p.gate + l;   // of this token's sequence
+    if (p.gate_mode == ULY_GATE_SEQUENCE) gv += (long long)((int)t / p.s % p.B) * p.vecs;
     F2 r[NV][E], q = f2(0.f);
     if (branch) {
       const uint4 *hv = ring.row(p.sh);
@@ -299,7 +328,7 @@ __global__ void __launch_bounds__(kMaxGroup) residual_norm_kernel(const __grid_c
       }
     }
     float ss[1] = {sum2(q)};
-    if (post || !WARP) row_sum<1, WARP>(ss, tpr, sh, turn);   // a CTA's barrier also frees the previous stage
+    if (post || !WARP) row_sum<1, WARP, STAGED>(ss, tpr, ring.team, sh, turn);   // its barrier also frees the previous stage
     if (WARP) __syncwarp();
     if (done >= 0 && ring.stages > 1) issue(t0 + (ring.stages - 1) * step, done);
     const F2 hs = f2(post ? rsqrtf(ss[0] * p.inv_d + p.eps) : 1.f), a = f2(p.res_scale);
@@ -314,13 +343,13 @@ __global__ void __launch_bounds__(kMaxGroup) residual_norm_kernel(const __grid_c
       if (branch) {
         if (post) {
           F2 w[E];
-          Vec<T>::unpack(ok ? __ldg(p.w_post + l + i * tpr) : zero, w);
+          Vec<T>::unpack(ok ? ring.common(p.all, 0, i * tpr) : zero, w);
 #pragma unroll
           for (int e = 0; e < E; ++e) r[i][e] = mul(r[i][e], mul(hs, w[e]));
         }
         if (gated) {
           F2 g[E];
-          Vec<T>::unpack(ok ? gv[i * tpr] : zero, g);
+          Vec<T>::unpack(!ok ? zero : all_gate ? ring.common(p.all, 2, i * tpr) : own_gate ? ring.row(p.sg)[i * tpr] : __ldg(gv + i * tpr), g);
 #pragma unroll
           for (int e = 0; e < E; ++e) r[i][e] = mul(r[i][e], g[e]);
         }
@@ -337,14 +366,14 @@ __global__ void __launch_bounds__(kMaxGroup) residual_norm_kernel(const __grid_c
     done = ring.at;
     if (!p.u) continue;
     ss[0] = sum2(q);
-    row_sum<1, WARP>(ss, tpr, sh, turn);
+    row_sum<1, WARP, STAGED>(ss, tpr, ring.team, sh, turn);
     const F2 rs = f2(rsqrtf(ss[0] * p.inv_d + p.eps));
     uint4 *uv = p.u + t * p.vecs + l;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       if ((i < NV - 1 || tail) && row_ok) {
         F2 w[E];
-        Vec<T>::unpack(__ldg(p.w_pre + l + i * tpr), w);
+        Vec<T>::unpack(ring.common(p.all, 1, i * tpr), w);
 #pragma unroll
         for (int e = 0; e < E; ++e) w[e] = mul(r[i][e], mul(rs, w[e]));
         uv[i * tpr] = Vec<T>::pack(w);
@@ -358,7 +387,8 @@ struct NormBwdParams {
   RingSrc src;
   RingShape ring;
   int sr, su, sh, sd, sg;        // stage slots of r, du, h, dr and a token's gate
-  const uint4 *gate, *w_post, *w_pre;
+  Shared3 all;                   // w_post, w_pre, a gate that all tokens share
+  const uint4 *gate;
   uint4 *dx, *dh, *dgate_tok;
   float *part_pre;               // [teams][vecs * 2 E]: sums of du rn; null where not asked for
   float *part_a;                 // [units][teams of a CTA][vecs * 2 E]: sums of dR hn (token gates: of dN hn)
@@ -368,19 +398,20 @@ struct NormBwdParams {
   float res_scale, eps, inv_d;
 };
 
-template <typename T, int NV, bool WARP>
+template <typename T, int NV, bool WARP, bool STAGED>
 __global__ void __maxnreg__(sizeof(T) == 4 && NV == 2 && !WARP ? 96 : 128) residual_norm_bwd_kernel(const __grid_constant__ NormBwdParams p) {
-  constexpr int E = Vec<T>::N, kTeams = WARP ? kWarpTeams : 1;
+  constexpr int E = Vec<T>::N;
   extern __shared__ __align__(128) uint8_t stage_mem[];
-  __shared__ uint64_t bars[kWarpTeams * kMaxStages];
+  __shared__ uint64_t bars[kMaxTeams * kMaxStages];
   __shared__ int abort_flag;
-  __shared__ float sh3[2 * (kMaxGroup / 32)][3], sh1[2 * (kMaxGroup / 32)][1];
+  __shared__ float sh3[2 * 32][3], sh1[2 * 32][1];
   int turn3 = 0, turn1 = 0;
-  Ring<WARP> ring(stage_mem, bars, &abort_flag, p.vecs, p.ring);
-  const int l = ring.l, tpr = ring.lanes, team = WARP ? threadIdx.x >> 5 : 0;
-  const int G = kTeams * ring.rows;   // tokens of a turn of the CTA's teams
+  Ring<WARP, STAGED> ring(stage_mem, bars, &abort_flag, p.vecs, p.ring, p.all);
+  const int l = ring.l, tpr = ring.lanes, team = ring.team, teams = WARP ? kWarpTeams : STAGED ? blockDim.x / tpr : 1;
+  const int G = teams * ring.rows;   // tokens of a turn of the CTA's teams
   const bool tail = l + (NV - 1) * tpr < p.vecs;   // this thread's last vector exists
-  const bool post = p.w_post != nullptr, gated = p.gate_mode != ULY_GATE_NONE;
+  const bool post = p.all.p[0] != nullptr, gated = p.gate_mode != ULY_GATE_NONE;
+  const bool all_gate = p.gate_mode == ULY_GATE_CHANNEL;
   F2 a_pre[NV][E], a_a[NV][E];
 #pragma unroll
   for (int i = 0; i < NV; ++i)
@@ -416,8 +447,8 @@ __global__ void __maxnreg__(sizeof(T) == 4 && NV == 2 && !WARP ? 96 : 128) resid
       if (p.bs == 1 || !WARP) ring.issue(p.src, token(k), n, st);
       else ring.issue_each(p.src, token(min(k + ring.sub, q1 - 1)), n, st);
     };
-    if (WARP) __syncwarp();
-    else if (unit != blockIdx.x) __syncthreads();   // every thread is done with the last unit's stages
+    const uint4 *seq_gate = p.gate + (long long)b * p.vecs + l;   // a channel gate's b is 0
+    if (WARP || unit != blockIdx.x) ring.barrier();   // every thread is done with the last unit's stages
     {
       int st = ring.at;
       for (int k = 0; k < ring.stages; ++k) {
@@ -432,13 +463,12 @@ __global__ void __maxnreg__(sizeof(T) == 4 && NV == 2 && !WARP ? 96 : 128) resid
       const bool row_ok = !WARP || k + ring.sub < q1;
       const bool ok_tail = tail && row_ok;
       if (ring.stages == 1 && done >= 0) {   // no stage to run ahead into
-        team_barrier<WARP>();
+        ring.barrier();
         issue(k, 0);
       }
       ring.wait(&abort_flag, p.ring.err);
       F2 rr = f2(0.f), ar = f2(0.f), hh = f2(0.f);   // sums of r^2, du w_pre r and h^2, taken together
       const uint4 *rv = ring.row(p.sr), *uv = ring.row(p.su), *hv = ring.row(p.sh), *dv = ring.row(p.sd);
-      const uint4 *gv = p.sg >= 0 ? ring.row(p.sg) : p.gate + (long long)b * p.vecs + l;
       F2 hn[NV][E];
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
@@ -455,7 +485,7 @@ __global__ void __maxnreg__(sizeof(T) == 4 && NV == 2 && !WARP ? 96 : 128) resid
             F2 r[E], u[E], w[E];
             Vec<T>::unpack(rv[v], r);
             Vec<T>::unpack(uv[v], u);
-            Vec<T>::unpack(__ldg(p.w_pre + l + v), w);
+            Vec<T>::unpack(ring.common(p.all, 1, v), w);
 #pragma unroll
             for (int e = 0; e < E; ++e) {
               rr = fma(r[e], r[e], rr);
@@ -465,7 +495,7 @@ __global__ void __maxnreg__(sizeof(T) == 4 && NV == 2 && !WARP ? 96 : 128) resid
         }
       }
       float s3[3] = {sum2(rr), sum2(ar), sum2(hh)};
-      row_sum<3, WARP>(s3, tpr, sh3, turn3);   // a CTA's barrier also frees the previous stage
+      row_sum<3, WARP, STAGED>(s3, tpr, team, sh3, turn3);   // its barrier also frees the previous stage
       if (WARP) __syncwarp();
       if (done >= 0 && ring.stages > 1) issue(k + (ring.stages - 1) * G, done);
       const float irs = rsqrtf(s3[0] * p.inv_d + p.eps);
@@ -488,7 +518,7 @@ __global__ void __maxnreg__(sizeof(T) == 4 && NV == 2 && !WARP ? 96 : 128) resid
             F2 r[E], u[E], w[E];
             Vec<T>::unpack(rv[v], r);
             Vec<T>::unpack(uv[v], u);
-            Vec<T>::unpack(__ldg(p.w_pre + l + v), w);
+            Vec<T>::unpack(ring.common(p.all, 1, v), w);
 #pragma unroll
             for (int e = 0; e < E; ++e) {
               d[e] = fma(ir, fma(nc1, r[e], mul(u[e], w[e])), d[e]);
@@ -504,7 +534,7 @@ __global__ void __maxnreg__(sizeof(T) == 4 && NV == 2 && !WARP ? 96 : 128) resid
           if (p.sh >= 0) {
             F2 w[E];
             if (post) {
-              Vec<T>::unpack(__ldg(p.w_post + l + v), w);
+              Vec<T>::unpack(ring.common(p.all, 0, v), w);
 #pragma unroll
               for (int e = 0; e < E; ++e) hn[i][e] = mul(hn[i][e], ih);
             }
@@ -514,7 +544,8 @@ __global__ void __maxnreg__(sizeof(T) == 4 && NV == 2 && !WARP ? 96 : 128) resid
             }
             if (gated) {
               F2 g[E];
-              Vec<T>::unpack(gv[v], g);
+              Vec<T>::unpack(p.sg >= 0 ? ring.row(p.sg)[v]
+                             : STAGED && all_gate ? ring.common(p.all, 2, v) : __ldg(seq_gate + v), g);
               if (p.sg >= 0) {
                 if (p.dgate_tok) {
                   F2 o[E];
@@ -548,7 +579,7 @@ __global__ void __maxnreg__(sizeof(T) == 4 && NV == 2 && !WARP ? 96 : 128) resid
       F2 nc2 = f2(0.f);
       if (post) {
         float s1[1] = {sum2(s1p)};
-        row_sum<1, WARP>(s1, tpr, sh1, turn1);
+        row_sum<1, WARP, STAGED>(s1, tpr, team, sh1, turn1);
         nc2 = f2(-s1[0] * p.inv_d);
       }
 #pragma unroll
@@ -562,50 +593,61 @@ __global__ void __maxnreg__(sizeof(T) == 4 && NV == 2 && !WARP ? 96 : 128) resid
         }
       }
     }
-    if (p.part_a) store_sums(a_a, p.part_a, (long long)unit * kTeams + team);
+    if (p.part_a) store_sums(a_a, p.part_a, (long long)unit * teams + team);
   }
-  if (p.part_pre) store_sums(a_pre, p.part_pre, (long long)blockIdx.x * kTeams + team);
+  if (p.part_pre) store_sums(a_pre, p.part_pre, (long long)blockIdx.x * teams + team);
   ring.end(&abort_flag);
 }
 
 // ------------------------------------------------------------------- host
 
 // Teams and stages for rows of `vecs` vectors: lanes of a warp (a power of two)
-// while `nv` vectors a lane cover a row, else the fewest warps that do; CTAs an
-// SM by the registers and by two stages each at least (one only where a single
-// CTA's do not fit).
+// while `nv` vectors a lane cover a row, several teams of one warp a CTA and
+// several CTAs an SM; else teams of the fewest warps that do, one CTA an SM with
+// the weights staged or CTAs of one team.  As many as the registers allow and two
+// stages each (one only where a single team's do not fit); `slots` tensors a stage.
 struct RowShape {
   int lanes, nv, teams, rows;   // threads of a row, vectors of each; teams of a CTA, rows of a team
   int threads, per_sm, stages;
+  bool staged;                  // the weights in shared memory
   uint32_t smem;
 };
 RowShape row_shape(int vecs, int slots, int nv, bool backward, bool f32) {
   RowShape r;
   auto need = [&](int lanes) { return (vecs + lanes - 1) / lanes; };
-  if (vecs <= 32 * nv) {
+  const bool warp = vecs <= 32 * nv;
+  if (warp) {
     r.lanes = 1;
     while (need(r.lanes) > nv) r.lanes *= 2;
-    r.teams = kWarpTeams;
-    r.rows = 32 / r.lanes;
-    r.threads = 32 * kWarpTeams;
   } else {
     r.lanes = (need(nv) + 31) / 32 * 32;
-    if (r.lanes > kMaxGroup) r.lanes = kMaxGroup;
-    r.teams = r.rows = 1;
-    r.threads = r.lanes;
+    if (r.lanes > kMaxLanes) r.lanes = kMaxLanes;
   }
   r.nv = need(r.lanes);
-  const uint32_t stage = (uint32_t)vecs * 16 * slots * r.teams * r.rows;
-  // threads an SM holds by the kernels' registers: up to 128; forward 112 where a
-  // team is a CTA and 64 up to two vectors a thread; backward 96 for two fp32
-  // vectors where a team is a CTA (50000 x 640: 155 -> 142 us by the fourth CTA)
-  const int room = backward ? (f32 && r.nv == 2 && r.teams == 1 ? 640 : 512) : r.nv <= 2 ? 1024 : r.teams > 1 ? 512 : 576;
-  r.per_sm = room / r.threads;
-  if (r.per_sm < 1) r.per_sm = 1;
-  while (r.per_sm > 1 && kRingBytes / (stage * r.per_sm) < 2) --r.per_sm;
-  r.stages = (int)(kRingBytes / (stage * r.per_sm));
-  if (r.stages > kMaxStages) r.stages = kMaxStages;
-  r.smem = stage * r.stages;
+  r.rows = warp ? 32 / r.lanes : 1;
+  // threads an SM holds by the kernels' registers: up to 128; forward 100 where a
+  // team is several warps and 64 up to two vectors a thread; backward 96 for two
+  // fp32 vectors where a team is several warps
+  const int room = backward ? (f32 && r.nv == 2 && !warp ? 640 : 512) : r.nv <= 2 ? 1024 : warp ? 512 : 640;
+  const int team = warp ? 32 : r.lanes;
+  const uint32_t row = (uint32_t)vecs * 16, stage = row * slots * r.rows;
+  int teams = room / team;   // of an SM
+  if (!warp && teams > kMaxTeams) teams = kMaxTeams;
+  if (teams < 1) teams = 1;
+  auto bytes = [&](int t, int stages) { return t * stages * stage + 3 * row * (warp ? (t + kWarpTeams - 1) / kWarpTeams : 1); };
+  while (teams > 1 && bytes(teams, 2) > kRingBytes) --teams;
+  if (warp && teams > kWarpTeams) teams = teams / kWarpTeams * kWarpTeams;
+  // the backward's two bf16 vectors need its 128 registers for themselves: CTAs of
+  // one team, the weights from L1 (65536 x 2560: 485 us so, 495 in one CTA)
+  const bool apart = backward && !warp && !f32;
+  r.staged = !apart && bytes(teams, 2) <= kRingBytes;
+  const uint32_t beside = r.staged ? 0 : 3 * row;   // what bytes() counts too much
+  r.stages = 1;
+  while (r.stages < kMaxStages && bytes(teams, r.stages + 1) - beside <= kRingBytes) ++r.stages;
+  r.teams = warp ? kWarpTeams : apart ? 1 : teams;
+  r.per_sm = warp ? (teams > kWarpTeams ? teams / kWarpTeams : 1) : apart ? teams : 1;
+  r.threads = r.teams * team;
+  r.smem = bytes(r.teams, r.stages) - beside;
   return r;
 }
 constexpr int kFwdVecs = 5, kBwdVecs = 2;
@@ -625,19 +667,27 @@ uly_status run(Entry<Params> &e, int grid, int threads, uint32_t smem, const Par
 }
 template <typename T>
 Entry<NormParams> &fwd_entry(const RowShape &r) {
-  static Entry<NormParams> warp[5] = {{residual_norm_kernel<T, 1, true>}, {residual_norm_kernel<T, 2, true>},
-                                      {residual_norm_kernel<T, 3, true>}, {residual_norm_kernel<T, 4, true>},
-                                      {residual_norm_kernel<T, 5, true>}};
-  static Entry<NormParams> cta[3] = {{residual_norm_kernel<T, 3, false>}, {residual_norm_kernel<T, 4, false>},
-                                     {residual_norm_kernel<T, 5, false>}};
-  return r.teams > 1 ? warp[r.nv - 1] : cta[r.nv < 3 ? 0 : r.nv - 3];
+  static Entry<NormParams> warp[5] = {{residual_norm_kernel<T, 1, true, true>}, {residual_norm_kernel<T, 2, true, true>},
+                                      {residual_norm_kernel<T, 3, true, true>}, {residual_norm_kernel<T, 4, true, true>},
+                                      {residual_norm_kernel<T, 5, true, true>}};
+  static Entry<NormParams> cta[3] = {{residual_norm_kernel<T, 3, false, true>}, {residual_norm_kernel<T, 4, false, true>},
+                                     {residual_norm_kernel<T, 5, false, true>}};
+  static Entry<NormParams> wide[2] = {{residual_norm_kernel<T, 4, false, false>}, {residual_norm_kernel<T, 5, false, false>}};
+  if (r.lanes <= 32) return warp[r.nv - 1];
+  return r.staged ? cta[r.nv - 3] : wide[r.nv - 4];
 }
 template <typename T>
 Entry<NormBwdParams> &bwd_entry(const RowShape &r) {
-  static Entry<NormBwdParams> warp[2] = {{residual_norm_bwd_kernel<T, 1, true>}, {residual_norm_bwd_kernel<T, 2, true>}};
-  static Entry<NormBwdParams> cta[3] = {{residual_norm_bwd_kernel<T, 2, false>}, {residual_norm_bwd_kernel<T, 3, false>},
-                                        {residual_norm_bwd_kernel<T, 4, false>}};
-  return r.teams > 1 ? warp[r.nv - 1] : cta[r.nv < 2 ? 0 : r.nv - 2];
+  static Entry<NormBwdParams> warp[2] = {{residual_norm_bwd_kernel<T, 1, true, true>},
+                                         {residual_norm_bwd_kernel<T, 2, true, true>}};
+  static Entry<NormBwdParams> cta[3] = {{residual_norm_bwd_kernel<T, 2, false, true>},
+                                        {residual_norm_bwd_kernel<T, 3, false, true>},
+                                        {residual_norm_bwd_kernel<T, 4, false, true>}};
+  static Entry<NormBwdParams> wide[3] = {{residual_norm_bwd_kernel<T, 2, false, false>},
+                                         {residual_norm_bwd_kernel<T, 3, false, false>},
+                                         {residual_norm_bwd_kernel<T, 4, false, false>}};
+  if (r.lanes <= 32) return warp[r.nv - 1];
+  return (r.staged ? cta : wide)[r.nv - 2];
 }
 
 // How the backward walks the tokens: `bs` gate rows, each cut into `upb` runs
@@ -765,8 +815,8 @@ uly_status residual_norm_launch(int32_t B, int32_t n, int32_t P, int32_t hidden,
   p.src.add(h, p.sh);
   p.src.add(gate_mode == ULY_GATE_TOKEN ? gate : nullptr, p.sg);
   p.gate = static_cast<const uint4 *>(gate);
-  p.w_post = static_cast<const uint4 *>(w_post);
-  p.w_pre = static_cast<const uint4 *>(w_pre);
+  p.all = {{static_cast<const uint4 *>(w_post), static_cast<const uint4 *>(w_pre),
+            gate_mode == ULY_GATE_CHANNEL ? p.gate : nullptr}};
   p.r = static_cast<uint4 *>(r);
   p.u = static_cast<uint4 *>(u);
   p.rows = B * n;
@@ -802,8 +852,8 @@ uly_status residual_norm_bwd_launch(int32_t B, int32_t n, int32_t P, int32_t hid
   p.src.add(gate_mode == ULY_GATE_TOKEN ? gate : nullptr, p.sg);
   p.ring = {q.slots, q.rs.stages, q.rs.lanes, error_word()};
   p.gate = static_cast<const uint4 *>(gate);
-  p.w_post = static_cast<const uint4 *>(w_post);
-  p.w_pre = static_cast<const uint4 *>(w_pre);
+  p.all = {{static_cast<const uint4 *>(w_post), static_cast<const uint4 *>(w_pre),
+            gate_mode == ULY_GATE_CHANNEL ? p.gate : nullptr}};
   p.dx = static_cast<uint4 *>(dx);
   p.dh = static_cast<uint4 *>(dh);
   p.dgate_tok = gate_mode == ULY_GATE_TOKEN ? static_cast<uint4 *>(dgate) : nullptr;
