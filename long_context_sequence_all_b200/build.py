@@ -2,6 +2,8 @@
 
     python -m long_context_sequence_all_b200.build [--force] [--verbose]
 
+and ``_native.so``, the Python binding of the token-wise operators (g++).
+
 Objects go to ``_build/``; the shared library lands next to this file so it
 travels with the source tree.  nvcc cross-compiles for sm_100a without a GPU.
 """
@@ -19,6 +21,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libulysses.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
+NATIVE = os.path.join(HERE, "_native.so")         # Python binding of the token-wise operators
+NATIVE_SRC = os.path.join(CSRC, "binding.cpp")
 
 SOURCES = ["api.cu", "prof.cu", "permute.cu", "loss.cu", "loss_noalloc.cu", "attn_f32.cu", "attn_fwd_sm100.cu",
            "attn_bwd_sm100.cu", "attn_bwd_fused_sm100.cu", "proj_sm100.cu", "kv_copy.cu", "labels.cu",
@@ -36,7 +40,7 @@ def nvcc() -> str:
 
 
 def _deps_mtime() -> float:
-    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(INCLUDE, "ulysses.h")]
+    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f != os.path.basename(NATIVE_SRC)] + [os.path.join(INCLUDE, "ulysses.h")]
     return max(os.path.getmtime(f) for f in files)
 
 
@@ -84,7 +88,33 @@ def _compile(src: str, verbose: bool) -> str:
     return obj
 
 
+def build_native(force: bool = False) -> str:
+    """The binding (g++ against the installed torch and Python)."""
+    newest = max(os.path.getmtime(f) for f in (NATIVE_SRC, os.path.join(INCLUDE, "ulysses.h")))
+    if not force and os.path.exists(NATIVE) and os.path.getmtime(NATIVE) >= newest:
+        return NATIVE
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+    inc = [INCLUDE, sysconfig.get_paths()["include"], os.path.join(os.path.dirname(nvcc()), "..", "include"),
+           *cpp_extension.include_paths()]
+    lib = cpp_extension.library_paths()
+    tmp = NATIVE + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *[x for d in inc for x in ("-isystem", d)], NATIVE_SRC, "-o", tmp,
+           *[x for d in lib for x in (f"-L{d}", f"-Wl,-rpath,{d}")],
+           "-lc10", "-lc10_cuda", "-ltorch", "-ltorch_cpu", "-ltorch_python", "-ldl"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {NATIVE_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, NATIVE)
+    return NATIVE
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
+    build_native(force)
     if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= _deps_mtime():
         return LIB
     os.makedirs(BUILD, exist_ok=True)

@@ -3,14 +3,15 @@
 Every entry point of the C ABI (``include/ulysses.h``) is exposed under the
 same name.  The functions take CUDA torch tensors (torch is used for device
 memory and streams only), pass raw device pointers and the current CUDA
-stream to the library, and raise :class:`UlyssesError` on a non-OK status.
+stream to the library, and raise :class:`UlyssesError` on a non-OK status
+(the token-wise operators through the native module built from
+``csrc/binding.cpp``, which does the same with less time on the host).
 All arithmetic happens in the library's kernels; there is no fallback: if the
 library is missing or cannot be loaded, every call fails loudly.
 """
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 import threading
 
@@ -524,55 +525,33 @@ def ulysses_loss_aggregate_noalloc(logits, labels, P, ignore_index=-100, shard_s
 
 # ------------------------------------------------------ token-wise operators
 
-# The smallest calls (one decoded token) take the GPU a few microseconds, so
-# these bindings keep their own work short: plain integers for pointers and
-# the stream, sizes of workspaces remembered per shape.
+# The smallest calls (one decoded token) take the GPU a few microseconds, so the
+# checks, the outputs and workspaces (on the stream the call runs on) and the call
+# itself are native: csrc/binding.cpp.  A refusal is an UlyssesError either way.
 
-_BF16, _F32 = torch.bfloat16, torch.float32
-
-
-def _want(where, name, t, shape, dtype, dev):
-    """Check one tensor of a call: dtype, shape, contiguous, on device `dev` (its index)."""
-    if t is not None and t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == dev:
-        return
-    if t is None:
-        raise UlyssesError(1, f"{where}: {name} is missing")
-    if t.dtype is not dtype:
-        raise UlyssesError(3, f"{where}: {name} has dtype {t.dtype}, expected {dtype}")
-    if t.shape != shape:
-        raise UlyssesError(2, f"{where}: {name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if not t.is_contiguous():
-        raise UlyssesError(6, f"{where}: {name} is not contiguous (strides {tuple(t.stride())})")
-    raise UlyssesError(7, f"{where}: {name} is on {t.device}, x on device {dev}")
+_native_module = None
 
 
-def _here(where, dev):
-    """The call's tensors are on the current CUDA device, where it launches."""
-    if dev < 0 or dev != torch.cuda.current_device():
-        raise UlyssesError(7, f"{where}: tensors on device {dev}, not on the current CUDA device")
+def _native():
+    global _native_module
+    if _native_module is None:
+        lib()
+        with _lock:
+            path = os.path.join(_HERE, "_native.so")
+            if not os.path.exists(path):
+                raise RuntimeError(f"{path} is missing; build it with `python -m long_context_sequence_all_b200.build`")
+            from . import _native as m
+            m.init(LIB_PATH, UlyssesError)
+            _native_module = m
+    return _native_module
 
 
-def _ptr(t):
-    return None if t is None else t.data_ptr()
-
-
-def _raw_stream(stream, dev):
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
-
-
-def _empty(like, shape, dtype, stream):
-    """An output or workspace whose memory belongs to the stream the call runs on."""
+def _run(name, stream, *args):
+    fn = getattr(_native_module or _native(), name)
     if stream is None:
-        return like.new_empty(shape, dtype=dtype)
+        return fn(*args)
     with torch.cuda.stream(stream):
-        return like.new_empty(shape, dtype=dtype)
-
-
-def _like(t, stream):
-    if stream is None:
-        return torch.empty_like(t)
-    with torch.cuda.stream(stream):
-        return torch.empty_like(t)
+        return fn(*args)
 
 
 def _size(fn, *args) -> int:
@@ -581,27 +560,8 @@ def _size(fn, *args) -> int:
     return n.value
 
 
-@functools.lru_cache(maxsize=4096)
-def _size_on(dev, fn, *args) -> int:
-    return _size(fn, *args)   # of the current device `dev`
-
-
-def _workspace(where, ws, need, like, stream, dev):
-    """(tensor or None, its bytes) of a call that needs `need` bytes."""
-    if ws is None:
-        if not need:
-            return None, 0
-        ws = _empty(like, need, torch.uint8, stream)
-    elif ws.dtype is not torch.uint8 or not ws.is_contiguous() or ws.get_device() != dev:
-        raise UlyssesError(3, f"{where}: the workspace is not contiguous bytes on device {dev}")
-    return ws, ws.numel()
-
-
-def _features(where, x, w, activation):
-    if x.dim() < 1 or w.dim() != 2 or (activation == ACT_SWIGLU and w.shape[0] % 2):
-        raise UlyssesError(2, f"{where}: x {tuple(x.shape)}, w {tuple(w.shape)}")
-    nz, k = w.shape
-    return x.shape[:-1], k, nz, nz // 2 if activation == ACT_SWIGLU else nz
+def _type_code(dtype) -> int:
+    return {torch.bfloat16: ULY_BF16, torch.float32: ULY_F32}.get(dtype, -1)
 
 
 def ulysses_linear_workspace_size(tokens: int, in_features: int, out_features: int, activation=ACT_NONE) -> int:
@@ -614,31 +574,7 @@ def ulysses_linear(x, w, bias=None, residual=None, activation=ACT_NONE, save_pre
     [N][K] (nn.Linear weight; ACT_SWIGLU: [2N][K], gate rows then up rows), bias
     like w's rows, residual like y -> y [..., N]; with save_pre (or a given pre)
     (y, pre), pre [..., rows of w] the product and bias before the activation."""
-    where = "ulysses_linear"
-    lead, k, nz, n = _features(where, x, w, activation)
-    dev = x.get_device()
-    y_shape = (*lead, n)
-    _want(where, "x", x, (*lead, k), _BF16, dev)
-    _want(where, "w", w, (nz, k), _BF16, dev)
-    if bias is not None:
-        _want(where, "bias", bias, (nz,), _BF16, dev)
-    if residual is not None:
-        _want(where, "residual", residual, y_shape, _BF16, dev)
-    if y is None:
-        y = _empty(x, y_shape, _BF16, stream)
-    else:
-        _want(where, "y", y, y_shape, _BF16, dev)
-    if pre is not None:
-        _want(where, "pre", pre, (*lead, nz), _BF16, dev)
-    elif save_pre:
-        pre = _empty(x, (*lead, nz), _BF16, stream)
-    _here(where, dev)
-    tokens = x.numel() // k if k else 0
-    need = _size_on(dev, "ulysses_linear_workspace_size", tokens, k, n, activation)
-    ws, ws_bytes = _workspace(where, workspace, need, x, stream, dev)
-    _check(lib().ulysses_linear(tokens, k, n, activation, x.data_ptr(), w.data_ptr(), _ptr(bias), _ptr(residual),
-                                y.data_ptr(), _ptr(pre), _ptr(ws), ws_bytes, _raw_stream(stream, dev)), where)
-    return y if pre is None else (y, pre)
+    return _run("linear", stream, x, w, bias, residual, activation, save_pre, y, pre, workspace)
 
 
 def ulysses_linear_bwd_workspace_size(tokens: int, in_features: int, out_features: int, activation=ACT_NONE) -> int:
@@ -650,59 +586,8 @@ def ulysses_linear_bwd(x, w, dy, pre=None, activation=ACT_NONE, bias_grad=False,
     """Backward of ulysses_linear: dy [..., N] and the forward's pre (not for
     ACT_NONE) -> (dx like x, dw like w in grad_dtype (float32 or bfloat16), dbias
     float32 [rows of w], or None without bias_grad).  The residual's gradient is dy."""
-    where = "ulysses_linear_bwd"
-    lead, k, nz, n = _features(where, x, w, activation)
-    dev = x.get_device()
-    _want(where, "x", x, (*lead, k), _BF16, dev)
-    _want(where, "w", w, (nz, k), _BF16, dev)
-    _want(where, "dy", dy, (*lead, n), _BF16, dev)
-    if activation == ACT_NONE:
-        pre = None
-    else:
-        _want(where, "pre", pre, (*lead, nz), _BF16, dev)
-    if dx is None:
-        dx = _like(x, stream)
-    else:
-        _want(where, "dx", dx, x.shape, _BF16, dev)
-    if dw is None:
-        dw = _empty(x, w.shape, grad_dtype, stream)
-    code = _dtype_code(dw)
-    _want(where, "dw", dw, w.shape, dw.dtype, dev)
-    if dbias is not None:
-        _want(where, "dbias", dbias, (nz,), _F32, dev)
-    elif bias_grad:
-        dbias = _empty(x, nz, _F32, stream)
-    _here(where, dev)
-    tokens = x.numel() // k if k else 0
-    need = _size_on(dev, "ulysses_linear_bwd_workspace_size", tokens, k, n, activation)
-    ws, ws_bytes = _workspace(where, workspace, need, x, stream, dev)
-    _check(lib().ulysses_linear_bwd(tokens, k, n, activation, x.data_ptr(), w.data_ptr(), _ptr(pre), dy.data_ptr(),
-                                    dx.data_ptr(), dw.data_ptr(), code, _ptr(dbias), _ptr(ws), ws_bytes,
-                                    _raw_stream(stream, dev)), where)
-    return dx, dw, dbias
-
-
-def _want_norm(where, shape, dtype, w_pre, w_post, gate, gate_mode, dev):
-    if len(shape) != 4:
-        raise UlyssesError(2, f"{where}: shape {tuple(shape)}, expected [P][B][n/P][hidden]")
-    if dtype is not _BF16 and dtype is not _F32:
-        raise UlyssesError(3, f"{where}: dtype {dtype}")
-    d = shape[3]
-    if w_pre is not None:
-        _want(where, "w_pre", w_pre, (d,), dtype, dev)
-    if w_post is not None:
-        _want(where, "w_post", w_post, (d,), dtype, dev)
-    if gate_mode == GATE_NONE:
-        if gate is not None:
-            raise UlyssesError(2, f"{where}: a gate with GATE_NONE")
-    elif gate_mode == GATE_CHANNEL:
-        _want(where, "gate", gate, (d,), dtype, dev)
-    elif gate_mode == GATE_SEQUENCE:
-        _want(where, "gate", gate, (shape[1], d), dtype, dev)
-    elif gate_mode == GATE_TOKEN:
-        _want(where, "gate", gate, shape, dtype, dev)
-    else:
-        raise UlyssesError(6, f"{where}: gate mode {gate_mode}")
+    return _run("linear_bwd", stream, x, w, dy, pre, activation, bias_grad, _type_code(grad_dtype), dx, dw, dbias,
+                workspace)
 
 
 def ulysses_residual_norm(x, h=None, w_pre=None, w_post=None, gate=None, gate_mode=GATE_NONE, res_scale=1.0,
@@ -711,32 +596,12 @@ def ulysses_residual_norm(x, h=None, w_pre=None, w_post=None, gate=None, gate_mo
     square norm: x, h seq layout [P][B][n/P][hidden] (bf16 or float32), weights
     [hidden], gate as its mode says -> (r, u).  Without w_pre u is None; without
     h (the first block) r is None unless a tensor for it is given."""
-    where = "ulysses_residual_norm"
-    shape, dtype, dev = x.shape, x.dtype, x.get_device()
-    _want_norm(where, shape, dtype, w_pre, w_post, gate, gate_mode, dev)
-    _want(where, "x", x, shape, dtype, dev)
-    if h is not None:
-        _want(where, "h", h, shape, dtype, dev)
-    if r is not None:
-        _want(where, "r", r, shape, dtype, dev)
-    elif h is not None or w_pre is None:
-        r = _like(x, stream)
-    if u is not None:
-        _want(where, "u", u, shape, dtype, dev)
-    elif w_pre is not None:
-        u = _like(x, stream)
-    _here(where, dev)
-    P, B, s, d = shape
-    _check(lib().ulysses_residual_norm(B, P * s, P, d, ULY_BF16 if dtype is _BF16 else ULY_F32, x.data_ptr(), _ptr(h),
-                                       _ptr(gate), gate_mode, _ptr(w_post), _ptr(w_pre), res_scale, eps, _ptr(r),
-                                       _ptr(u), _raw_stream(stream, dev)), where)
-    return r, u
+    return _run("residual_norm", stream, x, h, w_pre, w_post, gate, gate_mode, res_scale, eps, r, u)
 
 
 def ulysses_residual_norm_bwd_workspace_size(B: int, n: int, hidden: int, dtype=torch.bfloat16,
                                              gate_mode=GATE_NONE) -> int:
-    return _size("ulysses_residual_norm_bwd_workspace_size", B, n, hidden,
-                 ULY_BF16 if dtype == torch.bfloat16 else ULY_F32, gate_mode)
+    return _size("ulysses_residual_norm_bwd_workspace_size", B, n, hidden, _type_code(dtype), gate_mode)
 
 
 def ulysses_residual_norm_bwd(r, h=None, dr=None, du=None, w_pre=None, w_post=None, gate=None, gate_mode=GATE_NONE,
@@ -746,63 +611,8 @@ def ulysses_residual_norm_bwd(r, h=None, dr=None, du=None, w_pre=None, w_post=No
     sum(r * dr) + sum(u * du) -> (dx, dh, dw_pre, dw_post, dgate); dw_pre, dw_post
     and a shared gate's gradient are float32, a token gate's is like the gate;
     None for what the forward did not have."""
-    where = "ulysses_residual_norm_bwd"
-    shape, dtype, dev = r.shape, r.dtype, r.get_device()
-    _want_norm(where, shape, dtype, w_pre, w_post, gate, gate_mode, dev)
-    _want(where, "r", r, shape, dtype, dev)
-    P, B, s, d = shape
-    for name, t in (("h", h), ("dr", dr), ("du", du)):
-        if t is not None:
-            _want(where, name, t, shape, dtype, dev)
-
-    def out(name, t, wanted, like, dt):
-        if t is not None:
-            _want(where, name, t, like, dt, dev)
-            return t
-        return _empty(r, like, dt, stream) if wanted else None
-
-    dx = out("dx", dx, True, shape, dtype)
-    dh = out("dh", dh, h is not None, shape, dtype)
-    dw_pre = out("dw_pre", dw_pre, du is not None, (d,), _F32)
-    dw_post = out("dw_post", dw_post, w_post is not None, (d,), _F32)
-    if gate is not None:
-        dgate = out("dgate", dgate, True, gate.shape, dtype if gate_mode == GATE_TOKEN else _F32)
-    elif dgate is not None:
-        raise UlyssesError(2, f"{where}: dgate without a gate")
-    _here(where, dev)
-    code = ULY_BF16 if dtype is _BF16 else ULY_F32
-    need = _size_on(dev, "ulysses_residual_norm_bwd_workspace_size", B, P * s, d, code, gate_mode)
-    ws, ws_bytes = _workspace(where, workspace, need, r, stream, dev)
-    _check(lib().ulysses_residual_norm_bwd(B, P * s, P, d, code, r.data_ptr(), _ptr(h), _ptr(dr), _ptr(du), _ptr(gate),
-                                           gate_mode, _ptr(w_post), _ptr(w_pre), res_scale, eps, _ptr(dx), _ptr(dh),
-                                           _ptr(dw_post), _ptr(dw_pre), _ptr(dgate), _ptr(ws), ws_bytes,
-                                           _raw_stream(stream, dev)), where)
-    return dx, dh, dw_pre, dw_post, dgate
-
-
-def _want_loss(where, x, w, labels):
-    if x.dim() != 2 or w.dim() != 2:
-        raise UlyssesError(2, f"{where}: x {tuple(x.shape)}, w {tuple(w.shape)}")
-    dev = x.get_device()
-    _want(where, "x", x, x.shape, _BF16, dev)
-    _want(where, "w", w, (w.shape[0], x.shape[1]), _BF16, dev)
-    if labels is not None and labels.dim() != 1 and labels.is_contiguous():
-        labels = labels.view(-1)
-    _want(where, "labels", labels, x.shape[:1], torch.int32, dev)
-    return dev
-
-
-def _loss_outputs(where, P, x, dev, shard_sum, shard_count, loss, stream):
-    if shard_sum is None:
-        shard_sum = _empty(x, P, _F32, stream)
-    if shard_count is None:
-        shard_count = _empty(x, P, torch.int64, stream)
-    if loss is None:
-        loss = _empty(x, 1, _F32, stream)
-    _want(where, "shard_sum", shard_sum, (P,), _F32, dev)
-    _want(where, "shard_count", shard_count, (P,), torch.int64, dev)
-    _want(where, "loss", loss, (1,), _F32, dev)
-    return shard_sum, shard_count, loss
+    return _run("residual_norm_bwd", stream, r, h, dr, du, w_pre, w_post, gate, gate_mode, res_scale, eps, dx, dh,
+                dw_pre, dw_post, dgate, workspace)
 
 
 def ulysses_linear_loss_workspace_size(P: int, tokens: int, hidden: int, vocab: int) -> int:
@@ -814,23 +624,13 @@ def ulysses_linear_loss(x, w, labels, P, ignore_index=-100, shard_sum=None, shar
     """ulysses_loss_aggregate without the logits: x [T][hidden] bf16 (shard r = rows
     [r*T/P, (r+1)*T/P)), w [V][hidden] bf16, labels int32 [T] (or the seq layout)
     -> (shard_sum, shard_count, loss) of the logits x w^T."""
-    where = "ulysses_linear_loss"
-    dev = _want_loss(where, x, w, labels)
-    (T, d), V = x.shape, w.shape[0]
-    shard_sum, shard_count, loss = _loss_outputs(where, P, x, dev, shard_sum, shard_count, loss, stream)
-    _here(where, dev)
-    need = _size_on(dev, "ulysses_linear_loss_workspace_size", P, T, d, V)
-    ws, ws_bytes = _workspace(where, workspace, need, x, stream, dev)
-    _check(lib().ulysses_linear_loss(P, T, d, V, x.data_ptr(), w.data_ptr(), labels.data_ptr(), ignore_index,
-                                     shard_sum.data_ptr(), shard_count.data_ptr(), loss.data_ptr(), _ptr(ws), ws_bytes,
-                                     _raw_stream(stream, dev)), where)
-    return shard_sum, shard_count, loss
+    return _run("linear_loss", stream, x, w, labels, P, ignore_index, shard_sum, shard_count, loss, workspace)
 
 
 def ulysses_linear_loss_bwd_workspace_size(P: int, tokens: int, hidden: int, vocab: int, grad_dtype=torch.float32,
                                            piece_tokens: int = 0) -> int:
-    return _size("ulysses_linear_loss_bwd_workspace_size", P, tokens, hidden, vocab,
-                 ULY_BF16 if grad_dtype == torch.bfloat16 else ULY_F32, piece_tokens)
+    return _size("ulysses_linear_loss_bwd_workspace_size", P, tokens, hidden, vocab, _type_code(grad_dtype),
+                 piece_tokens)
 
 
 def ulysses_linear_loss_bwd(x, w, labels, P, ignore_index=-100, grad_dtype=torch.float32, piece_tokens=0, dx=None,
@@ -839,26 +639,8 @@ def ulysses_linear_loss_bwd(x, w, labels, P, ignore_index=-100, grad_dtype=torch
     shard_count, loss, dx bf16 like x, dw like w in grad_dtype (float32 or
     bfloat16)).  piece_tokens: tokens whose exponentials the workspace holds at
     a time (0: as many as fit 4 GiB)."""
-    where = "ulysses_linear_loss_bwd"
-    dev = _want_loss(where, x, w, labels)
-    (T, d), V = x.shape, w.shape[0]
-    if dx is None:
-        dx = _like(x, stream)
-    else:
-        _want(where, "dx", dx, x.shape, _BF16, dev)
-    if dw is None:
-        dw = _empty(x, w.shape, grad_dtype, stream)
-    code = _dtype_code(dw)
-    _want(where, "dw", dw, w.shape, dw.dtype, dev)
-    shard_sum, shard_count, loss = _loss_outputs(where, P, x, dev, shard_sum, shard_count, loss, stream)
-    _here(where, dev)
-    need = _size_on(dev, "ulysses_linear_loss_bwd_workspace_size", P, T, d, V, code, piece_tokens)
-    ws, ws_bytes = _workspace(where, workspace, need, x, stream, dev)
-    _check(lib().ulysses_linear_loss_bwd(P, T, d, V, x.data_ptr(), w.data_ptr(), labels.data_ptr(), ignore_index,
-                                         dx.data_ptr(), dw.data_ptr(), code, piece_tokens, shard_sum.data_ptr(),
-                                         shard_count.data_ptr(), loss.data_ptr(), _ptr(ws), ws_bytes,
-                                         _raw_stream(stream, dev)), where)
-    return shard_sum, shard_count, loss, dx, dw
+    return _run("linear_loss_bwd", stream, x, w, labels, P, ignore_index, _type_code(grad_dtype), piece_tokens, dx, dw,
+                shard_sum, shard_count, loss, workspace)
 
 
 # -------------------------------------------------------------------- misc

@@ -381,3 +381,51 @@ def test_tokenwise_binding_refuses_tensors_it_cannot_take(L):
     refused(3, U.ulysses_linear_loss, x.float(), w, y, 1)
     refused(2, U.ulysses_linear_loss, q, w, y, 1)
     refused(7, U.ulysses_linear_loss, x, w, y, 1)
+
+
+def test_tokenwise_binding_refuses_arguments_it_cannot_take(L):
+    """What is no tensor, no number or no fitting output is an error before any launch, and the binding goes on."""
+    import torch
+    from long_context_sequence_all_b200 import ulysses as U
+    bf = torch.bfloat16
+    x, w = torch.zeros(4, 64, dtype=bf), torch.zeros(16, 64, dtype=bf)
+    y = torch.zeros(4, dtype=torch.int32)
+    q = torch.zeros(2, 1, 3, 64, dtype=bf)
+
+    def refused(status, fn, *a, **k):
+        for _ in range(2):
+            with pytest.raises(U.UlyssesError) as e:
+                fn(*a, **k)
+            assert e.value.status == status, e.value
+
+    before = L.ulysses_launch_count()
+    refused(1, U.ulysses_linear, None, w)
+    refused(1, U.ulysses_linear, x, None)
+    refused(3, U.ulysses_linear, [1.0], w)
+    refused(2, U.ulysses_linear, torch.zeros((), dtype=bf), w)
+    refused(2, U.ulysses_linear, x, w, bias=torch.zeros(15, dtype=bf))
+    refused(2, U.ulysses_linear, x, w, y=torch.zeros(4, 17, dtype=bf))
+    refused(3, U.ulysses_linear, x, w, pre=torch.zeros(4, 16))
+    refused(1, U.ulysses_linear_bwd, x, w, None)
+    refused(1, U.ulysses_linear_bwd, x, w, torch.zeros(4, 16, dtype=bf), activation=U.ACT_GELU)   # without pre
+    refused(3, U.ulysses_linear_bwd, x, w, torch.zeros(4, 16, dtype=bf), grad_dtype=torch.float16)
+    refused(3, U.ulysses_linear_bwd, x, w, torch.zeros(4, 16, dtype=bf), dw=torch.zeros(16, 64, dtype=torch.float64))
+    refused(1, U.ulysses_residual_norm, None)
+    refused(1, U.ulysses_residual_norm_bwd, None)
+    refused(1, U.ulysses_residual_norm, q, q, gate_mode=U.GATE_TOKEN)                            # without a gate
+    refused(2, U.ulysses_residual_norm_bwd, q, dgate=q)
+    refused(1, U.ulysses_linear_loss, x, w, None, 1)
+    refused(2, U.ulysses_linear_loss, x, w, y, 0)
+    refused(2, U.ulysses_linear_loss, x, w, y, 1 << 40)
+    refused(2, U.ulysses_linear_loss, x, w, y[:3], 1)
+    refused(3, U.ulysses_linear_loss, x, w, y.long(), 1)
+    refused(3, U.ulysses_linear_loss_bwd, x, w, y, 1, grad_dtype=torch.int32)
+    for fn, a, k in ((U.ulysses_linear, (x, w), dict(activation="gelu")),
+                     (U.ulysses_residual_norm, (q, q), dict(gate_mode=None)),
+                     (U.ulysses_linear_loss, (x, w, y, 1.5), {})):
+        with pytest.raises(TypeError):
+            fn(*a, **k)
+    for k in (dict(ignore_index=1 << 70), dict(ignore_index=1 << 40)):
+        with pytest.raises(OverflowError):
+            U.ulysses_linear_loss(x, w, y, 1, **k)
+    assert L.ulysses_launch_count() == before
