@@ -559,14 +559,18 @@ uly_status launch_join(const typename Epi::Params &p, const Shape &s, const Cut 
 }
 
 // --------------------------------------------------------- plain epilogue
-// out = A B^T + add, in bf16 or fp32; N is a multiple of 8.
+// out = A B^T / max(*over, 1) + add, in bf16 or fp32; N is a multiple of 8.
 struct PlainParams {
   CUtensorMap out_map;      // of out (launch_plain fills it in)
   void *out;
   const float *add;         // nullable fp32 [M][N] (may be `out` itself, fp32)
+  const long long *over;    // nullable: 1
   long long M;
   int N, out_f32;
 };
+__device__ __forceinline__ float one_over(const long long *n) {
+  return n ? (float)(1.0 / (double)max(__ldg(n), 1ll)) : 1.f;
+}
 struct EpiPlain {
   using Params = PlainParams;
   static constexpr bool kGated = false;
@@ -578,6 +582,11 @@ struct EpiPlain {
   }
   static __device__ __forceinline__ void join8(const Params &p, long long row, int col, float (&z)[8],
                                                const float (&)[8]) {
+    if (p.over) {
+      const float f = one_over(p.over);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) z[e] *= f;
+    }
     if (p.add) add8(p, row, col, z);
     if (p.out_f32) store8(static_cast<float *>(p.out) + row * p.N + col, z);
     else store8(static_cast<__nv_bfloat16 *>(p.out) + row * p.N + col, z);
@@ -586,12 +595,16 @@ struct EpiPlain {
   static __device__ __forceinline__ void tile(const Params &p, const Unit &w, uint32_t acc, int row, int half,
                                               OutRing &out) {
     const int row0 = row - out.lane;
+    const float f = one_over(p.over);
 #pragma unroll 1
     for (int c = 0; c < TN / 2; c += 64) {
       const int col0 = w.nt * TN + half * TN / 2 + c;
       uint32_t a[64], v[16];
       tmem_ld64(acc + half * TN / 2 + c, a);
       if (col0 >= p.N || row0 >= p.M) continue;   // the whole warp
+      if (p.over)
+#pragma unroll
+        for (int e = 0; e < 64; ++e) a[e] = __float_as_uint(__uint_as_float(a[e]) * f);
       if (p.add && row < p.M) {
 #pragma unroll
         for (int g = 0; g < 8; ++g)

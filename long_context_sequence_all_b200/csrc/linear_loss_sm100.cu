@@ -2,7 +2,7 @@
 // z = x W^T over the whole vocabulary, without a logits tensor:
 //
 //   l_t = logsumexp_v(z_tv) - z_t[y_t],  S_r, C_r, L as ulysses_loss_aggregate
-//   dx = dz W,  dW = dz^T x,  dz_tv = (softmax(z_t)_v - [v == y_t]) / C
+//   dx = dz W / C,  dW = dz^T x / C,  dz_tv = softmax(z_t)_v - [v == y_t]
 //
 // Forward: the product's epilogue keeps, for each 128 columns of a row, their
 // maximum and the sum of exp(z - maximum) (fp32); a second kernel folds a
@@ -13,10 +13,13 @@
 // columns, so every value is at most 2^15 and keeps 11 significant bits down
 // to e^-20 of that maximum (2^-40 of it absolute below).  When the row's pairs
 // have given its logsumexp, one pass brings p to
-//   dz_tv = (softmax_tv - [v == y_t]) / C   in bf16, in place
-// (the label's element as expm1(z_y - lse) / C, exact for confident tokens
-// too), and dx = dz W and dW = dz^T x are plain products.  So dz is rounded to
-// bf16 once, 2^-8 relative at most, after 2^-11 of the stored exponential.
+//   dz_tv = softmax_tv - [v == y_t]   in bf16, in place
+// (the label's element as expm1(z_y - lse), exact for confident tokens too),
+// and dz W and dz^T x are plain products, divided by C in fp32 as they leave
+// the tensor memory.  So dz is rounded to bf16 once, 2^-8 relative at most,
+// after 2^-11 of the stored exponential.  Where the labels' softmax is small
+// their elements, which then are nearly all of a gradient, are close to -1 and
+// lose nothing; divided by C first they would all be off by the same part.
 //
 // Three products of 2 T D V operations, the fewest that do not keep the
 // logits in a wider type; bound by the tensor cores, with few tokens by W's
@@ -184,13 +187,12 @@ struct SkinnyLoss {
 
 // Four rows a CTA: their pairs (one 32-byte sector for a slot of all four) are
 // folded in a fixed order into lse and the rows' losses.  GRAD: and each slot's
-// factor exp(maximum - lse) / C of its stored exponentials, [row][slot].
+// factor exp(maximum - lse) of its stored exponentials, [row][slot].
 struct RowsParams {
   const float2 *pairs;
   const float *target;
   const int32_t *labels;
   float *row_loss, *row_lse;  // of the piece's rows
-  const long long *count;
   float *factor;              // [rows][slots]
   long long rows_pad;
   int rows, slots, vocab, ignore_index;
@@ -241,11 +243,10 @@ __global__ void __launch_bounds__(kRowThreads) loss_rows_kernel(const RowsParams
   }
   if (!GRAD) return;
   __syncthreads();
-  const float f = (float)(1.0 / (double)max(*p.count, 1ll)) / kScale;   // no counted token: no row uses it
   for (int k = threadIdx.x; k < p.slots; k += kRowThreads) {
     const float2 *v = p.pairs + (long long)k * p.rows_pad + row0;
     for (int r = 0; r < nrows; ++r)
-      p.factor[(long long)(row0 + r) * p.slots + k] = exp2f((v[r].x - sh_lse[r]) * kLog2e) * f;
+      p.factor[(long long)(row0 + r) * p.slots + k] = exp2f((v[r].x - sh_lse[r]) * kLog2e) / kScale;
   }
 }
 
@@ -255,7 +256,6 @@ __global__ void __launch_bounds__(kRowThreads) loss_rows_kernel(const RowsParams
 struct GradParams {
   const float *factor, *row_lse, *target;
   const int32_t *labels;
-  const long long *count;
   uint4 *p;                   // [rows][ldp / 8]: fp16 in, bf16 out
   const uint4 *x;
   uint4 *xk;                  // [rows][hidden / 8]
@@ -294,7 +294,7 @@ __global__ void __launch_bounds__(kGradThreads) loss_grad_kernel(const GradParam
       }
       if (i == y / 8) {
         // z_y <= lse but for rounding: the label's softmax is at most 1
-        const float dy = (float)(1.0 / (double)*p.count) * expm1f(fminf(p.target[row] - p.row_lse[row], 0.f));
+        const float dy = expm1f(fminf(p.target[row] - p.row_lse[row], 0.f));
 #pragma unroll
         for (int e = 0; e < 8; ++e)
           if (e == y % 8) v[e] = dy;
@@ -561,9 +561,8 @@ uly_status linear_loss_bwd_launch(int32_t P, int64_t tokens, int32_t D, int32_t 
     RowsParams r = rows_of(q, p, ws, t0);
     r.row_lse = at<float>(ws, q.row_lse);
     r.factor = at<float>(ws, q.factor);
-    r.count = count;
     GradParams g = {};
-    g.factor = r.factor; g.row_lse = r.row_lse; g.target = r.target; g.labels = r.labels; g.count = count;
+    g.factor = r.factor; g.row_lse = r.row_lse; g.target = r.target; g.labels = r.labels;
     g.p = static_cast<uint4 *>(pp);
     g.x = reinterpret_cast<const uint4 *>(xb + t0 * D);
     g.xk = static_cast<uint4 *>(xk);
@@ -579,15 +578,17 @@ uly_status linear_loss_bwd_launch(int32_t P, int64_t tokens, int32_t D, int32_t 
     // dx = dz W
     PlainParams o = {};
     o.out = dxb + t0 * D;
+    o.over = count;
     o.M = rows; o.N = D;
     float *part = at<float>(ws, q.part);
     st = rows <= skinny::kMaxTokens
-             ? skinny::launch_plain_mn(pp, q.ldp, w, o.out, rows, D, V, prof::K_LINEAR_LOSS_DX, stream)
+             ? skinny::launch_plain_mn(pp, q.ldp, w, o.out, count, rows, D, V, prof::K_LINEAR_LOSS_DX, stream)
              : launch_plain<false>(tz, tw_mn, o, V, part, q.part_bytes, prof::K_LINEAR_LOSS_DX, stream);
     if (st != ULY_OK) return st;
     // dW (+)= dz^T x; the last piece writes the caller's type
     const bool last = t0 + rows >= tokens;
     o = PlainParams{};
+    o.over = count;
     o.M = V; o.N = D;
     float *acc = q.dw_acc ? at<float>(ws, q.acc) : static_cast<float *>(dw);
     o.add = t0 > 0 ? acc : nullptr;

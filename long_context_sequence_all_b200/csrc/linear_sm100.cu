@@ -401,7 +401,7 @@ uly_status linear_bwd_launch(int64_t tokens, int32_t in, int32_t out, int32_t ac
   }
   CUtensorMap ta, tb;
   if (dx && few_tokens(tokens)) {   // dx[tokens][in] = dz[tokens][nz] W[nz][in]
-    const uly_status st = skinny::launch_plain_mn(dz, q.nz, w, dx, tokens, in, q.nz, prof::K_LINEAR_DX, stream);
+    const uly_status st = skinny::launch_plain_mn(dz, q.nz, w, dx, nullptr, tokens, in, q.nz, prof::K_LINEAR_DX, stream);
     if (st != ULY_OK) return st;
   } else if (dx) {
     if (!make_map(&ta, dz, q.nz, tokens, q.nz, kHalf) || !make_map(&tb, w, in, q.nz, in, 64)) return ULY_ERR_CUDA;

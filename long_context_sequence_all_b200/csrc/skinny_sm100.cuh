@@ -266,28 +266,32 @@ uly_status launch(const void *w, long long w_inner, long long w_rows, const void
   }
 }
 
-// out[tokens][N] in bf16, nothing else.
+// out[tokens][N] in bf16, the sums over max(*over, 1) (over null: 1).
 struct SkinnyPlain {
   struct Params {
     __nv_bfloat16 *out;
+    const long long *over;
     int T, N;
   };
   static __device__ __forceinline__ void finish(const Params &p, const Tile &tile, int index, int rank, int ranks) {
+    const float f = gemm::one_over(p.over);
     for_slice(kRows, rank, ranks, p.T, [&](int row, int t) {
       float v[4];
       tile.sum4(row, t, v);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] *= f;
       const int col = index * kRows + row;   // N is a multiple of 8
       if (col < p.N) store4(p.out + (long long)t * p.N + col, v);
     });
   }
 };
 
-// out[T][N] = x [T][K] w, w [K][N].
-inline uly_status launch_plain_mn(const void *x, long long x_stride, const void *w, void *out, long long T, int N,
-                                  long long K, int kernel_id, cudaStream_t stream) {
+// out[T][N] = x [T][K] w / max(*over, 1), w [K][N].
+inline uly_status launch_plain_mn(const void *x, long long x_stride, const void *w, void *out, const long long *over,
+                                  long long T, int N, long long K, int kernel_id, cudaStream_t stream) {
   prof::Scope scope(kernel_id, stream);
   const int tiles = (N + kRows - 1) / kRows;
-  const SkinnyPlain::Params p = {static_cast<__nv_bfloat16 *>(out), (int)T, N};
+  const SkinnyPlain::Params p = {static_cast<__nv_bfloat16 *>(out), over, (int)T, N};
   return launch<SkinnyPlain, true>(w, N, K, x, x_stride, T, K, tiles, cluster_size(T, tiles, (K + kBK - 1) / kBK), kRows,
                                    64, p, stream);
 }
