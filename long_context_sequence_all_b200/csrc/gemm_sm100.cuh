@@ -409,7 +409,8 @@ inline bool make_out_map(CUtensorMap *map, const void *base, long long inner, lo
 // tile, bound by its loads), the last one ceil(tiles left * splits / pairs) of
 // k_steps / splits and, if cut, a second kernel over fp32 partial tiles (written
 // and read once, mostly in L2) of at most `budget` bytes; the last tile's epilogue
-// is not hidden.
+// is not hidden.  A tile of many steps has as many parts as there are pairs (32
+// tokens' dx over 143987 columns, 88 wide: MEASUREPARTS).
 // 320 tiles of 320 steps on 74 pairs: 4 turns and 24 tiles cut in 3, 4.33 turns
 // instead of 5.  1003 x 1032 -> 1544: 52 narrow tiles 11.9 us, 28 wide ones 13.8;
 // 256 x 10240 -> 2560: 10 wide tiles cut in 7 20.6 us, narrow ones 25.7.
@@ -417,31 +418,33 @@ struct Cut {
   int tn = kTile;     // columns of a tile
   int full = 0, splits = 1;
   size_t bytes = 0;   // of the partial tiles
+  double us = 0;      // the sum
 };
 inline Cut choose_cut(long long m_tiles, long long n_tiles, long long n_narrow, long long k_steps,
                       size_t budget = SIZE_MAX) {
-  const long long pairs = device_sm_count() / 2;
+  const int pairs = device_sm_count() / 2, steps = (int)k_steps;
   Cut best;
-  double best_us = 1e300;
+  double best_us = 1e300;   // the parts looked at: 1 to 8, then an eighth more each time
   for (int tn : {kTile, kNarrow}) {
     const long long tiles = m_tiles * (tn == kTile ? n_tiles : n_narrow);
-    const long long full = tiles / pairs * pairs, left = tiles - full;
+    const int left = (int)(tiles % pairs);
     const double step = tn == kTile ? 0.3 : 0.25, end = tn == kTile ? 2.0 : 1.2;
-    for (int s = 1; s <= 32 && (s == 1 || (left > 0 && s * 2 <= k_steps)); ++s) {
+    const double fixed = (double)(tiles / pairs) * (double)k_steps * step + end;
+    for (int s = 1; s <= pairs && (s == 1 || (left > 0 && s * 2 <= steps)); s += 1 + s / 8) {
       const size_t bytes = s == 1 ? 0 : (size_t)left * s * kTile * tn * sizeof(float);
       if (bytes > budget) break;
-      const double us = (double)(full / pairs * k_steps) * step + end +
-                        (double)((left * s + pairs - 1) / pairs) * (double)((k_steps + s - 1) / s) * step +
+      const double us = fixed + (double)((left * s + pairs - 1) / pairs) * (double)((steps + s - 1) / s) * step +
                         (s == 1 ? 0.0 : 3.5 + (double)bytes * 2.0 / 1e7);
       if (us < best_us * 0.98) {
         best_us = us;
         best.tn = tn;
-        best.full = (int)(s == 1 ? tiles : full);
+        best.full = (int)(s == 1 ? tiles : tiles - left);
         best.splits = s;
         best.bytes = bytes;
       }
     }
   }
+  best.us = best_us;
   return best;
 }
 inline long long tiles_of(long long n, int tile = kTile) { return (n + tile - 1) / tile; }
@@ -513,47 +516,63 @@ __device__ __forceinline__ void store8(float *p, const float (&x)[8]) {
   reinterpret_cast<float4 *>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
 }
 
-// Sum of the cut tiles' partials, in the order of the parts, and
-// Epi::join8(params, row, col, z, up) of eight columns (up: those half a tile
-// further on, in a tile whose B holds two rows for each column).
+// Sum of the cut tiles' partials, in a fixed order, and Epi::join8(params, row,
+// col, z, up) of eight columns (up: those half a tile further on, in a tile whose
+// B holds two rows for each column).  2^lanes_log2 lanes share the parts of eight
+// columns: one thread for 74 parts waits for memory some 15 times (MEASUREJOIN).
 template <class Epi, int TN>
 __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ typename Epi::Params p,
                                                    const __grid_constant__ Shape s, const float *__restrict__ part,
-                                                   long long M, int N) {
+                                                   long long M, int N, int lanes_log2) {
   constexpr int cols = Epi::kGated ? TN / 2 : TN, vecs = cols / 8;
-  const int tiles = s.m_tiles * s.n_tiles - s.full;
-  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < (long long)tiles * kTile * vecs;
-       i += (long long)gridDim.x * 256) {
-    const int c = (int)(i % vecs) * 8, r = (int)(i / vecs % kTile), t = (int)(i / (vecs * kTile));
+  const int tiles = s.m_tiles * s.n_tiles - s.full, lanes = 1 << lanes_log2, lane = threadIdx.x & (lanes - 1);
+  const int rows = (int)min((long long)kTile, M);   // a single row of tiles may be short
+  const long long all = (long long)tiles * rows * vecs;
+  // whole warps go round together
+  for (long long i0 = ((long long)blockIdx.x * 256 + (threadIdx.x & ~31)) >> lanes_log2; i0 < all;
+       i0 += ((long long)gridDim.x * 256) >> lanes_log2) {
+    const long long i = i0 + ((threadIdx.x & 31) >> lanes_log2);
+    const int c = (int)(i % vecs) * 8, r = (int)(i / vecs % rows), t = (int)(i / ((long long)vecs * rows));
     int mt, nt;
-    place_of(s, s.full + t, mt, nt);
+    place_of(s, s.full + min(t, tiles - 1), mt, nt);
     const long long row = (long long)mt * kTile + r;
     const int col = nt * cols + c;
-    if (row >= M || col >= N) continue;
+    const bool ok = i < all && row < M && col < N;
     float z[8] = {}, up[8] = {};
-    const float *src = part + ((long long)t * s.splits * kTile + r) * TN + c;
-    for (int k = 0; k < s.splits; ++k, src += kTile * TN) {
-      float v[8];
-      load8(src, v);
+    if (ok) {
+      const float *src = part + (((long long)t * s.splits + lane) * kTile + r) * TN + c;
+#pragma unroll 4
+      for (int k = lane; k < s.splits; k += lanes, src += (long long)lanes * kTile * TN) {
+        float v[8];
+        load8(src, v);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) z[e] += v[e];
-      if (Epi::kGated) {
-        load8(src + TN / 2, v);
+        for (int e = 0; e < 8; ++e) z[e] += v[e];
+        if (Epi::kGated) {
+          load8(src + TN / 2, v);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) up[e] += v[e];
+          for (int e = 0; e < 8; ++e) up[e] += v[e];
+        }
       }
     }
-    Epi::join8(p, row, col, z, up);
+    for (int off = lanes >> 1; off > 0; off >>= 1)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        z[e] += __shfl_xor_sync(0xffffffffu, z[e], off);
+        if (Epi::kGated) up[e] += __shfl_xor_sync(0xffffffffu, up[e], off);
+      }
+    if (ok && lane == 0) Epi::join8(p, row, col, z, up);
   }
 }
 template <class Epi>
 uly_status launch_join(const typename Epi::Params &p, const Shape &s, const Cut &cut, const float *part, long long M,
                        int N, cudaStream_t stream) {
   if (s.splits == 1) return ULY_OK;
-  const long long vecs = (long long)(s.m_tiles * s.n_tiles - s.full) * kTile * (cut.tn / (Epi::kGated ? 2 : 1)) / 8;
-  const long long want = (vecs + 255) / 256, most = (long long)device_sm_count() * 8;
+  const int lanes_log2 = s.splits > 32 ? 4 : s.splits > 16 ? 3 : s.splits > 8 ? 2 : 0;
+  const long long vecs = (long long)(s.m_tiles * s.n_tiles - s.full) * (M < kTile ? M : kTile) *
+                         (cut.tn / (Epi::kGated ? 2 : 1)) / 8;
+  const long long want = ((vecs << lanes_log2) + 255) / 256, most = (long long)device_sm_count() * 8;
   auto kernel = cut.tn == kTile ? join_kernel<Epi, kTile> : join_kernel<Epi, kNarrow>;
-  kernel<<<(unsigned)(want < most ? want : most), 256, 0, stream>>>(p, s, part, M, N);
+  kernel<<<(unsigned)(want < most ? want : most), 256, 0, stream>>>(p, s, part, M, N, lanes_log2);
   note_launches(1);
   return last_launch_status();
 }
@@ -569,7 +588,7 @@ struct PlainParams {
   int N, out_f32;
 };
 __device__ __forceinline__ float one_over(const long long *n) {
-  return n ? (float)(1.0 / (double)max(__ldg(n), 1ll)) : 1.f;
+  return n ? 1.f / (float)max(__ldg(n), 1ll) : 1.f;
 }
 struct EpiPlain {
   using Params = PlainParams;

@@ -581,7 +581,7 @@ uly_status linear_loss_bwd_launch(int32_t P, int64_t tokens, int32_t D, int32_t 
     o.over = count;
     o.M = rows; o.N = D;
     float *part = at<float>(ws, q.part);
-    st = rows <= skinny::kMaxTokens
+    st = skinny::faster(rows, D, V, q.part_bytes)
              ? skinny::launch_plain_mn(pp, q.ldp, w, o.out, count, rows, D, V, prof::K_LINEAR_LOSS_DX, stream)
              : launch_plain<false>(tz, tw_mn, o, V, part, q.part_bytes, prof::K_LINEAR_LOSS_DX, stream);
     if (st != ULY_OK) return st;

@@ -400,7 +400,7 @@ uly_status linear_bwd_launch(int64_t tokens, int32_t in, int32_t out, int32_t ac
     }
   }
   CUtensorMap ta, tb;
-  if (dx && few_tokens(tokens)) {   // dx[tokens][in] = dz[tokens][nz] W[nz][in]
+  if (dx && skinny::faster(tokens, in, q.nz, q.part)) {   // dx[tokens][in] = dz[tokens][nz] W[nz][in]
     const uly_status st = skinny::launch_plain_mn(dz, q.nz, w, dx, nullptr, tokens, in, q.nz, prof::K_LINEAR_DX, stream);
     if (st != ULY_OK) return st;
   } else if (dx) {

@@ -216,6 +216,16 @@ inline int cluster_size(long long T, long long tiles, long long k_steps) {
   return s;
 }
 
+// Whether this kernel or the pair product is the faster way to out[T][N] over K:
+// here a CTA takes 0.37 us a k-step, with what its ring holds under way, and at
+// most eight share a tile's; the pair product cuts a tile in as many parts as the
+// GPU has pairs.  MEASUREWAY
+inline bool faster(long long T, long long N, long long K, size_t part_bytes = SIZE_MAX) {
+  if (T > kMaxTokens) return false;
+  const long long steps = (K + kBK - 1) / kBK, tiles = (N + kRows - 1) / kRows, ranks = cluster_size(T, tiles, steps);
+  return (double)((steps + ranks - 1) / ranks) * 0.37 <= plain_cut(T, N, K, part_bytes).us + 1.0;
+}
+
 template <class Epi, int NT, bool W_MN>
 uly_status launch_nt(const CUtensorMap &tw, const CUtensorMap &tx, const SkinnyShape &sh, const typename Epi::Params &ep,
                      int tiles, int ranks, cudaStream_t stream) {
