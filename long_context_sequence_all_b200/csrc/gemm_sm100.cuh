@@ -23,8 +23,8 @@
 //
 // A thread holds one row of C, so its own 16-byte stores would fill half a
 // 32-byte sector each, 32 rows apart.  Outputs go through shared memory
-// instead, 64 bytes of a warp's 32 rows at a time, and leave by TMA (8192
-// x 2560 -> 2 x 10240 gated with z kept: 711 -> 675 us).
+// instead, 64 or 128 bytes of a warp's 32 rows at a time, and leave by TMA
+// (8192 x 2560 -> 2 x 10240 gated with z kept: 711 -> 675 us).
 //
 // Every wait is bounded (ULY_ERR_TIMEOUT); a launch that gives up lets its
 // copies land before it frees its tensor memory and returns.
@@ -86,8 +86,11 @@ __device__ __forceinline__ uint32_t map_cta(uint32_t addr, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
   return r;
 }
+// Relaxed: what it hands over is tensor memory that has been read into registers.
+// A release would wait for this thread's stores too (37 tokens' dW over 151936 x
+// 2560, one k-step a tile: 207 us; this way, and with 128-byte rows, 157).
 __device__ __forceinline__ void arrive_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 // Tile load into this CTA's shared memory, completing on a barrier of the
 // CTA pair's leader.
@@ -162,6 +165,23 @@ struct OutRing {
     }
     turn ^= 1;
   }
+  // Both slots as one of 128 bytes a row (128-byte swizzle of make_wide_map()):
+  // half i of it, and one store.
+  __device__ __forceinline__ void write_wide(int i, const uint32_t (&v)[16]) const {
+    const uint32_t at = slot(0) + lane * 128;
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      st_shared_v4(at + (((4 * i + c) ^ (lane & 7)) << 4), v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+  }
+  __device__ __forceinline__ void end_wide(const CUtensorMap *map, int col0, int row0) {
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      tma_store_2d(map, slot(0), col0, row0);
+      bulk_commit_group();
+    }
+    turn ^= 1;
+  }
 };
 
 // A tile's place; tiles go down group_m rows before the next column.
@@ -211,9 +231,9 @@ __device__ __forceinline__ void store_partial(const CUtensorMap *map, const Unit
     for (int h = 0; h < 2; ++h) {
 #pragma unroll
       for (int e = 0; e < 16; ++e) v[e] = a[16 * h + e];
-      out.write(h, v);
+      out.write_wide(h, v);
     }
-    out.end(map, c, map, c + 16, w.part * kTile + row_in_tile);
+    out.end_wide(map, c, w.part * kTile + row_in_tile);
   }
 }
 
@@ -402,6 +422,10 @@ inline bool make_out_map(CUtensorMap *map, const void *base, long long inner, lo
                          bool f32 = false) {
   return make_map_of(map, base, inner, rows, stride, f32 ? 16 : 32, 32, CU_TENSOR_MAP_SWIZZLE_64B, f32);
 }
+inline bool make_wide_map(CUtensorMap *map, const void *base, long long inner, long long rows, long long stride,
+                          bool f32 = false) {
+  return make_map_of(map, base, inner, rows, stride, f32 ? 32 : 64, 32, CU_TENSOR_MAP_SWIZZLE_128B, f32);
+}
 
 // The tiles' width, how many of them are taken whole and the parts of each of the
 // others: the least of a sum of microseconds.  Whole tiles in full turns of the SM
@@ -410,7 +434,7 @@ inline bool make_out_map(CUtensorMap *map, const void *base, long long inner, lo
 // k_steps / splits and, if cut, a second kernel over fp32 partial tiles (written
 // and read once, mostly in L2) of at most `budget` bytes; the last tile's epilogue
 // is not hidden.  A tile of many steps has as many parts as there are pairs (32
-// tokens' dx over 143987 columns, 88 wide: MEASUREPARTS).
+// tokens' dx over 143987 columns, 88 wide: 26 us, 106 in eight parts).
 // 320 tiles of 320 steps on 74 pairs: 4 turns and 24 tiles cut in 3, 4.33 turns
 // instead of 5.  1003 x 1032 -> 1544: 52 narrow tiles 11.9 us, 28 wide ones 13.8;
 // 256 x 10240 -> 2560: 10 wide tiles cut in 7 20.6 us, narrow ones 25.7.
@@ -479,7 +503,7 @@ uly_status launch_tn(const CUtensorMap &ta, const CUtensorMap &tb, const Shape &
   const int units = units_of(s), pairs = device_sm_count() / 2;
   const int grid = 2 * (units < pairs ? units : pairs);
   CUtensorMap tp = ta;
-  if (s.splits > 1 && !make_out_map(&tp, part, TN, (long long)(units - s.full) * kTile, TN, true)) return ULY_ERR_CUDA;
+  if (s.splits > 1 && !make_wide_map(&tp, part, TN, (long long)(units - s.full) * kTile, TN, true)) return ULY_ERR_CUDA;
   kernel<<<grid, kThreads, Layout<TN>::kBytes, stream>>>(ta, tb, tp, s, ep);
   note_launches(1);
   return last_launch_status();
@@ -519,7 +543,8 @@ __device__ __forceinline__ void store8(float *p, const float (&x)[8]) {
 // Sum of the cut tiles' partials, in a fixed order, and Epi::join8(params, row,
 // col, z, up) of eight columns (up: those half a tile further on, in a tile whose
 // B holds two rows for each column).  2^lanes_log2 lanes share the parts of eight
-// columns: one thread for 74 parts waits for memory some 15 times (MEASUREJOIN).
+// columns: one thread for 74 parts waits for memory some 15 times (1 row of 136 columns over
+// 105315: 39 us with the product, 27 this way).
 template <class Epi, int TN>
 __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ typename Epi::Params p,
                                                    const __grid_constant__ Shape s, const float *__restrict__ part,
@@ -648,9 +673,9 @@ struct EpiPlain {
           for (int i = 0; i < 2; ++i) {
 #pragma unroll
             for (int e = 0; e < 16; ++e) v[e] = a[32 * h + 16 * i + e];
-            out.write(i, v);
+            out.write_wide(i, v);
           }
-          out.end(map, c0, c0 + 16 < p.N ? map : nullptr, c0 + 16, row0);
+          out.end_wide(map, c0, row0);
         }
       } else {
         out.begin();
@@ -659,9 +684,9 @@ struct EpiPlain {
 #pragma unroll
           for (int e = 0; e < 16; ++e)
             v[e] = pack_bf16x2(__uint_as_float(a[32 * i + 2 * e]), __uint_as_float(a[32 * i + 2 * e + 1]));
-          out.write(i, v);
+          out.write_wide(i, v);
         }
-        out.end(map, col0, col0 + 32 < p.N ? map : nullptr, col0 + 32, row0);
+        out.end_wide(map, col0, row0);
       }
     }
   }
@@ -674,7 +699,7 @@ inline Cut plain_cut(long long M, long long N, long long K, size_t budget = SIZE
 template <bool A_MN>
 uly_status launch_plain(const CUtensorMap &ta, const CUtensorMap &tb, PlainParams p, long long K, float *part,
                         size_t part_bytes, int kernel_id, cudaStream_t stream) {
-  if (!make_out_map(&p.out_map, p.out, p.N, p.M, p.N, p.out_f32 != 0)) return ULY_ERR_CUDA;
+  if (!make_wide_map(&p.out_map, p.out, p.N, p.M, p.N, p.out_f32 != 0)) return ULY_ERR_CUDA;
   const Cut cut = plain_cut(p.M, p.N, K, part_bytes);
   const Shape s = make_shape(p.M, p.N, K, 1, cut);
   prof::Scope scope(kernel_id, stream);

@@ -118,6 +118,9 @@ struct EpiLinear {
   };
 
   template <int TN>
+  static constexpr bool kWide = TN / (kGated ? 4 : 2) % 64 == 0;   // y_map's boxes, without pre
+
+  template <int TN>
   static __device__ __forceinline__ void tile(const Params &p, const Unit &w, uint32_t acc, int row, int half,
                                               OutRing &out) {
     constexpr int cols = kGated ? TN / 4 : TN / 2;   // output columns of one warpgroup
@@ -157,6 +160,13 @@ struct EpiLinear {
         for (int e = 0; e < 4; ++e) vy[4 * g + e] = pack_bf16x2(z[2 * e], z[2 * e + 1]);
       }
       __syncwarp();
+      if (kWide<TN> && !p.pre) {   // two steps a store
+        const int h = c >> 5 & 1;
+        if (h == 0) out.begin();
+        out.write_wide(h, vy);
+        if (h == 1 || col0 + 32 >= p.N) out.end_wide(&p.y_map, col0 - 32 * h, row0);
+        continue;
+      }
       out.begin();
       out.write(0, vy);
       if (p.pre) out.write(1, vz);
@@ -232,12 +242,13 @@ Cut linear_cut(int64_t tokens, int32_t in, int32_t out, int32_t act) {
 template <int ACT>
 uly_status run_linear(const void *x, const void *w, LinearParams p, int K, float *part, cudaStream_t stream) {
   const Cut cut = linear_cut(p.M, K, p.N, ACT);
+  using Epi = EpiLinear<ACT>;
+  const bool wide = !p.pre && (cut.tn == kTile ? Epi::template kWide<kTile> : Epi::template kWide<kNarrow>);
   CUtensorMap ta, tb;
   if (!make_map(&ta, x, K, p.M, K, kHalf) || !make_map(&tb, w, K, p.NZ, K, b_box(cut)) ||
-      !make_out_map(&p.y_map, p.y, p.N, p.M, p.N) || (p.pre && !make_out_map(&p.pre_map, p.pre, p.N, p.M, p.NZ)) ||
+      !(wide ? make_wide_map : make_out_map)(&p.y_map, p.y, p.N, p.M, p.N, false) || (p.pre && !make_out_map(&p.pre_map, p.pre, p.N, p.M, p.NZ)) ||
       (p.pre && p.NZ > p.N && !make_out_map(&p.up_map, p.pre + p.N, p.N, p.M, p.NZ)))
     return ULY_ERR_CUDA;
-  using Epi = EpiLinear<ACT>;
   const Shape s = make_shape(p.M, p.N, K, gated(ACT), cut);
   prof::Scope scope(prof::K_LINEAR, stream);
   const uly_status st = launch<Epi, false, false>(ta, tb, s, cut, p, part, stream);
