@@ -30,6 +30,8 @@
 // copies land before it frees its tensor memory and returns.
 #pragma once
 
+#include <limits.h>
+
 #include <type_traits>
 
 #include "prof.cuh"
@@ -44,11 +46,11 @@ constexpr int kTile = 256;       // rows of a cluster's tile, and its columns un
 constexpr int kNarrow = 128;
 constexpr int kHalf = 128;       // rows of A in one CTA
 constexpr int kBK = 64;
-constexpr int kOutSlots = 4;
+constexpr int kOutSlots = 2;
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 128 + 32 * kEpiWarps;
 constexpr uint32_t kABytes = kHalf * kBK * 2;             // 16 KB
-constexpr uint32_t kOutSlot = 32 * 64;                    // 32 rows of 32 two-byte or 16 four-byte columns
+constexpr uint32_t kOutSlot = 32 * 128;                   // 32 rows of 64 two-byte or 32 four-byte columns
 // Shared memory of one CTA for tiles of TN columns: the ring of k-steps, the
 // epilogue warps' output slots, barriers.
 template <int TN>
@@ -135,49 +137,46 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, uint32_t sr
                : "memory");
 }
 
-// One epilogue warp's way out: 32 rows (one a lane) x 64 bytes of columns a slot,
-// staged with the 64-byte swizzle of make_out_map(); two slots are one turn (one
-// proxy fence, two stores), two turns are under way at a time.
+// One epilogue warp's way out: 32 rows (one a lane) x 128 bytes of columns a slot,
+// staged with the 128-byte swizzle of make_out_map(); two slots, one leaves while
+// the other is filled.
 struct OutRing {
-  uint32_t base, turn;   // turn: which two of the four slots
+  uint32_t base, turn;   // turn: which slot
   int lane;
-  // All lanes of the warp together: the turn's slots are free ...
+  __device__ __forceinline__ uint32_t chunk(int row, int c) const {   // 16 bytes
+    return base + turn * kOutSlot + row * 128 + ((c ^ (row & 7)) << 4);
+  }
+  // All lanes of the warp together: the slot is free ...
   __device__ __forceinline__ void begin() {
     if (lane == 0) bulk_wait_group_read<1>();
     __syncwarp();
   }
-  // ... take this lane's columns (32 of two bytes, packed, or 16 of four) ...
-  __device__ __forceinline__ uint32_t slot(int i) const { return base + (2 * turn + i) * kOutSlot; }
+  // ... take something read along the rows (v[i]: chunk lane % 8 of row 4 i + lane / 8)
+  // to give it back a row a lane, half i of the row ...
+  __device__ __forceinline__ void stage(const uint4 (&v)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) st_shared_v4(chunk(4 * i + (lane >> 3), lane & 7), v[i].x, v[i].y, v[i].z, v[i].w);
+    __syncwarp();
+  }
+  __device__ __forceinline__ void read(int i, uint32_t (&v)[16]) const {
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(v[4 * c]), "=r"(v[4 * c + 1]), "=r"(v[4 * c + 2]), "=r"(v[4 * c + 3])
+                   : "r"(chunk(lane, 4 * i + c))
+                   : "memory");
+  }
+  // ... take half i of this lane's columns (64 of two bytes, packed, or 32 of four) ...
   __device__ __forceinline__ void write(int i, const uint32_t (&v)[16]) const {
-    const uint32_t at = slot(i) + lane * 64;
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
-      st_shared_v4(at + ((c ^ ((lane >> 1) & 3)) << 4), v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+    for (int c = 0; c < 4; ++c) st_shared_v4(chunk(lane, 4 * i + c), v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
   }
-  // ... and leave: slot i for columns from col<i> of map<i> (a null map: nothing).
-  __device__ __forceinline__ void end(const CUtensorMap *map0, int col0, const CUtensorMap *map1, int col1, int row0) {
+  // ... and leave.
+  __device__ __forceinline__ void end(const CUtensorMap *map, int col0, int row0) {
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) {
-      if (map0) tma_store_2d(map0, slot(0), col0, row0);
-      if (map1) tma_store_2d(map1, slot(1), col1, row0);
-      bulk_commit_group();
-    }
-    turn ^= 1;
-  }
-  // Both slots as one of 128 bytes a row (128-byte swizzle of make_wide_map()):
-  // half i of it, and one store.
-  __device__ __forceinline__ void write_wide(int i, const uint32_t (&v)[16]) const {
-    const uint32_t at = slot(0) + lane * 128;
-#pragma unroll
-    for (int c = 0; c < 4; ++c)
-      st_shared_v4(at + (((4 * i + c) ^ (lane & 7)) << 4), v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
-  }
-  __device__ __forceinline__ void end_wide(const CUtensorMap *map, int col0, int row0) {
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) {
-      tma_store_2d(map, slot(0), col0, row0);
+      tma_store_2d(map, base + turn * kOutSlot, col0, row0);
       bulk_commit_group();
     }
     turn ^= 1;
@@ -231,16 +230,20 @@ __device__ __forceinline__ void store_partial(const CUtensorMap *map, const Unit
     for (int h = 0; h < 2; ++h) {
 #pragma unroll
       for (int e = 0; e < 16; ++e) v[e] = a[16 * h + e];
-      out.write_wide(h, v);
+      out.write(h, v);
     }
-    out.end_wide(map, c, w.part * kTile + row_in_tile);
+    out.end(map, c, w.part * kTile + row_in_tile);
   }
 }
 
-// Epi::Params, and
-//   Epi::tile<TN>(params, unit, acc, row, half, out): one thread's TN / 2
+// Epi::Params,
+//   Epi::before<TN>(params, unit, row0, half, lane): what the epilogue of a whole
+//   tile asks for before its product is there (rows [row0, row0 + 32)), and
+//   Epi::tile<TN>(params, unit, acc, row, half, asked, out): one thread's TN / 2
 //   accumulators (read from tensor memory, that half of the columns from acc on,
 //   before it returns) of C row `row`, in tile column unit.nt.
+struct Nothing {};
+
 template <class Epi, int TN, bool A_MN, bool B_MN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     gemm_pair_sm100_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
@@ -357,14 +360,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     for (int u = cluster; u < units; u += clusters, ++it) {
       const int buf = it & 1;
       const Unit w = unit_of(sh, u);
+      const int row0 = (int)rank * kHalf + quarter * 32;
+      auto asked = Epi::template before<TN>(ep, w, w.part < 0 ? w.mt * kTile + row0 : INT_MAX, half, lane);
       if (!__all_sync(0xffffffffu, mbar_wait(bar(B_ACCF + buf), (uint32_t)((it >> 1) & 1), abort_flag, sh.err,
                                              sh.wait_limit)))
         break;
       tc_fence_after();
       const uint32_t acc = tmem + ((uint32_t)(quarter * 32) << 16) + buf * TN;
-      const int row0 = (int)rank * kHalf + quarter * 32;
       if (w.part >= 0) store_partial<TN>(&tmPart, w, acc, row0, half, out);
-      else Epi::template tile<TN>(ep, w, acc, w.mt * kTile + row0 + lane, half, out);
+      else Epi::template tile<TN>(ep, w, acc, w.mt * kTile + row0 + lane, half, asked, out);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) arrive_cluster(map_cta(bar(B_ACCE + buf), 0));
@@ -420,10 +424,6 @@ inline bool make_map(CUtensorMap *map, const void *base, long long inner, long l
 // An output leaving through an OutRing.
 inline bool make_out_map(CUtensorMap *map, const void *base, long long inner, long long rows, long long stride,
                          bool f32 = false) {
-  return make_map_of(map, base, inner, rows, stride, f32 ? 16 : 32, 32, CU_TENSOR_MAP_SWIZZLE_64B, f32);
-}
-inline bool make_wide_map(CUtensorMap *map, const void *base, long long inner, long long rows, long long stride,
-                          bool f32 = false) {
   return make_map_of(map, base, inner, rows, stride, f32 ? 32 : 64, 32, CU_TENSOR_MAP_SWIZZLE_128B, f32);
 }
 
@@ -503,7 +503,7 @@ uly_status launch_tn(const CUtensorMap &ta, const CUtensorMap &tb, const Shape &
   const int units = units_of(s), pairs = device_sm_count() / 2;
   const int grid = 2 * (units < pairs ? units : pairs);
   CUtensorMap tp = ta;
-  if (s.splits > 1 && !make_wide_map(&tp, part, TN, (long long)(units - s.full) * kTile, TN, true)) return ULY_ERR_CUDA;
+  if (s.splits > 1 && !make_out_map(&tp, part, TN, (long long)(units - s.full) * kTile, TN, true)) return ULY_ERR_CUDA;
   kernel<<<grid, kThreads, Layout<TN>::kBytes, stream>>>(ta, tb, tp, s, ep);
   note_launches(1);
   return last_launch_status();
@@ -618,6 +618,8 @@ __device__ __forceinline__ float one_over(const long long *n) {
 struct EpiPlain {
   using Params = PlainParams;
   static constexpr bool kGated = false;
+  template <int TN>
+  static __device__ __forceinline__ Nothing before(const Params &, const Unit &, int, int, int) { return {}; }
   static __device__ __forceinline__ void add8(const Params &p, long long row, int col, float (&z)[8]) {
     float a[8];
     load8(p.add + row * p.N + col, a);
@@ -637,7 +639,7 @@ struct EpiPlain {
   }
   template <int TN>
   static __device__ __forceinline__ void tile(const Params &p, const Unit &w, uint32_t acc, int row, int half,
-                                              OutRing &out) {
+                                              Nothing &, OutRing &out) {
     const int row0 = row - out.lane;
     const float f = one_over(p.over);
 #pragma unroll 1
@@ -673,9 +675,9 @@ struct EpiPlain {
           for (int i = 0; i < 2; ++i) {
 #pragma unroll
             for (int e = 0; e < 16; ++e) v[e] = a[32 * h + 16 * i + e];
-            out.write_wide(i, v);
+            out.write(i, v);
           }
-          out.end_wide(map, c0, row0);
+          out.end(map, c0, row0);
         }
       } else {
         out.begin();
@@ -684,9 +686,9 @@ struct EpiPlain {
 #pragma unroll
           for (int e = 0; e < 16; ++e)
             v[e] = pack_bf16x2(__uint_as_float(a[32 * i + 2 * e]), __uint_as_float(a[32 * i + 2 * e + 1]));
-          out.write_wide(i, v);
+          out.write(i, v);
         }
-        out.end_wide(map, col0, row0);
+        out.end(map, col0, row0);
       }
     }
   }
@@ -699,7 +701,7 @@ inline Cut plain_cut(long long M, long long N, long long K, size_t budget = SIZE
 template <bool A_MN>
 uly_status launch_plain(const CUtensorMap &ta, const CUtensorMap &tb, PlainParams p, long long K, float *part,
                         size_t part_bytes, int kernel_id, cudaStream_t stream) {
-  if (!make_wide_map(&p.out_map, p.out, p.N, p.M, p.N, p.out_f32 != 0)) return ULY_ERR_CUDA;
+  if (!make_out_map(&p.out_map, p.out, p.N, p.M, p.N, p.out_f32 != 0)) return ULY_ERR_CUDA;
   const Cut cut = plain_cut(p.M, p.N, K, part_bytes);
   const Shape s = make_shape(p.M, p.N, K, 1, cut);
   prof::Scope scope(kernel_id, stream);

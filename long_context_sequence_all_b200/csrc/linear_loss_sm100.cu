@@ -55,8 +55,10 @@ template <bool STORE_P>
 struct EpiLoss {
   using Params = LossParams;
   template <int TN>
+  static __device__ __forceinline__ Nothing before(const Params &, const Unit &, int, int, int) { return {}; }
+  template <int TN>
   static __device__ __forceinline__ void tile(const Params &p, const Unit &w, uint32_t acc, int row, int half,
-                                              OutRing &out) {
+                                              Nothing &, OutRing &out) {
     static_assert(TN / 2 == kSlot, "a warpgroup's columns are one slot");
     const int col0 = w.nt * kTile + half * kSlot;
     const int ncol = min(kSlot, p.vocab - col0);   // columns of the vocabulary here; may be <= 0
@@ -105,10 +107,10 @@ struct EpiLoss {
             v[e / 2] = *reinterpret_cast<const uint32_t *>(&x);
           }
         }
-        if (STORE_P) out.write_wide(h, v);
+        if (STORE_P) out.write(h, v);
       }
       if (STORE_P)
-        out.end_wide(&p.p_map, col0 + c, row0);
+        out.end(&p.p_map, col0 + c, row0);
     }
     if (ok) p.pairs[(long long)(w.nt * 2 + half) * p.rows_pad + row] = make_float2(ref, (s[0] + s[1]) + (s[2] + s[3]));
   }
@@ -464,7 +466,7 @@ uly_status logits_pass(const __nv_bfloat16 *x, const void *w, int D, LossParams 
   }
   CUtensorMap tx, tw;
   if (!make_map(&tw, w, D, V, D, kHalf) || !make_map(&tx, x, D, rows, D, kHalf) ||
-      (GRAD && !make_wide_map(&p.p_map, pp, V, rows, ldp)))
+      (GRAD && !make_out_map(&p.p_map, pp, V, rows, ldp)))
     return ULY_ERR_CUDA;
   return launch_tn<EpiLoss<GRAD>, kTile, false, false>(tx, tw, make_shape(rows, V, D, 1, whole(rows, V)), p, nullptr, stream);
 }
