@@ -411,8 +411,8 @@ enum {
                         * out_features up rows (bias and pre alike)                */
 };
 
-/* Bytes of device workspace ulysses_linear needs on the current device (0 for
- * products with enough tiles to fill it: the workspace may then be NULL). */
+/* Bytes of device workspace ulysses_linear needs on the current device (0 for up
+ * to 128 tokens and where whole tiles fill it: the workspace may then be NULL). */
 uly_status ulysses_linear_workspace_size(int64_t tokens, int32_t in_features, int32_t out_features,
                                          int32_t activation, size_t *bytes);
 
@@ -429,9 +429,10 @@ uly_status ulysses_linear_workspace_size(int64_t tokens, int32_t in_features, in
  *   y:        DEVICE bf16 [tokens][out_features]
  *   pre:      NULL or DEVICE bf16 [tokens][nz]: z, kept for the backward
  * tokens >= 0 (0 does nothing); in_features and out_features multiples of 8
- * (else ULY_ERR_ALIGN).  Few tokens are bound by w's bytes: the product is then
- * cut along in_features over all SMs into fp32 partials (`workspace`), added in
- * a fixed order.  Bitwise repeatable.  Outputs must not overlap anything else.
+ * (else ULY_ERR_ALIGN).  Tiles of the output that would leave SMs idle are cut
+ * along in_features into fp32 partials (`workspace`), added in a fixed order; up
+ * to 128 tokens, bound by w's bytes, the parts of a sum meet on the chip instead.
+ * Bitwise repeatable.  Outputs must not overlap anything else.
  */
 uly_status ulysses_linear(int64_t tokens, int32_t in_features, int32_t out_features, int32_t activation,
                           const void *x, const void *w, const void *bias, const void *residual, void *y, void *pre,

@@ -46,6 +46,10 @@ constexpr int kTile = 256;       // rows of a cluster's tile, and its columns un
 constexpr int kNarrow = 128;
 constexpr int kHalf = 128;       // rows of A in one CTA
 constexpr int kBK = 64;
+// Elements: operands of this library's own making have rows of whole 128-byte
+// lines (dW of 1503 tokens, 520 over 32003: 73 us with rows of 1040 and 64016
+// bytes, 60 this way).
+constexpr int kRowAlign = 64;
 constexpr int kOutSlots = 2;
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 128 + 32 * kEpiWarps;

@@ -321,8 +321,8 @@ struct GradParams {
   const int32_t *labels;
   uint4 *p;                   // [rows][ldp / 8]: fp16 in, bf16 out
   const uint4 *x;
-  uint4 *xk;                  // [rows][hidden / 8]
-  long long ldp;
+  uint4 *xk;                  // [rows][ldx / 8]
+  long long ldp, ldx;
   int slots, vocab, ignore_index, hidden, rows;
   CloseParams close;          // of CTA (rows, 0)
 };
@@ -337,8 +337,8 @@ __global__ void __launch_bounds__(kGradThreads) loss_grad_kernel(const __grid_co
   const int y = __ldg(p.labels + row);
   const bool counted = y != p.ignore_index && y >= 0 && y < p.vocab;
   const uint4 zero = make_uint4(0, 0, 0, 0);
-  const int vecs = (int)(p.ldp / 8), i0 = blockIdx.y * (kGradCols / 8) + threadIdx.x;
-  uint4 *o = p.p + (long long)row * vecs;
+  const int vecs = (p.vocab + 7) / 8, i0 = blockIdx.y * (kGradCols / 8) + threadIdx.x;
+  uint4 *o = p.p + row * (p.ldp / 8);
   uint4 h[kGradVecs];
   float f[kGradVecs];
 #pragma unroll
@@ -375,7 +375,7 @@ __global__ void __launch_bounds__(kGradThreads) loss_grad_kernel(const __grid_co
   if (blockIdx.y == 0) {
     const int xv = p.hidden / 8;
     for (int i = threadIdx.x; i < xv; i += kGradThreads)
-      p.xk[(long long)row * xv + i] = counted ? __ldg(p.x + (long long)row * xv + i) : zero;
+      p.xk[row * (p.ldx / 8) + i] = counted ? __ldg(p.x + (long long)row * xv + i) : zero;
   }
 }
 
@@ -423,7 +423,7 @@ long long piece_of(long long tokens, long long row_bytes, long long budget) {
 }
 
 struct Plan {
-  long long piece, rows_pad, ldp;
+  long long piece, rows_pad, ldp, ldx;   // ldp, ldx: row strides of p and of the copy of x
   int slots;
   bool dw_acc;   // dW of several pieces is summed in an fp32 array of the workspace
   size_t psum, pcnt, count, row_loss, row_lse, target, pairs, factor, p, xk, part, acc, bytes;   // offsets, total
@@ -433,7 +433,8 @@ struct Plan {
 Plan make_plan(int P, long long T, int D, int V, bool grad, int dw_dtype, long long piece_tokens) {
   Plan q = {};
   q.slots = (V + kTile - 1) / kTile * 2;
-  q.ldp = round_up(V, 8);
+  q.ldp = round_up(V, kRowAlign);
+  q.ldx = round_up(D, kRowAlign);
   q.piece = piece_tokens > 0 ? (piece_tokens < T ? piece_tokens : (T > 0 ? T : 1))
             : grad           ? piece_of(T, q.ldp * 2, kPieceBytes)
                              : piece_of(T, (long long)q.slots * 8, kPairBytes);
@@ -451,7 +452,7 @@ Plan make_plan(int P, long long T, int D, int V, bool grad, int dw_dtype, long l
     q.row_lse = take((size_t)q.piece * sizeof(float));
     q.factor = take((size_t)q.piece * q.slots * sizeof(float));
     q.p = take((size_t)q.piece * q.ldp * 2);
-    q.xk = take((size_t)q.piece * D * 2);
+    q.xk = take((size_t)q.piece * q.ldx * 2);
     const size_t a = plain_cut(q.piece, D, V).bytes, b = plain_cut(V, D, q.piece).bytes;
     q.part_bytes = a > b ? a : b;
     q.part = take(q.part_bytes);
@@ -585,7 +586,7 @@ uly_status linear_loss_bwd_launch(int32_t P, int64_t tokens, int32_t D, int32_t 
     void *pp = at<char>(ws, q.p), *xk = at<char>(ws, q.xk);
     LossParams p = {};
     if (!make_map(&tz, pp, V, rows, q.ldp, kHalf) || !make_map(&tz_mn, pp, V, rows, q.ldp, 64) ||
-        !make_map(&tk_mn, xk, D, rows, D, 64))
+        !make_map(&tk_mn, xk, D, rows, q.ldx, 64))
       return ULY_ERR_CUDA;
     p.labels = labels + t0;
     p.pairs = at<float2>(ws, q.pairs);
@@ -602,12 +603,12 @@ uly_status linear_loss_bwd_launch(int32_t P, int64_t tokens, int32_t D, int32_t 
     g.p = static_cast<uint4 *>(pp);
     g.x = reinterpret_cast<const uint4 *>(xb + t0 * D);
     g.xk = static_cast<uint4 *>(xk);
-    g.ldp = q.ldp; g.slots = r.slots; g.vocab = V; g.ignore_index = ignore_index; g.hidden = D; g.rows = rows;
+    g.ldp = q.ldp; g.ldx = q.ldx; g.slots = r.slots; g.vocab = V; g.ignore_index = ignore_index; g.hidden = D; g.rows = rows;
     g.close = close;
     {
       prof::Scope scope(prof::K_LINEAR_LOSS_ROWS, stream);
       loss_rows_kernel<true><<<(rows + kRowsCta - 1) / kRowsCta, kRowThreads, 0, stream>>>(r);
-      const long long cols = (q.ldp + kGradCols - 1) / kGradCols;
+      const long long cols = (V + kGradCols - 1) / kGradCols;
       loss_grad_kernel<<<dim3(rows + closed, (unsigned)cols), kGradThreads, 0, stream>>>(g);
       note_launches(2);
       if (last_launch_status() != ULY_OK) return ULY_ERR_CUDA;

@@ -301,6 +301,7 @@ struct DzParams {
   float *part;                     // [gridDim.y * 8][NZ]; null without a bias gradient
   long long M;
   int N, NZ, rows_per_cta;
+  long long ld;                    // row stride of dz
 };
 
 template <int ACT>
@@ -332,15 +333,15 @@ __global__ void __launch_bounds__(256) linear_dz_kernel(const DzParams p) {
         s0[e] += a[e];
         s1[e] += b[e];
       }
-      store8(p.dz + r * p.NZ + col, a);
-      store8(p.dz + r * p.NZ + p.N + col, b);
+      store8(p.dz + r * p.ld + col, a);
+      store8(p.dz + r * p.ld + p.N + col, b);
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         d[e] *= dact_of<ACT>(z[e]);
         s0[e] += d[e];
       }
-      store8(p.dz + r * p.NZ + col, d);
+      store8(p.dz + r * p.ld + col, d);
     }
   }
   if (p.part) {
@@ -362,6 +363,7 @@ int dz_row_ctas(int64_t tokens, int32_t out) {
 // partials (the two products run one after the other and share them).
 struct BwdPlan {
   int nz, row_ctas;
+  long long ld;   // row stride of dz (dy itself without an activation)
   size_t off_bias, off_part, part, bytes;
 };
 size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
@@ -369,7 +371,8 @@ BwdPlan bwd_plan(int64_t tokens, int32_t in, int32_t out, int32_t act) {
   BwdPlan q;
   q.nz = out * gated(act);
   q.row_ctas = dz_row_ctas(tokens, out);
-  q.off_bias = act == ULY_ACT_NONE ? 0 : up256((size_t)tokens * q.nz * 2);
+  q.ld = act == ULY_ACT_NONE ? q.nz : (q.nz + kRowAlign - 1) / kRowAlign * kRowAlign;
+  q.off_bias = act == ULY_ACT_NONE ? 0 : up256((size_t)tokens * q.ld * 2);
   q.off_part = q.off_bias + up256((size_t)q.row_ctas * 8 * q.nz * sizeof(float));
   const size_t a = plain_cut(tokens, in, q.nz).bytes, b = plain_cut(q.nz, in, tokens).bytes;
   q.part = a > b ? a : b;
@@ -429,7 +432,7 @@ uly_status linear_bwd_launch(int64_t tokens, int32_t in, int32_t out, int32_t ac
     p.dy = static_cast<const __nv_bfloat16 *>(dy);
     p.dz = static_cast<__nv_bfloat16 *>(workspace);
     p.part = dbias ? bias_part : nullptr;
-    p.M = tokens; p.N = out; p.NZ = q.nz;
+    p.M = tokens; p.N = out; p.NZ = q.nz; p.ld = q.ld;
     p.rows_per_cta = (int)((tokens + q.row_ctas - 1) / q.row_ctas);
     const dim3 grid((out / 8 + 31) / 32, q.row_ctas);
     prof::Scope scope(prof::K_LINEAR_DZ, stream);
@@ -449,17 +452,17 @@ uly_status linear_bwd_launch(int64_t tokens, int32_t in, int32_t out, int32_t ac
   }
   CUtensorMap ta, tb;
   if (dx && skinny::faster(tokens, in, q.nz, q.part)) {   // dx[tokens][in] = dz[tokens][nz] W[nz][in]
-    const uly_status st = skinny::launch_plain_mn(dz, q.nz, w, dx, nullptr, tokens, in, q.nz, prof::K_LINEAR_DX, stream);
+    const uly_status st = skinny::launch_plain_mn(dz, q.ld, w, dx, nullptr, tokens, in, q.nz, prof::K_LINEAR_DX, stream);
     if (st != ULY_OK) return st;
   } else if (dx) {
-    if (!make_map(&ta, dz, q.nz, tokens, q.nz, kHalf) || !make_map(&tb, w, in, q.nz, in, 64)) return ULY_ERR_CUDA;
+    if (!make_map(&ta, dz, q.nz, tokens, q.ld, kHalf) || !make_map(&tb, w, in, q.nz, in, 64)) return ULY_ERR_CUDA;
     PlainParams p = {};
     p.out = dx; p.M = tokens; p.N = in;
     const uly_status st = launch_plain<false>(ta, tb, p, q.nz, part, q.part, prof::K_LINEAR_DX, stream);
     if (st != ULY_OK) return st;
   }
   if (dw) {   // dW[nz][in] = dz^T x
-    if (!make_map(&ta, dz, q.nz, tokens, q.nz, 64) || !make_map(&tb, x, in, tokens, in, 64)) return ULY_ERR_CUDA;
+    if (!make_map(&ta, dz, q.nz, tokens, q.ld, 64) || !make_map(&tb, x, in, tokens, in, 64)) return ULY_ERR_CUDA;
     PlainParams p = {};
     p.out = dw; p.out_f32 = dw_dtype == ULY_F32; p.M = q.nz; p.N = in;
     return launch_plain<true>(ta, tb, p, tokens, part, q.part, prof::K_LINEAR_DW, stream);
