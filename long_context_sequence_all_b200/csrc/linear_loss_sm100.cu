@@ -311,8 +311,8 @@ __device__ __forceinline__ void close_shards(const CloseParams &p) {
 }
 __global__ void __launch_bounds__(1024) loss_close_kernel(const __grid_constant__ CloseParams p) { close_shards(p); }
 
-// p becomes dz: kGradCols columns of one row a CTA.  The first CTA of a row also
-// copies x, with zeros in the rows that do not count (a row of a padded batch
+// p becomes dz: kGradCols columns of a CTA's rows.  Those of the first columns also
+// copy x, with zeros in the rows that do not count (a row of a padded batch
 // may hold anything, and 0 times NaN is not 0).  Where the piece is all there is, a
 // row of CTAs more closes the losses, which saves two launches (16 tokens of 296
 // over 17192: 55 -> 50 us, 40 -> 36 in a graph).
@@ -323,36 +323,49 @@ struct GradParams {
   const uint4 *x;
   uint4 *xk;                  // [rows][ldx / 8]
   long long ldp, ldx;
-  int slots, vocab, ignore_index, hidden, rows;
-  CloseParams close;          // of CTA (rows, 0)
+  int slots, vocab, ignore_index, hidden, rows, closing;
+  CloseParams close;          // of the last column of CTAs, if `closing`
 };
-constexpr int kGradThreads = 256, kGradVecs = 4, kGradCols = kGradThreads * kGradVecs * 8;
+constexpr int kGradPerSm = 4, kGradThreads = 256, kGradVecs = 4, kGradCols = kGradThreads * kGradVecs * 8;
 
+// A CTA goes down the rows of its columns; a row's values are asked for while the
+// row before is worked on, its label two rows ahead.
 __global__ void __launch_bounds__(kGradThreads) loss_grad_kernel(const __grid_constant__ GradParams p) {
-  const int row = blockIdx.x;
-  if (row == p.rows) {
+  const int step = gridDim.x - p.closing;
+  if (blockIdx.x == step) {
     if (blockIdx.y == 0) close_shards(p.close);
     return;
   }
-  const int y = __ldg(p.labels + row);
-  const bool counted = y != p.ignore_index && y >= 0 && y < p.vocab;
   const uint4 zero = make_uint4(0, 0, 0, 0);
   const int vecs = (p.vocab + 7) / 8, i0 = blockIdx.y * (kGradCols / 8) + threadIdx.x;
-  uint4 *o = p.p + row * (p.ldp / 8);
-  uint4 h[kGradVecs];
-  float f[kGradVecs];
+  auto label = [&](int row) { return row < p.rows ? __ldg(p.labels + row) : p.ignore_index; };
+  auto counts = [&](int y) { return y != p.ignore_index && y >= 0 && y < p.vocab; };
+  uint4 next[kGradVecs];
+  float fnext[kGradVecs];
+  auto ask = [&](int row, int y) {
 #pragma unroll
-  for (int k = 0; k < kGradVecs; ++k) {
-    const int i = i0 + k * kGradThreads;
-    h[k] = counted && i < vecs ? __ldcs(o + i) : zero;
-    f[k] = counted && i < vecs ? __ldg(p.factor + (long long)row * p.slots + i / (kSlot / 8)) : 0.f;
-  }
+    for (int k = 0; k < kGradVecs; ++k) {
+      const int i = i0 + k * kGradThreads;
+      const bool ok = counts(y) && i < vecs;
+      next[k] = ok ? __ldcs(p.p + row * (p.ldp / 8) + i) : zero;
+      fnext[k] = ok ? __ldg(p.factor + (long long)row * p.slots + i / (kSlot / 8)) : 0.f;
+    }
+  };
+  int y = label(blockIdx.x), y1 = label(blockIdx.x + step);
+  ask(blockIdx.x, y);
+  for (int row = blockIdx.x; row < p.rows; row += step) {
+    const bool counted = counts(y);
+    uint4 h[kGradVecs];
+    float f[kGradVecs];
 #pragma unroll
-  for (int k = 0; k < kGradVecs; ++k) {
-    const int i = i0 + k * kGradThreads;
-    if (i >= vecs) break;
-    uint4 q = zero;
-    if (counted) {
+    for (int k = 0; k < kGradVecs; ++k) { h[k] = next[k]; f[k] = fnext[k]; }
+    const int y2 = label(row + 2 * step);
+    ask(row + step, y1);
+    uint4 *o = p.p + row * (p.ldp / 8);
+#pragma unroll
+    for (int k = 0; k < kGradVecs; ++k) {
+      const int i = i0 + k * kGradThreads;
+      if (i >= vecs) break;
       const __half2 *hp = reinterpret_cast<const __half2 *>(&h[k]);
       float v[8];
 #pragma unroll
@@ -361,21 +374,22 @@ __global__ void __launch_bounds__(kGradThreads) loss_grad_kernel(const __grid_co
         v[2 * e] = t.x * f[k];
         v[2 * e + 1] = t.y * f[k];
       }
-      if (i == y / 8) {
+      if (counted && i == y / 8) {
         // z_y <= lse but for rounding: the label's softmax is at most 1
         const float dy = expm1f(fminf(p.target[row] - p.row_lse[row], 0.f));
 #pragma unroll
         for (int e = 0; e < 8; ++e)
           if (e == y % 8) v[e] = dy;
       }
-      q = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+      o[i] = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
     }
-    o[i] = q;
-  }
-  if (blockIdx.y == 0) {
-    const int xv = p.hidden / 8;
-    for (int i = threadIdx.x; i < xv; i += kGradThreads)
-      p.xk[row * (p.ldx / 8) + i] = counted ? __ldg(p.x + (long long)row * xv + i) : zero;
+    if (blockIdx.y == 0) {
+      const int xv = p.hidden / 8;
+      for (int i = threadIdx.x; i < xv; i += kGradThreads)
+        p.xk[row * (p.ldx / 8) + i] = counted ? __ldg(p.x + (long long)row * xv + i) : zero;
+    }
+    y = y1;
+    y1 = y2;
   }
 }
 
@@ -603,13 +617,14 @@ uly_status linear_loss_bwd_launch(int32_t P, int64_t tokens, int32_t D, int32_t 
     g.p = static_cast<uint4 *>(pp);
     g.x = reinterpret_cast<const uint4 *>(xb + t0 * D);
     g.xk = static_cast<uint4 *>(xk);
-    g.ldp = q.ldp; g.ldx = q.ldx; g.slots = r.slots; g.vocab = V; g.ignore_index = ignore_index; g.hidden = D; g.rows = rows;
+    g.ldp = q.ldp; g.ldx = q.ldx; g.slots = r.slots; g.vocab = V; g.ignore_index = ignore_index; g.hidden = D; g.rows = rows; g.closing = closed;
     g.close = close;
     {
       prof::Scope scope(prof::K_LINEAR_LOSS_ROWS, stream);
       loss_rows_kernel<true><<<(rows + kRowsCta - 1) / kRowsCta, kRowThreads, 0, stream>>>(r);
       const long long cols = (V + kGradCols - 1) / kGradCols;
-      loss_grad_kernel<<<dim3(rows + closed, (unsigned)cols), kGradThreads, 0, stream>>>(g);
+      const long long ctas = ((long long)device_sm_count() * kGradPerSm + cols - 1) / cols;
+      loss_grad_kernel<<<dim3((unsigned)((rows < ctas ? rows : ctas) + closed), (unsigned)cols), kGradThreads, 0, stream>>>(g);
       note_launches(2);
       if (last_launch_status() != ULY_OK) return ULY_ERR_CUDA;
     }

@@ -351,10 +351,16 @@ __global__ void __launch_bounds__(256) linear_dz_kernel(const DzParams p) {
   }
 }
 
-// CTAs along the tokens: about eight an SM in all, no shorter than 64 rows.
+// CTAs along the tokens: about eight an SM in all, of at least 64 rows, or of 16
+// where that leaves SMs without one (391 x 808: 10.2 -> 4.9 us).
 int dz_row_ctas(int64_t tokens, int32_t out) {
   const long long cols = (out / 8 + 31) / 32;
-  long long ctas = (long long)device_sm_count() * 8 / cols, most = (tokens + 63) / 64;
+  const long long sms = device_sm_count();
+  long long ctas = sms * 8 / cols, most = (tokens + 63) / 64;
+  if (most * cols < sms) {
+    most = (tokens + 15) / 16;
+    if (most * cols > sms) most = (sms + cols - 1) / cols;
+  }
   if (ctas > most) ctas = most;
   return (int)(ctas < 1 ? 1 : ctas);
 }
