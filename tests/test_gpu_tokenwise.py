@@ -635,3 +635,70 @@ assert U.ulysses_read_error() == 0
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stdout + r.stderr
+
+
+# ------------------------------------------- tiles, parts and folds at their edges
+
+@pytest.mark.parametrize("T,K,N,act,bias,residual", [
+    (300, 64, 72, "swiglu", True, True),        # narrow gated tiles, the last one of 8 features
+    (2050, 64, 1000, "swiglu", False, True),    # wide ones, a residual that ends inside the last
+    (700, 72, 200, "none", True, True),
+    (5000, 128, 2600, "gelu", True, True),      # the residual asked for a tile ahead, several tiles an SM pair
+    (4099, 8, 4104, "silu", False, True),       # one k-step a tile
+    (1, 8, 40000, "none", True, False),         # dx of few tokens over a long sum, cut over the SM pairs
+    (17, 72, 30000, "gelu", True, False),
+    (128, 200, 20000, "silu", False, False),
+    (390, 72, 808, "gelu", True, False),        # dz of few tokens in strips of two rows
+    (20000, 16, 72, "none", True, False),       # a bias gradient of many partials and few columns
+])
+def test_linear_at_the_edges(T, K, N, act, bias, residual):
+    test_linear_forward(T, K, N, act, bias, residual)
+    test_linear_backward(T, K, N, act, bias, residual, torch.float32)
+
+
+@pytest.mark.parametrize("P,T,D,V", [(1, 1, 136, 50001), (3, 33, 72, 30011), (8, 128, 72, 20000), (2, 1502, 72, 4003),
+                                     (8, 16384, 8, 72), (1, 700, 1000, 264)])
+def test_linear_loss_at_the_edges(P, T, D, V):
+    test_linear_loss(P, T, D, V, 1.0, 0.2, 0, torch.bfloat16)
+
+
+@pytest.mark.parametrize("P,B,s,D,gate", [(1, 1, 30000, 64, "channel"), (2, 3, 5000, 64, "sequence"), (1, 2, 9000, 512, "channel")])
+def test_residual_norm_of_many_short_rows(P, B, s, D, gate):
+    test_residual_norm_backward(P, B, s, D, torch.bfloat16, gate, True)
+
+
+@pytest.mark.parametrize("tokens", [48, 300])
+def test_linear_loss_count_is_no_rounding(tokens):
+    """w = 0: softmax = 1/V.  A label's dz, 1/V - 1, rounds to -1 (off by 1/V), the
+    others', 1/V, are off by half a step (2^-8 of themselves) and 2^-11; 1/C, no
+    power of two, is applied in fp32 (two roundings) and is no part of it."""
+    V, D = 65536, 64
+    w = torch.zeros(V, D, device="cuda", dtype=torch.bfloat16)
+    x = torch.ones(tokens, D, device="cuda", dtype=torch.bfloat16)
+    y = (torch.arange(tokens, device="cuda", dtype=torch.int32) * 211) % V
+    _, _, loss, dx, dw = U.ulysses_linear_loss_bwd(x, w, y, 1, grad_dtype=torch.float32)
+    ref = torch.full((V, D), 1.0 / V, device="cuda", dtype=torch.float64)
+    ref[y.long()] -= 1.0 / tokens
+    bound = (1 + tokens * (HALF + 2.0 ** -11)) / V / tokens + 2 * U32 * ref.abs()
+    _within(dw, ref, MORE * bound, "dw")
+    assert not dx.any() and abs(loss.item() - math.log(V)) <= 4 * U32 * math.log(V)
+
+
+def test_linear_loss_does_not_read_what_it_padded():
+    """Scratch rows are longer than the vocabulary and the hidden size: what lies behind is NaN and not used."""
+    g = _gen(90)
+    for T, D, V in ((20, 72, 1001), (300, 72, 1001)):
+        x, w = _rnd(g, T, D), _rnd(g, V, D, scale=D ** -0.5)
+        y = torch.randint(0, V, (T,), generator=g, device="cuda", dtype=torch.int32)
+        n = U.ulysses_linear_loss_bwd_workspace_size(1, T, D, V, torch.float32)
+        got = []
+        for fill in (0, 255):   # bytes 255: NaN in every type
+            ws = torch.full((n,), fill, device="cuda", dtype=torch.uint8)
+            got.append(U.ulysses_linear_loss_bwd(x, w, y, 1, workspace=ws))
+        assert all(torch.equal(a, b) for a, b in zip(*got)) and torch.isfinite(got[1][4]).all()
+    T, K, N = 300, 72, 136
+    x, w, dy, pre = _rnd(g, T, K), _rnd(g, N, K), _rnd(g, T, N), _rnd(g, T, N)
+    n = U.ulysses_linear_bwd_workspace_size(T, K, N, U.ACT_GELU)
+    a, b = (U.ulysses_linear_bwd(x, w, dy, pre=pre, activation=U.ACT_GELU, bias_grad=True,
+                                 workspace=torch.full((n,), f, device="cuda", dtype=torch.uint8)) for f in (0, 255))
+    assert all(torch.equal(p, q) for p, q in zip(a, b))
