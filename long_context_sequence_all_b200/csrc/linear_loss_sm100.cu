@@ -187,71 +187,6 @@ struct SkinnyLoss {
   }
 };
 
-// Four rows a CTA: their pairs (one 32-byte sector for a slot of all four) are
-// folded in a fixed order into lse and the rows' losses.  GRAD: and each slot's
-// factor exp(maximum - lse) of its stored exponentials, [row][slot].
-struct RowsParams {
-  const float2 *pairs;
-  const float *target;
-  const int32_t *labels;
-  float *row_loss, *row_lse;  // of the piece's rows
-  float *factor;              // [rows][slots]
-  long long rows_pad;
-  int rows, slots, vocab, ignore_index;
-  int *err;
-};
-constexpr int kRowsCta = 4, kRowThreads = 512;
-
-template <bool GRAD>
-__global__ void __launch_bounds__(kRowThreads) loss_rows_kernel(const RowsParams p) {
-  constexpr int kWarps = kRowThreads / 32;
-  __shared__ float sh_m[kWarps][kRowsCta], sh_s[kWarps][kRowsCta];
-  __shared__ float sh_lse[kRowsCta];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int row0 = blockIdx.x * kRowsCta, nrows = min(kRowsCta, p.rows - row0);
-  float m[kRowsCta], s[kRowsCta];
-#pragma unroll
-  for (int r = 0; r < kRowsCta; ++r) { m[r] = 0.f; s[r] = 0.f; }
-  for (int k = threadIdx.x; k < p.slots; k += kRowThreads) {
-    // rows past the last one are in the padding of the array: read, not used
-    const float4 *v = reinterpret_cast<const float4 *>(p.pairs + (long long)k * p.rows_pad + row0);
-    const float4 a = __ldg(v), b = __ldg(v + 1);
-    merge(m[0], s[0], a.x, a.y);
-    merge(m[1], s[1], a.z, a.w);
-    merge(m[2], s[2], b.x, b.y);
-    merge(m[3], s[3], b.z, b.w);
-  }
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1)
-#pragma unroll
-    for (int r = 0; r < kRowsCta; ++r) {
-      const float m2 = __shfl_down_sync(0xffffffffu, m[r], off), s2 = __shfl_down_sync(0xffffffffu, s[r], off);
-      merge(m[r], s[r], m2, s2);
-    }
-  if (lane == 0)
-#pragma unroll
-    for (int r = 0; r < kRowsCta; ++r) { sh_m[warp][r] = m[r]; sh_s[warp][r] = s[r]; }
-  __syncthreads();
-  if (threadIdx.x < nrows) {
-    const int r = threadIdx.x;
-    float mm = sh_m[0][r], ss = sh_s[0][r];
-    for (int k = 1; k < kWarps; ++k) merge(mm, ss, sh_m[k][r], sh_s[k][r]);
-    const float lse = mm + logf(ss);
-    const int y = __ldg(p.labels + row0 + r);
-    const bool counted = y != p.ignore_index && y >= 0 && y < p.vocab;
-    if (y != p.ignore_index && !counted) raise_error(p.err, ULY_ERR_LABEL);
-    p.row_loss[row0 + r] = counted ? lse - p.target[row0 + r] : 0.f;
-    if (GRAD) p.row_lse[row0 + r] = sh_lse[r] = lse;
-  }
-  if (!GRAD) return;
-  __syncthreads();
-  for (int k = threadIdx.x; k < p.slots; k += kRowThreads) {
-    const float2 *v = p.pairs + (long long)k * p.rows_pad + row0;
-    for (int r = 0; r < nrows; ++r)
-      p.factor[(long long)(row0 + r) * p.slots + k] = exp2f((v[r].x - sh_lse[r]) * kLog2e) / kScale;
-  }
-}
-
 // The shards' losses and valid labels and the fold over the shards by one CTA, for
 // up to 8 shards of a modest batch: 32 parts, as many a shard as fit, a warp each
 // (fewer warps take several), joined in their order.
@@ -310,6 +245,86 @@ __device__ __forceinline__ void close_shards(const CloseParams &p) {
   }
 }
 __global__ void __launch_bounds__(1024) loss_close_kernel(const __grid_constant__ CloseParams p) { close_shards(p); }
+
+// Four rows a CTA: their pairs (one 32-byte sector for a slot of all four) are
+// folded in a fixed order into lse and the rows' losses.  GRAD: and each slot's
+// factor exp(maximum - lse) of its stored exponentials, [row][slot].
+struct RowsParams {
+  const float2 *pairs;
+  const float *target;
+  const int32_t *labels;
+  float *row_loss, *row_lse;  // of the piece's rows
+  float *factor;              // [rows][slots]
+  long long rows_pad;
+  int rows, slots, vocab, ignore_index;
+  int *err;
+  CloseParams close;
+};
+constexpr int kRowsCta = 4, kRowThreads = 512;
+
+template <bool GRAD>
+__device__ __forceinline__ void rows_of_cta(const RowsParams &p, int row0) {
+  constexpr int kWarps = kRowThreads / 32;
+  __shared__ float sh_m[kWarps][kRowsCta], sh_s[kWarps][kRowsCta];
+  __shared__ float sh_lse[kRowsCta];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int nrows = min(kRowsCta, p.rows - row0);
+  float m[kRowsCta], s[kRowsCta];
+#pragma unroll
+  for (int r = 0; r < kRowsCta; ++r) { m[r] = 0.f; s[r] = 0.f; }
+  for (int k = threadIdx.x; k < p.slots; k += kRowThreads) {
+    // rows past the last one are in the padding of the array: read, not used
+    const float4 *v = reinterpret_cast<const float4 *>(p.pairs + (long long)k * p.rows_pad + row0);
+    const float4 a = __ldg(v), b = __ldg(v + 1);
+    merge(m[0], s[0], a.x, a.y);
+    merge(m[1], s[1], a.z, a.w);
+    merge(m[2], s[2], b.x, b.y);
+    merge(m[3], s[3], b.z, b.w);
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1)
+#pragma unroll
+    for (int r = 0; r < kRowsCta; ++r) {
+      const float m2 = __shfl_down_sync(0xffffffffu, m[r], off), s2 = __shfl_down_sync(0xffffffffu, s[r], off);
+      merge(m[r], s[r], m2, s2);
+    }
+  if (lane == 0)
+#pragma unroll
+    for (int r = 0; r < kRowsCta; ++r) { sh_m[warp][r] = m[r]; sh_s[warp][r] = s[r]; }
+  __syncthreads();
+  if (threadIdx.x < nrows) {
+    const int r = threadIdx.x;
+    float mm = sh_m[0][r], ss = sh_s[0][r];
+    for (int k = 1; k < kWarps; ++k) merge(mm, ss, sh_m[k][r], sh_s[k][r]);
+    const float lse = mm + logf(ss);
+    const int y = __ldg(p.labels + row0 + r);
+    const bool counted = y != p.ignore_index && y >= 0 && y < p.vocab;
+    if (y != p.ignore_index && !counted) raise_error(p.err, ULY_ERR_LABEL);
+    p.row_loss[row0 + r] = counted ? lse - p.target[row0 + r] : 0.f;
+    if (GRAD) p.row_lse[row0 + r] = sh_lse[r] = lse;
+  }
+  if (!GRAD) return;
+  __syncthreads();
+  for (int k = threadIdx.x; k < p.slots; k += kRowThreads) {
+    const float2 *v = p.pairs + (long long)k * p.rows_pad + row0;
+    for (int r = 0; r < nrows; ++r)
+      p.factor[(long long)(row0 + r) * p.slots + k] = exp2f((v[r].x - sh_lse[r]) * kLog2e) / kScale;
+  }
+}
+
+template <bool GRAD>
+__global__ void __launch_bounds__(kRowThreads) loss_rows_kernel(const __grid_constant__ RowsParams p) {
+  rows_of_cta<GRAD>(p, blockIdx.x * kRowsCta);
+}
+// Few rows, all there are: the CTAs are one cluster, and its first also closes the
+// losses (12 tokens of 2536 over 1103: 26.7 -> 24.6 us; a launch of more CTAs costs
+// what the second one did).
+constexpr int kOneCluster = 4, kOneRows = kOneCluster * kRowsCta;
+__global__ void __launch_bounds__(kRowThreads) loss_rows_close_kernel(const __grid_constant__ RowsParams p) {
+  if ((int)blockIdx.x * kRowsCta < p.rows) rows_of_cta<false>(p, blockIdx.x * kRowsCta);
+  cluster_sync();   // the rows' losses are there for the whole cluster
+  if (blockIdx.x == 0) close_shards(p.close);
+}
 
 // p becomes dz: kGradCols columns of a CTA's rows.  Those of the first columns also
 // copy x, with zeros in the rows that do not count (a row of a padded batch
@@ -528,6 +543,27 @@ CloseParams close_of(const Plan &q, int P, long long T, int V, const int32_t *la
   return c;
 }
 
+uly_status rows_close(const RowsParams &r, cudaStream_t stream) {
+  unsigned ctas = 1;
+  while (ctas < kOneCluster && (int)ctas * kRowsCta < r.rows) ctas *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(kRowThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = ctas;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, loss_rows_close_kernel, r) != cudaSuccess) {
+    cudaGetLastError();
+    return ULY_ERR_CUDA;
+  }
+  note_launches(1);
+  return last_launch_status();
+}
+
 uly_status finish(const Plan &q, const CloseParams &c, long long T, void *ws, cudaStream_t stream) {
   if (one_close(c.P, T)) {
     prof::Scope scope(prof::K_LOSS_FINALIZE, stream);
@@ -554,6 +590,7 @@ uly_status linear_loss_launch(int32_t P, int64_t tokens, int32_t D, int32_t V, c
                               float *loss, void *ws, cudaStream_t stream) {
   const Plan q = make_plan(P, tokens, D, V, false, ULY_F32, 0);
   const __nv_bfloat16 *xb = static_cast<const __nv_bfloat16 *>(x);
+  const CloseParams close = close_of(q, P, tokens, V, labels, ignore_index, shard_sum, shard_count, loss, ws);
   for (long long t0 = 0; t0 < tokens; t0 += q.piece) {
     const int rows = (int)(tokens - t0 < q.piece ? tokens - t0 : q.piece);
     LossParams p = {};
@@ -566,11 +603,15 @@ uly_status linear_loss_launch(int32_t P, int64_t tokens, int32_t D, int32_t V, c
     if (st != ULY_OK) return st;
     RowsParams r = rows_of(q, p, ws, t0);
     prof::Scope scope(prof::K_LINEAR_LOSS_ROWS, stream);
+    if (tokens <= kOneRows && q.piece >= tokens && one_close(P, tokens)) {
+      r.close = close;
+      return rows_close(r, stream);
+    }
     loss_rows_kernel<false><<<(rows + kRowsCta - 1) / kRowsCta, kRowThreads, 0, stream>>>(r);
     note_launches(1);
     if (last_launch_status() != ULY_OK) return ULY_ERR_CUDA;
   }
-  return finish(q, close_of(q, P, tokens, V, labels, ignore_index, shard_sum, shard_count, loss, ws), tokens, ws, stream);
+  return finish(q, close, tokens, ws, stream);
 }
 
 size_t linear_loss_bwd_workspace_bytes(int32_t P, int64_t tokens, int32_t hidden, int32_t vocab, int32_t dw_dtype,

@@ -702,3 +702,9 @@ def test_linear_loss_does_not_read_what_it_padded():
     a, b = (U.ulysses_linear_bwd(x, w, dy, pre=pre, activation=U.ACT_GELU, bias_grad=True,
                                  workspace=torch.full((n,), f, device="cuda", dtype=torch.uint8)) for f in (0, 255))
     assert all(torch.equal(p, q) for p, q in zip(a, b))
+
+
+@pytest.mark.parametrize("P,T,D,V", [(1, 1, 64, 1003), (3, 3, 64, 20001), (1, 5, 72, 300), (8, 16, 64, 5000), (7, 28, 72, 2049),
+                                     (1, 33, 64, 1003), (2, 64, 128, 4099), (1, 65, 64, 1003), (9, 63, 64, 777)])
+def test_linear_loss_of_few_tokens(P, T, D, V):
+    test_linear_loss(P, T, D, V, 1.0, 0.3, 0, torch.float32)
