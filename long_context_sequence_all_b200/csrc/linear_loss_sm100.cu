@@ -134,12 +134,14 @@ struct SkinnyLossParams {
 };
 struct SkinnyLoss {
   using Params = SkinnyLossParams;
-  static __device__ __forceinline__ void finish(const Params &q, const skinny::Tile &tile, int index, int, int) {
+  static __device__ __forceinline__ void finish(const Params &q, const skinny::Tile &tile, int index, int rank, int ranks) {
     const LossParams &p = q.l;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int col = index * kSlot + 4 * lane, ncol = p.vocab - index * kSlot;
-    // four tokens of a warp at a time: their shuffles overlap
-    for (int t0 = warp * 4; t0 < p.rows; t0 += skinny::kSkinnyThreads / 8) {
+    // four tokens of a warp at a time: their shuffles overlap; the tile's CTAs share
+    // the tokens, a row's slot is one warp's
+    for (int t0 = (rank * (skinny::kSkinnyThreads / 32) + warp) * 4; t0 < p.rows;
+         t0 += ranks * (skinny::kSkinnyThreads / 8)) {
       float z[4][4], m[4], s[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -501,17 +503,30 @@ Cut whole(long long rows, long long V) {
   return c;
 }
 
+// Whether the weights' side of few rows' logits is the M side: up to 64 rows always,
+// bound by w's bytes (64 to 128 rows: 165 against 191 us over 151936 x 2560 for the
+// pair product); up to 128 where the vocabulary gives few tiles, whose k-steps only
+// that way are shared by several SMs (100 x 2536 over 1103: 33 us
+// on the pair product, 23 this way).
+bool few_rows(long long rows, long long steps, long long slots) {
+  if (rows > skinny::kMaxTokens) return false;
+  if (rows <= 64) return true;
+  const long long ranks = skinny::cluster_size(rows, slots, steps), pairs = device_sm_count() / 2;
+  const long long turns = (tiles_of(rows) * ((slots + 1) / 2) + pairs - 1) / pairs;
+  return skinny::micros(rows, slots * kSlot, steps, ranks) < (double)(turns * steps) * 0.3 + 8.0;
+}
+
 // The pairs, targets and (grad) exponentials of a piece's rows.
 template <bool GRAD>
 uly_status logits_pass(const __nv_bfloat16 *x, const void *w, int D, LossParams &p, void *pp, long long ldp,
                        cudaStream_t stream) {
   prof::Scope scope(prof::K_LINEAR_LOSS, stream);
   const int rows = p.rows, V = p.vocab;
-  // w's bytes bound the product; from 64 rows on the pair product streams them
-  // as fast (128 rows: 165 against 191 us over 151936 x 2560)
-  if (rows <= 64) {
+  const long long steps = (D + kBK - 1) / kBK, slots = (V + kSlot - 1) / kSlot;
+  if (few_rows(rows, steps, slots)) {
     SkinnyLossParams s = {p, GRAD ? static_cast<__half *>(pp) : nullptr, ldp};
-    return skinny::launch<SkinnyLoss, false>(w, D, V, x, D, rows, D, (V + kSlot - 1) / kSlot, 1, kSlot, 64, s, stream);
+    return skinny::launch<SkinnyLoss, false>(w, D, V, x, D, rows, D, (int)slots, skinny::cluster_size(rows, slots, steps),
+                                             kSlot, 64, s, stream);
   }
   CUtensorMap tx, tw;
   if (!make_map(&tw, w, D, V, D, kHalf) || !make_map(&tx, x, D, rows, D, kHalf) ||

@@ -216,17 +216,21 @@ inline int cluster_size(long long T, long long tiles, long long k_steps) {
   return s;
 }
 
-// Whether this kernel or the pair product is the faster way to out[T][N] over K.
-// Here a CTA takes 0.35 us a k-step (what its ring holds is always under way), at
-// most eight share a tile's, and all of them together move 5.2 TB/s; the pair
-// product cuts a tile in as many parts as the GPU has pairs.
+// About how long the product takes: a CTA 0.35 us a k-step (what its ring holds is
+// always under way), all of them together move 5.2 TB/s.
+inline double micros(long long T, long long N, long long steps, long long ranks) {
+  const double latency = (double)((steps + ranks - 1) / ranks) * 0.35, bytes = (double)N * (double)steps * kBK * 2.0 / 5.2e6;
+  return 4.0 + 0.05 * (double)T + (latency > bytes ? latency : bytes);
+}
+// Whether this kernel or the pair product is the faster way to out[T][N] over K:
+// at most eight CTAs share a tile's k-steps here; the pair product cuts a tile in
+// as many parts as the GPU has pairs.
 // 16 tokens over 17192, 296 wide: 15 us here, 18 there; 1 over 105315, 136 wide:
 // 62 and 23; 100 over 151936, 2560 wide: 156 and 143.
 inline bool faster(long long T, long long N, long long K, size_t part_bytes = SIZE_MAX) {
   if (T > kMaxTokens) return false;
-  const long long steps = (K + kBK - 1) / kBK, tiles = (N + kRows - 1) / kRows, ranks = cluster_size(T, tiles, steps);
-  const double latency = (double)((steps + ranks - 1) / ranks) * 0.35, bytes = (double)N * (double)K * 2.0 / 5.2e6;
-  return 4.0 + 0.05 * (double)T + (latency > bytes ? latency : bytes) <= plain_cut(T, N, K, part_bytes).us + 7.0;
+  const long long steps = (K + kBK - 1) / kBK, ranks = cluster_size(T, (N + kRows - 1) / kRows, steps);
+  return micros(T, N, steps, ranks) <= plain_cut(T, N, K, part_bytes).us + 7.0;
 }
 
 template <class Epi, int NT, bool W_MN>

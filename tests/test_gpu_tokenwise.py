@@ -708,3 +708,9 @@ def test_linear_loss_does_not_read_what_it_padded():
                                      (1, 33, 64, 1003), (2, 64, 128, 4099), (1, 65, 64, 1003), (9, 63, 64, 777)])
 def test_linear_loss_of_few_tokens(P, T, D, V):
     test_linear_loss(P, T, D, V, 1.0, 0.3, 0, torch.float32)
+
+
+@pytest.mark.parametrize("P,T,D,V", [(1, 100, 1000, 1103), (3, 33, 2560, 5000), (8, 128, 648, 300), (1, 12, 2536, 1103),
+                                     (2, 66, 4096, 100), (1, 1, 4096, 130)])
+def test_linear_loss_of_tiles_shared_by_clusters(P, T, D, V):
+    test_linear_loss(P, T, D, V, 1.0, 0.3, 0, torch.float32)
