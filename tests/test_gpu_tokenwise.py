@@ -714,3 +714,117 @@ def test_linear_loss_of_few_tokens(P, T, D, V):
                                      (2, 66, 4096, 100), (1, 1, 4096, 130)])
 def test_linear_loss_of_tiles_shared_by_clusters(P, T, D, V):
     test_linear_loss(P, T, D, V, 1.0, 0.3, 0, torch.float32)
+
+
+# ------------------------------------------------------ offsets past 32 bits
+
+def test_linear_past_32_bit_offsets():
+    """2.5e9 elements in y, pre, residual and dz: the first, middle and last rows, and the sums over all."""
+    g = _gen(101)
+    T, K, N = 600001, 64, 4096
+    x, w, b = _rnd(g, T, K), _rnd(g, N, K, scale=K ** -0.5), _rnd(g, N, scale=0.5)
+    r = torch.empty(T, N, device="cuda", dtype=torch.bfloat16)
+    for t in range(0, T, 65536):
+        r[t:t + 65536] = _rnd(g, min(65536, T - t), N)
+    y, pre = U.ulysses_linear(x, w, bias=b, residual=r, activation=U.ACT_GELU, save_pre=True)
+    dx, dw, db = U.ulysses_linear_bwd(x, w, r, pre=pre, activation=U.ACT_GELU, bias_grad=True)
+    wd = w.double()
+    dw_ref, dw_bound = (torch.zeros(N, K, device="cuda", dtype=torch.float64) for _ in range(2))
+    db_ref, db_bound = (torch.zeros(N, device="cuda", dtype=torch.float64) for _ in range(2))
+    for t in range(0, T, 40000):
+        at = slice(t, min(t + 40000, T))
+        xd, rd, zd = x[at].double(), r[at].double(), pre[at].double()
+        z = xd @ wd.t() + b.double()
+        ez = (K + 2) * U32 * (xd.abs() @ wd.abs().t() + b.double().abs())
+        _within(pre[at], z, HALF * z.abs() + MORE * ez + 1e-30, "pre")
+        a, _ = _act64(z, "gelu")
+        ref = a + rd
+        ea = 1.13 * ez + 2.0 ** -18 * (2 + z.abs())
+        _within(y[at], ref, HALF * ref.abs() + MORE * ea + U32 * (a.abs() + ref.abs()) + 1e-30, "y")
+        _, d = _act64(zd, "gelu")
+        dz, e32 = rd * d, 2.0 ** -18 * (2 + zd.abs()) * rd.abs()
+        ref = dz @ wd
+        _within(dx[at], ref, HALF * ref.abs() + MORE * ((HALF * dz.abs() + e32 + N * U32 * dz.abs()) @ wd.abs()) + 1e-30, "dx")
+        dw_ref += dz.t() @ xd
+        dw_bound += (HALF * dz.abs() + e32 + T * U32 * dz.abs()).t() @ xd.abs()
+        db_ref += dz.sum(0)
+        db_bound += (e32 + T * U32 * dz.abs()).sum(0)
+    _within(dw, dw_ref, MORE * dw_bound + 1e-30, "dw")
+    _within(db, db_ref, MORE * db_bound + 1e-30, "dbias")
+
+
+def test_residual_norm_past_32_bit_offsets():
+    """2.5e9 elements a tensor: every row against 64 bits in pieces, both directions."""
+    g = _gen(102)
+    P, B, s, D, a, eps = 2, 1, 150001, 8192, 0.75, 1e-6
+    mk = lambda: torch.cat([_rnd(g, 1, B, s, D) for _ in range(P)])
+    x, h, w1, w2 = mk(), mk(), _rnd(g, D, mean=1.0), _rnd(g, D, mean=1.0)
+    r, u = U.ulysses_residual_norm(x, h, w_pre=w1, w_post=w2, res_scale=a, eps=eps)
+    dx, dh, dw1, dw2, _ = U.ulysses_residual_norm_bwd(r, h, dr=x, du=h, w_pre=w1, w_post=w2, res_scale=a, eps=eps)
+    esum, e = (D / 2 + 8) * 2.0 ** -24, (2 * D + 32) * 2.0 ** -24
+    flat = lambda t: t.view(-1, D)
+    w1d, w2d = w1.double(), w2.double()
+    dw1_ref, dw1_terms, dw2_ref, dw2_terms = (torch.zeros(D, device="cuda", dtype=torch.float64) for _ in range(4))
+    for t in range(0, P * s, 20000):
+        at = slice(t, min(t + 20000, P * s))
+        xd, hd, rd = (flat(v)[at].double() for v in (x, h, r))
+        branch, ih = _rms64(hd, w2d, eps)
+        ref = a * xd + branch
+        er = esum * branch.abs() + 4 * U32 * (branch.abs() + (a * xd).abs())
+        _within(flat(r)[at], ref, HALF * ref.abs() + MORE * er + 1e-30, "r")
+        un, i = _rms64(ref, w1d, eps)
+        em = (ref.abs() * er).mean(-1, keepdim=True) * i * i
+        eu = er * i * w1d.abs() + (esum + em + 4 * U32) * un.abs()
+        _within(flat(u)[at], un, HALF * un.abs() + MORE * eu + 1e-30, "u")
+        # backward, from the stored r, with dr = x and du = h
+        rn, i = _rms64(rd, None, eps)
+        aw = hd * w1d
+        dR = xd + i * (aw - rn * (aw * rn).mean(-1, keepdim=True))
+        m1 = xd.abs() + i * (aw.abs() + rn.abs() * (aw * rn).abs().mean(-1, keepdim=True))
+        _within(flat(dx)[at], a * dR, HALF * (a * dR).abs() + e * a * m1 + 1e-30, "dx")
+        hn, b, bm = hd * ih, dR * w2d, m1 * w2d.abs()
+        ref = ih * (b - hn * (b * hn).mean(-1, keepdim=True))
+        mh = ih * (bm + hn.abs() * (bm * hn.abs()).mean(-1, keepdim=True))
+        _within(flat(dh)[at], ref, HALF * ref.abs() + 2 * e * mh + 1e-30, "dh")
+        dw1_ref += (hd * rn).sum(0)
+        dw1_terms += (hd * rn).abs().sum(0)
+        dw2_ref += (dR * hn).sum(0)
+        dw2_terms += (m1 * hn.abs()).sum(0)
+    es = e + (P * s + 8) * 2.0 ** -24
+    _within(dw1, dw1_ref, es * dw1_terms + 1e-30, "dw_pre")
+    _within(dw2, dw2_ref, 2 * es * dw2_terms + 1e-30, "dw_post")
+
+
+def test_linear_loss_past_32_bit_offsets():
+    """2.5e9 logits in one piece, their exponentials in 4.9 GB of the workspace."""
+    g = _gen(103)
+    T, D, V = 4097, 64, 600011
+    x, w = _rnd(g, T, D), _rnd(g, V, D, scale=D ** -0.5)
+    y = torch.randint(0, V, (T,), generator=g, device="cuda", dtype=torch.int32)
+    y[::7] = -100
+    y[-1] = V - 1
+    S, C, L, dx, dw = U.ulysses_linear_loss_bwd(x, w, y, 1, piece_tokens=T)
+    assert torch.equal(L, U.ulysses_linear_loss(x, w, y, 1)[2])
+    keep = y != -100
+    count = int(keep.sum())
+    wd, xd = w.double(), x.double()
+    ez = D * U32 * (xd.abs().max() * wd.abs().max() * D)   # above every logit's error
+    total = 0.0
+    dw_ref, dw_bound = (torch.zeros(V, D, device="cuda", dtype=torch.float64) for _ in range(2))
+    for t in range(0, T, 500):
+        at = slice(t, min(t + 500, T))
+        z = xd[at] @ wd.t()
+        lse = torch.logsumexp(z, 1)
+        idx = torch.where(keep[at], y[at], 0).long()[:, None]
+        total += ((lse - z.gather(1, idx)[:, 0]) * keep[at]).sum().item()
+        dz = torch.exp_(z.sub_(lse[:, None]))
+        dz.scatter_add_(1, idx, -torch.ones_like(idx, dtype=torch.float64))
+        dz *= keep[at][:, None] / count
+        soft = dz.abs()
+        e = HALF + 2.0 ** -11 + 2 * ez
+        ref = dz @ wd
+        _within(dx[at], ref, HALF * ref.abs() + MORE * (e + V * U32) * (soft @ wd.abs()) + 1e-12, "dx")
+        dw_ref += dz.t() @ xd[at]
+        dw_bound += (e + T * U32) * (soft.t() @ xd[at].abs())
+    assert C.item() == count and abs(L.item() - total / count) <= LOSS_REL * total / count + 2 * ez
+    _within(dw, dw_ref, MORE * dw_bound + 1e-12, "dw")
