@@ -543,7 +543,8 @@ uly_status ulysses_linear_loss_bwd_workspace_size(int32_t world, int64_t tokens,
  * with the global count C as the only denominator, as ulysses_loss_aggregate_bwd.
  * The tokens are taken in pieces: a piece's exponentials, then its dz, are held
  * in the workspace in 16 bits (piece_tokens x vocab x 2 bytes), all tokens' never
- * are; dz is rounded to bf16 once, as the products' operand.
+ * are; dz C is rounded to bf16 once, as the products' operand, and the products'
+ * fp32 sums are divided by C.
  * piece_tokens = 0: as many tokens as fit 4 GiB of them (at least 256).
  * Several pieces sum dw in fp32 (for ULY_BF16 in vocab x hidden x 4 bytes of
  * the workspace) and round it once.  Rows of ignored or invalid labels give
