@@ -134,7 +134,8 @@ struct SkinnyLossParams {
 };
 struct SkinnyLoss {
   using Params = SkinnyLossParams;
-  static __device__ __forceinline__ void finish(const Params &q, const skinny::Tile &tile, int index, int rank, int ranks) {
+  template <class T>
+  static __device__ __forceinline__ void finish(const Params &q, const T &tile, int index, int rank, int ranks) {
     const LossParams &p = q.l;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int col = index * kSlot + 4 * lane, ncol = p.vocab - index * kSlot;

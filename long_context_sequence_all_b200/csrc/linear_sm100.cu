@@ -226,7 +226,8 @@ struct SkinnyLinear {
   using Params = LinearParams;
   static constexpr bool kGated = ACT == ULY_ACT_SWIGLU;
   static constexpr int kCols = kGated ? 64 : 128;
-  static __device__ __forceinline__ void finish(const Params &p, const skinny::Tile &tile, int index, int rank,
+  template <class T>
+  static __device__ __forceinline__ void finish(const Params &p, const T &tile, int index, int rank,
                                                 int ranks) {
     skinny::for_slice(kCols, rank, ranks, (int)p.M, [&](int row, int t) {
       const int col = index * kCols + row;   // N is a multiple of 8

@@ -5,7 +5,7 @@
 // The roles are swapped: 128 rows of the weight matrix are the M side of the
 // tensor-core product (with N = the tokens, 16 to 128), so a k-step of 64 costs
 // 16 KB of weights and little else.  A tile's k-steps are shared by a cluster of
-// up to eight CTAs, which meet in distributed shared memory: each adds one slice
+// up to sixteen CTAs, which meet in distributed shared memory: each adds one slice
 // of the tile's rows over the cluster in a fixed order and runs the epilogue on
 // it.  No partial leaves the chip, no second launch, no counters.  Several CTAs
 // share an SM (one loads while another finishes), so no CTA is persistent.
@@ -26,7 +26,7 @@ using namespace gemm;
 constexpr int kRows = 128;               // weight rows of a tile
 constexpr int kSkinnyThreads = 128;
 constexpr int kMaxTokens = 128;
-constexpr int kMaxCluster = 8;
+constexpr int kCluster = 8, kMaxCluster = 16;   // CTAs of a tile; the second for long sums of few tokens
 constexpr uint32_t kWBytes = kRows * kBK * 2;   // 16 KB
 
 template <int NT>
@@ -63,15 +63,16 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map
 
 // A tile's sums, when every CTA of the cluster has staged its own: element
 // (row, token) is the sum over the cluster, in rank order.
+template <int MAX>
 struct Tile {
-  uint32_t part[kMaxCluster];   // cluster addresses of [token][row] fp32
+  uint32_t part[MAX];   // cluster addresses of [token][row] fp32
   int ranks;
   // rows [row, row + 4), row a multiple of 4
   __device__ __forceinline__ void sum4(int row, int token, float (&v)[4]) const {
     const uint32_t at = (token * kRows + row) * 4;
     float4 a = ld_cluster4(part[0] + at);
 #pragma unroll
-    for (int r = 1; r < kMaxCluster; ++r)
+    for (int r = 1; r < MAX; ++r)
       if (r < ranks) {
         const float4 b = ld_cluster4(part[r] + at);
         a.x += b.x; a.y += b.y; a.z += b.z; a.w += b.w;
@@ -101,7 +102,7 @@ __device__ __forceinline__ void for_slice(int cols, int rank, int ranks, int T, 
 // The `ranks` CTAs of a tile are a cluster.
 // Epi::Params, and Epi::finish(params, tile, index, rank, ranks): all threads
 // of the CTA, its slice of tile `index`.
-template <class Epi, int NT, bool W_MN>
+template <class Epi, int NT, bool W_MN, int MAX>
 __global__ void __launch_bounds__(kSkinnyThreads)
     skinny_sm100_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                         const SkinnyShape sh, const __grid_constant__ typename Epi::Params ep) {
@@ -190,10 +191,10 @@ __global__ void __launch_bounds__(kSkinnyThreads)
   tc_fence_before();
   if (ranks > 1) cluster_sync();
   else __syncthreads();
-  Tile tile;
+  Tile<MAX> tile;
   tile.ranks = ranks;
 #pragma unroll
-  for (int r = 0; r < kMaxCluster; ++r) tile.part[r] = r < ranks ? map_cta(sb, r) : 0;
+  for (int r = 0; r < MAX; ++r) tile.part[r] = r < ranks ? map_cta(sb, r) : 0;
   Epi::finish(ep, tile, index, rank, ranks);
   if (ranks > 1) cluster_sync();   // the peers have read this CTA's sums
   else __syncthreads();
@@ -207,13 +208,26 @@ __global__ void __launch_bounds__(kSkinnyThreads)
 
 inline int tokens_padded(long long T) { return T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : 128; }
 
-// CTAs that share a tile's k-steps: as many as the SMs have room for at once,
-// at least four k-steps each.
+// CTAs that share a tile's k-steps: as many as the SMs have room for at once, of at
+// least four k-steps each and up to eight; sixteen of at least eight for up to 32
+// tokens (24 x 10240 -> 2560: 18.2 us with eight, 16.6 so; 64 x 8192 -> 2048, whose
+// sums over the cluster are longer: 17.0 and 19.4).
 inline int cluster_size(long long T, long long tiles, long long k_steps) {
   const long long room = (long long)device_sm_count() * (tokens_padded(T) == 128 ? Shared<128>::kPerSm : Shared<64>::kPerSm);
   int s = 1;
-  while (s < kMaxCluster && tiles * s * 2 <= room && k_steps >= 8 * s) s *= 2;
-  return s;
+  while (s < kCluster && tiles * s * 2 <= room && k_steps >= 8 * s) s *= 2;
+  return s == kCluster && T <= 32 && tiles * kMaxCluster <= room && k_steps >= 8 * kMaxCluster ? kMaxCluster : s;
+}
+// Opt `kernel` into clusters of more than eight CTAs, once per device.
+template <typename Kernel>
+inline bool wide_optin(Kernel kernel, std::atomic<uint64_t> &done) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+  const uint64_t bit = uint64_t(1) << dev;
+  if (done.load(std::memory_order_acquire) & bit) return true;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) return false;
+  done.fetch_or(bit, std::memory_order_acq_rel);
+  return true;
 }
 
 // About how long the product takes: a CTA 0.35 us a k-step (what its ring holds is
@@ -223,7 +237,7 @@ inline double micros(long long T, long long N, long long steps, long long ranks)
   return 4.0 + 0.05 * (double)T + (latency > bytes ? latency : bytes);
 }
 // Whether this kernel or the pair product is the faster way to out[T][N] over K:
-// at most eight CTAs share a tile's k-steps here; the pair product cuts a tile in
+// at most sixteen CTAs share a tile's k-steps here; the pair product cuts a tile in
 // as many parts as the GPU has pairs.
 // 16 tokens over 17192, 296 wide: 15 us here, 18 there; 1 over 105315, 136 wide:
 // 62 and 23; 100 over 151936, 2560 wide: 156 and 143.
@@ -233,12 +247,13 @@ inline bool faster(long long T, long long N, long long K, size_t part_bytes = SI
   return micros(T, N, steps, ranks) <= plain_cut(T, N, K, part_bytes).us + 7.0;
 }
 
-template <class Epi, int NT, bool W_MN>
+template <class Epi, int NT, bool W_MN, int MAX = kCluster>
 uly_status launch_nt(const CUtensorMap &tw, const CUtensorMap &tx, const SkinnyShape &sh, const typename Epi::Params &ep,
                      int tiles, int ranks, cudaStream_t stream) {
-  static std::atomic<uint64_t> optin{0};
-  auto kernel = skinny_sm100_kernel<Epi, NT, W_MN>;
+  static std::atomic<uint64_t> optin{0}, wide{0};
+  auto kernel = skinny_sm100_kernel<Epi, NT, W_MN, MAX>;
   if (!smem_optin(kernel, (int)Shared<NT>::kBytes, optin)) return ULY_ERR_CUDA;
+  if (MAX > kCluster && !wide_optin(kernel, wide)) return ULY_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)tiles * ranks);
   cfg.blockDim = dim3(kSkinnyThreads);
@@ -275,6 +290,9 @@ uly_status launch(const void *w, long long w_inner, long long w_rows, const void
   sh.w_half = w_half;
   sh.err = error_word();
   sh.wait_limit = wait_limit_cycles();
+  if (ranks > kCluster)   // an instance of its own: eight more parts cost the others a microsecond
+    return nt == 16 ? launch_nt<Epi, 16, W_MN, kMaxCluster>(tw, tx, sh, ep, tiles, ranks, stream)
+                    : launch_nt<Epi, 32, W_MN, kMaxCluster>(tw, tx, sh, ep, tiles, ranks, stream);
   switch (nt) {
     case 16: return launch_nt<Epi, 16, W_MN>(tw, tx, sh, ep, tiles, ranks, stream);
     case 32: return launch_nt<Epi, 32, W_MN>(tw, tx, sh, ep, tiles, ranks, stream);
@@ -290,7 +308,8 @@ struct SkinnyPlain {
     const long long *over;
     int T, N;
   };
-  static __device__ __forceinline__ void finish(const Params &p, const Tile &tile, int index, int rank, int ranks) {
+  template <class T>
+  static __device__ __forceinline__ void finish(const Params &p, const T &tile, int index, int rank, int ranks) {
     const float f = gemm::one_over(p.over);
     for_slice(kRows, rank, ranks, p.T, [&](int row, int t) {
       float v[4];

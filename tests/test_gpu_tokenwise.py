@@ -828,3 +828,14 @@ def test_linear_loss_past_32_bit_offsets():
         dw_bound += (e + T * U32) * (soft.t() @ xd[at].abs())
     assert C.item() == count and abs(L.item() - total / count) <= LOSS_REL * total / count + 2 * ez
     _within(dw, dw_ref, MORE * dw_bound + 1e-12, "dw")
+
+
+@pytest.mark.parametrize("T,K,N,act,bias,residual", [
+    (24, 8200, 264, "none", True, True),        # sixteen CTAs a tile
+    (1, 8192, 72, "swiglu", True, True),
+    (32, 12288 + 8, 136, "gelu", False, False),
+    (33, 8192, 136, "silu", True, True),        # eight again
+])
+def test_linear_of_few_tokens_over_long_sums(T, K, N, act, bias, residual):
+    test_linear_forward(T, K, N, act, bias, residual)
+    test_linear_backward(T, N, K, act, bias, residual, torch.float32)   # dx over K
