@@ -217,7 +217,7 @@ struct Ring {
       if (STAGED && all.p[k])
         for (int i = threadIdx.x; i < vecs; i += blockDim.x)
           reinterpret_cast<uint4 *>(mem + k * row_bytes)[i] = __ldg(all.p[k] + i);
-    base = mem + (STAGED ? 3 * row_bytes : 0) + (size_t)team * stages * stage_bytes;
+    base = first_stage() + (size_t)team * stages * stage_bytes;
     bars = barriers + team * kMaxStages;
     at = 0;
     phase = 0;
@@ -227,6 +227,8 @@ struct Ring {
     sm100::fence_mbar_init();
     __syncthreads();
   }
+  // the first team's stages, the others' behind them
+  __device__ __forceinline__ uint8_t *first_stage() const { return mem + (STAGED ? 3 * row_bytes : 0); }
   // vector i * lanes + l of those that all rows share
   __device__ __forceinline__ uint4 common(const Shared3 &all, int k, int at) const {
     return STAGED ? reinterpret_cast<const uint4 *>(mem + k * row_bytes)[l + at] : __ldg(all.p[k] + l + at);
@@ -392,8 +394,8 @@ struct NormBwdParams {
   Shared3 all;                   // w_post, w_pre, a gate that all tokens share
   const uint4 *gate;
   uint4 *dx, *dh, *dgate_tok;
-  float *part_pre;               // [teams][vecs * 2 E]: sums of du rn; null where not asked for
-  float *part_a;                 // [units][teams of a CTA][vecs * 2 E]: sums of dR hn (token gates: of dN hn)
+  float *part_pre;               // [CTAs][vecs * 2 E]: sums of du rn; null where not asked for
+  float *part_a;                 // [units][vecs * 2 E]: sums of dR hn (token gates: of dN hn)
   int rows_per_b;                // tokens of one gate row (P * s, or all of them)
   int vecs, gate_mode, B, s;
   int bs, upb;                   // gate rows that units walk (B for sequence gates, else 1); units (runs of tokens) each
@@ -419,9 +421,12 @@ __global__ void __maxnreg__(sizeof(T) == 4 && NV == 2 && !WARP ? 96 : 128) resid
   for (int i = 0; i < NV; ++i)
 #pragma unroll
     for (int e = 0; e < E; ++e) a_pre[i][e] = a_a[i][e] = f2(0.f);
-  // Column sums of a warp's rows: lanes of the same columns, then the first row's lanes store.
+  // Column sums of a CTA's rows: lanes of the same columns, then its teams in order,
+  // through the memory of the stages, which all are done with.
   auto store_sums = [&](F2 (&v)[NV][E], float *part, long long index) {
-    F2 *o = reinterpret_cast<F2 *>(part) + (index * p.vecs + l) * E;
+    F2 *o = reinterpret_cast<F2 *>(part) + index * p.vecs * E;
+    F2 *buf = teams > 1 ? reinterpret_cast<F2 *>(ring.first_stage()) + team * p.vecs * E : o;
+    if (teams > 1) __syncthreads();
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
@@ -432,9 +437,20 @@ __global__ void __maxnreg__(sizeof(T) == 4 && NV == 2 && !WARP ? 96 : 128) resid
             w.v = __shfl_xor_sync(0xffffffffu, v[i][e].v, off);
             v[i][e] = add(v[i][e], w);
           }
-        if ((i < NV - 1 || tail) && ring.sub == 0) o[(long long)i * tpr * E + e] = v[i][e];
+        if ((i < NV - 1 || tail) && ring.sub == 0) buf[(l + (long long)i * tpr) * E + e] = v[i][e];
         v[i][e] = f2(0.f);
       }
+    if (teams > 1) {
+      __syncthreads();
+      const F2 *all = reinterpret_cast<const F2 *>(ring.first_stage());
+      for (int c = threadIdx.x; c < p.vecs * E; c += blockDim.x) {
+        F2 a = all[c];
+        for (int t = 1; t < teams; ++t) a = add(a, all[t * p.vecs * E + c]);
+        o[c] = a;
+      }
+      sm100::fence_proxy_async_smem();   // bulk copies may follow
+      __syncthreads();
+    }
   };
   const int units = p.bs * p.upb;
   for (int unit = blockIdx.x; unit < units; unit += gridDim.x) {
@@ -595,9 +611,9 @@ __global__ void __maxnreg__(sizeof(T) == 4 && NV == 2 && !WARP ? 96 : 128) resid
         }
       }
     }
-    if (p.part_a) store_sums(a_a, p.part_a, (long long)unit * teams + team);
+    if (p.part_a) store_sums(a_a, p.part_a, unit);
   }
-  if (p.part_pre) store_sums(a_pre, p.part_pre, (long long)blockIdx.x * teams + team);
+  if (p.part_pre) store_sums(a_pre, p.part_pre, blockIdx.x);
   ring.end(&abort_flag);
 }
 
@@ -712,7 +728,7 @@ BwdPlan bwd_plan(int B, long long n, int hidden, int e, int gate_mode) {
   q.upb = (int)upb;
   const long long units = (long long)q.bs * q.upb;
   q.grid = (int)(units < want ? units : want);
-  const size_t col = (size_t)hidden * sizeof(float) * q.rs.teams;
+  const size_t col = (size_t)hidden * sizeof(float);
   q.off_pre = 0;
   q.off_a = q.off_pre + col * q.grid;
   q.bytes = q.off_a + col * units;
@@ -921,11 +937,11 @@ uly_status residual_norm_bwd_launch(int32_t B, int32_t n, int32_t P, int32_t hid
                               q.rs.threads, q.rs.smem, p, stream);
     if (st != ULY_OK) return st;
   }
-  const int run = q.upb * q.rs.teams;   // partials of one gate row
+  const int run = q.upb;   // partials of one gate row
   FoldJobs jobs = {};
   jobs.cols = hidden;
   jobs.bf16 = bf;
-  if (dw_pre) jobs.job[jobs.n++] = {p.part_pre, dw_pre, (long long)q.grid * q.rs.teams, 1, nullptr, nullptr, 1};
+  if (dw_pre) jobs.job[jobs.n++] = {p.part_pre, dw_pre, (long long)q.grid, 1, nullptr, nullptr, 1};
   if (dw_post) {
     FoldJob &f = jobs.job[jobs.n++];
     f = {p.part_a, dw_post, (long long)q.bs * run, 1, nullptr, nullptr, run};
