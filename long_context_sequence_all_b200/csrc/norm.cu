@@ -756,11 +756,17 @@ __device__ __forceinline__ float vector_at(const void *p, long long i, int bf16)
   return bf16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[i]) : static_cast<const float *>(p)[i];
 }
 
-// Rows of all jobs along grid.y, 32 columns a CTA; strips of partials are added
+// Grid rows a job takes: one for each of its rows, or, where these have few
+// partials (a gate of every one of 2000 sequences, whose tokens one run takes), one
+// for as many as there are strips (2000 x 8 x 512: 162 -> 27 us).
+__host__ __device__ __forceinline__ int fold_units(const FoldJob &f, int ranks) {
+  return f.parts < kStrips ? (f.rows + kStrips * ranks - 1) / (kStrips * ranks) : f.rows;
+}
+
+// Units of all jobs along grid.y, 32 columns a CTA; strips of partials are added
 // in a fixed order and joined through shared memory.  The CTAs of a cluster (along
 // grid.z) share the partials of a column: short rows have few columns and many
-// partials (65536 x 160: 2368 of each column on five CTAs took 16.6 us,
-// in clusters of eight 10.8).
+// partials.
 constexpr int kFoldCluster = 8;
 template <bool CLUSTER>
 __global__ void __launch_bounds__(32 * kStrips) fold_columns_kernel(const __grid_constant__ FoldJobs jobs) {
@@ -769,13 +775,25 @@ __global__ void __launch_bounds__(32 * kStrips) fold_columns_kernel(const __grid
   const int lane = threadIdx.x & 31, strip = threadIdx.x >> 5, cols = jobs.cols;
   const int ranks = CLUSTER ? gridDim.z : 1, rank = CLUSTER ? blockIdx.z : 0, stride = kStrips * ranks;
   int total = 0;
-  for (int j = 0; j < jobs.n; ++j) total += jobs.job[j].rows;
-  for (int row = blockIdx.y; row < total; row += gridDim.y) {
-    int k = row, j = 0;
-    while (k >= jobs.job[j].rows) k -= jobs.job[j++].rows;
+  for (int j = 0; j < jobs.n; ++j) total += fold_units(jobs.job[j], ranks);
+  for (int unit = blockIdx.y; unit < total; unit += gridDim.y) {
+    int k = unit, j = 0;
+    while (k >= fold_units(jobs.job[j], ranks)) k -= fold_units(jobs.job[j++], ranks);
     const FoldJob &f = jobs.job[j];
     const long long parts = f.parts;
     const int c = blockIdx.x * 32 + lane;
+    if (parts < kStrips) {   // a row a strip
+      k = (k * ranks + rank) * kStrips + strip;
+      if (k < f.rows && c < cols) {
+        const float *s = f.src + (long long)k * parts * cols + c;
+        float v = 0.f;
+        for (int i = 0; i < (int)parts; ++i, s += cols)
+          v += f.weight ? *s * vector_at(f.weight, (long long)(i / f.per_weight) * cols + c, jobs.bf16) : *s;
+        if (f.mul) v *= vector_at(f.mul, c, jobs.bf16);
+        f.dst[(long long)k * cols + c] = v;
+      }
+      continue;
+    }
     const float *s = f.src + (long long)k * parts * cols;
     float a[8] = {};
     if (c < cols) {
@@ -827,21 +845,24 @@ __global__ void __launch_bounds__(32 * kStrips) fold_columns_kernel(const __grid
 }
 
 uly_status fold_launch(const FoldJobs &jobs, cudaStream_t stream) {
-  long long rows = 0, parts = 0;
+  const long long cols = (jobs.cols + 31) / 32;
+  long long rows = 0, many = 0, parts = 0;   // many: rows of many partials
   for (int j = 0; j < jobs.n; ++j) {
     rows += jobs.job[j].rows;
+    if (jobs.job[j].parts >= kStrips) many += jobs.job[j].rows;
     if (jobs.job[j].parts > parts) parts = jobs.job[j].parts;
   }
   if (rows == 0) return ULY_OK;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((jobs.cols + 31) / 32, (unsigned)(rows < 65535 ? rows : 65535));
-  const long long ctas = (long long)cfg.gridDim.x * cfg.gridDim.y;
-  // where the SMs have room and a thread would have more than 32 partials (444 of
-  // 1028 columns: 8.6 us alone, 9.8 in clusters; 1024 of 512: 10.8 and 8.7)
+  // where the SMs have room and a thread would have more than 32 partials (weighted
+  // ones, 2 x 3 x 9000 x 256 with sequence gates: 13.9 us alone, 10.7 in clusters;
+  // 444 of 1028 columns: 8.6 and 9.8)
   unsigned ranks = 1;
   if (parts > 32 * kStrips)
-    while (ranks < kFoldCluster && ctas * ranks <= device_sm_count()) ranks *= 2;
-  cfg.gridDim.z = ranks;
+    while (ranks < kFoldCluster && cols * many * ranks <= device_sm_count()) ranks *= 2;
+  long long units = 0;
+  for (int j = 0; j < jobs.n; ++j) units += fold_units(jobs.job[j], (int)ranks);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)cols, (unsigned)(units < 65535 ? units : 65535), ranks);
   cfg.blockDim = dim3(32 * kStrips);
   cfg.stream = stream;
   cudaLaunchAttribute attr = {};

@@ -839,3 +839,9 @@ def test_linear_loss_past_32_bit_offsets():
 def test_linear_of_few_tokens_over_long_sums(T, K, N, act, bias, residual):
     test_linear_forward(T, K, N, act, bias, residual)
     test_linear_backward(T, N, K, act, bias, residual, torch.float32)   # dx over K
+
+
+@pytest.mark.parametrize("P,B,s,D,dtype", [(1, 40, 30, 2560, torch.bfloat16), (1, 2000, 8, 512, torch.bfloat16), (2, 17, 1, 72, torch.bfloat16),
+                                           (1, 300, 3, 204, torch.float32), (1, 16, 400, 64, torch.bfloat16)])
+def test_residual_norm_of_many_sequences(P, B, s, D, dtype):
+    test_residual_norm_backward(P, B, s, D, dtype, "sequence", True)
