@@ -18,8 +18,9 @@
 // A gate shared by the tokens of a run is a factor of that run's sums, so with
 // A = sum_t dR hn over the run, dw_post = sum gate A and dgate = w_post A: two
 // column sums (A and dw_pre's) stay in fp32 registers over all rows of a group.
-// Each group writes one partial per column and run, and a second kernel folds
-// the partials in a fixed order, so every output is bitwise repeatable.
+// A CTA's groups add theirs in shared memory and write one partial per column and
+// run, and a second kernel folds the partials, all in a fixed order, so every
+// output is bitwise repeatable.
 //
 // How: persistent teams of a warp or of several.  A team's rows arrive by bulk
 // copies in a ring of shared-memory stages, so the loads run ahead of the two row
