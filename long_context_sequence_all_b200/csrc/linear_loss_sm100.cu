@@ -45,7 +45,7 @@ constexpr long long kPairBytes = 128ll << 20;   // pairs of one forward piece
 struct LossParams {
   CUtensorMap p_map;       // STORE_P: fp16 [rows][ldp]
   const int32_t *labels;   // of the piece's rows
-  float2 *pairs;           // [slots][rows_pad]: (maximum, sum of exp(z - maximum))
+  float2 *pairs;           // [slots][rows_pad]: (maximum, sum of exp(z - maximum)); (-inf, 0) where every z is -inf
   float *target;           // [rows]: z[label]
   long long rows_pad;
   int rows, vocab, ignore_index;
@@ -112,7 +112,7 @@ struct EpiLoss {
       if (STORE_P)
         out.end(&p.p_map, col0 + c, row0);
     }
-    if (ok) p.pairs[(long long)(w.nt * 2 + half) * p.rows_pad + row] = make_float2(ref, (s[0] + s[1]) + (s[2] + s[3]));
+    if (ok) p.pairs[(long long)(w.nt * 2 + half) * p.rows_pad + row] = make_float2(m, (s[0] + s[1]) + (s[2] + s[3]));
   }
 };
 
@@ -162,12 +162,12 @@ struct SkinnyLoss {
         const bool ok = t < p.rows;
         const int y = ok ? __ldg(p.labels + t) : p.ignore_index;
         const bool counted = y != p.ignore_index && y >= 0 && y < p.vocab;
-        if (m[k] == -INFINITY) m[k] = 0.f;   // every logit -inf: each term is 0
+        const float ref = m[k] == -INFINITY ? 0.f : m[k];   // every logit -inf: each term is 0
         s[k] = 0.f;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           if (counted && y == col + e) p.target[t] = z[k][e];
-          z[k][e] = 4 * lane + e < ncol ? ex2_approx((z[k][e] - m[k]) * kLog2e) : 0.f;
+          z[k][e] = 4 * lane + e < ncol ? ex2_approx((z[k][e] - ref) * kLog2e) : 0.f;
           s[k] += z[k][e];
         }
         if (q.p && ok && 4 * lane < ncol) {
@@ -251,7 +251,8 @@ __global__ void __launch_bounds__(1024) loss_close_kernel(const __grid_constant_
 
 // Four rows a CTA: their pairs (one 32-byte sector for a slot of all four) are
 // folded in a fixed order into lse and the rows' losses.  GRAD: and each slot's
-// factor exp(maximum - lse) of its stored exponentials, [row][slot].
+// factor exp(maximum - lse) of its stored exponentials, [row][slot]: at most about 1,
+// as a slot with nothing in it has -inf for its maximum and 0 for its factor.
 struct RowsParams {
   const float2 *pairs;
   const float *target;

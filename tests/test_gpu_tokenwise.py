@@ -845,3 +845,40 @@ def test_linear_of_few_tokens_over_long_sums(T, K, N, act, bias, residual):
                                            (1, 300, 3, 204, torch.float32), (1, 16, 400, 64, torch.bfloat16)])
 def test_residual_norm_of_many_sequences(P, B, s, D, dtype):
     test_residual_norm_backward(P, B, s, D, dtype, "sequence", True)
+
+
+# --------------------------------------- slots of the vocabulary with nothing in them
+
+@pytest.mark.parametrize("shift", [0.0, -250.0])
+@pytest.mark.parametrize("fill", [-1e30, torch.finfo(torch.bfloat16).min, float("-inf")])
+@pytest.mark.parametrize("T,piece", [(5, 0), (64, 0), (300, 0), (300, 130)])   # either product, whole and in pieces
+def test_linear_loss_of_dead_vocabulary_blocks(T, piece, fill, shift):
+    """Blocks of 128 columns whose logits are all -inf (the lowest value's sums
+    overflow) have no weight and no gradient, also where every other logit of a
+    row is far below zero: x's first column is one, w's is the shift.  The live
+    columns against 64 bits, with the bounds of test_linear_loss."""
+    g = _gen(43)
+    D, V, lo, hi = 64, 1400, 300, 850
+    x = _rnd(g, T, D).abs() + 0.125          # positive: the sign of w is the logit's
+    w = _rnd(g, V, D, scale=0.2)
+    x[:, 0], w[:, 0] = 1.0, shift
+    dead = torch.ones(V, dtype=torch.bool, device="cuda")
+    dead[lo:hi] = False                      # the first two blocks, parts of two, the last four
+    w[dead] = fill
+    y = torch.randint(lo, hi, (T,), generator=g, device="cuda", dtype=torch.int32)
+    y[1::4] = -100
+    S, C, L, dx, dw = U.ulysses_linear_loss_bwd(x, w, y, 1, piece_tokens=piece)
+    assert torch.equal(U.ulysses_linear_loss(x, w, y, 1)[2], L)
+    live, x64 = w[lo:hi], x.double()
+    _, Cr, Lr, dz = _loss64(x, live, torch.where(y == -100, y, y - lo), 1, -100)
+    ez = D * U32 * (x64 @ live.double().abs().t()).amax(1, keepdim=True)
+    assert torch.equal(C, Cr) and abs(L.double() - Lr) <= LOSS_REL * Lr + 2 * ez.max()
+    soft = dz.abs()
+    assert not dw[dead].any()
+    ref = dz.t() @ x64
+    _within(dw[lo:hi], ref, MORE * (((HALF + 2.0 ** -11 + 2 * ez + T * U32) * soft).t() @ x64) + 1e-12, "dw")
+    if fill != float("-inf"):                # the product's own 0 times infinity is NaN
+        ref = dz @ live.double()
+        terms = ((HALF + 2.0 ** -11 + 2 * ez + V * U32) * soft) @ live.double().abs()
+        _within(dx, ref, HALF * ref.abs() + MORE * terms + 1e-12, "dx")
+    assert U.ulysses_read_error() == 0
