@@ -394,8 +394,9 @@ __global__ void __launch_bounds__(kGradThreads) loss_grad_kernel(const __grid_co
         v[2 * e + 1] = t.y * f[k];
       }
       if (counted && i == y / 8) {
-        // z_y <= lse but for rounding: the label's softmax is at most 1
-        const float dy = expm1f(fminf(p.target[row] - p.row_lse[row], 0.f));
+        // z_y <= lse but for rounding: the label's softmax is at most 1 (or NaN, which stays)
+        const float d = p.target[row] - p.row_lse[row];
+        const float dy = expm1f(d > 0.f ? 0.f : d);
 #pragma unroll
         for (int e = 0; e < 8; ++e)
           if (e == y % 8) v[e] = dy;

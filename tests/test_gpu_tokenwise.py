@@ -882,3 +882,18 @@ def test_linear_loss_of_dead_vocabulary_blocks(T, piece, fill, shift):
         terms = ((HALF + 2.0 ** -11 + 2 * ez + V * U32) * soft) @ live.double().abs()
         _within(dx, ref, HALF * ref.abs() + MORE * terms + 1e-12, "dx")
     assert U.ulysses_read_error() == 0
+
+
+@pytest.mark.parametrize("T", [1, 70])
+def test_linear_loss_keeps_nan(T):
+    """A counted token without a softmax (a NaN logit, or every logit -inf) has a NaN loss and NaN
+    in the whole of its gradient, the label's element among it."""
+    for fill, V in ((float("nan"), 5), (float("nan"), 400), (float("-inf"), 400)):
+        x = torch.ones(T, 64, device="cuda", dtype=torch.bfloat16)
+        w = torch.full((V, 64), fill, device="cuda", dtype=torch.bfloat16)
+        if fill != fill:
+            w[1:] = 1.0
+        y = torch.full((T,), V - 2, device="cuda", dtype=torch.int32)
+        _, C, L, dx, dw = U.ulysses_linear_loss_bwd(x, w, y, 1)
+        assert C.item() == T and torch.isnan(L).all() and torch.isnan(dx).all() and torch.isnan(dw).all()
+        assert torch.isnan(U.ulysses_linear_loss(x, w, y, 1)[2]).all()
