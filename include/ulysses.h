@@ -577,7 +577,7 @@ uly_status ulysses_read_error_info(int32_t *info, int32_t n);
 /*
  * Failure detection (no counterpart on the pages: the tcgen05 kernels wait on
  * mbarriers, and every such wait is bounded).  Sets how many SM clock cycles a
- * pipeline wait of the attention, projection and linear kernels launched from now on
+ * pipeline wait of the attention, projection and token-wise kernels launched from now on
  * may last before the kernel records ULY_ERR_TIMEOUT (and where, see
  * ulysses_read_error_info), drains its copies and MMAs, frees its tensor
  * memory and returns.  cycles = 0 restores the built-in limit (2e9 cycles,

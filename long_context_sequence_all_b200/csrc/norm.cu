@@ -178,6 +178,7 @@ struct RingShape {
   int slots, stages;   // tensors of a stage, stages of a team
   int lanes;           // threads of a row: of a warp, or a whole team of warps
   int *err;
+  long long wait_limit;
 };
 
 // Vectors that all rows share.
@@ -190,11 +191,12 @@ struct Shared3 {
 // STAGED: the vectors all rows share are brought into shared memory first.
 template <bool WARP, bool STAGED>
 struct Ring {
+  static constexpr uint32_t kGaveUp = 2;
   uint8_t *base;
   uint64_t *bars;
   uint32_t row_bytes, slot_bytes, stage_bytes;
   int stages, at;        // at: the stage the next rows are taken from
-  uint32_t phase;
+  uint32_t phase;        // of `at`'s barrier; kGaveUp: this thread has given up a wait
   int l, lanes, sub, rows;
 
   int team;
@@ -240,7 +242,7 @@ struct Ring {
   }
   // The team: `n` rows of every tensor from token `t` on, into stage `st`.
   __device__ __forceinline__ void issue(const RingSrc &src, long long t, int n, int st) const {
-    if (l != 0 || sub != 0) return;
+    if (l != 0 || sub != 0 || phase >= kGaveUp) return;
     const uint32_t bar = sm100::smem_u32(&bars[st]);
     sm100::mbar_arrive_expect_tx(bar, src.n * n * row_bytes);
     for (int k = 0; k < src.n; ++k)
@@ -248,6 +250,7 @@ struct Ring {
   }
   // The same for rows that do not follow one another: `t` is this thread's row.
   __device__ __forceinline__ void issue_each(const RingSrc &src, long long t, int n, int st) const {
+    if (WARP ? __any_sync(0xffffffffu, phase >= kGaveUp) : phase >= kGaveUp) return;   // all lanes or none
     const uint32_t bar = sm100::smem_u32(&bars[st]);
     if (l == 0 && sub == 0) sm100::mbar_arrive_expect_tx(bar, src.n * n * row_bytes);
     if (WARP) __syncwarp();
@@ -256,9 +259,13 @@ struct Ring {
         sm100::bulk_load(slot(st, k) + sub * row_bytes, static_cast<const uint8_t *>(src.p[k]) + t * row_bytes, row_bytes,
                          bar);
   }
-  __device__ __forceinline__ void wait(volatile int *abort, int *err) const {
-    // giving up raises the error; the rows are then computed from what is there
-    sm100::mbar_wait(sm100::smem_u32(&bars[at]), phase, abort, err);
+  // Giving up raises the error.  The barriers of the team are met all the same, so
+  // its rows are then computed from what is there; but this thread waits no more,
+  // and it sends for no more rows: a stage is only filled again by a thread that
+  // saw it full.
+  __device__ __forceinline__ void wait(volatile int *abort, const RingShape &s) {
+    if (phase < kGaveUp && !sm100::mbar_wait(sm100::smem_u32(&bars[at]), phase, abort, s.err, s.wait_limit))
+      phase |= kGaveUp;
   }
   // this thread's first vector of its row of tensor `k`
   __device__ __forceinline__ const uint4 *row(int k) const {
@@ -291,7 +298,7 @@ struct NormParams {
 // Thread `l` of a row's `tpr` takes its vectors l, l + tpr, ...: NV of them, of
 // which only the last can lie behind the row's end.
 template <typename T, int NV, bool WARP, bool STAGED>
-__global__ void __launch_bounds__(!WARP ? 640 : NV <= 2 ? 1024 : 512) residual_norm_kernel(const __grid_constant__ NormParams p) {
+__global__ void __launch_bounds__(!WARP ? 640 : NV <= 2 ? 1024 : 512, 1) residual_norm_kernel(const __grid_constant__ NormParams p) {
   constexpr int E = Vec<T>::N;
   extern __shared__ __align__(128) uint8_t stage_mem[];
   __shared__ uint64_t bars[kMaxTeams * kMaxStages];
@@ -316,7 +323,7 @@ __global__ void __launch_bounds__(!WARP ? 640 : NV <= 2 ? 1024 : 512) residual_n
       ring.barrier();
       issue(t0, 0);
     }
-    ring.wait(&abort_flag, p.ring.err);
+    ring.wait(&abort_flag, p.ring);
     const long long t = t0 + ring.sub;
     const bool row_ok = !WARP || t < rows;
     const bool own_gate = p.sg >= 0, all_gate = p.gate_mode == ULY_GATE_CHANNEL;
@@ -485,7 +492,7 @@ __global__ void __maxnreg__(sizeof(T) == 4 && NV == 2 && !WARP ? 96 : 128) resid
         ring.barrier();
         issue(k, 0);
       }
-      ring.wait(&abort_flag, p.ring.err);
+      ring.wait(&abort_flag, p.ring);
       F2 rr = f2(0.f), ar = f2(0.f), hh = f2(0.f);   // sums of r^2, du w_pre r and h^2, taken together
       const uint4 *rv = ring.row(p.sr), *uv = ring.row(p.su), *hv = ring.row(p.sh), *dv = ring.row(p.sd);
       F2 hn[NV][E];
@@ -913,7 +920,7 @@ uly_status residual_norm_launch(int32_t B, int32_t n, int32_t P, int32_t hidden,
   p.gate_mode = gate_mode; p.B = B; p.s = n / P;
   p.res_scale = res_scale; p.eps = eps; p.inv_d = 1.0f / hidden;
   const RowShape rs = row_shape(p.vecs, p.src.n, kFwdVecs, false, !bf);
-  p.ring = {p.src.n, rs.stages, rs.lanes, error_word()};
+  p.ring = {p.src.n, rs.stages, rs.lanes, error_word(), wait_limit_cycles()};
   const long long want = (long long)device_sm_count() * rs.per_sm, turn = rs.teams * rs.rows, ctas = (p.rows + turn - 1) / turn;
   const int grid = (int)(ctas < want ? ctas : want);
   prof::Scope scope(prof::K_RESIDUAL_NORM, stream);
@@ -939,7 +946,7 @@ uly_status residual_norm_bwd_launch(int32_t B, int32_t n, int32_t P, int32_t hid
   p.src.add(h, p.sh);
   p.src.add(dr, p.sd);
   p.src.add(gate_mode == ULY_GATE_TOKEN ? gate : nullptr, p.sg);
-  p.ring = {q.slots, q.rs.stages, q.rs.lanes, error_word()};
+  p.ring = {q.slots, q.rs.stages, q.rs.lanes, error_word(), wait_limit_cycles()};
   p.gate = static_cast<const uint4 *>(gate);
   p.all = {{static_cast<const uint4 *>(w_post), static_cast<const uint4 *>(w_pre),
             gate_mode == ULY_GATE_CHANNEL ? p.gate : nullptr}};

@@ -897,3 +897,41 @@ def test_linear_loss_keeps_nan(T):
         _, C, L, dx, dw = U.ulysses_linear_loss_bwd(x, w, y, 1)
         assert C.item() == T and torch.isnan(L).all() and torch.isnan(dx).all() and torch.isnan(dw).all()
         assert torch.isnan(U.ulysses_linear_loss(x, w, y, 1)[2]).all()
+
+
+# ----------------------------------------------------- the norms' bounded waits
+
+@pytest.mark.parametrize("P,B,s,D,dtype,gate", [
+    (2, 1, 400, 64, torch.bfloat16, "channel"),      # rows that share a warp
+    (2, 3, 90, 160, torch.bfloat16, "sequence"),     # the same, brought row by row in the backward
+    (1, 1, 700, 2560, torch.bfloat16, "channel"),    # teams of several warps
+    (1, 2, 300, 1028, torch.float32, "token"),
+    (1, 1, 200, 16384, torch.bfloat16, "none"),      # a CTA a row
+    (1, 1, 155, 16384, torch.bfloat16, "token"),     # one stage only
+])
+def test_residual_norm_reports_a_wait_that_ran_out(P, B, s, D, dtype, gate):
+    """A wait for rows cut short is reported in the error word and the launch
+    ends, in both directions; the next call is right again.  (Rows that L2 holds
+    are there before a thread has sent for the whole ring and first looks.)"""
+    g = _gen(81)
+    t = _norm_inputs(g, P, B, s, D, dtype, gate, True)
+    dr, du = (_rnd(g, P, B, s, D, dtype=dtype) for _ in range(2))
+    kw = dict(w_pre=t["w_pre"], w_post=t["w_post"], gate=t["gate"], gate_mode=MODES[gate])
+    for call in (lambda: U.ulysses_residual_norm(t["x"], t["h"], **kw),
+                 lambda: U.ulysses_residual_norm_bwd(t["x"], t["h"], dr=dr, du=du, **kw)):
+        want = call()
+        torch.empty(1 << 28, device="cuda", dtype=torch.uint8).zero_()     # L2 holds something else
+        torch.cuda.synchronize()
+        assert U.ulysses_read_error() == 0
+        U.ulysses_set_wait_limit(200)                # cycles; rows from memory take thousands
+        try:
+            call()
+            torch.cuda.synchronize()
+        finally:
+            U.ulysses_set_wait_limit(0)
+        info = U.ulysses_read_error_info()
+        assert info[0] == 1 << 9 and info[1] == 1 and info[8] >= 1, info[:9]
+        again = call()
+        torch.cuda.synchronize()
+        assert all((p is None) == (q is None) and (p is None or torch.equal(p, q)) for p, q in zip(want, again))
+        assert U.ulysses_read_error() == 0
