@@ -520,8 +520,7 @@ uly_status launch(const CUtensorMap &ta, const CUtensorMap &tb, const Shape &s, 
 }
 
 // ---------------------------------------------------- vectors of 8 columns
-__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&x)[8]) {
-  const uint4 u = __ldg(reinterpret_cast<const uint4 *>(p));
+__device__ __forceinline__ void unpack8(const uint4 &u, float (&x)[8]) {
   const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&u);
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
@@ -529,6 +528,10 @@ __device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&x)[8]) {
     x[2 * e] = f.x;
     x[2 * e + 1] = f.y;
   }
+}
+// Of memory that the kernel does not write (the read-only path must not see it change).
+__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&x)[8]) {
+  unpack8(__ldg(reinterpret_cast<const uint4 *>(p)), x);
 }
 __device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&x)[8]) {
   *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),

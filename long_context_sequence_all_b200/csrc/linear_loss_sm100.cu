@@ -134,6 +134,7 @@ struct SkinnyLossParams {
 };
 struct SkinnyLoss {
   using Params = SkinnyLossParams;
+  static __device__ __forceinline__ void prefetch(const Params &, int, int, int) {}
   template <class T>
   static __device__ __forceinline__ void finish(const Params &q, const T &tile, int index, int rank, int ranks) {
     const LossParams &p = q.l;

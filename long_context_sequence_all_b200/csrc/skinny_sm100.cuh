@@ -81,27 +81,34 @@ struct Tile {
   }
 };
 
-__device__ __forceinline__ void load4(const __nv_bfloat16 *p, float (&x)[4]) {
-  const uint2 u = __ldg(reinterpret_cast<const uint2 *>(p));
+__device__ __forceinline__ void unpack4(const uint2 &u, float (&x)[4]) {
   x[0] = __uint_as_float(u.x << 16); x[1] = __uint_as_float(u.x & 0xffff0000u);
   x[2] = __uint_as_float(u.y << 16); x[3] = __uint_as_float(u.y & 0xffff0000u);
+}
+__device__ __forceinline__ void load4(const __nv_bfloat16 *p, float (&x)[4]) {   // not written by the kernel
+  unpack4(__ldg(reinterpret_cast<const uint2 *>(p)), x);
 }
 __device__ __forceinline__ void store4(__nv_bfloat16 *p, const float (&x)[4]) {
   *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
 }
 
 // This thread's share of a CTA's slice of `cols` output columns of a tile:
-// f(first column of four, in the tile; token).
+// f(first column of four, in the tile; token).  From thread `first` on.
 template <class F>
-__device__ __forceinline__ void for_slice(int cols, int rank, int ranks, int T, F f) {
+__device__ __forceinline__ void for_slice(int cols, int rank, int ranks, int T, F f, int first = 0) {
   const int quads = cols / 4 / ranks, shift = 31 - __clz(quads);   // powers of two
 #pragma unroll 2
-  for (int i = threadIdx.x; i < quads * T; i += kSkinnyThreads) f((rank * quads + (i & (quads - 1))) * 4, i >> shift);
+  for (int i = threadIdx.x - first; i < quads * T; i += kSkinnyThreads - first)
+    f((rank * quads + (i & (quads - 1))) * 4, i >> shift);
 }
+__device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 // The `ranks` CTAs of a tile are a cluster.
-// Epi::Params, and Epi::finish(params, tile, index, rank, ranks): all threads
-// of the CTA, its slice of tile `index`.
+// Epi::Params,
+//   Epi::prefetch(params, index, rank, ranks): warps 2 and 3, while the product
+//   runs: what finish() reads of memory may be sent for to L2, and
+//   Epi::finish(params, tile, index, rank, ranks): all threads of the CTA, its
+//   slice of tile `index`.
 template <class Epi, int NT, bool W_MN, int MAX>
 __global__ void __launch_bounds__(kSkinnyThreads)
     skinny_sm100_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
@@ -166,6 +173,8 @@ __global__ void __launch_bounds__(kSkinnyThreads)
       if (++stage == S::kStages) { stage = 0; phase ^= 1; }
     }
     tc_commit(bar(B_DONE));
+  } else if (warp >= 2) {
+    Epi::prefetch(ep, index, rank, ranks);
   }
   __syncwarp();
   // Every MMA has completed (so every copy was consumed): the ring's memory is
@@ -308,6 +317,7 @@ struct SkinnyPlain {
     const long long *over;
     int T, N;
   };
+  static __device__ __forceinline__ void prefetch(const Params &, int, int, int) {}
   template <class T>
   static __device__ __forceinline__ void finish(const Params &p, const T &tile, int index, int rank, int ranks) {
     const float f = gemm::one_over(p.over);

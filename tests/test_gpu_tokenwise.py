@@ -935,3 +935,24 @@ def test_residual_norm_reports_a_wait_that_ran_out(P, B, s, D, dtype, gate):
         torch.cuda.synchronize()
         assert all((p is None) == (q is None) and (p is None or torch.equal(p, q)) for p, q in zip(want, again))
         assert U.ulysses_read_error() == 0
+
+
+@pytest.mark.parametrize("T,K,N,act,bias", [
+    (1, 64, 8, "none", True),              # few tokens
+    (24, 8200, 264, "silu", False),        # the same, sixteen CTAs a tile
+    (128, 520, 136, "swiglu", True),
+    (222, 64, 72, "swiglu", True),         # narrow gated tiles
+    (4100, 128, 2600, "gelu", False),      # several tiles an SM pair, the residual a tile ahead
+    (600, 4096, 3320, "swiglu", True),     # the last tiles cut along K: joined by a second kernel
+    (2300, 8192, 2304, "none", False),
+])
+def test_linear_residual_in_place(T, K, N, act, bias):
+    """The residual may be y itself, in every kernel that adds it."""
+    g = _gen(T + N)
+    nz = 2 * N if act == "swiglu" else N
+    x, w, r = _rnd(g, T, K), _rnd(g, nz, K, scale=K ** -0.5), _rnd(g, T, N)
+    b = _rnd(g, nz, scale=0.5) if bias else None
+    want = U.ulysses_linear(x, w, bias=b, residual=r, activation=ACTS[act])
+    y = r.clone()
+    got = U.ulysses_linear(x, w, bias=b, residual=y, activation=ACTS[act], y=y)
+    assert got.data_ptr() == y.data_ptr() and torch.equal(got, want)
