@@ -638,8 +638,8 @@ struct RowShape {
   bool staged;                  // the weights in shared memory
   uint32_t smem;
 };
-RowShape row_shape(int vecs, int slots, int nv, bool backward, bool f32) {
-  RowShape r;
+constexpr RowShape row_shape(int vecs, int slots, int nv, bool backward, bool f32) {
+  RowShape r = {};
   auto need = [&](int lanes) { return (vecs + lanes - 1) / lanes; };
   const bool warp = vecs <= 32 * nv;
   if (warp) {
@@ -691,6 +691,34 @@ uly_status run(Entry<Params> &e, int grid, int threads, uint32_t smem, const Par
   note_launches(1);
   return last_launch_status();
 }
+// The kernels there are, and that row_shape() chooses each of them and no other.
+constexpr bool fwd_kernel(const RowShape &r) {
+  return r.lanes <= 32 ? r.staged && r.nv <= 5 : r.staged ? r.nv >= 3 && r.nv <= 5 : r.nv == 5;
+}
+constexpr bool bwd_kernel(const RowShape &r, bool f32) {
+  return r.lanes <= 32 ? r.staged && r.nv <= 2 : r.staged ? f32 && r.nv >= 2 && r.nv <= 3 : r.nv >= 2 && r.nv <= 4;
+}
+constexpr bool kernels_fit_shapes(bool backward, bool f32) {
+  unsigned chosen = 0, there = 0;
+  auto bit = [](const RowShape &r) { return 1u << ((r.lanes <= 32 ? 0 : r.staged ? 8 : 16) + r.nv); };
+  for (int vecs = 1; vecs <= kMaxVecs; ++vecs)
+    for (int slots = backward ? 4 : 1; slots <= (backward ? 5 : 3); ++slots) {
+      const RowShape r = row_shape(vecs, slots, backward ? kBwdVecs : kFwdVecs, backward, f32);
+      if (!(backward ? bwd_kernel(r, f32) : fwd_kernel(r))) return false;
+      chosen |= bit(r);
+    }
+  for (int lanes = 32; lanes <= 64; lanes += 32)
+    for (int staged = 0; staged <= 1; ++staged)
+      for (int nv = 1; nv <= 5; ++nv) {
+        RowShape r = {};
+        r.lanes = lanes, r.staged = staged, r.nv = nv;
+        if (backward ? bwd_kernel(r, f32) : fwd_kernel(r)) there |= bit(r);
+      }
+  return chosen == there;
+}
+static_assert(kernels_fit_shapes(false, false) && kernels_fit_shapes(false, true), "forward kernels");
+static_assert(kernels_fit_shapes(true, false) && kernels_fit_shapes(true, true), "backward kernels");
+
 template <typename T>
 Entry<NormParams> &fwd_entry(const RowShape &r) {
   static Entry<NormParams> warp[5] = {{residual_norm_kernel<T, 1, true, true>}, {residual_norm_kernel<T, 2, true, true>},
@@ -698,22 +726,23 @@ Entry<NormParams> &fwd_entry(const RowShape &r) {
                                       {residual_norm_kernel<T, 5, true, true>}};
   static Entry<NormParams> cta[3] = {{residual_norm_kernel<T, 3, false, true>}, {residual_norm_kernel<T, 4, false, true>},
                                      {residual_norm_kernel<T, 5, false, true>}};
-  static Entry<NormParams> wide[2] = {{residual_norm_kernel<T, 4, false, false>}, {residual_norm_kernel<T, 5, false, false>}};
-  if (r.lanes <= 32) return warp[r.nv - 1];
-  return r.staged ? cta[r.nv - 3] : wide[r.nv - 4];
+  static Entry<NormParams> wide = {residual_norm_kernel<T, 5, false, false>};
+  return r.lanes <= 32 ? warp[r.nv - 1] : r.staged ? cta[r.nv - 3] : wide;
 }
 template <typename T>
 Entry<NormBwdParams> &bwd_entry(const RowShape &r) {
   static Entry<NormBwdParams> warp[2] = {{residual_norm_bwd_kernel<T, 1, true, true>},
                                          {residual_norm_bwd_kernel<T, 2, true, true>}};
-  static Entry<NormBwdParams> cta[3] = {{residual_norm_bwd_kernel<T, 2, false, true>},
-                                        {residual_norm_bwd_kernel<T, 3, false, true>},
-                                        {residual_norm_bwd_kernel<T, 4, false, true>}};
   static Entry<NormBwdParams> wide[3] = {{residual_norm_bwd_kernel<T, 2, false, false>},
                                          {residual_norm_bwd_kernel<T, 3, false, false>},
                                          {residual_norm_bwd_kernel<T, 4, false, false>}};
   if (r.lanes <= 32) return warp[r.nv - 1];
-  return (r.staged ? cta : wide)[r.nv - 2];
+  if constexpr (sizeof(T) == 4) {
+    static Entry<NormBwdParams> cta[2] = {{residual_norm_bwd_kernel<T, 2, false, true>},
+                                          {residual_norm_bwd_kernel<T, 3, false, true>}};
+    if (r.staged) return cta[r.nv - 2];
+  }
+  return wide[r.nv - 2];
 }
 
 // How the backward walks the tokens: `bs` gate rows, each cut into `upb` runs
