@@ -10,11 +10,13 @@ travels with the source tree.  nvcc cross-compiles for sm_100a without a GPU.
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.metadata
 import os
 import re
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -88,13 +90,22 @@ def _compile(src: str, verbose: bool) -> str:
     return obj
 
 
+def native_tag() -> str:
+    """What a binding is built for, as it stands in ``_native.so``."""
+    return f"ulysses binding: torch {importlib.metadata.version('torch')}, {sysconfig.get_config_var('SOABI')}"
+
+
+def native_fits(path: str = None) -> bool:
+    """Whether the built binding is for the torch and Python at hand."""
+    with open(path or NATIVE, "rb") as f:
+        return native_tag().encode() + b"\0" in f.read()
+
+
 def build_native(force: bool = False) -> str:
     """The binding (g++ against the installed torch and Python)."""
     newest = max(os.path.getmtime(f) for f in (NATIVE_SRC, os.path.join(INCLUDE, "ulysses.h")))
-    if not force and os.path.exists(NATIVE) and os.path.getmtime(NATIVE) >= newest:
+    if not force and os.path.exists(NATIVE) and os.path.getmtime(NATIVE) >= newest and native_fits(NATIVE):
         return NATIVE
-    import sysconfig
-
     import torch
     from torch.utils import cpp_extension
     inc = [INCLUDE, sysconfig.get_paths()["include"], os.path.join(os.path.dirname(nvcc()), "..", "include"),
@@ -103,6 +114,7 @@ def build_native(force: bool = False) -> str:
     tmp = NATIVE + f".tmp{os.getpid()}"
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f'-DULY_BINDING_TAG="{native_tag()}"',
            *[x for d in inc for x in ("-isystem", d)], NATIVE_SRC, "-o", tmp,
            *[x for d in lib for x in (f"-L{d}", f"-Wl,-rpath,{d}")],
            "-lc10", "-lc10_cuda", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python", "-ldl"]
@@ -113,8 +125,7 @@ def build_native(force: bool = False) -> str:
     return NATIVE
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
-    build_native(force)
+def build_library(force: bool = False, verbose: bool = False) -> str:
     if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= _deps_mtime():
         return LIB
     os.makedirs(BUILD, exist_ok=True)
@@ -127,6 +138,13 @@ def build(force: bool = False, verbose: bool = False) -> str:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
     return LIB
+
+
+def build(force: bool = False, verbose: bool = False) -> str:
+    """Both; the library, which needs nvcc alone, is there also where the binding fails."""
+    path = build_library(force, verbose)
+    build_native(force)
+    return path
 
 
 if __name__ == "__main__":

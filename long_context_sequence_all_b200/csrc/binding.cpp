@@ -516,4 +516,11 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_native", "Binding of the token-wi
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__native(void) { return PyModule_Create(&module); }
+#ifndef ULY_BINDING_TAG
+#error "the build says what the binding is for (build.py)"
+#endif
+PyMODINIT_FUNC PyInit__native(void) {
+  PyObject *m = PyModule_Create(&module);
+  if (m && PyModule_AddStringConstant(m, "tag", ULY_BINDING_TAG) < 0) Py_CLEAR(m);
+  return m;
+}

@@ -540,6 +540,10 @@ def _native():
             path = os.path.join(_HERE, "_native.so")
             if not os.path.exists(path):
                 raise RuntimeError(f"{path} is missing; build it with `python -m long_context_sequence_all_b200.build`")
+            from . import build
+            if not build.native_fits(path):
+                raise RuntimeError(f"{path} is built for another torch or Python; build it again with "
+                                   "`python -m long_context_sequence_all_b200.build`")
             from . import _native as m
             m.init(LIB_PATH, UlyssesError)
             _native_module = m
