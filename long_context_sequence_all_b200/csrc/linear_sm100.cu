@@ -242,8 +242,6 @@ struct SkinnyLinear {
       const int col = index * kCols + row;   // N is a multiple of 8
       if (col >= p.N) return;
       float z[4], up[4] = {}, b[4];
-      uint2 r = make_uint2(0, 0);   // asked for before the sums over the cluster
-      if (p.residual) r = *reinterpret_cast<const uint2 *>(p.residual + (long long)t * p.N + col);
       tile.sum4(row, t, z);
       if (kGated) tile.sum4(64 + row, t, up);
       if (p.bias) {
@@ -263,7 +261,7 @@ struct SkinnyLinear {
 #pragma unroll
       for (int e = 0; e < 4; ++e) z[e] = act_of<ACT>(z[e], up[e]);
       if (p.residual) {
-        skinny::unpack4(r, b);
+        skinny::unpack4(*reinterpret_cast<const uint2 *>(p.residual + (long long)t * p.N + col), b);
 #pragma unroll
         for (int e = 0; e < 4; ++e) z[e] += b[e];
       }
