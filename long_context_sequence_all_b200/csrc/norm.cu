@@ -191,18 +191,18 @@ struct Shared3 {
 // STAGED: the vectors all rows share are brought into shared memory first.
 template <bool WARP, bool STAGED>
 struct Ring {
-  static constexpr uint32_t kGaveUp = 2;
   uint8_t *base;
   uint64_t *bars;
   uint32_t row_bytes, slot_bytes, stage_bytes;
   int stages, at;        // at: the stage the next rows are taken from
-  uint32_t phase;        // of `at`'s barrier; kGaveUp: this thread has given up a wait
+  uint32_t phase;        // of `at`'s barrier
+  volatile int *abort;   // a thread of the CTA has given up a wait
   int l, lanes, sub, rows;
 
   int team;
   uint8_t *mem;
 
-  __device__ __forceinline__ Ring(uint8_t *smem, uint64_t *barriers, volatile int *abort, int vecs, const RingShape &s,
+  __device__ __forceinline__ Ring(uint8_t *smem, uint64_t *barriers, volatile int *abort_flag, int vecs, const RingShape &s,
                                   const Shared3 &all) {
     const int lane = threadIdx.x & 31;
     lanes = WARP || STAGED ? s.lanes : blockDim.x;
@@ -224,6 +224,7 @@ struct Ring {
     bars = barriers + team * kMaxStages;
     at = 0;
     phase = 0;
+    abort = abort_flag;
     if (l == 0 && sub == 0)
       for (int i = 0; i < stages; ++i) sm100::mbar_init(sm100::smem_u32(&bars[i]), 1);
     if (threadIdx.x == 0) *abort = 0;
@@ -242,7 +243,7 @@ struct Ring {
   }
   // The team: `n` rows of every tensor from token `t` on, into stage `st`.
   __device__ __forceinline__ void issue(const RingSrc &src, long long t, int n, int st) const {
-    if (l != 0 || sub != 0 || phase >= kGaveUp) return;
+    if (l != 0 || sub != 0 || *abort) return;
     const uint32_t bar = sm100::smem_u32(&bars[st]);
     sm100::mbar_arrive_expect_tx(bar, src.n * n * row_bytes);
     for (int k = 0; k < src.n; ++k)
@@ -250,7 +251,7 @@ struct Ring {
   }
   // The same for rows that do not follow one another: `t` is this thread's row.
   __device__ __forceinline__ void issue_each(const RingSrc &src, long long t, int n, int st) const {
-    if (WARP ? __any_sync(0xffffffffu, phase >= kGaveUp) : phase >= kGaveUp) return;   // all lanes or none
+    if (WARP ? __any_sync(0xffffffffu, *abort) : *abort) return;   // all lanes or none
     const uint32_t bar = sm100::smem_u32(&bars[st]);
     if (l == 0 && sub == 0) sm100::mbar_arrive_expect_tx(bar, src.n * n * row_bytes);
     if (WARP) __syncwarp();
@@ -260,12 +261,10 @@ struct Ring {
                          bar);
   }
   // Giving up raises the error.  The barriers of the team are met all the same, so
-  // its rows are then computed from what is there; but this thread waits no more,
-  // and it sends for no more rows: a stage is only filled again by a thread that
-  // saw it full.
-  __device__ __forceinline__ void wait(volatile int *abort, const RingShape &s) {
-    if (phase < kGaveUp && !sm100::mbar_wait(sm100::smem_u32(&bars[at]), phase, abort, s.err, s.wait_limit))
-      phase |= kGaveUp;
+  // its rows are then computed from what is there, but nothing more is sent for: a
+  // stage is only filled again by a thread that saw it full.
+  __device__ __forceinline__ void wait(const RingShape &s) const {
+    sm100::mbar_wait(sm100::smem_u32(&bars[at]), phase, abort, s.err, s.wait_limit);
   }
   // this thread's first vector of its row of tensor `k`
   __device__ __forceinline__ const uint4 *row(int k) const {
@@ -276,7 +275,7 @@ struct Ring {
   }
   // After a wait that gave up the copies may still be in flight: let them land
   // before the CTA's shared memory is given away.
-  __device__ __forceinline__ void end(volatile int *abort) const {
+  __device__ __forceinline__ void end() const {
     __syncthreads();
     if (!*abort) return;
     const long long t0 = clock64();
@@ -323,7 +322,7 @@ __global__ void __launch_bounds__(!WARP ? 640 : NV <= 2 ? 1024 : 512, 1) residua
       ring.barrier();
       issue(t0, 0);
     }
-    ring.wait(&abort_flag, p.ring);
+    ring.wait(p.ring);
     const long long t = t0 + ring.sub;
     const bool row_ok = !WARP || t < rows;
     const bool own_gate = p.sg >= 0, all_gate = p.gate_mode == ULY_GATE_CHANNEL;
@@ -392,7 +391,7 @@ __global__ void __launch_bounds__(!WARP ? 640 : NV <= 2 ? 1024 : 512, 1) residua
       }
     }
   }
-  ring.end(&abort_flag);
+  ring.end();
 }
 
 struct NormBwdParams {
@@ -492,7 +491,7 @@ __global__ void __maxnreg__(sizeof(T) == 4 && NV == 2 && !WARP ? 96 : 128) resid
         ring.barrier();
         issue(k, 0);
       }
-      ring.wait(&abort_flag, p.ring);
+      ring.wait(p.ring);
       F2 rr = f2(0.f), ar = f2(0.f), hh = f2(0.f);   // sums of r^2, du w_pre r and h^2, taken together
       const uint4 *rv = ring.row(p.sr), *uv = ring.row(p.su), *hv = ring.row(p.sh), *dv = ring.row(p.sd);
       F2 hn[NV][E];
@@ -622,7 +621,7 @@ __global__ void __maxnreg__(sizeof(T) == 4 && NV == 2 && !WARP ? 96 : 128) resid
     if (p.part_a) store_sums(a_a, p.part_a, unit);
   }
   if (p.part_pre) store_sums(a_pre, p.part_pre, blockIdx.x);
-  ring.end(&abort_flag);
+  ring.end();
 }
 
 // ------------------------------------------------------------------- host
