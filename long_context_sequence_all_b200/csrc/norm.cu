@@ -28,17 +28,18 @@
 // gate that all tokens share, in shared memory (where two stages fit beside them):
 // from L1, which the streams keep emptying, their latency was the forward's
 // largest stall.  A thread takes up to five 16-byte vectors of a
-// row (backward: two, its column sums take the registers).  Short rows share a
+// row (backward: two, its column sums take the registers; up to four of the rows of
+// more than 1024 vectors, which 512 threads share).  Short rows share a
 // warp, a power of two of lanes each, and arrive several at a time (253074 x 160:
 // 142 us with one row a warp, 65 us so); of long ones few warps share a row: at
 // 2560 bf16 columns two warps (backward: five) instead of ten, which had left both
 // directions waiting for barriers and shuffles at 3.2 and 2.6 TB/s.  Arithmetic
 // runs on pairs of fp32 values.
-// 65536 x 2560 bf16 with a channel gate: forward 249 us (5.4 TB/s of its 1.34
-// GB), backward 416 us (4.8 TB/s of 2.01 GB) + 10 us of folding.  The forward is
+// 65536 x 2560 bf16 with a channel gate: forward 251 us (5.4 TB/s of its 1.34
+// GB), backward 416 us (4.8 TB/s of 2.01 GB) + 9 us of folding.  The forward is
 // near the memory's rate (a copy: 6.5 TB/s); the backward issues about 3800
-// instructions a row and is bound by their latency (with a gate of every token it
-// moves a third more in 452 us).
+// instructions a row and its two row sums, one after the other, leave their latency
+// in the open (with a gate of every token it moves a third more in 460 us).
 #include <cooperative_groups.h>
 
 #include <atomic>
@@ -217,9 +218,7 @@ struct Ring {
     mem = smem;
 #pragma unroll
     for (int k = 0; k < 3; ++k)
-      if (STAGED && all.p[k])
-        for (int i = threadIdx.x; i < vecs; i += blockDim.x)
-          reinterpret_cast<uint4 *>(mem + k * row_bytes)[i] = __ldg(all.p[k] + i);
+      if (STAGED && all.p[k]) share(k, all.p[k], vecs);
     base = first_stage() + (size_t)team * stages * stage_bytes;
     bars = barriers + team * kMaxStages;
     at = 0;
@@ -230,6 +229,10 @@ struct Ring {
     if (threadIdx.x == 0) *abort = 0;
     sm100::fence_mbar_init();
     __syncthreads();
+  }
+  // The CTA: vector `k` of those that all rows share.
+  __device__ __forceinline__ void share(int k, const uint4 *v, int vecs) const {
+    for (int i = threadIdx.x; i < vecs; i += blockDim.x) reinterpret_cast<uint4 *>(mem + k * row_bytes)[i] = __ldg(v + i);
   }
   // the first team's stages, the others' behind them
   __device__ __forceinline__ uint8_t *first_stage() const { return mem + (STAGED ? 3 * row_bytes : 0); }
@@ -412,6 +415,7 @@ struct NormBwdParams {
 template <typename T, int NV, bool WARP, bool STAGED>
 __global__ void __maxnreg__(sizeof(T) == 4 && NV == 2 && !WARP ? 96 : 128) residual_norm_bwd_kernel(const __grid_constant__ NormBwdParams p) {
   constexpr int E = Vec<T>::N;
+  constexpr bool kUnitGate = STAGED && !WARP;   // a unit's gate is staged beside the weights
   extern __shared__ __align__(128) uint8_t stage_mem[];
   __shared__ uint64_t bars[kMaxTeams * kMaxStages];
   __shared__ int abort_flag;
@@ -480,6 +484,11 @@ __global__ void __maxnreg__(sizeof(T) == 4 && NV == 2 && !WARP ? 96 : 128) resid
         issue(q0 + k * G, st);
         if (++st == ring.stages) st = 0;
       }
+    }
+    if (kUnitGate && p.gate_mode == ULY_GATE_SEQUENCE) {   // the gate of the unit's tokens
+      __syncthreads();
+      ring.share(2, p.gate + (long long)b * p.vecs, p.vecs);
+      __syncthreads();
     }
     int done = -1;
     int pos = p.bs == 1 ? 0 : (q0 + ring.sub) % p.s, t = token(q0 + ring.sub);
@@ -570,7 +579,7 @@ __global__ void __maxnreg__(sizeof(T) == 4 && NV == 2 && !WARP ? 96 : 128) resid
             if (gated) {
               F2 g[E];
               Vec<T>::unpack(p.sg >= 0 ? ring.row(p.sg)[v]
-                             : STAGED && all_gate ? ring.common(p.all, 2, v) : __ldg(seq_gate + v), g);
+                             : STAGED && all_gate || kUnitGate ? ring.common(p.all, 2, v) : __ldg(seq_gate + v), g);
               if (p.sg >= 0) {
                 if (p.dgate_tok) {
                   F2 o[E];
@@ -629,15 +638,16 @@ __global__ void __maxnreg__(sizeof(T) == 4 && NV == 2 && !WARP ? 96 : 128) resid
 // Teams and stages for rows of `vecs` vectors: lanes of a warp (a power of two)
 // while `nv` vectors a lane cover a row, several teams of one warp a CTA and
 // several CTAs an SM; else teams of the fewest warps that do, one CTA an SM with
-// the weights staged or CTAs of one team.  As many as the registers allow and two
-// stages each (one only where a single team's do not fit); `slots` tensors a stage.
+// the weights staged or (`apart`, and where two stages do not fit beside them) CTAs
+// of one team.  As many as the registers allow and two stages each (one only where
+// a single team's do not fit); `slots` tensors a stage.
 struct RowShape {
   int lanes, nv, teams, rows;   // threads of a row, vectors of each; teams of a CTA, rows of a team
   int threads, per_sm, stages;
   bool staged;                  // the weights in shared memory
   uint32_t smem;
 };
-constexpr RowShape row_shape(int vecs, int slots, int nv, bool backward, bool f32) {
+constexpr RowShape row_shape(int vecs, int slots, int nv, bool backward, bool f32, bool apart = false) {
   RowShape r = {};
   auto need = [&](int lanes) { return (vecs + lanes - 1) / lanes; };
   const bool warp = vecs <= 32 * nv;
@@ -662,10 +672,9 @@ constexpr RowShape row_shape(int vecs, int slots, int nv, bool backward, bool f3
   auto bytes = [&](int t, int stages) { return t * stages * stage + 3 * row * (warp ? (t + kWarpTeams - 1) / kWarpTeams : 1); };
   while (teams > 1 && bytes(teams, 2) > kRingBytes) --teams;
   if (warp && teams > kWarpTeams) teams = teams / kWarpTeams * kWarpTeams;
-  // the backward's two bf16 vectors need its 128 registers for themselves: CTAs of
-  // one team, the weights from L1 (65536 x 2560: 485 us so, 495 in one CTA)
-  const bool apart = backward && !warp && !f32;
-  r.staged = !apart && bytes(teams, 2) <= kRingBytes;
+  // the backward's three and four bf16 vectors need its 128 registers for themselves:
+  // their weights come from L1
+  r.staged = (warp || !apart) && !(backward && !f32 && r.nv > 2) && bytes(teams, 2) <= kRingBytes;
   const uint32_t beside = r.staged ? 0 : 3 * row;   // what bytes() counts too much
   r.stages = 1;
   while (r.stages < kMaxStages && bytes(teams, r.stages + 1) - beside <= kRingBytes) ++r.stages;
@@ -695,17 +704,18 @@ constexpr bool fwd_kernel(const RowShape &r) {
   return r.lanes <= 32 ? r.staged && r.nv <= 5 : r.staged ? r.nv >= 3 && r.nv <= 5 : r.nv == 5;
 }
 constexpr bool bwd_kernel(const RowShape &r, bool f32) {
-  return r.lanes <= 32 ? r.staged && r.nv <= 2 : r.staged ? f32 && r.nv >= 2 && r.nv <= 3 : r.nv >= 2 && r.nv <= 4;
+  return r.lanes <= 32 ? r.staged && r.nv <= 2 : r.staged ? r.nv >= 2 && r.nv <= (f32 ? 3 : 2) : r.nv >= 2 && r.nv <= 4;
 }
 constexpr bool kernels_fit_shapes(bool backward, bool f32) {
   unsigned chosen = 0, there = 0;
   auto bit = [](const RowShape &r) { return 1u << ((r.lanes <= 32 ? 0 : r.staged ? 8 : 16) + r.nv); };
   for (int vecs = 1; vecs <= kMaxVecs; ++vecs)
-    for (int slots = backward ? 4 : 1; slots <= (backward ? 5 : 3); ++slots) {
-      const RowShape r = row_shape(vecs, slots, backward ? kBwdVecs : kFwdVecs, backward, f32);
-      if (!(backward ? bwd_kernel(r, f32) : fwd_kernel(r))) return false;
-      chosen |= bit(r);
-    }
+    for (int slots = backward ? 4 : 1; slots <= (backward ? 5 : 3); ++slots)
+      for (int apart = 0; apart <= (backward && !f32); ++apart) {
+        const RowShape r = row_shape(vecs, slots, backward ? kBwdVecs : kFwdVecs, backward, f32, apart);
+        if (!(backward ? bwd_kernel(r, f32) : fwd_kernel(r))) return false;
+        chosen |= bit(r);
+      }
   for (int lanes = 32; lanes <= 64; lanes += 32)
     for (int staged = 0; staged <= 1; ++staged)
       for (int nv = 1; nv <= 5; ++nv) {
@@ -736,10 +746,13 @@ Entry<NormBwdParams> &bwd_entry(const RowShape &r) {
                                          {residual_norm_bwd_kernel<T, 3, false, false>},
                                          {residual_norm_bwd_kernel<T, 4, false, false>}};
   if (r.lanes <= 32) return warp[r.nv - 1];
-  if constexpr (sizeof(T) == 4) {
-    static Entry<NormBwdParams> cta[2] = {{residual_norm_bwd_kernel<T, 2, false, true>},
-                                          {residual_norm_bwd_kernel<T, 3, false, true>}};
-    if (r.staged) return cta[r.nv - 2];
+  if (r.staged) {
+    static Entry<NormBwdParams> cta = {residual_norm_bwd_kernel<T, 2, false, true>};
+    if constexpr (sizeof(T) == 4) {
+      static Entry<NormBwdParams> cta3 = {residual_norm_bwd_kernel<T, 3, false, true>};
+      if (r.nv == 3) return cta3;
+    }
+    return cta;
   }
   return wide[r.nv - 2];
 }
@@ -754,20 +767,35 @@ struct BwdPlan {
 BwdPlan bwd_plan(int B, long long n, int hidden, int e, int gate_mode) {
   BwdPlan q;
   q.slots = gate_mode == ULY_GATE_TOKEN ? 5 : 4;
-  q.rs = row_shape(hidden / e, q.slots, kBwdVecs, true, e == 4);
   q.bs = gate_mode == ULY_GATE_SEQUENCE ? B : 1;
   const long long rows = gate_mode == ULY_GATE_SEQUENCE ? n : (long long)B * n;
-  const long long want = (long long)device_sm_count() * q.rs.per_sm;
-  long long upb = want / q.bs, turn = q.rs.teams * q.rs.rows, most = (rows + turn - 1) / turn;
-  if (upb < 1) upb = 1;
-  if (upb > most) upb = most;
-  q.upb = (int)upb;
-  const long long units = (long long)q.bs * q.upb;
-  q.grid = (int)(units < want ? units : want);
+  // Turns of the CTAs that take most: a unit costs its rows and about two more.
+  auto plan = [&](bool apart) {
+    q.rs = row_shape(hidden / e, q.slots, kBwdVecs, true, e == 4, apart);
+    const long long want = (long long)device_sm_count() * q.rs.per_sm, turn = q.rs.teams * q.rs.rows;
+    long long upb = want / q.bs, most = (rows + turn - 1) / turn;
+    if (upb < 1) upb = 1;
+    if (upb > most) upb = most;
+    q.upb = (int)upb;
+    const long long units = (long long)q.bs * q.upb, each = (rows + upb - 1) / upb;
+    q.grid = (int)(units < want ? units : want);
+    return (double)((units + q.grid - 1) / q.grid) * (double)((each + turn - 1) / turn + 2);
+  };
+  // bf16 teams of several warps: in one CTA an SM they share the weights and a unit's
+  // gate in shared memory; CTAs of their own balance short units better and start
+  // sooner, which counts up to some three rows an SM.  (In one CTA and apart, us:
+  // 65536 x 2560 with a channel gate 419 and 452, 19531 x 4096 205 and 273; 2000
+  // sequences of 8 x 2560 with their gates 270 and 227, 1000 of 50 419 and 500; 20
+  // rows of 2560 16.7 and 13.6, 700 20.8 and 23.3.)
+  const double together = plan(false);
+  if (e == 8 && q.rs.lanes > 32 && q.rs.staged) {
+    const bool few = q.bs * rows <= 3ll * device_sm_count();
+    if (plan(true) > 0.9 * together && !few) plan(false);
+  }
   const size_t col = (size_t)hidden * sizeof(float);
   q.off_pre = 0;
   q.off_a = q.off_pre + col * q.grid;
-  q.bytes = q.off_a + col * units;
+  q.bytes = q.off_a + col * q.bs * q.upb;
   return q;
 }
 

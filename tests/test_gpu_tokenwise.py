@@ -956,3 +956,20 @@ def test_linear_residual_in_place(T, K, N, act, bias):
     y = r.clone()
     got = U.ulysses_linear(x, w, bias=b, residual=y, activation=ACTS[act], y=y)
     assert got.data_ptr() == y.data_ptr() and torch.equal(got, want)
+
+
+@pytest.mark.parametrize("P,B,s,D,dtype,gate", [
+    (1, 200, 60, 2560, torch.bfloat16, "sequence"),    # several sequences a CTA, each with its gate
+    (2, 300, 100, 1280, torch.bfloat16, "sequence"),
+    (1, 300, 20, 1280, torch.bfloat16, "sequence"),    # sequences too short for that
+    (3, 160, 7, 520, torch.bfloat16, "sequence"),
+    (1, 1, 444, 2560, torch.bfloat16, "channel"),      # the most rows that have a CTA each, and more
+    (1, 1, 445, 2560, torch.bfloat16, "channel"),
+    (1, 1, 1500, 2560, torch.bfloat16, "none"),
+    (1, 2, 500, 8192, torch.bfloat16, "sequence"),
+    (1, 1, 700, 8192, torch.bfloat16, "token"),        # two stages do not fit beside the weights
+    (1, 1, 30, 8192, torch.bfloat16, "channel"),
+    (1, 200, 50, 2056, torch.float32, "sequence"),
+])
+def test_residual_norm_backward_in_one_cta_or_several(P, B, s, D, dtype, gate):
+    test_residual_norm_backward(P, B, s, D, dtype, gate, True)
