@@ -49,7 +49,9 @@ uly_status linear_shape(int64_t tokens, int32_t in, int32_t out, int32_t act) {
   if (in % 8 || out % 8) return ULY_ERR_ALIGN;
   if (out > kMaxRows / 2 || in > kMaxRows) return ULY_ERR_SHAPE;
   auto tiles = [](long long v) { return (v + 127) / 128; };
-  const long long most = 0x7fffffffLL / 32;   // work units, cut up to 32 ways
+  // 32-bit work units: a tile each, fewer than (SM pairs)^2 more where the last turn's
+  // are cut, and eight rows of tiles at a time in the raster
+  const long long most = 0x7fffffffLL / 32;
   if (tiles(tokens) * tiles(out) > most || tiles(tokens) * tiles(in) > most || 2 * tiles(out) * tiles(in) > most)
     return ULY_ERR_SHAPE;
   return ULY_OK;
