@@ -37,7 +37,7 @@
 // runs on pairs of fp32 values.
 // 65536 x 2560 bf16 with a channel gate: forward 251 us (5.4 TB/s of its 1.34
 // GB), backward 416 us (4.8 TB/s of 2.01 GB) + 9 us of folding.  The forward is
-// near the memory's rate (a copy: 6.5 TB/s); the backward issues about 3800
+// near the memory's rate (a copy: 6.5 TB/s); the backward issues about 4100
 // instructions a row and its two row sums, one after the other, leave their latency
 // in the open (with a gate of every token it moves a third more in 460 us).
 #include <cooperative_groups.h>
