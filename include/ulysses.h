@@ -549,7 +549,9 @@ uly_status ulysses_linear_loss_bwd_workspace_size(int32_t world, int64_t tokens,
  * Several pieces sum dw in fp32 (for ULY_BF16 in vocab x hidden x 4 bytes of
  * the workspace) and round it once.  Rows of ignored or invalid labels give
  * zeros whatever x holds there.  With no counted token dx and dw are 0 and
- * *loss is NaN.  Same rules as ulysses_linear_loss; bitwise repeatable.
+ * *loss is NaN.  Logits of -inf (a masked part of the vocabulary) weigh nothing;
+ * a counted row that has no others, or a NaN, makes the loss and its gradient
+ * NaN.  Same rules as ulysses_linear_loss; bitwise repeatable.
  */
 uly_status ulysses_linear_loss_bwd(int32_t world, int64_t tokens, int32_t hidden, int32_t vocab, const void *x,
                                    const void *w, const int32_t *labels, int32_t ignore_index, void *dx, void *dw,
